@@ -336,6 +336,138 @@ MLA_API mla_status mla_decode_paged_static_ws(const mla_plan_info* info, const v
                             float softmax_scale, void* o_lat, float* lse, uint32_t* dev_error,
                             void* stream);
 
+/* ---------------------------------------------------------------- rotary positions
+ *
+ * The calls above take q_R and k_R already rotated (P1 section 1: the decoupled RoPE part of a
+ * head).  A rotation is a host struct of constants, filled once by mla_rope_init and passed to
+ * the calls below, which read it before they return:
+ *   pair i of the rotated `dim` elements of a head turns by the angle a = position * inv_freq[i],
+ *     y0 = m (x0 cos a - x1 sin a),  y1 = m (x0 sin a + x1 cos a),
+ *   with (x0, x1) the elements (2i, 2i + 1) (MLA_ROPE_INTERLEAVED) or (i, i + dim / 2)
+ *   (MLA_ROPE_HALF).  The angle is kept as a 64-bit fixed-point fraction of a turn, exact modulo
+ *   whole turns, so that far positions lose nothing; sines, cosines and sums are fp32 and the
+ *   result is rounded once.  Negative positions turn back. */
+#define MLA_ROPE_MAX_DIM 256
+typedef enum mla_rope_layout { MLA_ROPE_INTERLEAVED = 0, MLA_ROPE_HALF = 1 } mla_rope_layout;
+typedef enum mla_rope_scaling {
+    MLA_ROPE_NONE = 0,   /* inv_freq[i] = base^(-2i / dim) */
+    MLA_ROPE_LINEAR = 1, /* the same divided by factor (positions interpolated) */
+    MLA_ROPE_YARN = 2    /* YaRN (Peng et al. 2023, "NTK-by-parts"): pairs that turn more than
+                            beta_fast times over original_len positions keep their frequency, those
+                            that turn fewer than beta_slow times have it divided by factor, with a
+                            linear ramp over the pair index between the two (both ends rounded
+                            outwards to whole indexes); m = 0.1 ln(factor) + 1 unless given */
+} mla_rope_scaling;
+typedef struct mla_rope_options {
+    int32_t dim;            /* even, 2 .. MLA_ROPE_MAX_DIM */
+    int32_t layout;         /* mla_rope_layout */
+    int32_t scaling;        /* mla_rope_scaling */
+    int32_t original_len;   /* YaRN: the trained length, > 0 */
+    double base;            /* > 1, finite; 0 = 10000 */
+    double factor;          /* linear: > 0; YaRN: >= 1 */
+    double beta_fast;       /* YaRN; 0 = 32 */
+    double beta_slow;       /* YaRN; 0 = 1; beta_fast > beta_slow > 0 */
+    double magnitude;       /* m; > 0, finite; 0 = the scaling's own (1, but for YaRN) */
+    const double* inv_freq; /* host [dim / 2], each finite and >= 0: used as they are in place of the
+                               frequencies above (scaling must be MLA_ROPE_NONE); NULL = computed */
+} mla_rope_options;
+typedef struct mla_rope_config {
+    int32_t dim;
+    int32_t layout;
+    float magnitude;
+    int32_t reserved;
+    uint64_t step[MLA_ROPE_MAX_DIM / 2]; /* turns per position, in units of 2^-64 turn */
+} mla_rope_config;
+/* Fills *rope.  Pure host code: needs no GPU. */
+MLA_API mla_status mla_rope_init(const mla_rope_options* opts, mla_rope_config* rope);
+
+typedef enum mla_dtype { MLA_BF16 = 0, MLA_FP16 = 1, MLA_FP32 = 2 } mla_dtype;
+
+/* Rotates elements [rot_offset, rot_offset + rope->dim) of every head of x [num_tokens][num_heads]
+ * [head_dim] by the token's position.
+ *   x          device, element strides x_token_stride and x_head_stride (either may be 0)
+ *   out        device, element strides given; `rest` NULL: out has head_dim elements per head, the
+ *              rotated ones and the others copied; `rest` given: out has rope->dim elements per
+ *              head and the other head_dim - rope->dim go to rest in order (q [T][128][192] ->
+ *              q_R [T][128][64] and q_c [T][128][128] in one pass)
+ *   positions  device int32 [num_tokens]
+ * In place: out == x with the same strides and rest NULL; only the rotated elements are then
+ * touched.  Otherwise out, rest and x share no element.  Strides lie in [0, 2^40]; the elements of
+ * out (and of rest) must be distinct, or the call is refused (MLA_ERR_INVALID_ARG).  Pointers are
+ * aligned to their element; 16-byte aligned pointers and strides (and rot_offset, dim and the rest
+ * in whole 16-byte pieces) take the vector path.  num_tokens 0 enqueues nothing; num_tokens *
+ * num_heads < 2^31 and head_dim <= 65536, else MLA_ERR_UNSUPPORTED. */
+MLA_API mla_status mla_rope(const mla_rope_config* rope, mla_dtype dtype, int32_t num_tokens, int32_t num_heads,
+                            int32_t head_dim, int32_t rot_offset, const void* x, int64_t x_token_stride,
+                            int64_t x_head_stride, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                            void* rest, int64_t rest_token_stride, int64_t rest_head_stride, const int32_t* positions,
+                            void* stream);
+
+/* mla_append_kv with the position rotation applied on the way, and the new tokens' queries split
+ * and rotated in the same launch (`q` may be NULL): everything between a layer's projections and
+ * its decode.  rope->dim must be 64.
+ *   c_kv       device bf16, token i's 512 latent values at c_kv + i * c_kv_stride
+ *   k_r        device bf16, token i's 64 un-rotated key values at k_r + i * k_r_stride (for one
+ *              down projection's row of 576 both strides are that row's)
+ *   positions  device int32 [num_tokens]
+ *   slots, kv_dtype, num_pool_pages, kv_pool, kv_scale, kr_pool, dev_error   as mla_append_kv; the
+ *              stored latent is the same bit for bit, the stored key the rotated one in bf16.
+ *              No two tokens have the same slot (of two that do, each element of the row is
+ *              either's).
+ *   q          device bf16 [num_tokens][128][192], 128 content then 64 un-rotated values per
+ *              head, strides q_token_stride and q_head_stride; q_c [num_tokens][128][128] receives
+ *              the content, q_r [num_tokens][128][64] the rotated part, both contiguous.  Tokens
+ *              whose slot is negative or past the pool have their queries written all the same.
+ * All bf16 pointers 16-byte aligned, all strides multiples of 8 elements in [0, 2^40]; num_tokens
+ * at most 2^23 (else MLA_ERR_UNSUPPORTED).  num_tokens 0 enqueues nothing. */
+MLA_API mla_status mla_rope_append_kv(const mla_rope_config* rope, int32_t num_tokens, const void* c_kv,
+                                      int64_t c_kv_stride, const void* k_r, int64_t k_r_stride,
+                                      const int32_t* positions, const int32_t* slots, mla_kv_dtype kv_dtype,
+                                      int32_t num_pool_pages, void* kv_pool, float* kv_scale, void* kr_pool,
+                                      const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_c,
+                                      void* q_r, uint32_t* dev_error, void* stream);
+
+/* ---------------------------------------------------------------- few-row products with 4-bit weights
+ *
+ *   out[r,h,n] = tensor_scale * sum_k x[r,h,k] W[h,n,k]
+ * with W in 4 bits and a scale for each `group` consecutive k: the step's absorb (heads 128, n 512,
+ * k 128, W[h,c,d] = W_UK[h,d,c]) and value projection (heads 128, n 128, k 512), and the dense
+ * projections around it (heads 1), for the few rows of a decode batch.
+ *   codes  device uint8 [heads][n][k / 2], value 2j in the low nibble of byte j, 16-byte aligned
+ *   MLA_W4_INT4:  W = (code - zero) * scale, code 0..15; group 32, 64 or 128
+ *          scale  device bf16 [heads][n][k / group], 2-byte aligned
+ *          zero   device uint8 [heads][n][k / group], each 0..15, or NULL: 8 everywhere
+ *   MLA_W4_NVFP4: W = e2m1(code) * e4m3(scale); group 16
+ *          scale  device uint8 [heads][n][k / 16], e4m3 codes; zero NULL
+ *   k is a multiple of group and of 32; heads <= 65535, n * heads and k < 2^31.
+ *   x    device bf16, element strides x_row_stride and x_head_stride (0: one row for all heads),
+ *        multiples of 8, 16-byte aligned
+ *   out  device bf16, element strides out_row_stride and out_head_stride, distinct elements, sharing
+ *        none with x; 2-byte aligned
+ * Products are exact and summed in fp32; out is rounded once.  rows 0 enqueues nothing. */
+typedef enum mla_w4_format { MLA_W4_INT4 = 0, MLA_W4_NVFP4 = 1 } mla_w4_format;
+typedef struct mla_w4_weight {
+    int32_t format; /* mla_w4_format */
+    int32_t heads;
+    int32_t n;
+    int32_t k;
+    int32_t group;
+    float tensor_scale; /* finite */
+    const void* codes;
+    const void* scale;
+    const void* zero;
+} mla_w4_weight;
+MLA_API mla_status mla_linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t x_head_stride,
+                                 const mla_w4_weight* w, void* out, int64_t out_row_stride, int64_t out_head_stride,
+                                 void* stream);
+/* The step's two products with such weights, in the place of mla_absorb_q and mla_out_proj (batch > 0,
+ * contiguous rows): w_uk has heads 128, n 512, k 128 and w_uv heads 128, n 128, k 512.  As with those
+ * calls, the step's next kernel may start before they end and waits for their output itself. */
+MLA_API mla_status mla_absorb_q_w4(const void* q_c, const mla_w4_weight* w_uk, void* q_abs, int32_t batch,
+                                   void* stream);
+MLA_API mla_status mla_out_proj_w4(const void* o_lat, const mla_w4_weight* w_uv, void* out, int32_t batch,
+                                   void* stream);
+
 /* ---- prefill chunk, decompressed form -------------------------------------------------------
  * P1 section 4 gives two forms of the same attention: path A decompresses per-head keys and
  * values (k_h = W_UK[h] c, v_h = W_UV[h] c) and attends with head dim 128 + 64; path B absorbs

@@ -24,6 +24,12 @@ MLA_ERR_WORKSPACE, MLA_ERR_CUDA, MLA_ERR_DEVICE_FAULT = 4, 5, 6
 # mla_kv_dtype
 MLA_KV_BF16, MLA_KV_FP8_E4M3, MLA_KV_NVFP4 = 0, 1, 2
 NVFP4_ROW = D_C // 2 + D_C // 16  # bytes of one token's NVFP4 row: packed e2m1 codes, then e4m3 block scales
+# mla_dtype, mla_rope_layout, mla_rope_scaling, mla_w4_format
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "yarn": 2}
+MLA_ROPE_MAX_DIM = 256
+MLA_W4_INT4, MLA_W4_NVFP4 = 0, 1
 # device error bits
 MLA_DEVERR_BAD_PAGE, MLA_DEVERR_TIMEOUT, MLA_DEVERR_SMEM_ALIGN, MLA_DEVERR_BAD_PLAN = 1, 2, 4, 8
 
@@ -53,7 +59,8 @@ EXPORTS = ("mla_status_string", "mla_last_error_string", "mla_plan_bytes_max", "
            "mla_combine_splits", "mla_out_proj", "mla_read_device_error", "mla_debug_wait_timeout",
            "mla_decode_paged_static_ws", "mla_decode_step_host", "mla_append_kv", "mla_merge_out_proj",
            "mla_absorb_decode_paged", "mla_gather_kv", "mla_step_graph_create", "mla_step_graph_run",
-           "mla_step_graph_destroy", "mla_prefill_workspace_bytes", "mla_prefill_decompressed")
+           "mla_step_graph_destroy", "mla_prefill_workspace_bytes", "mla_prefill_decompressed",
+           "mla_rope_init", "mla_rope", "mla_rope_append_kv", "mla_linear_w4", "mla_absorb_q_w4", "mla_out_proj_w4")
 
 # capacity of the library's fixed split-partial array (mla_decode_paged_static_ws)
 MLA_STATIC_WS_MAX_PARTIALS = 128
@@ -68,6 +75,24 @@ class StepBuffers(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t), ("o_lat", ctypes.c_void_p), ("lse", ctypes.c_void_p),
                 ("out", ctypes.c_void_p), ("dev_error", ctypes.c_void_p), ("plan_host", ctypes.c_void_p),
                 ("plan_capacity", ctypes.c_size_t)]
+
+
+class RopeOptions(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("original_len", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double), ("magnitude", ctypes.c_double),
+                ("inv_freq", ctypes.c_void_p)]
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("step", ctypes.c_uint64 * (MLA_ROPE_MAX_DIM // 2))]
+
+
+class W4Struct(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("heads", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("tensor_scale", ctypes.c_float), ("codes", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p)]
 
 
 def lib() -> ctypes.CDLL:
@@ -126,6 +151,18 @@ def lib() -> ctypes.CDLL:
                                            P, sz, P, u32p, P]
     L.mla_append_kv.restype = ctypes.c_int
     L.mla_append_kv.argtypes = [i32, P, P, P, ctypes.c_int, i32, P, P, P, u32p, P]
+    L.mla_rope_init.restype = ctypes.c_int
+    L.mla_rope_init.argtypes = [P, P]
+    L.mla_rope.restype = ctypes.c_int
+    L.mla_rope.argtypes = [P, ctypes.c_int, i32, i32, i32, i32, P, i64, i64, P, i64, i64, P, i64, i64, P, P]
+    L.mla_rope_append_kv.restype = ctypes.c_int
+    L.mla_rope_append_kv.argtypes = [P, i32, P, i64, P, i64, P, P, ctypes.c_int, i32, P, P, P, P, i64, i64, P, P, P, P]
+    L.mla_linear_w4.restype = ctypes.c_int
+    L.mla_linear_w4.argtypes = [i32, P, i64, i64, P, P, i64, i64, P]
+    L.mla_absorb_q_w4.restype = ctypes.c_int
+    L.mla_absorb_q_w4.argtypes = [P, P, P, i32, P]
+    L.mla_out_proj_w4.restype = ctypes.c_int
+    L.mla_out_proj_w4.argtypes = [P, P, P, i32, P]
     L.mla_read_device_error.restype = ctypes.c_int
     L.mla_read_device_error.argtypes = [u32p, ctypes.POINTER(ctypes.c_uint32), P]
     L.mla_debug_wait_timeout.restype = ctypes.c_int
@@ -379,6 +416,210 @@ def mla_gather_kv(*, kv_pool: torch.Tensor, block_table: torch.Tensor, seq_lens:
     _check("mla_gather_kv", st)
 
 
+# --------------------------------------------------------------------------- rotary positions
+
+class Rope:
+    """The constants of a rotation (``mla_rope_config``), made once: ``dim`` rotated elements per
+    head, ``layout`` "interleaved" (pairs 2i, 2i + 1) or "half" (pairs i, i + dim / 2), frequencies
+    base^(-2i / dim) with ``scaling`` "none", "linear" (divided by ``factor``) or "yarn" (``factor``
+    over ``original_len`` trained positions), or the caller's ``inv_freq`` [dim / 2] as they are.
+    ``magnitude`` multiplies cos and sin (0: the scaling's own)."""
+
+    def __init__(self, dim: int = D_R, *, base: float = 10000.0, layout: str = "interleaved", scaling: str = "none",
+                 factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 magnitude: float = 0.0, inv_freq=None):
+        if layout not in _ROPE_LAYOUTS:
+            raise ValueError(f"layout must be one of {tuple(_ROPE_LAYOUTS)}, got {layout!r}")
+        if scaling not in _ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {tuple(_ROPE_SCALINGS)}, got {scaling!r}")
+        freq = None
+        if inv_freq is not None:
+            freq = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
+            if freq.shape != (int(dim) // 2,):
+                raise ValueError("inv_freq must hold dim / 2 frequencies")
+        opts = RopeOptions(int(dim), _ROPE_LAYOUTS[layout], _ROPE_SCALINGS[scaling], int(original_len), float(base),
+                           float(factor), float(beta_fast), float(beta_slow), float(magnitude),
+                           None if freq is None else freq.ctypes.data)
+        self.config = RopeConfig()
+        _check("mla_rope_init", lib().mla_rope_init(ctypes.byref(opts), ctypes.byref(self.config)))
+        self.dim, self.layout, self.magnitude = int(dim), layout, float(self.config.magnitude)
+        self._ref = ctypes.byref(self.config)
+
+
+def _here(device: int, **tensors) -> None:
+    """Every tensor (None skipped) is on the current CUDA device, where the kernel is launched."""
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name}: must be on the current CUDA device ({device}), is on {t.device}")
+
+
+def _rows3(t: torch.Tensor, name: str, dtype, shape) -> None:
+    """[a, b, width] of the given type and shape; any strides, the last one 1."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def mla_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, out: Optional[torch.Tensor] = None, *,
+             rest: Optional[torch.Tensor] = None, rot_offset: int = 0, stream=None) -> torch.Tensor:
+    """Rotate elements [rot_offset, rot_offset + rope.dim) of every head of x [tokens, heads,
+    head_dim] (bf16, fp16 or fp32; any strides, the last 1) by positions (int32 [tokens]) into
+    out, which it returns: x itself (None: in place), a tensor like x (the other elements copied),
+    or, with ``rest`` [tokens, heads, head_dim - dim], one of [tokens, heads, dim]."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be [tokens, heads, head_dim]")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"x: expected bfloat16, float16 or float32, got {x.dtype}")
+    T, H, D = x.shape
+    out = x if out is None else out
+    _rows3(x, "x", x.dtype, (T, H, D))
+    _rows3(out, "out", x.dtype, (T, H, D if rest is None else rope.dim))
+    if rest is not None:
+        _rows3(rest, "rest", x.dtype, (T, H, D - rope.dim))
+    _need(positions, "positions", torch.int32, (T,))
+    _here(torch.cuda.current_device(), x=x, out=out, rest=rest, positions=positions)
+    rs = (0, 0) if rest is None else rest.stride()
+    xs, os_ = x.stride(), out.stride()
+    st = lib().mla_rope(rope._ref, _DTYPES[x.dtype], T, H, D, int(rot_offset), x.data_ptr(), xs[0], xs[1],
+                        out.data_ptr(), os_[0], os_[1], None if rest is None else rest.data_ptr(), rs[0], rs[1],
+                        positions.data_ptr(), _stream(stream))
+    _check("mla_rope", st)
+    return out
+
+
+def mla_rope_append_kv(rope: Rope, c_kv: torch.Tensor, k_r: torch.Tensor, positions: torch.Tensor,
+                       slots: torch.Tensor, *, kv_pool: torch.Tensor, dev_error: torch.Tensor,
+                       kv_scale: Optional[torch.Tensor] = None, kr_pool: Optional[torch.Tensor] = None,
+                       q: Optional[torch.Tensor] = None, q_c: Optional[torch.Tensor] = None,
+                       q_r: Optional[torch.Tensor] = None, stream=None) -> None:
+    """mla_append_kv with k_r rotated by the tokens' positions on the way; c_kv [n, 512] and k_r
+    [n, 64] may be columns of a wider row.  With q [n, 128, 192] (content, then un-rotated part;
+    any strides, the last 1), q_c [n, 128, 128] and q_r [n, 128, 64] receive the split and rotated
+    queries in the same launch."""
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be a 1-d tensor")
+    n = int(slots.shape[0])
+    _need(slots, "slots", torch.int32, (n,))
+    _need(positions, "positions", torch.int32, (n,))
+    _rows3(c_kv, "c_kv", torch.bfloat16, (n, D_C))
+    _rows3(k_r, "k_r", torch.bfloat16, (n, D_R))
+    _need(dev_error, "dev_error", torch.int32, (1,))
+    dtype = _kv_dtype(kv_pool, kv_scale, kr_pool)
+    qs, q_ptr, qc_ptr, qr_ptr = (0, 0), None, None, None
+    if q is not None:
+        _rows3(q, "q", torch.bfloat16, (n, NUM_HEADS, D_HC + D_R))
+        _need(q_c, "q_c", torch.bfloat16, (n, NUM_HEADS, D_HC))
+        _need(q_r, "q_r", torch.bfloat16, (n, NUM_HEADS, D_R))
+        qs, q_ptr, qc_ptr, qr_ptr = q.stride(), q.data_ptr(), q_c.data_ptr(), q_r.data_ptr()
+    elif q_c is not None or q_r is not None:
+        raise ValueError("q_c and q_r need q")
+    _here(torch.cuda.current_device(), c_kv=c_kv, k_r=k_r, positions=positions, slots=slots, kv_pool=kv_pool,
+          kv_scale=kv_scale, kr_pool=kr_pool, dev_error=dev_error, q=q, q_c=q_c, q_r=q_r)
+    st = lib().mla_rope_append_kv(rope._ref, n, c_kv.data_ptr(), c_kv.stride(0), k_r.data_ptr(), k_r.stride(0),
+                                  positions.data_ptr(), slots.data_ptr(), dtype, int(kv_pool.shape[0]),
+                                  kv_pool.data_ptr(), None if kv_scale is None else kv_scale.data_ptr(),
+                                  None if kr_pool is None else kr_pool.data_ptr(), q_ptr, qs[0], qs[1], qc_ptr, qr_ptr,
+                                  dev_error.data_ptr(), _stream(stream))
+    _check("mla_rope_append_kv", st)
+
+
+# --------------------------------------------------------------------------- 4-bit weights
+
+class W4Weight:
+    """Weights [heads, n, k] in 4 bits (``mla_w4_weight``): ``codes`` uint8 [heads, n, k / 2] (value
+    2j in the low nibble of byte j) and a ``scale`` per group of k.  A bfloat16 scale [heads, n,
+    k / group], group 32, 64 or 128: int4, (code - zero) * scale, ``zero`` uint8 of the scale's shape
+    (None: 8).  A uint8 or float8_e4m3fn scale [heads, n, k / 16]: NVFP4, e2m1(code) * e4m3(scale).
+    ``tensor_scale`` multiplies every output.  Tensors without the leading dimension are one head.
+    For the decode step: W_UK as [128, 512, 128] (c, then d) and W_UV as [128, 128, 512]."""
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor, *, zero: Optional[torch.Tensor] = None,
+                 group: Optional[int] = None, tensor_scale: float = 1.0):
+        for name, t in (("codes", codes), ("scale", scale)) + ((("zero", zero),) if zero is not None else ()):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}: expected a tensor")
+            if t.dim() not in (2, 3) or t.dim() != codes.dim():
+                raise ValueError(f"{name}: must be [heads, n, ...] or [n, ...] like codes")
+        if scale.dtype == torch.float8_e4m3fn:
+            scale = scale.view(torch.uint8)
+        if scale.dtype not in (torch.bfloat16, torch.uint8):
+            raise TypeError(f"scale: expected bfloat16 (int4), uint8 or float8_e4m3fn (NVFP4), got {scale.dtype}")
+        self.format = MLA_W4_INT4 if scale.dtype == torch.bfloat16 else MLA_W4_NVFP4
+        heads, n = (1, codes.shape[0]) if codes.dim() == 2 else codes.shape[:2]
+        k = 2 * codes.shape[-1]
+        groups = scale.shape[-1]
+        if groups < 1 or k % groups or (group is not None and k != groups * group):
+            raise ValueError(f"scale: {groups} groups do not divide k = {k}" +
+                             ("" if group is None else f" into groups of {group}"))
+        self.heads, self.n, self.k, self.group = int(heads), int(n), int(k), k // groups
+        self.tensor_scale = float(tensor_scale)
+        allowed = (32, 64, 128) if self.format == MLA_W4_INT4 else (16,)
+        if self.group not in allowed or k % 32:
+            raise ValueError(f"groups of {self.group} over k = {k}: expected groups of {allowed} and k a multiple of 32")
+        if zero is not None and self.format == MLA_W4_NVFP4:
+            raise ValueError("zero points are for int4")
+        _need(codes, "codes", torch.uint8, device=False)
+        _need(scale, "scale", scale.dtype, tuple(codes.shape[:-1]) + (groups,), device=False)
+        if zero is not None:
+            _need(zero, "zero", torch.uint8, tuple(scale.shape), device=False)
+        self.codes, self.scale, self.zero = codes, scale, zero
+        self.device_index = codes.get_device()
+        if scale.get_device() != self.device_index or (zero is not None and zero.get_device() != self.device_index):
+            raise ValueError("codes, scale and zero: must be on one device")
+        self.struct = W4Struct(self.format, self.heads, self.n, self.k, self.group, self.tensor_scale,
+                               codes.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr())
+        self._ref = ctypes.byref(self.struct)
+
+
+def mla_linear_w4(x: torch.Tensor, w: W4Weight, out: torch.Tensor, stream=None) -> None:
+    """out[r, h, :] = W[h] x[r, h, :] for the few rows of a decode batch: x [rows, heads, k] and out
+    [rows, heads, n] bf16 (heads 1: [rows, k] and [rows, n] too), any strides, the last 1; x may be
+    expanded over the heads."""
+    if not isinstance(x, torch.Tensor) or not isinstance(out, torch.Tensor):
+        raise TypeError("x and out: expected tensors")
+    if w.heads == 1:
+        x = x.unsqueeze(1) if x.dim() == 2 else x
+        out = out.unsqueeze(1) if out.dim() == 2 else out
+    rows = x.shape[0]
+    _rows3(x, "x", torch.bfloat16, (rows, w.heads, w.k))
+    _rows3(out, "out", torch.bfloat16, (rows, w.heads, w.n))
+    device = torch.cuda.current_device()
+    _here(device, x=x, out=out)
+    if w.device_index != device:
+        raise ValueError(f"w: must be on the current CUDA device ({device})")
+    xs, os_ = x.stride(), out.stride()
+    st = lib().mla_linear_w4(rows, x.data_ptr(), xs[0], xs[1], w._ref, out.data_ptr(), os_[0], os_[1], _stream(stream))
+    _check("mla_linear_w4", st)
+
+
+def _head_product(fn: str, x: torch.Tensor, w: W4Weight, out: torch.Tensor, names, k: int, n: int, stream) -> None:
+    B = x.shape[0]
+    _need(x, names[0], torch.bfloat16, (B, NUM_HEADS, k))
+    _need(out, names[1], torch.bfloat16, (B, NUM_HEADS, n))
+    if (w.heads, w.n, w.k) != (NUM_HEADS, n, k):
+        raise ValueError(f"weights: expected [{NUM_HEADS}, {n}, {k}], got [{w.heads}, {w.n}, {w.k}]")
+    device = torch.cuda.current_device()
+    _here(device, **{names[0]: x, names[1]: out})
+    if w.device_index != device:
+        raise ValueError(f"weights: must be on the current CUDA device ({device})")
+    _check(fn, getattr(lib(), fn)(x.data_ptr(), w._ref, out.data_ptr(), B, _stream(stream)))
+
+
+def mla_absorb_q_w4(q_c: torch.Tensor, w_uk: W4Weight, q_abs: torch.Tensor, stream=None) -> None:
+    """mla_absorb_q with W_UK in 4 bits, laid out [128, 512, 128] (groups along d_hc)."""
+    _head_product("mla_absorb_q_w4", q_c, w_uk, q_abs, ("q_c", "q_abs"), D_HC, D_C, stream)
+
+
+def mla_out_proj_w4(o_lat: torch.Tensor, w_uv: W4Weight, out: torch.Tensor, stream=None) -> None:
+    """mla_out_proj with W_UV in 4 bits, laid out [128, 128, 512] (groups along d_c)."""
+    _head_product("mla_out_proj_w4", o_lat, w_uv, out, ("o_lat", "out"), D_C, D_HC, stream)
+
+
 # Chunks of at least this many new tokens take the decompressed form, shorter ones the absorbed
 # decode (page 1 section 3, kPrefillThresh in mla_config.h; section 6 measures the switch).
 PREFILL_THRESHOLD = 256
@@ -425,6 +666,8 @@ def prefill_chunk(seq_len: int, q_c: torch.Tensor, q_r: torch.Tensor, *, w_uk: t
                           kv_scale=kv_scale, kr_pool=kr_pool, device=q_c.device, queries_per_seq=T,
                           softmax_scale=softmax_scale)
         return step.run(q_c, q_r, stream), step.dev_error
+    if isinstance(w_uk, W4Weight) or isinstance(w_uv, W4Weight):
+        raise ValueError(f"prefill_chunk: chunks of {threshold} or more new tokens read bf16 weights")
     out = torch.empty(T, NUM_HEADS, D_HC, dtype=torch.bfloat16, device=q_c.device)
     err = torch.zeros(1, dtype=torch.int32, device=q_c.device)
     mla_prefill_decompressed(kv_pool=kv_pool, block_table_row=bt[0], seq_len=seq_len, q_c=q_c, q_r=q_r, w_uk=w_uk,
@@ -470,14 +713,21 @@ class DecodeStep:
     measured fastest order at every workload of the benchmark).  fused_absorb runs the absorb as
     the bf16 decode kernel's prologue (mla_absorb_decode_paged); fused_tail runs merge and
     projection as one kernel (mla_merge_out_proj).  All buffers are allocated here, by torch, once.
+    w_uk and w_uv may be 4-bit weights (W4Weight): the absorb and the projection are then
+    mla_absorb_q_w4 and mla_out_proj_w4 (not with the fused kernels, nor from host memory).  With
+    ``rope``, run_tokens takes the new tokens as their projections give them.
     """
 
-    def __init__(self, seq_lens, *, w_uk: torch.Tensor, w_uv: torch.Tensor, kv_pool: torch.Tensor,
+    def __init__(self, seq_lens, *, w_uk, w_uv, kv_pool: torch.Tensor,
                  block_table: torch.Tensor, kv_scale: Optional[torch.Tensor] = None,
                  kr_pool: Optional[torch.Tensor] = None, device=None, min_pages_per_split: int = 0,
                  max_clusters: int = 0, wait_timeout_ns: int = 0, item_cost_pages: int = 0,
                  softmax_scale: float = SOFTMAX_SCALE, fused_absorb: bool = False, fused_tail: bool = False,
-                 queries_per_seq: int = 1):
+                 queries_per_seq: int = 1, rope: Optional[Rope] = None):
+        if (fused_absorb and isinstance(w_uk, W4Weight)) or (fused_tail and isinstance(w_uv, W4Weight)):
+            raise ValueError("4-bit weights: the fused kernels read bf16 weights")
+        if rope is not None and rope.dim != D_R:
+            raise ValueError(f"rope: the step rotates {D_R} elements, got {rope.dim}")
         self.device = torch.device(device if device is not None else "cuda")
         self.seq_lens = np.asarray(seq_lens, dtype=np.int32)
         self.num_seqs = int(self.seq_lens.size)
@@ -505,6 +755,10 @@ class DecodeStep:
         self.out = torch.empty(B, NUM_HEADS, D_HC, dtype=torch.bfloat16, device=self.device)
         self.dev_error = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.absorb_sync = torch.zeros(2, dtype=torch.int32, device=self.device)  # absorb-in-decode job counter
+        self.rope = rope
+        if rope is not None:  # the split and rotated queries of run_tokens
+            self.q_c = torch.empty(B, NUM_HEADS, D_HC, dtype=torch.bfloat16, device=self.device)
+            self.q_r = torch.empty(B, NUM_HEADS, D_R, dtype=torch.bfloat16, device=self.device)
         self._h_stage = self._d_stage = None  # pinned host / device staging of run_host
         self._host_graph = None  # (mla_step_graph handle, key of the buffers and lengths it was made for)
 
@@ -515,15 +769,34 @@ class DecodeStep:
         if self.fused_absorb:
             mla_absorb_decode_paged(self.info, self.plan_dev, q_c, self.w_uk, self.q_abs, self.absorb_sync, q_r, **kv)
         else:
-            mla_absorb_q(q_c, self.w_uk, self.q_abs, stream)
+            absorb = mla_absorb_q_w4 if isinstance(self.w_uk, W4Weight) else mla_absorb_q
+            absorb(q_c, self.w_uk, self.q_abs, stream)
             mla_decode_paged(self.info, self.plan_dev, self.q_abs, q_r, **kv)
         if self.fused_tail:
             mla_merge_out_proj(self.info, self.plan_dev, self.workspace, self.o_lat, self.lse, self.w_uv, self.out,
                                self.dev_error, stream)
         else:
             mla_combine_splits(self.info, self.plan_dev, self.workspace, self.o_lat, self.lse, stream)
-            mla_out_proj(self.o_lat, self.w_uv, self.out, stream)
+            project = mla_out_proj_w4 if isinstance(self.w_uv, W4Weight) else mla_out_proj
+            project(self.o_lat, self.w_uv, self.out, stream)
         return self.out
+
+    def run_tokens(self, q: torch.Tensor, c_kv: torch.Tensor, k_r: torch.Tensor, positions: torch.Tensor,
+                   slots: torch.Tensor, stream=None) -> torch.Tensor:
+        """The step from the new tokens' projections: their rows into the cache with the keys
+        rotated, their queries q [rows, 128, 192] split and rotated (mla_rope_append_kv, one
+        launch), then ``run``.  Row b * queries_per_seq + t is new token t of sequence b, whose
+        length counts it; slots and positions are its place in the pool and in the sequence."""
+        if self.rope is None:
+            raise ValueError("run_tokens: construct the step with rope=")
+        if tuple(slots.shape) != (self.batch,):
+            raise ValueError(f"run_tokens: expected {self.batch} tokens, got slots {tuple(slots.shape)}")
+        if q is None:
+            raise ValueError("run_tokens: q is needed")
+        mla_rope_append_kv(self.rope, c_kv, k_r, positions, slots, kv_pool=self.kv_pool, kv_scale=self.kv_scale,
+                           kr_pool=self.kr_pool, dev_error=self.dev_error, q=q, q_c=self.q_c, q_r=self.q_r,
+                           stream=stream)
+        return self.run(self.q_c, self.q_r, stream)
 
     @staticmethod
     def _host_key(q_c, q_r, block_table, lens, out):
@@ -556,6 +829,8 @@ class DecodeStep:
         later calls with the same tensors and lengths only launch it (``mla_step_graph_run``),
         so a serving loop that writes each step's queries into the same pinned tensors pays for
         the copies and kernels only.  Otherwise each call is one ``mla_decode_step_host``."""
+        if isinstance(self.w_uk, W4Weight) or isinstance(self.w_uv, W4Weight):
+            raise ValueError("run_host: the step from host memory reads bf16 weights")
         lens = self.seq_lens if seq_lens is None else np.ascontiguousarray(np.asarray(seq_lens, dtype=np.int32))
         if self._host_graph is not None and out is not None:
             if self._host_key(q_c, q_r, block_table, lens, out) == self._host_graph[1]:

@@ -30,7 +30,8 @@ def _nvcc() -> str:
 
 
 def _sources():
-    return [os.path.join(CSRC, f) for f in ("api.cu", "static_ws.cu", "append.cu", "gather.cu", "plan.cpp")]
+    return [os.path.join(CSRC, f) for f in ("api.cu", "static_ws.cu", "append.cu", "gather.cu", "rope.cu", "w4.cu",
+                                           "plan.cpp")]
 
 
 def _deps():

@@ -1,0 +1,290 @@
+"""GPU parity of the products with 4-bit weights (mla_linear_w4, and as the decode step's absorb and
+value projection) against the formula in 64 bits.
+
+Tolerance, counted: the weights' values have at most 13 significant bits and x has 8, so that each
+product is exact in fp32.  An output is the sum of chains of at most k / 16 additions of tensor-core
+or fp32 partial sums and 16 more to join them and to apply the scales, each off by at most 2^-22 of
+the partial sum (the tensor core may truncate), so by at most 2^-22 (k / 16 + 16) sum |x| |W|; then
+half a bf16 step, 2^-8 of the value.  Over all outputs the partial sums are no larger than the
+outputs in the mean (terms of random sign), which bounds the relative L2 error by
+2^-8 + 2^-22 (k / 16 + 16).
+"""
+import os
+import sys
+
+import pytest
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+from parity_util import SCALE, TOL_BF16, assert_close  # noqa: E402
+
+from mla_latent_kv_absorb_gb300 import binding, synth  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+E2M1 = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64)
+
+
+def _weight(heads, n, k, fmt, group, zero, seed):
+    """(W4Weight, its values in 64 bits [heads, n, k])."""
+    g = torch.Generator().manual_seed(seed)
+    codes = torch.randint(0, 256, (heads, n, k // 2), generator=g, dtype=torch.uint8)
+    both = torch.stack([codes & 15, codes >> 4], -1).view(heads, n, k // group, group)
+    z = None
+    if fmt == "int4":
+        scale = (torch.randn(heads, n, k // group, generator=g) * 2 / k ** 0.5).bfloat16()
+        scale[0, 0, 0] = 0.0
+        if zero:
+            z = torch.randint(0, 16, (heads, n, k // group), generator=g, dtype=torch.uint8)
+        value = (both.double() - (8.0 if z is None else z.double()[..., None])) * scale.double()[..., None]
+        t = 1.0
+    else:
+        scale = torch.randint(0, 0x7F, (heads, n, k // group), generator=g, dtype=torch.uint8)  # subnormals and 0 too
+        scale |= torch.randint(0, 2, scale.shape, generator=g, dtype=torch.uint8) << 7
+        value = E2M1[both.long()] * scale.view(torch.float8_e4m3fn).double()[..., None]
+        t = 0.75 / 256
+    w = binding.W4Weight(codes.to(DEV), scale.to(DEV), zero=None if z is None else z.to(DEV), group=group, tensor_scale=t)
+    return w, (value.view(heads, n, k) * t).to(DEV)
+
+
+def _assert_product(out, x, value):
+    """out [rows, heads, n] against x [rows, heads, k] and value [heads, n, k]."""
+    x = x.double()
+    ref = torch.einsum("rhk,hnk->rhn", x, value)
+    size = torch.einsum("rhk,hnk->rhn", x.abs(), value.abs())
+    chain = 2.0 ** -22 * (x.shape[-1] / 16 + 16)
+    far = (out.double() - ref).abs()
+    tol = chain * size
+    bad = far > tol + 2.0 ** -8 * (ref.abs() + tol) + 1e-38
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} past the tolerance, first at {bad.nonzero()[0].tolist()}"
+    norm = float(ref.norm())
+    assert norm == 0 or float(far.norm()) / norm <= 2.0 ** -8 + chain
+
+
+FORMATS = [("int4", 32, False), ("int4", 64, True), ("int4", 128, True), ("int4", 128, False), ("nvfp4", 16, False)]
+
+
+@pytest.mark.parametrize("fmt,group,zero", FORMATS)
+@pytest.mark.parametrize("rows", [1, 2, 7, 8, 9, 16, 17, 31, 33, 64, 65, 130])
+def test_linear_rows(fmt, group, zero, rows):
+    w, value = _weight(1, 200, 640, fmt, group, zero, rows)
+    x = torch.randn(rows, 640, generator=torch.Generator().manual_seed(rows)).bfloat16().to(DEV)
+    out = torch.full((rows, 200), float("nan"), dtype=torch.bfloat16, device=DEV)
+    binding.mla_linear_w4(x, w, out)
+    _assert_product(out[:, None], x[:, None], value)
+
+
+@pytest.mark.parametrize("fmt,group,zero", FORMATS)
+@pytest.mark.parametrize("heads,n,k", [(1, 1, 128), (1, 16, 16384), (3, 15, 256), (1, 17, 384), (2, 129, 1152),
+                                       (1, 1000, 128), (1, 4099, 2048), (5, 64, 4224)])
+def test_linear_sizes(fmt, group, zero, heads, n, k):
+    for rows in (1, 11):
+        w, value = _weight(heads, n, k, fmt, group, zero, n + k)
+        x = torch.randn(rows, heads, k, generator=torch.Generator().manual_seed(k)).bfloat16().to(DEV)
+        out = torch.full((rows, heads, n), float("nan"), dtype=torch.bfloat16, device=DEV)
+        binding.mla_linear_w4(x, w, out)
+        _assert_product(out, x, value)
+
+
+@pytest.mark.parametrize("k", [32, 64, 96, 160, 2016])
+def test_linear_groups_of_32_at_any_multiple(k):
+    w, value = _weight(1, 40, k, "int4", 32, True, k)
+    x = torch.randn(5, 1, k, generator=torch.Generator().manual_seed(k)).bfloat16().to(DEV)
+    out = torch.empty(5, 1, 40, dtype=torch.bfloat16, device=DEV)
+    binding.mla_linear_w4(x, w, out)
+    _assert_product(out, x, value)
+
+
+def test_nvfp4_k_of_32():
+    w, value = _weight(2, 40, 32, "nvfp4", 16, False, 3)
+    x = torch.randn(3, 2, 32, generator=torch.Generator().manual_seed(4)).bfloat16().to(DEV)
+    out = torch.empty(3, 2, 40, dtype=torch.bfloat16, device=DEV)
+    binding.mla_linear_w4(x, w, out)
+    _assert_product(out, x, value)
+
+
+@pytest.mark.parametrize("rows", [1, 16, 130])
+@pytest.mark.parametrize("fmt,group,zero", FORMATS)
+def test_step_products(rows, fmt, group, zero):
+    g = torch.Generator().manual_seed(rows)
+    for fn, n, k in ((binding.mla_absorb_q_w4, 512, 128), (binding.mla_out_proj_w4, 128, 512)):
+        w, value = _weight(128, n, k, fmt, group, zero, n)
+        x = torch.randn(rows, 128, k, generator=g).bfloat16().to(DEV)
+        out = torch.full((rows, 128, n), float("nan"), dtype=torch.bfloat16, device=DEV)
+        fn(x, w, out)
+        _assert_product(out, x, value)
+        again = torch.empty_like(out)
+        binding.mla_linear_w4(x, w, again)
+        assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+def test_linear_strides(rows):
+    """Columns of wider rows, one row for all heads, outputs with odd strides: the contiguous call's
+    bits, and nothing around them touched."""
+    w, value = _weight(4, 100, 256, "int4", 64, True, 5)
+    g = torch.Generator().manual_seed(6)
+    wide = torch.randn(rows, 4 * 256 + 8, generator=g).bfloat16().to(DEV)
+    x = wide[:, 8:].unflatten(1, (4, 256))
+    want = torch.empty(rows, 4, 100, dtype=torch.bfloat16, device=DEV)
+    binding.mla_linear_w4(x.contiguous(), w, want)
+    _assert_product(want, x, value)
+    buf = torch.full((rows * 4 * 101 + 1,), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[1:].view(rows, 4, 101)[:, :, :100]
+    binding.mla_linear_w4(x, w, out)
+    assert torch.equal(out, want) and (buf[1:].view(rows, 4, 101)[:, :, 100] == 7.0).all() and buf[0] == 7.0
+    swapped = torch.empty(4, rows, 100, dtype=torch.bfloat16, device=DEV)
+    binding.mla_linear_w4(x, w, swapped.transpose(0, 1))
+    assert torch.equal(swapped.transpose(0, 1), want)
+    shared = x[:, :1].expand(rows, 4, 256)
+    out = torch.empty_like(want)
+    binding.mla_linear_w4(shared, w, out)
+    _assert_product(out, shared, value)
+    same_row = x[:1].expand(rows, 4, 256)
+    binding.mla_linear_w4(same_row, w, out)
+    assert torch.equal(out, want[:1].expand(rows, 4, 100))
+
+
+def test_linear_special_values():
+    """Zeros give zeros, a NaN or an infinity in one row of x stays in that row, infinite scales (int4)
+    reach the outputs of their own column only."""
+    w, _ = _weight(1, 50, 256, "int4", 64, False, 9)
+    x = torch.randn(12, 256, generator=torch.Generator().manual_seed(2)).bfloat16().to(DEV)
+    clean = torch.empty(12, 50, dtype=torch.bfloat16, device=DEV)
+    binding.mla_linear_w4(x, w, clean)
+    y = x.clone()
+    y[3, 100], y[9, 7] = float("nan"), float("inf")
+    out = torch.empty_like(clean)
+    binding.mla_linear_w4(y, w, out)
+    keep = [r for r in range(12) if r not in (3, 9)]
+    assert torch.equal(out[keep], clean[keep]) and out[3].isnan().all() and not out[9].isfinite().all()
+    binding.mla_linear_w4(torch.zeros_like(x), w, out)
+    assert (out == 0).all()
+    w.scale[0, 20, 1] = float("inf")
+    binding.mla_linear_w4(x, w, out)
+    keep = [c for c in range(50) if c != 20]
+    assert torch.equal(out[:, keep], clean[:, keep]) and not out[:, 20].isfinite().any()
+
+
+def test_linear_is_repeatable_and_runs_on_any_stream():
+    w, value = _weight(1, 2048, 4096, "int4", 128, True, 12)
+    x = torch.randn(4, 1, 4096, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    out = torch.empty(4, 1, 2048, dtype=torch.bfloat16, device=DEV)
+    binding.mla_linear_w4(x, w, out)
+    _assert_product(out, x, value)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    outs = [torch.empty_like(out) for _ in streams]
+    for s, o in zip(streams, outs):   # at once on three streams
+        for _ in range(5):
+            binding.mla_linear_w4(x, w, o, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, out) for o in outs)
+    graph = torch.cuda.CUDAGraph()
+    static = torch.zeros_like(x)
+    mid = torch.empty_like(out)
+    with torch.cuda.graph(graph):   # its output is the next call's input
+        binding.mla_linear_w4(static, w, mid)
+        binding.mla_linear_w4(static, w, out)
+    static.copy_(x)
+    graph.replay()
+    assert torch.equal(mid, outs[0]) and torch.equal(out, outs[0])
+
+
+def test_linear_chain_sees_the_previous_call():
+    """A product of a product, many times over in one stream: each call reads what the one before it
+    wrote."""
+    w, value = _weight(1, 256, 256, "int4", 32, False, 21)
+    x = torch.randn(2, 1, 256, generator=torch.Generator().manual_seed(3)).bfloat16().to(DEV)
+    bufs = [x.clone(), torch.empty_like(x)]
+    want = x
+    for _ in range(6):
+        out = torch.empty_like(x)
+        binding.mla_linear_w4(want, w, out)
+        torch.cuda.synchronize()
+        want = out
+    for i in range(6):
+        binding.mla_linear_w4(bufs[i % 2], w, bufs[(i + 1) % 2])
+    assert torch.equal(bufs[0], want)
+
+
+def test_linear_empty_and_refusals():
+    w, _ = _weight(1, 50, 256, "int4", 64, False, 9)
+    binding.mla_linear_w4(torch.empty(0, 256, dtype=torch.bfloat16, device=DEV), w,
+                          torch.empty(0, 50, dtype=torch.bfloat16, device=DEV))
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device=DEV)
+    out = torch.zeros(4, 50, dtype=torch.bfloat16, device=DEV)
+    for bad_x, bad_out in ((x[:, :128], out), (x, out[:, :49]), (x[:3], out), (x.t().contiguous().t(), out),
+                           (x.cpu(), out), (x, out.cpu())):
+        with pytest.raises(ValueError):
+            binding.mla_linear_w4(bad_x, w, bad_out)
+    for bad_x, bad_out in ((x.float(), out), (x, out.half())):
+        with pytest.raises(TypeError):
+            binding.mla_linear_w4(bad_x, w, bad_out)
+    with pytest.raises(binding.MlaError):
+        binding.mla_linear_w4(x, w, out[:1].expand(4, 50))
+    with pytest.raises(ValueError):
+        binding.mla_absorb_q_w4(torch.zeros(1, 128, 128, dtype=torch.bfloat16, device=DEV), w,
+                                torch.zeros(1, 128, 512, dtype=torch.bfloat16, device=DEV))
+    cpu = binding.W4Weight(w.codes.cpu(), w.scale.cpu())
+    with pytest.raises(ValueError):
+        binding.mla_linear_w4(x, cpu, out)
+
+
+def _attention(inp, q_c, q_r, k_val, v_val):
+    """The step in 64 bits: out [rows, 128, 128] for one query row per sequence."""
+    outs = []
+    pool = inp.pool.double().reshape(-1, 576).to(DEV)
+    for b, S in enumerate(inp.seq_lens):
+        idx = torch.tensor([int(inp.block_table[b, p // 64]) * 64 + p % 64 for p in range(int(S))], device=DEV)
+        c, kr = pool[idx, :512], pool[idx, 512:]
+        q_lat = torch.einsum("hd,hcd->hc", q_c[b].double(), k_val)
+        p = ((q_lat @ c.t() + q_r[b].double() @ kr.t()) * SCALE).softmax(-1)
+        outs.append(torch.einsum("hc,hdc->hd", p @ c, v_val))
+    return torch.stack(outs)
+
+
+@pytest.mark.parametrize("fmt,group,zero", FORMATS[:1] + FORMATS[2:3] + FORMATS[4:])
+def test_step_with_4_bit_weights(fmt, group, zero):
+    inp = synth.make_inputs([300, 1, 700], seed=71)
+    q_c, q_r, w_uk, w_uv, kv, bt = binding.inputs_to_device(inp, DEV)
+    uk, k_val = _weight(128, 512, 128, fmt, group, zero, 1)
+    uv, v_val = _weight(128, 128, 512, fmt, group, zero, 2)
+    # absolute bounds of the step's tolerance are for outputs of about 1: weights of unit rows
+    for w, v in ((uk, k_val), (uv, v_val)):
+        s = 1.0 / float(v.square().sum(-1).mean().sqrt()) * (0.5 if w is uk else 1.0)
+        w.struct.tensor_scale = s * w.tensor_scale
+        v *= w.struct.tensor_scale / w.tensor_scale
+    step = binding.DecodeStep(inp.seq_lens, w_uk=uk, w_uv=uv, block_table=bt, min_pages_per_split=2, **kv)
+    out = step.run(q_c, q_r).clone()
+    assert step.device_error() == 0
+    assert_close(out, _attention(inp, q_c, q_r, k_val, v_val), TOL_BF16, "out")
+    graph = step.capture(q_c, q_r)
+    step.out.zero_()
+    graph.replay()
+    assert torch.equal(step.out, out)
+    if step.graph_kernel_nodes is not None:
+        assert step.graph_kernel_nodes == step.launches_per_step
+    # one product in 4 bits, the other in bf16
+    mixed = binding.DecodeStep(inp.seq_lens, w_uk=uk, w_uv=w_uv, block_table=bt, fused_tail=True, **kv)
+    got = mixed.run(q_c, q_r)
+    assert_close(got, _attention(inp, q_c, q_r, k_val, w_uv.double()), TOL_BF16, "out (bf16 projection)")
+
+
+def test_4_bit_step_refusals():
+    inp = synth.make_inputs([300], seed=72)
+    q_c, q_r, w_uk, w_uv, kv, bt = binding.inputs_to_device(inp, DEV)
+    uk, _ = _weight(128, 512, 128, "int4", 32, False, 1)
+    uv, _ = _weight(128, 128, 512, "int4", 32, False, 2)
+    for kw in (dict(w_uk=uk, w_uv=w_uv, fused_absorb=True), dict(w_uk=w_uk, w_uv=uv, fused_tail=True)):
+        with pytest.raises(ValueError):
+            binding.DecodeStep(inp.seq_lens, block_table=bt, **kv, **kw)
+    step = binding.DecodeStep(inp.seq_lens, w_uk=uk, w_uv=uv, block_table=bt, **kv)
+    with pytest.raises(ValueError):
+        step.run_host(inp.q_c, inp.q_r)
+    with pytest.raises(ValueError):
+        binding.prefill_chunk(300, torch.zeros(260, 128, 128, dtype=torch.bfloat16, device=DEV),
+                              torch.zeros(260, 128, 64, dtype=torch.bfloat16, device=DEV), w_uk=uk, w_uv=uv,
+                              kv_pool=kv["kv_pool"], block_table_row=bt[0])
+    out, err = binding.prefill_chunk(300, q_c, q_r, w_uk=uk, w_uv=uv, kv_pool=kv["kv_pool"], block_table_row=bt[0])
+    assert torch.equal(out, step.run(q_c, q_r))
