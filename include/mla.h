@@ -410,8 +410,12 @@ MLA_API mla_status mla_rope(const mla_rope_config* rope, mla_dtype dtype, int32_
  *   k_r        device bf16, token i's 64 un-rotated key values at k_r + i * k_r_stride (for one
  *              down projection's row of 576 both strides are that row's)
  *   positions  device int32 [num_tokens]
- *   slots, kv_dtype, num_pool_pages, kv_pool, kv_scale, kr_pool, dev_error   as mla_append_kv; the
- *              stored latent is the same bit for bit, the stored key the rotated one in bf16.
+ *   slots, kv_dtype, num_pool_pages, kv_pool, kv_scale, kr_pool, dev_error   as mla_append_kv: the
+ *              stored latent of the bf16 and FP8 caches is the same bit for bit, the stored key the
+ *              rotated one in bf16.  NVFP4: sigma = max|c| * fp32(1 / 2688) and the block scale is
+ *              the e4m3 nearest (max|c| of the block / sigma) * fp32(1 / 6), where mla_append_kv has
+ *              quotients by 2688 and 6; the values differ only where a quotient lies at the border
+ *              of two codes (about 1 in 700 of N(0,1) latents, by one step of the format).
  *              No two tokens have the same slot (of two that do, each element of the row is
  *              either's).
  *   q          device bf16 [num_tokens][128][192], 128 content then 64 un-rotated values per

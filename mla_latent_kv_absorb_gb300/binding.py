@@ -191,9 +191,9 @@ def _addr(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+def _stream(stream):
+    if stream is None:  # the current stream's handle, without making a torch.cuda.Stream of it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -446,23 +446,34 @@ class Rope:
         self._ref = ctypes.byref(self.config)
 
 
-def _here(device: int, **tensors) -> None:
-    """Every tensor (None skipped) is on the current CUDA device, where the kernel is launched."""
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"{name}: must be on the current CUDA device ({device}), is on {t.device}")
-
-
-def _rows3(t: torch.Tensor, name: str, dtype, shape) -> None:
-    """[a, b, width] of the given type and shape; any strides, the last one 1."""
+def _refuse(t, name: str, dtype, shape, device: int):
+    """The error of a tensor that failed one of its checks."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if tuple(t.shape) != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and shape[-1] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: must be on the current CUDA device ({device}), is on {t.device}")
+    raise ValueError(f"{name}: must be contiguous (rows of a wider tensor: in the last dimension)")
+
+
+def _rows(t, name: str, dtype, shape, device: int) -> int:
+    """The address of a tensor of that type and shape on the current device (where the kernel is
+    launched); any strides but the last, which is 1."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != device or \
+            (t.stride(-1) != 1 and shape[-1] > 1):
+        _refuse(t, name, dtype, shape, device)
+    return t.data_ptr()
+
+
+def _whole(t, name: str, dtype, shape, device: int) -> int:
+    """The address of a contiguous tensor of that type and shape on the current device."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != device or \
+            not t.is_contiguous():
+        _refuse(t, name, dtype, shape, device)
+    return t.data_ptr()
 
 
 def mla_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, out: Optional[torch.Tensor] = None, *,
@@ -476,19 +487,22 @@ def mla_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, out: Optional
     if x.dtype not in _DTYPES:
         raise TypeError(f"x: expected bfloat16, float16 or float32, got {x.dtype}")
     T, H, D = x.shape
-    out = x if out is None else out
-    _rows3(x, "x", x.dtype, (T, H, D))
-    _rows3(out, "out", x.dtype, (T, H, D if rest is None else rope.dim))
-    if rest is not None:
-        _rows3(rest, "rest", x.dtype, (T, H, D - rope.dim))
-    _need(positions, "positions", torch.int32, (T,))
-    _here(torch.cuda.current_device(), x=x, out=out, rest=rest, positions=positions)
-    rs = (0, 0) if rest is None else rest.stride()
-    xs, os_ = x.stride(), out.stride()
-    st = lib().mla_rope(rope._ref, _DTYPES[x.dtype], T, H, D, int(rot_offset), x.data_ptr(), xs[0], xs[1],
-                        out.data_ptr(), os_[0], os_[1], None if rest is None else rest.data_ptr(), rs[0], rs[1],
-                        positions.data_ptr(), _stream(stream))
-    _check("mla_rope", st)
+    device, dtype, dim = torch._C._cuda_getDevice(), x.dtype, rope.dim
+    x_ptr, (xt, xh, _) = _rows(x, "x", dtype, (T, H, D), device), x.stride()
+    if rest is None:
+        if out is None:
+            out, out_ptr, ot, oh = x, x_ptr, xt, xh
+        else:
+            out_ptr, (ot, oh, _) = _rows(out, "out", dtype, (T, H, D), device), out.stride()
+        rest_ptr, rt, rh = None, 0, 0
+    else:
+        out_ptr, (ot, oh, _) = _rows(out, "out", dtype, (T, H, dim), device), out.stride()
+        rest_ptr, (rt, rh, _) = _rows(rest, "rest", dtype, (T, H, D - dim), device), rest.stride()
+    p_ptr = _whole(positions, "positions", torch.int32, (T,), device)
+    st = lib().mla_rope(rope._ref, _DTYPES[dtype], T, H, D, rot_offset, x_ptr, xt, xh, out_ptr, ot, oh, rest_ptr, rt,
+                        rh, p_ptr, _stream(stream))
+    if st:
+        _check("mla_rope", st)
     return out
 
 
@@ -503,29 +517,33 @@ def mla_rope_append_kv(rope: Rope, c_kv: torch.Tensor, k_r: torch.Tensor, positi
     queries in the same launch."""
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a 1-d tensor")
-    n = int(slots.shape[0])
-    _need(slots, "slots", torch.int32, (n,))
-    _need(positions, "positions", torch.int32, (n,))
-    _rows3(c_kv, "c_kv", torch.bfloat16, (n, D_C))
-    _rows3(k_r, "k_r", torch.bfloat16, (n, D_R))
-    _need(dev_error, "dev_error", torch.int32, (1,))
+    n, bf16, i32 = slots.shape[0], torch.bfloat16, torch.int32
+    device = torch._C._cuda_getDevice()
+    slots_ptr = _whole(slots, "slots", i32, (n,), device)
+    pos_ptr = _whole(positions, "positions", i32, (n,), device)
+    c_ptr = _rows(c_kv, "c_kv", bf16, (n, D_C), device)
+    k_ptr = _rows(k_r, "k_r", bf16, (n, D_R), device)
+    err_ptr = _whole(dev_error, "dev_error", i32, (1,), device)
     dtype = _kv_dtype(kv_pool, kv_scale, kr_pool)
-    qs, q_ptr, qc_ptr, qr_ptr = (0, 0), None, None, None
+    pages = kv_pool.shape[0]
+    scale_ptr = kr_ptr = q_ptr = qc_ptr = qr_ptr = None
+    if dtype != MLA_KV_BF16:
+        scale_ptr = _whole(kv_scale, "kv_scale", torch.float32, (pages, PAGE), device)
+        kr_ptr = _whole(kr_pool, "kr_pool", bf16, (pages, PAGE, D_R), device)
+    if kv_pool.get_device() != device:
+        _refuse(kv_pool, "kv_pool", kv_pool.dtype, tuple(kv_pool.shape), device)
+    qt = qh = 0
     if q is not None:
-        _rows3(q, "q", torch.bfloat16, (n, NUM_HEADS, D_HC + D_R))
-        _need(q_c, "q_c", torch.bfloat16, (n, NUM_HEADS, D_HC))
-        _need(q_r, "q_r", torch.bfloat16, (n, NUM_HEADS, D_R))
-        qs, q_ptr, qc_ptr, qr_ptr = q.stride(), q.data_ptr(), q_c.data_ptr(), q_r.data_ptr()
+        q_ptr, (qt, qh, _) = _rows(q, "q", bf16, (n, NUM_HEADS, D_HC + D_R), device), q.stride()
+        qc_ptr = _whole(q_c, "q_c", bf16, (n, NUM_HEADS, D_HC), device)
+        qr_ptr = _whole(q_r, "q_r", bf16, (n, NUM_HEADS, D_R), device)
     elif q_c is not None or q_r is not None:
         raise ValueError("q_c and q_r need q")
-    _here(torch.cuda.current_device(), c_kv=c_kv, k_r=k_r, positions=positions, slots=slots, kv_pool=kv_pool,
-          kv_scale=kv_scale, kr_pool=kr_pool, dev_error=dev_error, q=q, q_c=q_c, q_r=q_r)
-    st = lib().mla_rope_append_kv(rope._ref, n, c_kv.data_ptr(), c_kv.stride(0), k_r.data_ptr(), k_r.stride(0),
-                                  positions.data_ptr(), slots.data_ptr(), dtype, int(kv_pool.shape[0]),
-                                  kv_pool.data_ptr(), None if kv_scale is None else kv_scale.data_ptr(),
-                                  None if kr_pool is None else kr_pool.data_ptr(), q_ptr, qs[0], qs[1], qc_ptr, qr_ptr,
-                                  dev_error.data_ptr(), _stream(stream))
-    _check("mla_rope_append_kv", st)
+    st = lib().mla_rope_append_kv(rope._ref, n, c_ptr, c_kv.stride(0), k_ptr, k_r.stride(0), pos_ptr, slots_ptr, dtype,
+                                  pages, kv_pool.data_ptr(), scale_ptr, kr_ptr, q_ptr, qt, qh, qc_ptr, qr_ptr, err_ptr,
+                                  _stream(stream))
+    if st:
+        _check("mla_rope_append_kv", st)
 
 
 # --------------------------------------------------------------------------- 4-bit weights
@@ -585,29 +603,28 @@ def mla_linear_w4(x: torch.Tensor, w: W4Weight, out: torch.Tensor, stream=None) 
     if w.heads == 1:
         x = x.unsqueeze(1) if x.dim() == 2 else x
         out = out.unsqueeze(1) if out.dim() == 2 else out
-    rows = x.shape[0]
-    _rows3(x, "x", torch.bfloat16, (rows, w.heads, w.k))
-    _rows3(out, "out", torch.bfloat16, (rows, w.heads, w.n))
-    device = torch.cuda.current_device()
-    _here(device, x=x, out=out)
+    rows, heads, device = x.shape[0], w.heads, torch._C._cuda_getDevice()
+    x_ptr = _rows(x, "x", torch.bfloat16, (rows, heads, w.k), device)
+    out_ptr = _rows(out, "out", torch.bfloat16, (rows, heads, w.n), device)
     if w.device_index != device:
         raise ValueError(f"w: must be on the current CUDA device ({device})")
-    xs, os_ = x.stride(), out.stride()
-    st = lib().mla_linear_w4(rows, x.data_ptr(), xs[0], xs[1], w._ref, out.data_ptr(), os_[0], os_[1], _stream(stream))
-    _check("mla_linear_w4", st)
+    (xr, xh, _), (o_r, oh, _) = x.stride(), out.stride()
+    st = lib().mla_linear_w4(rows, x_ptr, xr, xh, w._ref, out_ptr, o_r, oh, _stream(stream))
+    if st:
+        _check("mla_linear_w4", st)
 
 
 def _head_product(fn: str, x: torch.Tensor, w: W4Weight, out: torch.Tensor, names, k: int, n: int, stream) -> None:
-    B = x.shape[0]
-    _need(x, names[0], torch.bfloat16, (B, NUM_HEADS, k))
-    _need(out, names[1], torch.bfloat16, (B, NUM_HEADS, n))
+    B, device = x.shape[0], torch._C._cuda_getDevice()
+    x_ptr = _whole(x, names[0], torch.bfloat16, (B, NUM_HEADS, k), device)
+    out_ptr = _whole(out, names[1], torch.bfloat16, (B, NUM_HEADS, n), device)
     if (w.heads, w.n, w.k) != (NUM_HEADS, n, k):
         raise ValueError(f"weights: expected [{NUM_HEADS}, {n}, {k}], got [{w.heads}, {w.n}, {w.k}]")
-    device = torch.cuda.current_device()
-    _here(device, **{names[0]: x, names[1]: out})
     if w.device_index != device:
         raise ValueError(f"weights: must be on the current CUDA device ({device})")
-    _check(fn, getattr(lib(), fn)(x.data_ptr(), w._ref, out.data_ptr(), B, _stream(stream)))
+    st = getattr(lib(), fn)(x_ptr, w._ref, out_ptr, B, _stream(stream))
+    if st:
+        _check(fn, st)
 
 
 def mla_absorb_q_w4(q_c: torch.Tensor, w_uk: W4Weight, q_abs: torch.Tensor, stream=None) -> None:

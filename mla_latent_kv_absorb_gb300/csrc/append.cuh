@@ -1,7 +1,7 @@
 // append.cuh -- what one warp writes of one token into the paged latent cache: the slot check and
 // the latent's 512 values as they are (bf16), as e4m3 codes with a scale per token, or as an NVFP4
-// row.  Shared by mla_append_kv (append.cu) and mla_rope_append_kv (rope.cu), whose rows are
-// therefore the same bit for bit.
+// row.  Shared by mla_append_kv (append.cu) and mla_rope_append_kv (rope.cu), whose bf16 and
+// e4m3 latents are therefore the same bit for bit.
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -132,7 +132,10 @@ __device__ __forceinline__ void store_latent_fp8(const uint4* __restrict__ src, 
 // byte j) then 32 e4m3 block scales.  Lane l owns block l, latent values [16 l, 16 l + 16): its
 // 8 code bytes and its scale byte.  All arithmetic in fp32 with IEEE division, in the order of the
 // format's definition; a block whose scale rounds to zero stores zeros of its values' signs.
-template <bool kLate = false>
+// kByProducts: the two constants are applied as products with their fp32 reciprocals, the way
+// tensor expressions divide by a number (max|c| / 2688.0 of a GPU tensor): values then differ from
+// the quotients' only where a quotient lies at the border between two codes.
+template <bool kLate = false, bool kByProducts = false>
 __device__ __forceinline__ void store_latent_nvfp4(const uint4* __restrict__ src, int lane, int64_t slot,
                                                    uint8_t* __restrict__ rows, float* __restrict__ scale)
 {
@@ -140,8 +143,10 @@ __device__ __forceinline__ void store_latent_nvfp4(const uint4* __restrict__ src
     float v[16];
     load_latent16<kLate>(src, lane, v);
     const float bmax = max_abs16(v), amax = warp_max(bmax);
-    const float sigma = amax > 0.f ? __fdiv_rn(amax, 2688.f) : 1.f;
-    const uint32_t s8 = e4m3x2(__fdiv_rn(__fdiv_rn(bmax, sigma), 6.f), 0.f) & 0xFFu;
+    const float over = kByProducts ? __fmul_rn(amax, 1.f / 2688.f) : __fdiv_rn(amax, 2688.f);
+    const float sigma = amax > 0.f ? over : 1.f;
+    const float sixes = __fdiv_rn(bmax, sigma);
+    const uint32_t s8 = e4m3x2(kByProducts ? __fmul_rn(sixes, 1.f / 6.f) : __fdiv_rn(sixes, 6.f), 0.f) & 0xFFu;
     const float den = __fmul_rn(sigma, e4m3_value(s8));
     uint32_t code[2] = {0u, 0u};
 #pragma unroll

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
         if constexpr (kCache == MLA_KV_FP8_E4M3)
             append::store_latent_fp8<true>(c, lane, slot, static_cast<uint4*>(a.pool), a.scale);
         else
-            append::store_latent_nvfp4<true>(c, lane, slot, static_cast<uint8_t*>(a.pool), a.scale);
+            append::store_latent_nvfp4<true, true>(c, lane, slot, static_cast<uint8_t*>(a.pool), a.scale);
         key = a.kr + slot * 64;
     }
     // lane l: pair l

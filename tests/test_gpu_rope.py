@@ -241,19 +241,50 @@ def _tokens(n, seed, pitch=576):
     return rows[:, :512], rows[:, 512:], pos, slots.to(DEV), q
 
 
+def _nvfp4_rows(c):
+    """The NVFP4 rows and scales of latents c [n, 512] by the rule of the rotated append, in fp32 on the
+    host: products with the reciprocals of 2688 and 6, the other quotients as they are."""
+    c = c.float().cpu().numpy()
+    top = np.abs(c).max(1)
+    sigma = np.where(top > 0, top * (np.float32(1) / np.float32(2688)), np.float32(1)).astype(np.float32)
+    blocks = c.reshape(-1, 32, 16)
+    unit = (np.abs(blocks).max(2) / sigma[:, None]) * (np.float32(1) / np.float32(6))
+    s8 = torch.from_numpy(unit).to(torch.float8_e4m3fn)
+    den = sigma[:, None, None] * s8.float().numpy()[:, :, None]
+    with np.errstate(divide="ignore", invalid="ignore"):
+        v = np.where(den == 0, blocks * np.float32(0), blocks / den)
+    a = np.abs(v)
+    code = np.zeros(v.shape, np.uint8)
+    for border, even_above in ((.25, False), (.75, True), (1.25, False), (1.75, True), (2.5, False), (3.5, True), (5.0, False)):
+        code += (a >= border) if even_above else (a > border)   # a tie goes to the even code
+    code = (code + 8 * np.signbit(v)).reshape(-1, 512).astype(np.uint8)
+    rows = np.concatenate([code[:, 0::2] | code[:, 1::2] << 4, s8.view(torch.uint8).numpy()], 1)
+    return torch.from_numpy(rows).to(DEV), torch.from_numpy(sigma).to(DEV)
+
+
 @pytest.mark.parametrize("layout", ["interleaved", "half"])
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "nvfp4"])
 @pytest.mark.parametrize("n,pitch,query", [(1, 576, True), (13, 2112, True), (300, 584, False), (65, 576, True)])
 def test_rope_append_is_rope_then_append(layout, kind, n, pitch, query):
     """The pools (untouched slots too) and the queries equal, bit for bit, those of mla_rope and
-    mla_append_kv one after the other, which have their own parity tests."""
+    mla_append_kv one after the other, which have their own parity tests; an NVFP4 row has its own
+    rule's bytes."""
     c_kv, k_r, pos, slots, q = _tokens(n, 40 + n, pitch)
+    if n > 8:
+        c_kv[3] = 0.0             # an all-zero row
+        c_kv[4, 16:32] *= 1e-9    # a block whose scale rounds to zero
+        c_kv[6, :16] = -0.0
     rope = binding.Rope(64, layout=layout, scaling="yarn", factor=8.0, original_len=4096)
     err = torch.zeros(1, dtype=torch.int32, device=DEV)
     a, b = _cache(kind), _cache(kind)
     rot = torch.empty(n, 1, 64, dtype=torch.bfloat16, device=DEV)
     binding.mla_rope(rope, k_r.unsqueeze(1), pos, rot)
     binding.mla_append_kv(c_kv.contiguous(), rot[:, 0].contiguous(), slots, dev_error=err, **a)
+    if kind == "nvfp4":
+        live = slots >= 0
+        rows, sigma = _nvfp4_rows(c_kv[live])
+        a["kv_pool"].view(-1, binding.NVFP4_ROW)[slots[live].long()] = rows
+        a["kv_scale"].view(-1)[slots[live].long()] = sigma
     outs = {}
     if query:
         outs = {"q": q, "q_c": torch.full((n, 128, 128), 9.0, dtype=torch.bfloat16, device=DEV),
