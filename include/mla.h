@@ -442,7 +442,7 @@ MLA_API mla_status mla_rope_append_kv(const mla_rope_config* rope, int32_t num_t
  *          scale  device bf16 [heads][n][k / group], 2-byte aligned
  *          zero   device uint8 [heads][n][k / group], each 0..15, or NULL: 8 everywhere
  *   MLA_W4_NVFP4: W = e2m1(code) * e4m3(scale); group 16
- *          scale  device uint8 [heads][n][k / 16], e4m3 codes; zero NULL
+ *          scale  device uint8 [heads][n][k / 16], finite e4m3 codes (not 0x7F or 0xFF); zero NULL
  *   k is a multiple of group and of 32; heads <= 65535, n * heads and k < 2^31.
  *   x    device bf16, element strides x_row_stride and x_head_stride (0: one row for all heads),
  *        multiples of 8, 16-byte aligned

@@ -1,8 +1,23 @@
 // w4.cu -- mla_linear_w4: out[r,h,n] = t * sum_k x[r,h,k] W[h,n,k] with W in 4 bits and a scale per
 // group of k (declared in include/mla.h).
 //
-// One warp per output column n of one head and per kRows rows of x: each lane takes 32 consecutive
-// k (16 bytes of codes) at a time, and the lanes' sums are joined at the end.
+// The weights are the M side of mma.sync m16n8k16 and eight rows of x its N side, so that a decode
+// batch fills the instruction and every weight is unpacked once for all rows (up to 64).  tcgen05
+// would want the unpacked weights in shared memory and a group's scale cannot be applied inside its
+// accumulator; at these row counts the product is bound by the weights' bytes, then by unpacking.
+//
+// A block takes 128 outputs of one head: eight warps, four over n (32 each) and two over k.  A stage
+// is 256 k: 16 KB of codes and 4 KB of x per eight rows, brought by cp.async into a ring.  Of a
+// warp's 128 k, lane 4 g + t holds word (q, t), the eight k from 32 q + 8 t, of rows g and g + 8:
+//   int4: (word >> 4 i) & 0x000F000F | 0x43004300 is the bf16 pair 128 + code of k i and i + 4; minus
+//         128 + zero it is exact.  The MMAs of a group start from zero, and the group's fp32 sums are
+//         scaled into the output's (the scale times a weight would round in bf16).
+//   NVFP4: the code's bits moved to bf16's sign, two exponent bits and one mantissa bit are its value
+//         times 2^-126; times scale 2^118 it is exact in bf16 (two times four significant bits), and
+//         the 2^8 left over goes into the tensor's scale.
+// x is taken in the same order of k (a byte permutation per pair).  Blocks of a cluster split k when
+// there are few output tiles; their sums, and the two k warps', are joined in a fixed order through
+// (distributed) shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -17,8 +32,25 @@
 
 namespace mla::w4 {
 
-constexpr int kWarps = 8;
-constexpr int kRows = 4;
+constexpr int kThreads = 256;
+constexpr int kTileN = 128;
+constexpr int kStageK = 256;
+constexpr int kCodeBytes = kTileN * kStageK / 2;
+constexpr int kRowTile = 8;                       // rows of x per MMA
+constexpr int kXBytes = kRowTile * kStageK * 2;   // of one row tile
+constexpr int kRedPitch = kTileN + 4;             // floats; the four lanes of a row hit different banks
+constexpr int kMaxRowTiles = 8;
+
+template <int RT>
+struct Ring {
+    static constexpr int kStageBytes = kCodeBytes + RT * kXBytes;
+    // two blocks per SM up to three row tiles, one above
+    static constexpr int kBlocks = RT <= 3 ? 2 : 1;
+    static constexpr int kStages = RT == 1 ? 5 : RT <= 3 ? 4 : RT <= 5 ? 5 : 4;
+    static constexpr int kBytes = kStages * kStageBytes;
+    static_assert(kBytes * kBlocks <= 225 * 1024, "shared memory of an SM");
+    static_assert(2 * RT * kRowTile * kRedPitch * 4 <= kBytes, "the sums are joined in the ring's memory");
+};
 
 struct Args {
     const __nv_bfloat16* x;
@@ -30,73 +62,357 @@ struct Args {
     int64_t out_row, out_head;
     float tensor_scale;
     int rows, n, k, group;
-    bool early;  // kernels behind this one may start before it ends (they wait for `out` themselves)
+    int splits;   // blocks of a cluster, over k
+    bool packed;  // the scales (and zeros) of 128 k are one aligned word
+    bool early;   // kernels behind this one may start before it ends (they wait for `out` themselves)
 };
 
-__device__ __forceinline__ float e2m1_value(uint32_t code)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid)
 {
-    const uint32_t m = code & 7u;
-    const float a = m < 2u ? 0.5f * (float)m : (float)(2u + (m & 1u)) * (float)(1u << (m >> 1)) * 0.25f;
-    return code & 8u ? -a : a;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ float e4m3_value(uint32_t code)
+__device__ __forceinline__ uint32_t lds32(uint32_t addr)
 {
-    uint32_t h2;
-    const uint16_t c = (uint16_t)(code & 0xFFu);
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
-    return __half2float(__ushort_as_half((unsigned short)(h2 & 0xFFFFu)));
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The pairs (i, i + 4), i = 0..3, of a word of eight int4 codes, minus 128 + zero (both halves of z).
+__device__ __forceinline__ void unpack_int4(uint32_t w, uint32_t z, uint32_t (&v)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = sub_bf16x2(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, z);
+}
+
+// The same pairs of e2m1 codes times s (scale 2^118 in both halves): values times scale 2^-8.
+__device__ __forceinline__ void unpack_e2m1(uint32_t w, uint32_t s, uint32_t (&v)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t mag = (i < 2 ? w << (6 - 4 * i) : w >> (4 * i - 6)) & 0x01C001C0u;
+        v[i] = mul_bf16x2(((w << (12 - 4 * i)) & 0x80008000u) | mag, s);
+    }
+}
+
+// e4m3 byte `sel` (0..7) of a row's eight scales as bf16 scale 2^118 in both halves: the byte's bits
+// at bf16's exponent and mantissa are scale 2^-120 (subnormals too); two exact products raise it.
+__device__ __forceinline__ uint32_t e4m3_scale(uint2 bytes, int sel)
+{
+    const uint32_t b = ((sel < 4 ? bytes.x : bytes.y) >> (8 * (sel & 3))) & 0xFFu;
+    const uint32_t one = ((b & 0x7Fu) << 4) | ((b & 0x80u) << 8);
+    const uint32_t two = __byte_perm(one, one, 0x1010);
+    constexpr uint32_t k127 = 0x7F007F00u, k111 = 0x77007700u;  // 2^127 and 2^111
+    return mul_bf16x2(mul_bf16x2(two, k127), k111);
+}
+
+// The scales (int4: up to four bf16; NVFP4: eight e4m3) and zeros of one row's 128 k from k0, packed;
+// groups at or past k read as 0.  `g` is the row's first scale.
 template <bool kInt4>
-__global__ void __launch_bounds__(kWarps * 32) linear_w4_kernel(const __grid_constant__ Args a)
+__device__ __forceinline__ void load_scales(const Args& a, int64_t g, int k0, uint2& s, uint32_t& z)
 {
-    dev::griddep_wait();
-    if (a.early) dev::griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, h = blockIdx.y, r0 = blockIdx.z * kRows;
-    const int n = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (n >= a.n) return;
-    const int64_t row = (int64_t)h * a.n + n;
-    const int groups = a.k / a.group;
-    float acc[kRows] = {};
-    for (int k = 32 * lane; k < a.k; k += 1024) {
-        const uint4 c4 = __ldcg(reinterpret_cast<const uint4*>(a.codes + row * (a.k / 2) + k / 2));
-        const uint32_t word[4] = {c4.x, c4.y, c4.z, c4.w};
+    s = make_uint2(0u, 0u);
+    z = 0x08080808u;
+    if constexpr (kInt4) {
+        const uint16_t* p = static_cast<const uint16_t*>(a.scale) + g + k0 / a.group;
+        const uint8_t* pz = a.zero + (a.zero ? g + k0 / a.group : 0);
+        if (a.packed) {
+            if (a.group == 128) {
+                s.x = __ldca(p);
+                if (a.zero) z = __ldca(pz);
+            } else if (a.group == 64) {
+                s.x = __ldca(reinterpret_cast<const uint32_t*>(p));
+                if (a.zero) z = __ldca(reinterpret_cast<const uint16_t*>(pz));
+            } else {
+                s = __ldca(reinterpret_cast<const uint2*>(p));
+                if (a.zero) z = __ldca(reinterpret_cast<const uint32_t*>(pz));
+            }
+        } else {
+            const int count = 128 / a.group;
+            for (int i = 0; i < count; ++i) {
+                if (k0 + i * a.group >= a.k) break;
+                const uint32_t v = __ldca(p + i);
+                (i < 2 ? s.x : s.y) |= v << (16 * (i & 1));
+                if (a.zero) z = (z & ~(0xFFu << (8 * i))) | ((uint32_t)__ldca(pz + i) << (8 * i));
+            }
+        }
+    } else {
+        const uint8_t* p = static_cast<const uint8_t*>(a.scale) + g + k0 / 16;
+        if (a.packed) {
+            s = __ldca(reinterpret_cast<const uint2*>(p));
+        } else {
+            for (int i = 0; i < 8; ++i) {
+                if (k0 + 16 * i >= a.k) break;
+                (i < 4 ? s.x : s.y) |= (uint32_t)__ldca(p + i) << (8 * (i & 3));
+            }
+        }
+    }
+}
+
+template <bool kInt4, int RT>
+__global__ void __launch_bounds__(kThreads, Ring<RT>::kBlocks) linear_w4_kernel(const __grid_constant__ Args a)
+{
+    using R = Ring<RT>;
+    using namespace dev;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int wn = warp & 3, wk = warp >> 2, g = lane >> 2, t = lane & 3;
+    const int rank = (int)blockIdx.x % a.splits, n0 = (int)blockIdx.x / a.splits * kTileN;
+    const int h = blockIdx.y, r0 = (int)blockIdx.z * (RT * kRowTile);
+    const int total = (a.k + kStageK - 1) / kStageK;
+    const int first = (int)((int64_t)total * rank / a.splits), last = (int)((int64_t)total * (rank + 1) / a.splits);
+
+    // this thread's part of a stage: 16-byte piece tid % 8 of code rows tid / 8 + 32 j, and piece
+    // tid % 32 of x rows tid / 32 + 8 j
+    const int crow = tid >> 3, cpiece = tid & 7, xrow = tid >> 5, xpiece = tid & 31;
+    const uint8_t* csrc = a.codes + ((int64_t)h * a.n + n0 + crow) * (a.k / 2) + cpiece * 16;
+    const uint32_t cdst = sbase + crow * 128 + ((cpiece ^ (crow & 7)) << 4);
+    const __nv_bfloat16* xsrc = a.x + (int64_t)(r0 + xrow) * a.x_row + (int64_t)h * a.x_head + xpiece * 8;
+    const uint32_t xdst = sbase + kCodeBytes + xrow * 512 + ((xpiece ^ ((xrow & 1) << 2)) << 4);
+    const auto load_codes = [&](int stage, int slot) {
+        const bool k_ok = stage * kStageK + cpiece * 32 < a.k;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int64_t g = row * groups + (k + 8 * j) / a.group;
-            float s, z = 0.f;
-            if (kInt4) {
-                s = __bfloat162float(__ldcg(static_cast<const __nv_bfloat16*>(a.scale) + g));
-                z = a.zero ? (float)__ldcg(a.zero + g) : 8.f;
-            } else {
-                s = e4m3_value(__ldcg(static_cast<const uint8_t*>(a.scale) + g));
+            const bool ok = k_ok && n0 + crow + 32 * j < a.n;
+            cp_async16(cdst + slot * R::kStageBytes + j * 32 * 128,
+                       ok ? csrc + (int64_t)j * 32 * (a.k / 2) + stage * (kStageK / 2) : a.codes, ok);
+        }
+    };
+    const auto load_x = [&](int stage, int slot) {
+        const bool k_ok = stage * kStageK + xpiece * 8 < a.k;
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+            const bool ok = k_ok && r0 + xrow + 8 * j < a.rows;
+            cp_async16(xdst + slot * R::kStageBytes + j * kXBytes,
+                       ok ? xsrc + (int64_t)j * 8 * a.x_row + stage * kStageK : a.x, ok);
+        }
+    };
+    constexpr int kAhead = R::kStages - 1;
+    if (a.early) {  // the step's weights do not depend on the kernel before this one
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (first + i < last) load_codes(first + i, i);
+    }
+    griddep_wait();
+    if (a.early) griddep_launch_dependents();
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        if (first + i < last) {
+            if (!a.early) load_codes(first + i, i);
+            load_x(first + i, i);
+        }
+        cp_async_commit();
+    }
+
+    float acc[2][RT][4] = {};
+    // first scale of the four rows (m, half): rows past n read row n - 1's, and their sums go nowhere
+    const int groups = a.k / a.group;
+    int64_t srow[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = n0 + 32 * wn + 8 * i + g;
+        srow[i] = ((int64_t)h * a.n + (n < a.n ? n : a.n - 1)) * groups;
+    }
+    const uint32_t crd = sbase + (32 * wn + g) * 128 + 4 * t, xrd = sbase + kCodeBytes + g * 512;
+    const int xswap = (g & 1) << 2;
+    const int shift = a.group == 32 ? 0 : a.group == 64 ? 1 : 2, mask = (1 << shift) - 1;  // int4: q's of a group
+
+    for (int stage = first, i = 0; stage < last; ++stage, ++i) {
+        const int k0 = stage * kStageK + wk * 128;
+        const bool busy = k0 < a.k;
+        uint2 s[4];
+        uint32_t z[4];
+        if (busy) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load_scales<kInt4>(a, srow[j], k0, s[j], z[j]);
+        }
+        cp_async_wait<kAhead - 1>();
+        __syncthreads();  // this stage has landed, and the slot of the one before is free
+        if (stage + kAhead < last) {
+            const int slot = (i + kAhead) % R::kStages;
+            load_codes(stage + kAhead, slot);
+            load_x(stage + kAhead, slot);
+        }
+        cp_async_commit();
+        if (!busy) continue;
+        const uint32_t at = (uint32_t)(i % R::kStages) * R::kStageBytes;
+        float part[2][RT][4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t b[RT][4];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const uint4 v = lds128(xrd + at + rt * kXBytes + (((16 * wk + 4 * q + t) ^ xswap) << 4));
+                b[rt][0] = __byte_perm(v.x, v.z, 0x5410);  // k 0 and 4
+                b[rt][1] = __byte_perm(v.x, v.z, 0x7632);  // 1 and 5
+                b[rt][2] = __byte_perm(v.y, v.w, 0x5410);
+                b[rt][3] = __byte_perm(v.y, v.w, 0x7632);
             }
-            float w[8];
+            if (kInt4 && (q & mask) == 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t code = (word[j] >> (4 * i)) & 15u;
-                w[i] = (kInt4 ? (float)code - z : e2m1_value(code)) * s;
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) part[m][rt][e] = 0.f;
             }
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                if (r0 + r >= a.rows) break;
-                const uint4 v = __ldcg(reinterpret_cast<const uint4*>(a.x + (r0 + r) * a.x_row + h * a.x_head + k + 8 * j));
-                const uint32_t xv[4] = {v.x, v.y, v.z, v.w};
+            for (int m = 0; m < 2; ++m) {
+                uint32_t lo[4], hi[4];  // rows g and g + 8
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[r] += dev::bf16_lo(xv[i]) * w[2 * i];
-                    acc[r] += dev::bf16_hi(xv[i]) * w[2 * i + 1];
+                for (int half = 0; half < 2; ++half) {
+                    const int row = 16 * m + 8 * half;  // (32 wn + row + g) & 7 = g
+                    const uint32_t w = lds32(crd + at + row * 128 + (((4 * wk + q) ^ g) << 4));
+                    uint32_t(&v)[4] = half ? hi : lo;
+                    if constexpr (kInt4) {
+                        const uint32_t zero = (z[2 * m + half] >> (8 * (q >> shift))) & 0xFFu;
+                        unpack_int4(w, __byte_perm(zero, zero, 0x1010) | 0x43004300u, v);
+                    } else {
+                        unpack_e2m1(w, e4m3_scale(s[2 * m + half], 2 * q + (t >> 1)), v);
+                    }
+                }
+                const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    mma(kInt4 ? part[m][rt] : acc[m][rt], a0, b[rt][0], b[rt][1]);
+                    mma(kInt4 ? part[m][rt] : acc[m][rt], a1, b[rt][2], b[rt][3]);
+                }
+            }
+            if (kInt4 && (q & mask) == mask) {
+                const int j = q >> shift;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    float sc[2];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t w = j < 2 ? s[2 * m + half].x : s[2 * m + half].y;
+                        sc[half] = j & 1 ? bf16_hi(w) : bf16_lo(w);
+                    }
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[m][rt][e] += sc[e >> 1] * part[m][rt][e];
                 }
             }
         }
     }
+
+    cp_async_wait<0>();
+    __syncthreads();  // every warp has left the ring: its memory takes the sums, [wk][row][n]
+    float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], off);
-        if (lane == 0 && r0 + r < a.rows)
-            a.out[(r0 + r) * a.out_row + h * a.out_head + n] = __float2bfloat16_rn(acc[r] * a.tensor_scale);
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                red[(wk * RT * kRowTile + rt * kRowTile + 2 * t + (e & 1)) * kRedPitch + 32 * wn + 16 * m + 8 * (e >> 1) + g] =
+                    acc[m][rt][e];
+    __syncwarp();
+    if (a.splits > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    const int rows = a.rows - r0 < RT * kRowTile ? a.rows - r0 : RT * kRowTile;
+    for (int e = rank * kThreads + tid; e < rows * kTileN; e += a.splits * kThreads) {
+        const int r = e / kTileN, n = e % kTileN;
+        if (n0 + n >= a.n) continue;
+        const uint32_t at = sbase + (r * kRedPitch + n) * 4, other = RT * kRowTile * kRedPitch * 4;
+        float sum = 0.f;
+        if (a.splits > 1) {
+            for (int p = 0; p < a.splits; ++p) {
+                const uint32_t peer = map_to_cta(at, p);
+                sum += ld_cluster_f32(peer) + ld_cluster_f32(peer + other);
+            }
+        } else {
+            sum = red[r * kRedPitch + n] + red[(RT * kRowTile + r) * kRedPitch + n];
+        }
+        a.out[(int64_t)(r0 + r) * a.out_row + (int64_t)h * a.out_head + n0 + n] = 
+            __float2bfloat16_rn((kInt4 ? sum : sum * 256.f) * a.tensor_scale);
+    }
+    __syncwarp();
+    if (a.splits > 1) cluster_sync();  // no block leaves while another reads its sums
+}
+
+template <bool kInt4, int RT>
+mla_status launch(const Args& a, int heads, void* stream)
+{
+    const auto kernel = linear_w4_kernel<kInt4, RT>;
+    const mla_status st = cuda_status(
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<RT>::kBytes),
+        "cudaFuncSetAttribute(max dynamic shared memory)");
+    if (st != MLA_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.n + kTileN - 1) / kTileN * a.splits), (unsigned)heads,
+                       (unsigned)((a.rows + RT * kRowTile - 1) / (RT * kRowTile)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Ring<RT>::kBytes;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, a), "4-bit product kernel launch");
+}
+
+template <bool kInt4>
+mla_status launch_rows(const Args& a, int heads, void* stream)
+{
+    switch ((a.rows + kRowTile - 1) / kRowTile) {
+        case 1: return launch<kInt4, 1>(a, heads, stream);
+        case 2: return launch<kInt4, 2>(a, heads, stream);
+        case 3: return launch<kInt4, 3>(a, heads, stream);
+        case 4: return launch<kInt4, 4>(a, heads, stream);
+        case 5: return launch<kInt4, 5>(a, heads, stream);
+        case 6: return launch<kInt4, 6>(a, heads, stream);
+        default: return launch<kInt4, 8>(a, heads, stream);
     }
 }
 
@@ -124,7 +440,7 @@ mla_status linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t 
     if (!is_aligned(x, 16) || !is_aligned(w->codes, 16) || !is_aligned(out, 2) || (int4 && !is_aligned(w->scale, 2)) ||
         (rows > 1 && x_row_stride % 8) || (w->heads > 1 && x_head_stride % 8))
         return MLA_ERR_ALIGNMENT;
-    if (w->heads > 65535 || (int64_t)w->heads * w->n >= ((int64_t)1 << 31) || rows > 65535 * kRows)
+    if (w->heads > 65535 || (int64_t)w->heads * w->n >= ((int64_t)1 << 31) || rows > 65535 * kMaxRowTiles * kRowTile)
         return MLA_ERR_UNSUPPORTED;
     Args a = {};
     a.x = static_cast<const __nv_bfloat16*>(x);
@@ -142,9 +458,15 @@ mla_status linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t 
     a.k = w->k;
     a.group = w->group;
     a.early = early;
-    const dim3 grid((unsigned)((w->n + kWarps - 1) / kWarps), (unsigned)w->heads, (unsigned)((rows + kRows - 1) / kRows));
-    return mla::launch_dependent("4-bit product kernel launch", int4 ? linear_w4_kernel<true> : linear_w4_kernel<false>,
-                                 grid, dim3(kWarps * 32), 0, stream, a);
+    a.packed = w->k % 128 == 0 && is_aligned(w->scale, 8) && is_aligned(w->zero, 4);
+    // blocks of a cluster over k: doubled while there are too few tiles for two blocks per SM and
+    // every block keeps two stages
+    const int64_t row_blocks = (rows + kMaxRowTiles * kRowTile - 1) / (kMaxRowTiles * kRowTile);
+    const int64_t tiles = (int64_t)((w->n + kTileN - 1) / kTileN) * w->heads * row_blocks;
+    const int stages = (w->k + kStageK - 1) / kStageK;
+    a.splits = 1;
+    while (a.splits < 8 && tiles * a.splits < 2 * 152 && stages >= 4 * a.splits) a.splits *= 2;
+    return int4 ? launch_rows<true>(a, w->heads, stream) : launch_rows<false>(a, w->heads, stream);
 }
 
 // The step's per-head products: 128 heads, contiguous rows.
