@@ -7,16 +7,22 @@
 // accumulator; at these row counts the product is bound by the weights' bytes, then by unpacking.
 //
 // A block takes 128 outputs of one head: eight warps, four over n (32 each) and two over k.  A stage
-// is 256 k: 16 KB of codes and 4 KB of x per eight rows, brought by cp.async into a ring.  Of a
-// warp's 128 k, lane 4 g + t holds word (q, t), the eight k from 32 q + 8 t, of rows g and g + 8:
-//   int4: (word >> 4 i) & 0x000F000F | 0x43004300 is the bf16 pair 128 + code of k i and i + 4; minus
-//         128 + zero it is exact.  The MMAs of a group start from zero, and the group's fp32 sums are
-//         scaled into the output's (the scale times a weight would round in bf16).
+// is 256 k: 16 KB of codes, brought by cp.async into a ring, and 4 KB of x per eight rows, which the
+// threads bring through registers one stage ahead.  Of a warp's 128 k, lane 4 g + t holds word (q,
+// t), the eight k from 32 q + 8 t, of rows g and g + 8.  Unpacking is bound by the integer pipe,
+// which runs at half the rate of the FMA pipes (measured: 54 % of it busy where the FMA pipes were
+// at 12 %), so it is built from as few integer operations as there are:
+//   int4: the bits (w & 0x000F000F) are, as a pair of bf16, code 2^-133 for k i and i + 4 (subnormal
+//         bf16 is linear in its bits, and still is one binade up, so (w & 0x00F000F0) is 16 code
+//         2^-133); one bf16 FMA with 2^127 or 2^123 and -zero / 64 makes (code - zero) / 64 exactly.
+//         Five integer operations and four FMAs a word.  The MMAs of a group start from zero, and
+//         the group's fp32 sums are scaled into the output's (the scale times a weight would round
+//         in bf16).
 //   NVFP4: the code's bits moved to bf16's sign, two exponent bits and one mantissa bit are its value
-//         times 2^-126; times scale 2^118 it is exact in bf16 (two times four significant bits), and
-//         the 2^8 left over goes into the tensor's scale.
-// x is taken in the same order of k (a byte permutation per pair).  Blocks of a cluster split k when
-// there are few output tiles; their sums, and the two k warps', are joined in a fixed order through
+//         times 2^-126; times scale 2^118 it is exact in bf16 (two times four significant bits).
+// The powers of two left over, 2^6 and 2^8, go into the end's product.  x is stored in the order of
+// k that the words have, (0, 4), (1, 5), (2, 6), (3, 7).  Blocks of a cluster split k when there are
+// few output tiles; their sums, and the two k warps', are joined in a fixed order through
 // (distributed) shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,12 +49,13 @@ constexpr int kMaxRowTiles = 8;
 
 template <int RT>
 struct Ring {
-    static constexpr int kStageBytes = kCodeBytes + RT * kXBytes;
     // two blocks per SM up to three row tiles, one above
     static constexpr int kBlocks = RT <= 3 ? 2 : 1;
-    static constexpr int kStages = RT == 1 ? 5 : RT <= 3 ? 4 : RT <= 5 ? 5 : 4;
-    static constexpr int kBytes = kStages * kStageBytes;
-    static_assert(kBytes * kBlocks <= 225 * 1024, "shared memory of an SM");
+    static constexpr int kStages = RT <= 2 ? 6 : RT == 3 ? 5 : RT <= 5 ? 8 : RT == 6 ? 7 : 6;
+    static constexpr int kXOff = kStages * kCodeBytes;
+    static constexpr int kXSlot = RT * kXBytes;
+    static constexpr int kBytes = kXOff + 2 * kXSlot;
+    static_assert((kBytes + 1024) * kBlocks <= 228 * 1024, "shared memory of an SM");
     static_assert(2 * RT * kRowTile * kRedPitch * 4 <= kBytes, "the sums are joined in the ring's memory");
 };
 
@@ -61,13 +68,18 @@ struct Args {
     __nv_bfloat16* out;
     int64_t out_row, out_head;
     float tensor_scale;
-    int rows, n, k, group;
+    int rows, n, k;
     int splits;   // blocks of a cluster, over k
     bool packed;  // the scales (and zeros) of 128 k are one aligned word
     bool early;   // kernels behind this one may start before it ends (they wait for `out` themselves)
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// 16 bytes of zeros where !valid (src is then not read)
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool valid)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
 }
@@ -90,6 +102,10 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr)
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
 {
     float v;
@@ -106,10 +122,10 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c)
 {
     uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
@@ -119,49 +135,61 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
     return r;
 }
 
-// The pairs (i, i + 4), i = 0..3, of a word of eight int4 codes, minus 128 + zero (both halves of z).
+// bf16 pairs of powers of two
+constexpr uint32_t k2p127 = 0x7F007F00u, k2p123 = 0x7D007D00u, k2p111 = 0x77007700u, kMinus2p127 = 0xFF00FF00u;
+
+// -zero / 64 in both halves, of byte j of z
+__device__ __forceinline__ uint32_t minus_zero(uint32_t z, int j)
+{
+    return mul_bf16x2(__byte_perm(z, 0u, 0x4040u | j | (j << 8)), kMinus2p127);
+}
+
+// The pairs (i, i + 4), i = 0..3, of a word of eight int4 codes: (code - zero) / 64.
 __device__ __forceinline__ void unpack_int4(uint32_t w, uint32_t z, uint32_t (&v)[4])
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = sub_bf16x2(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, z);
+    const uint32_t u = w >> 8;
+    v[0] = fma_bf16x2(w & 0x000F000Fu, k2p127, z);
+    v[1] = fma_bf16x2(w & 0x00F000F0u, k2p123, z);
+    v[2] = fma_bf16x2(u & 0x000F000Fu, k2p127, z);
+    v[3] = fma_bf16x2(u & 0x00F000F0u, k2p123, z);
 }
 
-// The same pairs of e2m1 codes times s (scale 2^118 in both halves): values times scale 2^-8.
+// The same pairs of e2m1 codes times s (scale 2^118 in both halves): values times scale 2^-8.  Left
+// shifts only, which the FMA pipe does as products.
 __device__ __forceinline__ void unpack_e2m1(uint32_t w, uint32_t s, uint32_t (&v)[4])
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t mag = (i < 2 ? w << (6 - 4 * i) : w >> (4 * i - 6)) & 0x01C001C0u;
-        v[i] = mul_bf16x2(((w << (12 - 4 * i)) & 0x80008000u) | mag, s);
-    }
+    const uint32_t u = w >> 8;
+    v[0] = mul_bf16x2(((w << 12) & 0x80008000u) | ((w << 6) & 0x01C001C0u), s);
+    v[1] = mul_bf16x2(((w << 8) & 0x80008000u) | ((w << 2) & 0x01C001C0u), s);
+    v[2] = mul_bf16x2(((u << 12) & 0x80008000u) | ((u << 6) & 0x01C001C0u), s);
+    v[3] = mul_bf16x2((w & 0x80008000u) | ((u << 2) & 0x01C001C0u), s);
 }
 
-// e4m3 byte `sel` (0..7) of a row's eight scales as bf16 scale 2^118 in both halves: the byte's bits
-// at bf16's exponent and mantissa are scale 2^-120 (subnormals too); two exact products raise it.
-__device__ __forceinline__ uint32_t e4m3_scale(uint2 bytes, int sel)
+// An e4m3 byte of `bytes` as bf16 scale 2^118 in both halves; `sel` places it in bytes 0 and 2.  The
+// byte's bits at bf16's exponent and mantissa are scale 2^-120 (subnormals too); two exact products
+// raise it.
+__device__ __forceinline__ uint32_t e4m3_scale(uint32_t bytes, uint32_t sel)
 {
-    const uint32_t b = ((sel < 4 ? bytes.x : bytes.y) >> (8 * (sel & 3))) & 0xFFu;
-    const uint32_t one = ((b & 0x7Fu) << 4) | ((b & 0x80u) << 8);
-    const uint32_t two = __byte_perm(one, one, 0x1010);
-    constexpr uint32_t k127 = 0x7F007F00u, k111 = 0x77007700u;  // 2^127 and 2^111
-    return mul_bf16x2(mul_bf16x2(two, k127), k111);
+    const uint32_t b = __byte_perm(bytes, 0u, sel);
+    return mul_bf16x2(mul_bf16x2(((b << 4) & 0x07F007F0u) | ((b << 8) & 0x80008000u), k2p127), k2p111);
 }
 
 // The scales (int4: up to four bf16; NVFP4: eight e4m3) and zeros of one row's 128 k from k0, packed;
 // groups at or past k read as 0.  `g` is the row's first scale.
-template <bool kInt4>
+template <int kGroup>
 __device__ __forceinline__ void load_scales(const Args& a, int64_t g, int k0, uint2& s, uint32_t& z)
 {
     s = make_uint2(0u, 0u);
     z = 0x08080808u;
-    if constexpr (kInt4) {
-        const uint16_t* p = static_cast<const uint16_t*>(a.scale) + g + k0 / a.group;
-        const uint8_t* pz = a.zero + (a.zero ? g + k0 / a.group : 0);
+    g += k0 / kGroup;
+    if constexpr (kGroup >= 32) {
+        const uint16_t* p = static_cast<const uint16_t*>(a.scale) + g;
+        const uint8_t* pz = a.zero + (a.zero ? g : 0);
         if (a.packed) {
-            if (a.group == 128) {
+            if constexpr (kGroup == 128) {
                 s.x = __ldca(p);
                 if (a.zero) z = __ldca(pz);
-            } else if (a.group == 64) {
+            } else if constexpr (kGroup == 64) {
                 s.x = __ldca(reinterpret_cast<const uint32_t*>(p));
                 if (a.zero) z = __ldca(reinterpret_cast<const uint16_t*>(pz));
             } else {
@@ -169,19 +197,19 @@ __device__ __forceinline__ void load_scales(const Args& a, int64_t g, int k0, ui
                 if (a.zero) z = __ldca(reinterpret_cast<const uint32_t*>(pz));
             }
         } else {
-            const int count = 128 / a.group;
-            for (int i = 0; i < count; ++i) {
-                if (k0 + i * a.group >= a.k) break;
-                const uint32_t v = __ldca(p + i);
-                (i < 2 ? s.x : s.y) |= v << (16 * (i & 1));
+#pragma unroll
+            for (int i = 0; i < 128 / kGroup; ++i) {
+                if (k0 + i * kGroup >= a.k) break;
+                (i < 2 ? s.x : s.y) |= (uint32_t)__ldca(p + i) << (16 * (i & 1));
                 if (a.zero) z = (z & ~(0xFFu << (8 * i))) | ((uint32_t)__ldca(pz + i) << (8 * i));
             }
         }
     } else {
-        const uint8_t* p = static_cast<const uint8_t*>(a.scale) + g + k0 / 16;
+        const uint8_t* p = static_cast<const uint8_t*>(a.scale) + g;
         if (a.packed) {
             s = __ldca(reinterpret_cast<const uint2*>(p));
         } else {
+#pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (k0 + 16 * i >= a.k) break;
                 (i < 4 ? s.x : s.y) |= (uint32_t)__ldca(p + i) << (8 * (i & 3));
@@ -190,11 +218,14 @@ __device__ __forceinline__ void load_scales(const Args& a, int64_t g, int k0, ui
     }
 }
 
-template <bool kInt4, int RT>
+// kGroup 32, 64, 128: int4; 16: NVFP4.
+template <int kGroup, int RT>
 __global__ void __launch_bounds__(kThreads, Ring<RT>::kBlocks) linear_w4_kernel(const __grid_constant__ Args a)
 {
     using R = Ring<RT>;
     using namespace dev;
+    constexpr bool kInt4 = kGroup >= 32;
+    constexpr int kQ = kInt4 ? kGroup / 32 : 1;  // q's of a group
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -204,29 +235,51 @@ __global__ void __launch_bounds__(kThreads, Ring<RT>::kBlocks) linear_w4_kernel(
     const int total = (a.k + kStageK - 1) / kStageK;
     const int first = (int)((int64_t)total * rank / a.splits), last = (int)((int64_t)total * (rank + 1) / a.splits);
 
-    // this thread's part of a stage: 16-byte piece tid % 8 of code rows tid / 8 + 32 j, and piece
-    // tid % 32 of x rows tid / 32 + 8 j
-    const int crow = tid >> 3, cpiece = tid & 7, xrow = tid >> 5, xpiece = tid & 31;
-    const uint8_t* csrc = a.codes + ((int64_t)h * a.n + n0 + crow) * (a.k / 2) + cpiece * 16;
-    const uint32_t cdst = sbase + crow * 128 + ((cpiece ^ (crow & 7)) << 4);
-    const __nv_bfloat16* xsrc = a.x + (int64_t)(r0 + xrow) * a.x_row + (int64_t)h * a.x_head + xpiece * 8;
-    const uint32_t xdst = sbase + kCodeBytes + xrow * 512 + ((xpiece ^ ((xrow & 1) << 2)) << 4);
-    const auto load_codes = [&](int stage, int slot) {
-        const bool k_ok = stage * kStageK + cpiece * 32 < a.k;
+    // Codes of a stage: this thread brings 16-byte piece tid % 8 of rows tid / 8 + 32 j.  Rows past n
+    // repeat row n - 1 (their sums go nowhere); pieces past k are zeros.
+    const int crow = tid >> 3, cpiece = tid & 7;
+    const uint8_t* csrc[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool ok = k_ok && n0 + crow + 32 * j < a.n;
-            cp_async16(cdst + slot * R::kStageBytes + j * 32 * 128,
-                       ok ? csrc + (int64_t)j * 32 * (a.k / 2) + stage * (kStageK / 2) : a.codes, ok);
+    for (int j = 0; j < 4; ++j) {
+        const int n = n0 + crow + 32 * j;
+        csrc[j] = a.codes + ((int64_t)h * a.n + (n < a.n ? n : a.n - 1)) * (a.k / 2) + (int64_t)first * (kStageK / 2) +
+                  cpiece * 16;
+    }
+    const uint32_t cdst = sbase + crow * 128 + ((cpiece ^ (crow & 7)) << 4);
+    const auto load_codes = [&](int stage, uint32_t slot) {
+        if ((stage + 1) * kStageK <= a.k) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cp_async16(cdst + slot * kCodeBytes + j * 32 * 128, csrc[j]);
+        } else {
+            const bool ok = stage * kStageK + cpiece * 32 < a.k;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                cp_async16_or_zero(cdst + slot * kCodeBytes + j * 32 * 128, ok ? csrc[j] : a.codes, ok);
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) csrc[j] += kStageK / 2;
     };
-    const auto load_x = [&](int stage, int slot) {
+    // x of a stage: piece tid % 32 of rows tid / 32 + 8 j; rows and pieces that are not there are zeros
+    const int xrow = tid >> 5, xpiece = tid & 31;
+    const __nv_bfloat16* xsrc = a.x + (int64_t)(r0 + xrow) * a.x_row + (int64_t)h * a.x_head + xpiece * 8;
+    const uint32_t xdst = sbase + R::kXOff + xrow * 512 + ((xpiece ^ ((xrow & 1) << 2)) << 4);
+    uint4 xv[RT];
+    const auto load_x = [&](int stage) {
         const bool k_ok = stage * kStageK + xpiece * 8 < a.k;
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
-            const bool ok = k_ok && r0 + xrow + 8 * j < a.rows;
-            cp_async16(xdst + slot * R::kStageBytes + j * kXBytes,
-                       ok ? xsrc + (int64_t)j * 8 * a.x_row + stage * kStageK : a.x, ok);
+            xv[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (k_ok && r0 + xrow + 8 * j < a.rows)
+                xv[j] = __ldca(reinterpret_cast<const uint4*>(xsrc + (int64_t)j * 8 * a.x_row + stage * kStageK));
+        }
+    };
+    const auto store_x = [&](int slot) {
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+            const uint4 v = xv[j];
+            sts128(xdst + slot * R::kXSlot + j * kXBytes,
+                   make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                              __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
         }
     };
     constexpr int kAhead = R::kStages - 1;
@@ -237,28 +290,33 @@ __global__ void __launch_bounds__(kThreads, Ring<RT>::kBlocks) linear_w4_kernel(
     }
     griddep_wait();
     if (a.early) griddep_launch_dependents();
+    load_x(first);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-        if (first + i < last) {
-            if (!a.early) load_codes(first + i, i);
-            load_x(first + i, i);
-        }
+        if (!a.early && first + i < last) load_codes(first + i, i);
         cp_async_commit();
     }
+    store_x(0);
+    if (first + 1 < last) load_x(first + 1);
 
     float acc[2][RT][4] = {};
-    // first scale of the four rows (m, half): rows past n read row n - 1's, and their sums go nowhere
-    const int groups = a.k / a.group;
+    // first scale of the four rows (m, half); rows past n as above
+    const int groups = a.k / kGroup;
     int64_t srow[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int n = n0 + 32 * wn + 8 * i + g;
         srow[i] = ((int64_t)h * a.n + (n < a.n ? n : a.n - 1)) * groups;
     }
-    const uint32_t crd = sbase + (32 * wn + g) * 128 + 4 * t, xrd = sbase + kCodeBytes + g * 512;
-    const int xswap = (g & 1) << 2;
-    const int shift = a.group == 32 ? 0 : a.group == 64 ? 1 : 2, mask = (1 << shift) - 1;  // int4: q's of a group
+    uint32_t crd[4], xrd[4];  // word (q, t) of row 32 wn + g, and x's
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        crd[q] = sbase + (32 * wn + g) * 128 + (((4 * wk + q) ^ g) << 4) + 4 * t;
+        xrd[q] = sbase + R::kXOff + g * 512 + (((16 * wk + 4 * q + t) ^ ((g & 1) << 2)) << 4);
+    }
+    const uint32_t sel0 = 0x4040u | (t >> 1) | ((t >> 1) << 8), sel1 = sel0 + 0x0202u;  // NVFP4: even and odd q
 
+    uint32_t slot = 0, next = kAhead;
     for (int stage = first, i = 0; stage < last; ++stage, ++i) {
         const int k0 = stage * kStageK + wk * 128;
         const bool busy = k0 < a.k;
@@ -266,31 +324,28 @@ __global__ void __launch_bounds__(kThreads, Ring<RT>::kBlocks) linear_w4_kernel(
         uint32_t z[4];
         if (busy) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) load_scales<kInt4>(a, srow[j], k0, s[j], z[j]);
+            for (int j = 0; j < 4; ++j) load_scales<kGroup>(a, srow[j], k0, s[j], z[j]);
         }
         cp_async_wait<kAhead - 1>();
-        __syncthreads();  // this stage has landed, and the slot of the one before is free
-        if (stage + kAhead < last) {
-            const int slot = (i + kAhead) % R::kStages;
-            load_codes(stage + kAhead, slot);
-            load_x(stage + kAhead, slot);
-        }
+        __syncthreads();  // this stage has landed, and every warp has left the one before
+        if (stage + kAhead < last) load_codes(stage + kAhead, next);
         cp_async_commit();
+        if (stage + 1 < last) store_x((i + 1) & 1);
+        if (stage + 2 < last) load_x(stage + 2);
+        const uint32_t cat = slot * kCodeBytes, xat = (i & 1) * R::kXSlot;
+        slot = slot + 1 == R::kStages ? 0 : slot + 1;
+        next = next + 1 == R::kStages ? 0 : next + 1;
         if (!busy) continue;
-        const uint32_t at = (uint32_t)(i % R::kStages) * R::kStageBytes;
         float part[2][RT][4];
+        uint32_t mz[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            uint32_t b[RT][4];
+            uint4 b[RT];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const uint4 v = lds128(xrd + at + rt * kXBytes + (((16 * wk + 4 * q + t) ^ xswap) << 4));
-                b[rt][0] = __byte_perm(v.x, v.z, 0x5410);  // k 0 and 4
-                b[rt][1] = __byte_perm(v.x, v.z, 0x7632);  // 1 and 5
-                b[rt][2] = __byte_perm(v.y, v.w, 0x5410);
-                b[rt][3] = __byte_perm(v.y, v.w, 0x7632);
-            }
-            if (kInt4 && (q & mask) == 0) {
+            for (int rt = 0; rt < RT; ++rt) b[rt] = lds128(xrd[q] + xat + rt * kXBytes);
+            if (kInt4 && q % kQ == 0) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mz[j] = minus_zero(z[j], q / kQ);
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -301,32 +356,30 @@ __global__ void __launch_bounds__(kThreads, Ring<RT>::kBlocks) linear_w4_kernel(
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 uint32_t lo[4], hi[4];  // rows g and g + 8
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int row = 16 * m + 8 * half;  // (32 wn + row + g) & 7 = g
-                    const uint32_t w = lds32(crd + at + row * 128 + (((4 * wk + q) ^ g) << 4));
-                    uint32_t(&v)[4] = half ? hi : lo;
-                    if constexpr (kInt4) {
-                        const uint32_t zero = (z[2 * m + half] >> (8 * (q >> shift))) & 0xFFu;
-                        unpack_int4(w, __byte_perm(zero, zero, 0x1010) | 0x43004300u, v);
-                    } else {
-                        unpack_e2m1(w, e4m3_scale(s[2 * m + half], 2 * q + (t >> 1)), v);
-                    }
+                const uint32_t w0 = lds32(crd[q] + cat + (16 * m) * 128), w1 = lds32(crd[q] + cat + (16 * m + 8) * 128);
+                if constexpr (kInt4) {
+                    unpack_int4(w0, mz[2 * m], lo);
+                    unpack_int4(w1, mz[2 * m + 1], hi);
+                } else {
+                    const uint32_t sel = q & 1 ? sel1 : sel0;
+                    unpack_e2m1(w0, e4m3_scale(q < 2 ? s[2 * m].x : s[2 * m].y, sel), lo);
+                    unpack_e2m1(w1, e4m3_scale(q < 2 ? s[2 * m + 1].x : s[2 * m + 1].y, sel), hi);
                 }
                 const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    mma(kInt4 ? part[m][rt] : acc[m][rt], a0, b[rt][0], b[rt][1]);
-                    mma(kInt4 ? part[m][rt] : acc[m][rt], a1, b[rt][2], b[rt][3]);
+                    mma(kInt4 ? part[m][rt] : acc[m][rt], a0, b[rt].x, b[rt].y);
+                    mma(kInt4 ? part[m][rt] : acc[m][rt], a1, b[rt].z, b[rt].w);
                 }
             }
-            if (kInt4 && (q & mask) == mask) {
-                const int j = q >> shift;
+            if (kInt4 && q % kQ == kQ - 1) {
+                constexpr int kHalf = 2;
+                const int j = q / kQ;
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    float sc[2];
+                    float sc[kHalf];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                    for (int half = 0; half < kHalf; ++half) {
                         const uint32_t w = j < 2 ? s[2 * m + half].x : s[2 * m + half].y;
                         sc[half] = j & 1 ? bf16_hi(w) : bf16_lo(w);
                     }
@@ -370,16 +423,16 @@ __global__ void __launch_bounds__(kThreads, Ring<RT>::kBlocks) linear_w4_kernel(
             sum = red[r * kRedPitch + n] + red[(RT * kRowTile + r) * kRedPitch + n];
         }
         a.out[(int64_t)(r0 + r) * a.out_row + (int64_t)h * a.out_head + n0 + n] = 
-            __float2bfloat16_rn((kInt4 ? sum : sum * 256.f) * a.tensor_scale);
+            __float2bfloat16_rn(sum * (kInt4 ? 64.f : 256.f) * a.tensor_scale);
     }
     __syncwarp();
     if (a.splits > 1) cluster_sync();  // no block leaves while another reads its sums
 }
 
-template <bool kInt4, int RT>
+template <int kGroup, int RT>
 mla_status launch(const Args& a, int heads, void* stream)
 {
-    const auto kernel = linear_w4_kernel<kInt4, RT>;
+    const auto kernel = linear_w4_kernel<kGroup, RT>;
     const mla_status st = cuda_status(
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<RT>::kBytes),
         "cudaFuncSetAttribute(max dynamic shared memory)");
@@ -402,17 +455,17 @@ mla_status launch(const Args& a, int heads, void* stream)
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, a), "4-bit product kernel launch");
 }
 
-template <bool kInt4>
+template <int kGroup>
 mla_status launch_rows(const Args& a, int heads, void* stream)
 {
     switch ((a.rows + kRowTile - 1) / kRowTile) {
-        case 1: return launch<kInt4, 1>(a, heads, stream);
-        case 2: return launch<kInt4, 2>(a, heads, stream);
-        case 3: return launch<kInt4, 3>(a, heads, stream);
-        case 4: return launch<kInt4, 4>(a, heads, stream);
-        case 5: return launch<kInt4, 5>(a, heads, stream);
-        case 6: return launch<kInt4, 6>(a, heads, stream);
-        default: return launch<kInt4, 8>(a, heads, stream);
+        case 1: return launch<kGroup, 1>(a, heads, stream);
+        case 2: return launch<kGroup, 2>(a, heads, stream);
+        case 3: return launch<kGroup, 3>(a, heads, stream);
+        case 4: return launch<kGroup, 4>(a, heads, stream);
+        case 5: return launch<kGroup, 5>(a, heads, stream);
+        case 6: return launch<kGroup, 6>(a, heads, stream);
+        default: return launch<kGroup, 8>(a, heads, stream);
     }
 }
 
@@ -456,7 +509,6 @@ mla_status linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t 
     a.rows = rows;
     a.n = w->n;
     a.k = w->k;
-    a.group = w->group;
     a.early = early;
     a.packed = w->k % 128 == 0 && is_aligned(w->scale, 8) && is_aligned(w->zero, 4);
     // blocks of a cluster over k: doubled while there are too few tiles for two blocks per SM and
@@ -466,7 +518,12 @@ mla_status linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t 
     const int stages = (w->k + kStageK - 1) / kStageK;
     a.splits = 1;
     while (a.splits < 8 && tiles * a.splits < 2 * 152 && stages >= 4 * a.splits) a.splits *= 2;
-    return int4 ? launch_rows<true>(a, w->heads, stream) : launch_rows<false>(a, w->heads, stream);
+    switch (w->group) {
+        case 16: return launch_rows<16>(a, w->heads, stream);
+        case 32: return launch_rows<32>(a, w->heads, stream);
+        case 64: return launch_rows<64>(a, w->heads, stream);
+        default: return launch_rows<128>(a, w->heads, stream);
+    }
 }
 
 // The step's per-head products: 128 heads, contiguous rows.
