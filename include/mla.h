@@ -436,19 +436,17 @@ MLA_API mla_status mla_rope_append_kv(const mla_rope_config* rope, int32_t num_t
  *   out[r,h,n] = tensor_scale * sum_k x[r,h,k] W[h,n,k]
  * with W in 4 bits and a scale for each `group` consecutive k: the step's absorb (heads 128, n 512,
  * k 128, W[h,c,d] = W_UK[h,d,c]) and value projection (heads 128, n 128, k 512), and the dense
- * projections around it (heads 1), for the few rows of a decode batch.
+ * projections around it (heads 1), for the few rows of a decode batch.  The weights are laid out
+ * once, by mla_w4_pack, in the order in which the products read them:
  *   codes  device uint8 [heads][n][k / 2], value 2j in the low nibble of byte j, 16-byte aligned
  *   MLA_W4_INT4:  W = (code - zero) * scale, code 0..15; group 32, 64 or 128
  *          scale  device bf16 [heads][n][k / group], 2-byte aligned
- *          zero   device uint8 [heads][n][k / group], each 0..15, or NULL: 8 everywhere
- *   MLA_W4_NVFP4: W = e2m1(code) * e4m3(scale); group 16
+ *          zero   device uint8 [heads][n][k / group], each 0..15 (has_zero 1), or NULL: 8 everywhere
+ *   MLA_W4_NVFP4: W = e2m1(code) * e4m3(scale); group 16, has_zero 0
  *          scale  device uint8 [heads][n][k / 16], finite e4m3 codes (not 0x7F or 0xFF); zero NULL
- *   k is a multiple of group and of 32; heads <= 65535, n * heads and k < 2^31.
- *   x    device bf16, element strides x_row_stride and x_head_stride (0: one row for all heads),
- *        multiples of 8, 16-byte aligned
- *   out  device bf16, element strides out_row_stride and out_head_stride, distinct elements, sharing
- *        none with x; 2-byte aligned
- * Products are exact and summed in fp32; out is rounded once.  rows 0 enqueues nothing. */
+ *   packed device, mla_w4_packed_bytes(w) bytes, 16-byte aligned, sharing none with the others, which
+ *          are not needed afterwards (w->packed is not read by mla_w4_pack)
+ *   k is a multiple of group and of 32; heads <= 65535, n * heads < 2^31, k <= 2^30. */
 typedef enum mla_w4_format { MLA_W4_INT4 = 0, MLA_W4_NVFP4 = 1 } mla_w4_format;
 typedef struct mla_w4_weight {
     int32_t format; /* mla_w4_format */
@@ -456,11 +454,21 @@ typedef struct mla_w4_weight {
     int32_t n;
     int32_t k;
     int32_t group;
+    int32_t has_zero;
     float tensor_scale; /* finite */
-    const void* codes;
-    const void* scale;
-    const void* zero;
+    const void* packed;
 } mla_w4_weight;
+/* Bytes of the packed weights of w's format and sizes (0 if they are not valid). */
+MLA_API size_t mla_w4_packed_bytes(const mla_w4_weight* w);
+MLA_API mla_status mla_w4_pack(const mla_w4_weight* w, const void* codes, const void* scale, const void* zero,
+                               void* packed, void* stream);
+/* The product.
+ *   x    device bf16, element strides x_row_stride and x_head_stride (0: one row for all heads),
+ *        multiples of 8, 16-byte aligned
+ *   out  device bf16, element strides out_row_stride and out_head_stride, distinct elements, sharing
+ *        none with x; 2-byte aligned
+ * Strides lie in [0, 2^40].  Products are exact and summed in fp32; out is rounded once.  rows 0
+ * enqueues nothing. */
 MLA_API mla_status mla_linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t x_head_stride,
                                  const mla_w4_weight* w, void* out, int64_t out_row_stride, int64_t out_head_stride,
                                  void* stream);

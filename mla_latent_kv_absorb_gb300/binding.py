@@ -60,7 +60,8 @@ EXPORTS = ("mla_status_string", "mla_last_error_string", "mla_plan_bytes_max", "
            "mla_decode_paged_static_ws", "mla_decode_step_host", "mla_append_kv", "mla_merge_out_proj",
            "mla_absorb_decode_paged", "mla_gather_kv", "mla_step_graph_create", "mla_step_graph_run",
            "mla_step_graph_destroy", "mla_prefill_workspace_bytes", "mla_prefill_decompressed",
-           "mla_rope_init", "mla_rope", "mla_rope_append_kv", "mla_linear_w4", "mla_absorb_q_w4", "mla_out_proj_w4")
+           "mla_rope_init", "mla_rope", "mla_rope_append_kv", "mla_w4_packed_bytes", "mla_w4_pack",
+           "mla_linear_w4", "mla_absorb_q_w4", "mla_out_proj_w4")
 
 # capacity of the library's fixed split-partial array (mla_decode_paged_static_ws)
 MLA_STATIC_WS_MAX_PARTIALS = 128
@@ -91,8 +92,8 @@ class RopeConfig(ctypes.Structure):
 
 class W4Struct(ctypes.Structure):
     _fields_ = [("format", ctypes.c_int32), ("heads", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
-                ("group", ctypes.c_int32), ("tensor_scale", ctypes.c_float), ("codes", ctypes.c_void_p),
-                ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p)]
+                ("group", ctypes.c_int32), ("has_zero", ctypes.c_int32), ("tensor_scale", ctypes.c_float),
+                ("packed", ctypes.c_void_p)]
 
 
 def lib() -> ctypes.CDLL:
@@ -157,6 +158,10 @@ def lib() -> ctypes.CDLL:
     L.mla_rope.argtypes = [P, ctypes.c_int, i32, i32, i32, i32, P, i64, i64, P, i64, i64, P, i64, i64, P, P]
     L.mla_rope_append_kv.restype = ctypes.c_int
     L.mla_rope_append_kv.argtypes = [P, i32, P, i64, P, i64, P, P, ctypes.c_int, i32, P, P, P, P, i64, i64, P, P, P, P]
+    L.mla_w4_packed_bytes.restype = sz
+    L.mla_w4_packed_bytes.argtypes = [P]
+    L.mla_w4_pack.restype = ctypes.c_int
+    L.mla_w4_pack.argtypes = [P, P, P, P, P, P]
     L.mla_linear_w4.restype = ctypes.c_int
     L.mla_linear_w4.argtypes = [i32, P, i64, i64, P, P, i64, i64, P]
     L.mla_absorb_q_w4.restype = ctypes.c_int
@@ -549,15 +554,16 @@ def mla_rope_append_kv(rope: Rope, c_kv: torch.Tensor, k_r: torch.Tensor, positi
 # --------------------------------------------------------------------------- 4-bit weights
 
 class W4Weight:
-    """Weights [heads, n, k] in 4 bits (``mla_w4_weight``): ``codes`` uint8 [heads, n, k / 2] (value
-    2j in the low nibble of byte j) and a ``scale`` per group of k.  A bfloat16 scale [heads, n,
-    k / group], group 32, 64 or 128: int4, (code - zero) * scale, ``zero`` uint8 of the scale's shape
-    (None: 8).  A uint8 or float8_e4m3fn scale [heads, n, k / 16]: NVFP4, e2m1(code) * e4m3(scale).
+    """Weights [heads, n, k] in 4 bits, laid out once for the products (``mla_w4_pack``, on the current
+    stream; the tensors given are not kept): ``codes`` uint8 [heads, n, k / 2] (value 2j in the low
+    nibble of byte j) and a ``scale`` per group of k.  A bfloat16 scale [heads, n, k / group], group
+    32, 64 or 128: int4, (code - zero) * scale, ``zero`` uint8 of the scale's shape (None: 8).  A
+    uint8 or float8_e4m3fn scale [heads, n, k / 16]: NVFP4, e2m1(code) * e4m3(scale).
     ``tensor_scale`` multiplies every output.  Tensors without the leading dimension are one head.
     For the decode step: W_UK as [128, 512, 128] (c, then d) and W_UV as [128, 128, 512]."""
 
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor, *, zero: Optional[torch.Tensor] = None,
-                 group: Optional[int] = None, tensor_scale: float = 1.0):
+                 group: Optional[int] = None, tensor_scale: float = 1.0, stream=None):
         for name, t in (("codes", codes), ("scale", scale)) + ((("zero", zero),) if zero is not None else ()):
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{name}: expected a tensor")
@@ -581,17 +587,21 @@ class W4Weight:
             raise ValueError(f"groups of {self.group} over k = {k}: expected groups of {allowed} and k a multiple of 32")
         if zero is not None and self.format == MLA_W4_NVFP4:
             raise ValueError("zero points are for int4")
-        _need(codes, "codes", torch.uint8, device=False)
-        _need(scale, "scale", scale.dtype, tuple(codes.shape[:-1]) + (groups,), device=False)
-        if zero is not None:
-            _need(zero, "zero", torch.uint8, tuple(scale.shape), device=False)
-        self.codes, self.scale, self.zero = codes, scale, zero
-        self.device_index = codes.get_device()
-        if scale.get_device() != self.device_index or (zero is not None and zero.get_device() != self.device_index):
-            raise ValueError("codes, scale and zero: must be on one device")
-        self.struct = W4Struct(self.format, self.heads, self.n, self.k, self.group, self.tensor_scale,
-                               codes.data_ptr(), scale.data_ptr(), None if zero is None else zero.data_ptr())
+        device = torch._C._cuda_getDevice()
+        codes_ptr = _whole(codes, "codes", torch.uint8, tuple(codes.shape), device)
+        scale_ptr = _whole(scale, "scale", scale.dtype, tuple(codes.shape[:-1]) + (groups,), device)
+        zero_ptr = None if zero is None else _whole(zero, "zero", torch.uint8, tuple(scale.shape), device)
+        self.device_index = device
+        self.struct = W4Struct(self.format, self.heads, self.n, self.k, self.group, int(zero is not None),
+                               self.tensor_scale, None)
         self._ref = ctypes.byref(self.struct)
+        size = int(lib().mla_w4_packed_bytes(self._ref))
+        if size == 0:
+            raise MlaError("mla_w4_packed_bytes", MLA_ERR_UNSUPPORTED, "sizes past the limits")
+        self.packed = torch.empty(size, dtype=torch.uint8, device=codes.device)
+        _check("mla_w4_pack", lib().mla_w4_pack(self._ref, codes_ptr, scale_ptr, zero_ptr, self.packed.data_ptr(),
+                                                _stream(stream)))
+        self.struct.packed = self.packed.data_ptr()
 
 
 def mla_linear_w4(x: torch.Tensor, w: W4Weight, out: torch.Tensor, stream=None) -> None:

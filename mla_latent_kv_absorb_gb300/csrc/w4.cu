@@ -1,31 +1,31 @@
 // w4.cu -- mla_linear_w4: out[r,h,n] = t * sum_k x[r,h,k] W[h,n,k] with W in 4 bits and a scale per
-// group of k (declared in include/mla.h).
+// group of k, and mla_w4_pack, which lays such weights out once (declared in include/mla.h).
 //
 // The weights are the M side of mma.sync m16n8k16 and eight rows of x its N side, so that a decode
 // batch fills the instruction and every weight is unpacked once for all rows (up to 64).  tcgen05
 // would want the unpacked weights in shared memory and a group's scale cannot be applied inside its
 // accumulator; at these row counts the product is bound by the weights' bytes, then by unpacking.
 //
-// A block takes 128 outputs of one head: eight warps, four over n (32 each) and two over k.  A stage
-// is 256 k: 16 KB of codes, brought by cp.async into a ring, and 4 KB of x per eight rows, which the
-// threads bring through registers one stage ahead.  Of a warp's 128 k, lane 4 g + t holds word (q,
-// t), the eight k from 32 q + 8 t, of rows g and g + 8.  Unpacking is bound by the integer pipe,
-// which runs at half the rate of the FMA pipes (measured: 54 % of it busy where the FMA pipes were
-// at 12 %), so it is built from as few integer operations as there are:
-//   int4: the bits (w & 0x000F000F) are, as a pair of bf16, code 2^-133 for k i and i + 4 (subnormal
-//         bf16 is linear in its bits, and still is one binade up, so (w & 0x00F000F0) is 16 code
-//         2^-133); one bf16 FMA with 2^127 or 2^123 and -zero / 64 makes (code - zero) / 64 exactly.
-//         Five integer operations and four FMAs a word.  The MMAs of a group start from zero, and
-//         the group's fp32 sums are scaled into the output's (the scale times a weight would round
-//         in bf16).
+// A warp works on blocks of 32 n x 128 k, which the packed layout keeps in 2 KB: lane 4 g + t finds
+// its words (q, t), the eight k from 32 q + 8 t, q = 0..3, of rows g, g + 8, g + 16 and g + 24 in four
+// 16-byte pieces, so that the codes go from memory to the registers that unpack them, the next
+// block's while this one's are worked on, and no barrier is in the loop.  (Codes by cp.async through
+// shared memory with a barrier a stage took 34 us where this takes TIME1, at one row, N 8192, K
+// 16384.)  Unpacking is bound by the integer pipe, which runs at half the rate of the FMA pipes, so
+// it is built from as few integer operations as there are.  A word has k 2 i and 2 i + 1 in nibbles i
+// and i + 4:
+//   int4: the bits (w & 0x000F000F) are, as a pair of bf16, code 2^-133 (subnormal bf16 is linear in
+//         its bits, and still is one binade up, so (w & 0x00F000F0) is 16 code 2^-133); one bf16 FMA
+//         with 2^127 or 2^123 and -zero / 64 makes (code - zero) / 64 exactly.  Five integer
+//         operations and four FMAs a word.  The MMAs of a group start from zero, and the group's fp32
+//         sums are scaled into the output's (the scale times a weight would round in bf16).
 //   NVFP4: the code's bits moved to bf16's sign, two exponent bits and one mantissa bit are its value
 //         times 2^-126; times scale 2^118 it is exact in bf16 (two times four significant bits).
-// The powers of two left over, 2^6 and 2^8, go into the end's product.  x is stored in the order of
-// k that the words have, (0, 4), (1, 5), (2, 6), (3, 7).  Blocks of a cluster split k when there are
-// few output tiles; their sums, and the two k warps', are joined in a fixed order through
-// (distributed) shared memory.
+// The powers of two left over, 2^6 and 2^8, go into the end's product.  x is read as it lies, through
+// L1, where the warps of an SM find each other's pieces.  The warps of a block split k (and n, when
+// there is little k), and so do the blocks of a cluster when there are few output tiles; the sums are
+// joined in a fixed order through (distributed) shared memory.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -38,79 +38,124 @@
 
 namespace mla::w4 {
 
-constexpr int kThreads = 256;
-constexpr int kTileN = 128;
-constexpr int kStageK = 256;
-constexpr int kCodeBytes = kTileN * kStageK / 2;
-constexpr int kRowTile = 8;                       // rows of x per MMA
-constexpr int kXBytes = kRowTile * kStageK * 2;   // of one row tile
-constexpr int kRedPitch = kTileN + 4;             // floats; the four lanes of a row hit different banks
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kBlockN = 32, kBlockK = 128;          // of a packed block
+constexpr int kBlockBytes = kBlockN * kBlockK / 2;  // its codes
+constexpr int kRowTile = 8;                         // rows of x per MMA
 constexpr int kMaxRowTiles = 8;
+constexpr int kRedPitch = kBlockN + 4;  // floats; the four lanes of a row hit different banks
 
-template <int RT>
-struct Ring {
-    // two blocks per SM up to three row tiles, one above
-    static constexpr int kBlocks = RT <= 3 ? 2 : 1;
-    static constexpr int kStages = RT <= 2 ? 6 : RT == 3 ? 5 : RT <= 5 ? 8 : RT == 6 ? 7 : 6;
-    static constexpr int kXOff = kStages * kCodeBytes;
-    static constexpr int kXSlot = RT * kXBytes;
-    static constexpr int kBytes = kXOff + 2 * kXSlot;
-    static_assert((kBytes + 1024) * kBlocks <= 228 * 1024, "shared memory of an SM");
-    static_assert(2 * RT * kRowTile * kRedPitch * 4 <= kBytes, "the sums are joined in the ring's memory");
+// Bytes of a block's scales (int4: bf16 [g][j][group], NVFP4: e4m3 [g][t / 2][j][q]) and of its zeros
+// (uint8 [g][j][group]), row 8 j + g of the block.
+__host__ __device__ constexpr int scale_bytes(int group) { return group == 16 ? kBlockN * 8 : kBlockN * (kBlockK / group) * 2; }
+__host__ __device__ constexpr int zero_bytes(int group) { return kBlockN * (kBlockK / group); }
+
+// The packed image: all blocks' codes [h][n / 32][k / 128], then their scales, then their zeros.
+struct Layout {
+    int64_t blocks_n, blocks_k;  // of one head
+    int64_t scale_off, zero_off, bytes;
 };
+__host__ inline Layout layout_of(const mla_w4_weight& w)
+{
+    Layout l;
+    l.blocks_n = ((int64_t)w.n + kBlockN - 1) / kBlockN;
+    l.blocks_k = ((int64_t)w.k + kBlockK - 1) / kBlockK;
+    const int64_t blocks = l.blocks_n * l.blocks_k * w.heads;
+    l.scale_off = blocks * kBlockBytes;
+    l.zero_off = l.scale_off + blocks * scale_bytes(w.group);
+    l.bytes = l.zero_off + (w.has_zero ? blocks * zero_bytes(w.group) : 0);
+    return l;
+}
+
+struct PackArgs {
+    const uint8_t* codes;
+    const void* scale;
+    const uint8_t* zero;
+    uint8_t* packed;
+    int64_t scale_off, zero_off;
+    int n, k, group;
+    int blocks_n, blocks_k;
+};
+
+// One warp per packed block; n and k past the weights' are filled with zeros of scale zero.
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a)
+{
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, h = blockIdx.y;
+    const int64_t b = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (b >= (int64_t)a.blocks_n * a.blocks_k) return;
+    const int n0 = (int)(b / a.blocks_k) * kBlockN, k0 = (int)(b % a.blocks_k) * kBlockK;
+    const int64_t block = (int64_t)h * a.blocks_n * a.blocks_k + b;
+    const int groups = a.k / a.group;  // of a row
+    const bool nv = a.group == 16;
+    for (int j = 0; j < 4; ++j) {
+        const int n = n0 + 8 * j + g;
+        const int64_t row = (int64_t)h * a.n + n;
+        uint32_t word[4];
+        for (int q = 0; q < 4; ++q) {
+            const int k = k0 + 32 * q + 8 * t;
+            uint32_t w = 0;
+            if (n < a.n && k < a.k) {
+                const uint32_t v = *reinterpret_cast<const uint32_t*>(a.codes + row * (a.k / 2) + k / 2);
+                for (int i = 0; i < 4; ++i)  // nibbles 2 i and 2 i + 1 to i and i + 4
+                    w |= ((v >> (8 * i)) & 15u) << (4 * i) | ((v >> (8 * i + 4)) & 15u) << (4 * i + 16);
+                // a negative scale's sign goes into its codes
+                if (nv && (static_cast<const uint8_t*>(a.scale)[row * groups + k / 16] & 0x80u)) w ^= 0x88888888u;
+            }
+            word[q] = w;
+        }
+        *reinterpret_cast<uint4*>(a.packed + block * kBlockBytes + j * 512 + lane * 16) =
+            make_uint4(word[0], word[1], word[2], word[3]);
+        if (nv) {
+            if (t & 1) continue;
+            uint32_t s = 0;
+            for (int q = 0; q < 4; ++q) {
+                const int k = k0 + 32 * q + 8 * t;
+                if (n < a.n && k < a.k)
+                    s |= (uint32_t)(static_cast<const uint8_t*>(a.scale)[row * groups + k / 16] & 0x7Fu) << (8 * q);
+            }
+            *reinterpret_cast<uint32_t*>(a.packed + a.scale_off + block * scale_bytes(16) + (g * 2 + (t >> 1)) * 16 + j * 4) = s;
+        } else {
+            const int count = kBlockK / a.group;
+            if (t >= count) continue;
+            const int k = k0 + t * a.group;
+            const bool in = n < a.n && k < a.k;
+            const int at = (g * 4 + j) * count + t;
+            reinterpret_cast<uint16_t*>(a.packed + a.scale_off + block * scale_bytes(a.group))[at] =
+                in ? static_cast<const uint16_t*>(a.scale)[row * groups + k / a.group] : (uint16_t)0;
+            if (a.zero)
+                (a.packed + a.zero_off + block * zero_bytes(a.group))[at] =
+                    in ? a.zero[row * groups + k / a.group] : (uint8_t)8;
+        }
+    }
+}
 
 struct Args {
     const __nv_bfloat16* x;
     int64_t x_row, x_head;
     const uint8_t* codes;
-    const void* scale;
-    const uint8_t* zero;
+    const uint8_t* scale;
+    const uint8_t* zero;  // NULL: 8
     __nv_bfloat16* out;
     int64_t out_row, out_head;
     float tensor_scale;
     int rows, n, k;
-    int splits;   // blocks of a cluster, over k
-    bool packed;  // the scales (and zeros) of 128 k are one aligned word
+    int blocks_n, blocks_k;
+    int k_warps;  // warps of a thread block over k; the others over n
+    int splits;   // thread blocks of a cluster, over k
     bool early;   // kernels behind this one may start before it ends (they wait for `out` themselves)
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// 16 bytes of zeros where !valid (src is then not read)
-__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool valid)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint32_t lds32(uint32_t addr)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t addr)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
-{
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
 {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
+}
+
+__device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -138,13 +183,13 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
 // bf16 pairs of powers of two
 constexpr uint32_t k2p127 = 0x7F007F00u, k2p123 = 0x7D007D00u, k2p111 = 0x77007700u, kMinus2p127 = 0xFF00FF00u;
 
-// -zero / 64 in both halves, of byte j of z
-__device__ __forceinline__ uint32_t minus_zero(uint32_t z, int j)
+// -zero / 64 in both halves, of byte i of z
+__device__ __forceinline__ uint32_t minus_zero(uint32_t z, int i)
 {
-    return mul_bf16x2(__byte_perm(z, 0u, 0x4040u | j | (j << 8)), kMinus2p127);
+    return mul_bf16x2(__byte_perm(z, 0u, 0x4040u | i | (i << 8)), kMinus2p127);
 }
 
-// The pairs (i, i + 4), i = 0..3, of a word of eight int4 codes: (code - zero) / 64.
+// The pairs (2 i, 2 i + 1), i = 0..3, of a word of eight int4 codes: (code - zero) / 64.
 __device__ __forceinline__ void unpack_int4(uint32_t w, uint32_t z, uint32_t (&v)[4])
 {
     const uint32_t u = w >> 8;
@@ -165,187 +210,132 @@ __device__ __forceinline__ void unpack_e2m1(uint32_t w, uint32_t s, uint32_t (&v
     v[3] = mul_bf16x2((w & 0x80008000u) | ((u << 2) & 0x01C001C0u), s);
 }
 
-// An e4m3 byte of `bytes` as bf16 scale 2^118 in both halves; `sel` places it in bytes 0 and 2.  The
-// byte's bits at bf16's exponent and mantissa are scale 2^-120 (subnormals too); two exact products
-// raise it.
-__device__ __forceinline__ uint32_t e4m3_scale(uint32_t bytes, uint32_t sel)
+// e4m3 byte i (no sign) of `bytes` as bf16 scale 2^118 in both halves: the byte's bits at bf16's
+// exponent and mantissa are scale 2^-120 (subnormals too); two exact products raise it.
+__device__ __forceinline__ uint32_t e4m3_scale(uint32_t bytes, int i)
 {
-    const uint32_t b = __byte_perm(bytes, 0u, sel);
-    return mul_bf16x2(mul_bf16x2(((b << 4) & 0x07F007F0u) | ((b << 8) & 0x80008000u), k2p127), k2p111);
+    const uint32_t b = __byte_perm(bytes, 0u, 0x4040u | i | (i << 8));
+    return mul_bf16x2(mul_bf16x2(b << 4, k2p127), k2p111);
 }
 
-// The scales (int4: up to four bf16; NVFP4: eight e4m3) and zeros of one row's 128 k from k0, packed;
-// groups at or past k read as 0.  `g` is the row's first scale.
+// What a lane holds of a block: the codes of its four rows, and their scales and zeros.
 template <int kGroup>
-__device__ __forceinline__ void load_scales(const Args& a, int64_t g, int k0, uint2& s, uint32_t& z)
-{
-    s = make_uint2(0u, 0u);
-    z = 0x08080808u;
-    g += k0 / kGroup;
-    if constexpr (kGroup >= 32) {
-        const uint16_t* p = static_cast<const uint16_t*>(a.scale) + g;
-        const uint8_t* pz = a.zero + (a.zero ? g : 0);
-        if (a.packed) {
-            if constexpr (kGroup == 128) {
-                s.x = __ldca(p);
-                if (a.zero) z = __ldca(pz);
-            } else if constexpr (kGroup == 64) {
-                s.x = __ldca(reinterpret_cast<const uint32_t*>(p));
-                if (a.zero) z = __ldca(reinterpret_cast<const uint16_t*>(pz));
-            } else {
-                s = __ldca(reinterpret_cast<const uint2*>(p));
-                if (a.zero) z = __ldca(reinterpret_cast<const uint32_t*>(pz));
-            }
+struct Held {
+    static constexpr int kScale = kGroup == 128 ? 2 : kGroup == 32 ? 8 : 4;  // 32-bit words
+    static constexpr int kZero = kGroup >= 32 ? 128 / kGroup : 1;
+    uint4 c[4];
+    uint32_t s[kScale];
+    uint32_t z[kZero];
+
+    // Through L2 only what is read once; the scales' sectors are shared by the four lanes of a row.
+    __device__ __forceinline__ void load(const Args& a, int64_t block, int lane)
+    {
+        const uint4* p = reinterpret_cast<const uint4*>(a.codes + block * kBlockBytes) + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c[j] = __ldcg(p + 32 * j);
+        const int g = lane >> 2;
+        const uint8_t* ps = a.scale + block * scale_bytes(kGroup);
+        if constexpr (kGroup == 16) {
+            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(ps) + (lane >> 1));
+            s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+        } else if constexpr (kGroup == 128) {
+            const uint2 v = __ldcg(reinterpret_cast<const uint2*>(ps) + g);
+            s[0] = v.x, s[1] = v.y;
         } else {
 #pragma unroll
-            for (int i = 0; i < 128 / kGroup; ++i) {
-                if (k0 + i * kGroup >= a.k) break;
-                (i < 2 ? s.x : s.y) |= (uint32_t)__ldca(p + i) << (16 * (i & 1));
-                if (a.zero) z = (z & ~(0xFFu << (8 * i))) | ((uint32_t)__ldca(pz + i) << (8 * i));
+            for (int i = 0; i < kScale / 4; ++i) {
+                const uint4 v = __ldcg(reinterpret_cast<const uint4*>(ps) + g * (kScale / 4) + i);
+                s[4 * i] = v.x, s[4 * i + 1] = v.y, s[4 * i + 2] = v.z, s[4 * i + 3] = v.w;
             }
         }
-    } else {
-        const uint8_t* p = static_cast<const uint8_t*>(a.scale) + g;
-        if (a.packed) {
-            s = __ldca(reinterpret_cast<const uint2*>(p));
-        } else {
+        if constexpr (kGroup >= 32) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (k0 + 16 * i >= a.k) break;
-                (i < 4 ? s.x : s.y) |= (uint32_t)__ldca(p + i) << (8 * (i & 3));
+            for (int i = 0; i < kZero; ++i) z[i] = 0x08080808u;
+            if (a.zero) {
+                const uint8_t* pz = a.zero + block * zero_bytes(kGroup);
+                if constexpr (kZero == 1) {
+                    z[0] = __ldcg(reinterpret_cast<const uint32_t*>(pz) + g);
+                } else if constexpr (kZero == 2) {
+                    const uint2 v = __ldcg(reinterpret_cast<const uint2*>(pz) + g);
+                    z[0] = v.x, z[1] = v.y;
+                } else {
+                    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(pz) + g);
+                    z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
+                }
             }
         }
     }
+    // int4: scale and zero of group i of row 8 j + g
+    __device__ __forceinline__ float scale(int j, int i) const
+    {
+        const int e = j * (kBlockK / kGroup) + i;
+        return e & 1 ? dev::bf16_hi(s[e / 2]) : dev::bf16_lo(s[e / 2]);
+    }
+    __device__ __forceinline__ uint32_t zero64(int j, int i) const
+    {
+        const int e = j * (kBlockK / kGroup) + i;
+        return minus_zero(z[e / 4], e & 3);
+    }
+};
+
+// x of a block's k: piece (q, t) of rows g + 8 rt
+template <int RT>
+struct XPieces {
+    uint4 v[RT];
+};
+
+template <int RT>
+__host__ __device__ constexpr int blocks_per_sm()
+{
+    return RT <= 2 ? 4 : RT <= 5 ? 3 : 2;
 }
 
 // kGroup 32, 64, 128: int4; 16: NVFP4.
 template <int kGroup, int RT>
-__global__ void __launch_bounds__(kThreads, Ring<RT>::kBlocks) linear_w4_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<RT>()) linear_w4_kernel(const __grid_constant__ Args a)
 {
-    using R = Ring<RT>;
     using namespace dev;
     constexpr bool kInt4 = kGroup >= 32;
     constexpr int kQ = kInt4 ? kGroup / 32 : 1;  // q's of a group
-    extern __shared__ __align__(128) uint8_t smem[];
-    const uint32_t sbase = smem_u32(smem);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wn = warp & 3, wk = warp >> 2, g = lane >> 2, t = lane & 3;
-    const int rank = (int)blockIdx.x % a.splits, n0 = (int)blockIdx.x / a.splits * kTileN;
+    extern __shared__ __align__(16) float red[];  // [warp][row][kRedPitch]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int n_warps = kWarps / a.k_warps, wk = warp % a.k_warps, wn = warp / a.k_warps;
+    const int rank = (int)blockIdx.x % a.splits, tile = (int)blockIdx.x / a.splits;
+    const int bn = tile * n_warps + wn;
     const int h = blockIdx.y, r0 = (int)blockIdx.z * (RT * kRowTile);
-    const int total = (a.k + kStageK - 1) / kStageK;
-    const int first = (int)((int64_t)total * rank / a.splits), last = (int)((int64_t)total * (rank + 1) / a.splits);
+    const int first = (int)((int64_t)a.blocks_k * rank / a.splits) + wk;
+    const int last = bn < a.blocks_n ? (int)((int64_t)a.blocks_k * (rank + 1) / a.splits) : 0;
+    const int64_t row_blocks = ((int64_t)h * a.blocks_n + bn) * a.blocks_k;
 
-    // Codes of a stage: this thread brings 16-byte piece tid % 8 of rows tid / 8 + 32 j.  Rows past n
-    // repeat row n - 1 (their sums go nowhere); pieces past k are zeros.
-    const int crow = tid >> 3, cpiece = tid & 7;
-    const uint8_t* csrc[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int n = n0 + crow + 32 * j;
-        csrc[j] = a.codes + ((int64_t)h * a.n + (n < a.n ? n : a.n - 1)) * (a.k / 2) + (int64_t)first * (kStageK / 2) +
-                  cpiece * 16;
-    }
-    const uint32_t cdst = sbase + crow * 128 + ((cpiece ^ (crow & 7)) << 4);
-    const auto load_codes = [&](int stage, uint32_t slot) {
-        if ((stage + 1) * kStageK <= a.k) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) cp_async16(cdst + slot * kCodeBytes + j * 32 * 128, csrc[j]);
-        } else {
-            const bool ok = stage * kStageK + cpiece * 32 < a.k;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                cp_async16_or_zero(cdst + slot * kCodeBytes + j * 32 * 128, ok ? csrc[j] : a.codes, ok);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) csrc[j] += kStageK / 2;
-    };
-    // x of a stage: piece tid % 32 of rows tid / 32 + 8 j; rows and pieces that are not there are zeros
-    const int xrow = tid >> 5, xpiece = tid & 31;
-    const __nv_bfloat16* xsrc = a.x + (int64_t)(r0 + xrow) * a.x_row + (int64_t)h * a.x_head + xpiece * 8;
-    const uint32_t xdst = sbase + R::kXOff + xrow * 512 + ((xpiece ^ ((xrow & 1) << 2)) << 4);
-    uint4 xv[RT];
-    const auto load_x = [&](int stage) {
-        const bool k_ok = stage * kStageK + xpiece * 8 < a.k;
-#pragma unroll
-        for (int j = 0; j < RT; ++j) {
-            xv[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (k_ok && r0 + xrow + 8 * j < a.rows)
-                xv[j] = __ldca(reinterpret_cast<const uint4*>(xsrc + (int64_t)j * 8 * a.x_row + stage * kStageK));
-        }
-    };
-    const auto store_x = [&](int slot) {
-#pragma unroll
-        for (int j = 0; j < RT; ++j) {
-            const uint4 v = xv[j];
-            sts128(xdst + slot * R::kXSlot + j * kXBytes,
-                   make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                              __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)));
-        }
-    };
-    constexpr int kAhead = R::kStages - 1;
-    if (a.early) {  // the step's weights do not depend on the kernel before this one
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (first + i < last) load_codes(first + i, i);
-    }
+    constexpr int kFar = 4;  // blocks of this warp from HBM to L2 ahead
+    // Bringing the weights to L2 is no read of them: it may come before the kernel ahead has ended.
+    if (lane < kFar && first + lane * a.k_warps < last)
+        prefetch_l2_bulk(a.codes + (row_blocks + first + lane * a.k_warps) * kBlockBytes, kBlockBytes);
     griddep_wait();
     if (a.early) griddep_launch_dependents();
-    load_x(first);
+
+    const __nv_bfloat16* xsrc = a.x + (int64_t)(r0 + g) * a.x_row + (int64_t)h * a.x_head + 8 * t;
+    const auto load_x = [&](int block, int q, XPieces<RT>& p) {
+        const int k = block * kBlockK + 32 * q;
+        const bool k_ok = k + 8 * t < a.k;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-        if (!a.early && first + i < last) load_codes(first + i, i);
-        cp_async_commit();
-    }
-    store_x(0);
-    if (first + 1 < last) load_x(first + 1);
+        for (int rt = 0; rt < RT; ++rt) {
+            p.v[rt] = make_uint4(0u, 0u, 0u, 0u);
+            if (k_ok && r0 + g + 8 * rt < a.rows)
+                p.v[rt] = __ldca(reinterpret_cast<const uint4*>(xsrc + (int64_t)rt * 8 * a.x_row + k));
+        }
+    };
 
     float acc[2][RT][4] = {};
-    // first scale of the four rows (m, half); rows past n as above
-    const int groups = a.k / kGroup;
-    int64_t srow[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int n = n0 + 32 * wn + 8 * i + g;
-        srow[i] = ((int64_t)h * a.n + (n < a.n ? n : a.n - 1)) * groups;
-    }
-    uint32_t crd[4], xrd[4];  // word (q, t) of row 32 wn + g, and x's
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        crd[q] = sbase + (32 * wn + g) * 128 + (((4 * wk + q) ^ g) << 4) + 4 * t;
-        xrd[q] = sbase + R::kXOff + g * 512 + (((16 * wk + 4 * q + t) ^ ((g & 1) << 2)) << 4);
-    }
-    const uint32_t sel0 = 0x4040u | (t >> 1) | ((t >> 1) << 8), sel1 = sel0 + 0x0202u;  // NVFP4: even and odd q
-
-    uint32_t slot = 0, next = kAhead;
-    for (int stage = first, i = 0; stage < last; ++stage, ++i) {
-        const int k0 = stage * kStageK + wk * 128;
-        const bool busy = k0 < a.k;
-        uint2 s[4];
-        uint32_t z[4];
-        if (busy) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) load_scales<kGroup>(a, srow[j], k0, s[j], z[j]);
-        }
-        cp_async_wait<kAhead - 1>();
-        __syncthreads();  // this stage has landed, and every warp has left the one before
-        if (stage + kAhead < last) load_codes(stage + kAhead, next);
-        cp_async_commit();
-        if (stage + 1 < last) store_x((i + 1) & 1);
-        if (stage + 2 < last) load_x(stage + 2);
-        const uint32_t cat = slot * kCodeBytes, xat = (i & 1) * R::kXSlot;
-        slot = slot + 1 == R::kStages ? 0 : slot + 1;
-        next = next + 1 == R::kStages ? 0 : next + 1;
-        if (!busy) continue;
+    const auto work = [&](const Held<kGroup>& w, int block, int after) {
+        if (lane == 0 && block + kFar * a.k_warps < last)
+            prefetch_l2_bulk(a.codes + (row_blocks + block + kFar * a.k_warps) * kBlockBytes, kBlockBytes);
         float part[2][RT][4];
-        uint32_t mz[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            uint4 b[RT];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) b[rt] = lds128(xrd[q] + xat + rt * kXBytes);
+            XPieces<RT> b;
+            load_x(block, q, b);
             if (kInt4 && q % kQ == 0) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mz[j] = minus_zero(z[j], q / kQ);
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -355,34 +345,27 @@ __global__ void __launch_bounds__(kThreads, Ring<RT>::kBlocks) linear_w4_kernel(
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                uint32_t lo[4], hi[4];  // rows g and g + 8
-                const uint32_t w0 = lds32(crd[q] + cat + (16 * m) * 128), w1 = lds32(crd[q] + cat + (16 * m + 8) * 128);
-                if constexpr (kInt4) {
-                    unpack_int4(w0, mz[2 * m], lo);
-                    unpack_int4(w1, mz[2 * m + 1], hi);
-                } else {
-                    const uint32_t sel = q & 1 ? sel1 : sel0;
-                    unpack_e2m1(w0, e4m3_scale(q < 2 ? s[2 * m].x : s[2 * m].y, sel), lo);
-                    unpack_e2m1(w1, e4m3_scale(q < 2 ? s[2 * m + 1].x : s[2 * m + 1].y, sel), hi);
+                uint32_t v[2][4];  // rows g and g + 8 of the m tile
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int j = 2 * m + half;
+                    const uint32_t word = q == 0 ? w.c[j].x : q == 1 ? w.c[j].y : q == 2 ? w.c[j].z : w.c[j].w;
+                    if constexpr (kInt4)
+                        unpack_int4(word, w.zero64(j, q / kQ), v[half]);
+                    else
+                        unpack_e2m1(word, e4m3_scale(w.s[j], q), v[half]);
                 }
-                const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+                const uint32_t a0[4] = {v[0][0], v[1][0], v[0][1], v[1][1]}, a1[4] = {v[0][2], v[1][2], v[0][3], v[1][3]};
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    mma(kInt4 ? part[m][rt] : acc[m][rt], a0, b[rt].x, b[rt].y);
-                    mma(kInt4 ? part[m][rt] : acc[m][rt], a1, b[rt].z, b[rt].w);
+                    mma(kInt4 ? part[m][rt] : acc[m][rt], a0, b.v[rt].x, b.v[rt].y);
+                    mma(kInt4 ? part[m][rt] : acc[m][rt], a1, b.v[rt].z, b.v[rt].w);
                 }
             }
             if (kInt4 && q % kQ == kQ - 1) {
-                constexpr int kHalf = 2;
-                const int j = q / kQ;
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    float sc[kHalf];
-#pragma unroll
-                    for (int half = 0; half < kHalf; ++half) {
-                        const uint32_t w = j < 2 ? s[2 * m + half].x : s[2 * m + half].y;
-                        sc[half] = j & 1 ? bf16_hi(w) : bf16_lo(w);
-                    }
+                    const float sc[2] = {w.scale(2 * m, q / kQ), w.scale(2 * m + 1, q / kQ)};
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -390,18 +373,26 @@ __global__ void __launch_bounds__(kThreads, Ring<RT>::kBlocks) linear_w4_kernel(
                 }
             }
         }
+    };
+    if (first < last) {
+        Held<kGroup> even, odd;  // the block worked on and the next one
+        even.load(a, row_blocks + first, lane);
+        for (int block = first; block < last; block += 2 * a.k_warps) {
+            const int second = block + a.k_warps, third = second + a.k_warps;
+            if (second < last) odd.load(a, row_blocks + second, lane);
+            work(even, block, second);
+            if (third < last) even.load(a, row_blocks + third, lane);
+            if (second < last) work(odd, second, third);
+        }
     }
 
-    cp_async_wait<0>();
-    __syncthreads();  // every warp has left the ring: its memory takes the sums, [wk][row][n]
-    float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                red[(wk * RT * kRowTile + rt * kRowTile + 2 * t + (e & 1)) * kRedPitch + 32 * wn + 16 * m + 8 * (e >> 1) + g] =
+                red[(warp * RT * kRowTile + rt * kRowTile + 2 * t + (e & 1)) * kRedPitch + 16 * m + 8 * (e >> 1) + g] =
                     acc[m][rt][e];
     __syncwarp();
     if (a.splits > 1)
@@ -409,20 +400,20 @@ __global__ void __launch_bounds__(kThreads, Ring<RT>::kBlocks) linear_w4_kernel(
     else
         __syncthreads();
     const int rows = a.rows - r0 < RT * kRowTile ? a.rows - r0 : RT * kRowTile;
-    for (int e = rank * kThreads + tid; e < rows * kTileN; e += a.splits * kThreads) {
-        const int r = e / kTileN, n = e % kTileN;
-        if (n0 + n >= a.n) continue;
-        const uint32_t at = sbase + (r * kRedPitch + n) * 4, other = RT * kRowTile * kRedPitch * 4;
+    const int width = n_warps * kBlockN, n0 = tile * width;
+    const uint32_t rbase = smem_u32(red);
+    for (int e = rank * kThreads + tid; e < rows * width; e += a.splits * kThreads) {
+        const int r = e / width, c = e % width, n = n0 + c;
+        if (n >= a.n) continue;
+        const int at = ((c / kBlockN) * a.k_warps * RT * kRowTile + r) * kRedPitch + c % kBlockN;
         float sum = 0.f;
-        if (a.splits > 1) {
-            for (int p = 0; p < a.splits; ++p) {
-                const uint32_t peer = map_to_cta(at, p);
-                sum += ld_cluster_f32(peer) + ld_cluster_f32(peer + other);
-            }
-        } else {
-            sum = red[r * kRedPitch + n] + red[(RT * kRowTile + r) * kRedPitch + n];
+        for (int p = 0; p < a.splits; ++p) {
+            const uint32_t peer = a.splits > 1 ? map_to_cta(rbase + at * 4, p) : 0u;
+            for (int i = 0; i < a.k_warps; ++i)
+                sum += a.splits > 1 ? ld_cluster_f32(peer + i * (RT * kRowTile * kRedPitch * 4))
+                                    : red[at + i * (RT * kRowTile * kRedPitch)];
         }
-        a.out[(int64_t)(r0 + r) * a.out_row + (int64_t)h * a.out_head + n0 + n] = 
+        a.out[(int64_t)(r0 + r) * a.out_row + (int64_t)h * a.out_head + n] =
             __float2bfloat16_rn(sum * (kInt4 ? 64.f : 256.f) * a.tensor_scale);
     }
     __syncwarp();
@@ -433,15 +424,18 @@ template <int kGroup, int RT>
 mla_status launch(const Args& a, int heads, void* stream)
 {
     const auto kernel = linear_w4_kernel<kGroup, RT>;
-    const mla_status st = cuda_status(
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<RT>::kBytes),
-        "cudaFuncSetAttribute(max dynamic shared memory)");
-    if (st != MLA_OK) return st;
+    constexpr int kBytes = kWarps * RT * kRowTile * kRedPitch * 4;
+    if (kBytes > 48 * 1024) {
+        const mla_status st = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes),
+                                          "cudaFuncSetAttribute(max dynamic shared memory)");
+        if (st != MLA_OK) return st;
+    }
+    const int n_warps = kWarps / a.k_warps;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.n + kTileN - 1) / kTileN * a.splits), (unsigned)heads,
+    cfg.gridDim = dim3((unsigned)((a.blocks_n + n_warps - 1) / n_warps * a.splits), (unsigned)heads,
                        (unsigned)((a.rows + RT * kRowTile - 1) / (RT * kRowTile)));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Ring<RT>::kBytes;
+    cfg.dynamicSmemBytes = kBytes;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -473,35 +467,50 @@ mla_status launch_rows(const Args& a, int heads, void* stream)
 
 namespace {
 
+using mla::is_aligned;
+
+// Format, sizes and group of a weight.
+mla_status check_shape(const mla_w4_weight* w)
+{
+    if (!w || (w->format != MLA_W4_INT4 && w->format != MLA_W4_NVFP4)) return MLA_ERR_INVALID_ARG;
+    const bool int4 = w->format == MLA_W4_INT4;
+    if (w->heads < 1 || w->n < 1 || w->k < 1 || !std::isfinite(w->tensor_scale)) return MLA_ERR_INVALID_ARG;
+    if (int4 ? (w->group != 32 && w->group != 64 && w->group != 128) : w->group != 16) return MLA_ERR_INVALID_ARG;
+    if (w->k % w->group || w->k % 32 || (w->has_zero != 0 && w->has_zero != 1) || (!int4 && w->has_zero))
+        return MLA_ERR_INVALID_ARG;
+    if (w->heads > 65535 || (int64_t)w->heads * w->n >= ((int64_t)1 << 31) || w->k > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+    const mla::w4::Layout l = mla::w4::layout_of(*w);
+    if (l.blocks_n * l.blocks_k >= ((int64_t)1 << 31)) return MLA_ERR_UNSUPPORTED;
+    return MLA_OK;
+}
+
 mla_status linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t x_head_stride, const mla_w4_weight* w,
                      void* out, int64_t out_row_stride, int64_t out_head_stride, bool early, void* stream)
 {
     using namespace mla::w4;
-    using mla::is_aligned;
     constexpr int64_t kMaxStride = (int64_t)1 << 40;
     const auto stride_ok = [](int64_t s) { return s >= 0 && s <= kMaxStride; };
-    if (rows < 0 || !w || (w->format != MLA_W4_INT4 && w->format != MLA_W4_NVFP4)) return MLA_ERR_INVALID_ARG;
-    const bool int4 = w->format == MLA_W4_INT4;
-    if (w->heads < 1 || w->n < 1 || w->k < 1 || !std::isfinite(w->tensor_scale)) return MLA_ERR_INVALID_ARG;
-    if (int4 ? (w->group != 32 && w->group != 64 && w->group != 128) : w->group != 16) return MLA_ERR_INVALID_ARG;
-    if (w->k % w->group || w->k % 32 || (!int4 && w->zero)) return MLA_ERR_INVALID_ARG;
+    if (rows < 0) return MLA_ERR_INVALID_ARG;
+    const mla_status shape = check_shape(w);
+    if (shape != MLA_OK) return shape;
     if (!stride_ok(x_row_stride) || !stride_ok(x_head_stride) || !stride_ok(out_row_stride) || !stride_ok(out_head_stride))
         return MLA_ERR_INVALID_ARG;
     if (rows == 0) return MLA_OK;
-    if (!x || !out || !w->codes || !w->scale || x == out) return MLA_ERR_INVALID_ARG;
+    if (!x || !out || !w->packed || x == out) return MLA_ERR_INVALID_ARG;
     if (!mla::distinct_elements(rows, out_row_stride, w->heads, out_head_stride, w->n)) return MLA_ERR_INVALID_ARG;
-    if (!is_aligned(x, 16) || !is_aligned(w->codes, 16) || !is_aligned(out, 2) || (int4 && !is_aligned(w->scale, 2)) ||
-        (rows > 1 && x_row_stride % 8) || (w->heads > 1 && x_head_stride % 8))
+    if (!is_aligned(x, 16) || !is_aligned(w->packed, 16) || !is_aligned(out, 2) || (rows > 1 && x_row_stride % 8) ||
+        (w->heads > 1 && x_head_stride % 8))
         return MLA_ERR_ALIGNMENT;
-    if (w->heads > 65535 || (int64_t)w->heads * w->n >= ((int64_t)1 << 31) || rows > 65535 * kMaxRowTiles * kRowTile)
-        return MLA_ERR_UNSUPPORTED;
+    if (rows > 65535 * kMaxRowTiles * kRowTile) return MLA_ERR_UNSUPPORTED;
+    const Layout l = layout_of(*w);
+    const uint8_t* packed = static_cast<const uint8_t*>(w->packed);
     Args a = {};
     a.x = static_cast<const __nv_bfloat16*>(x);
     a.x_row = x_row_stride;
     a.x_head = x_head_stride;
-    a.codes = static_cast<const uint8_t*>(w->codes);
-    a.scale = w->scale;
-    a.zero = static_cast<const uint8_t*>(w->zero);
+    a.codes = packed;
+    a.scale = packed + l.scale_off;
+    a.zero = w->has_zero ? packed + l.zero_off : nullptr;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.out_row = out_row_stride;
     a.out_head = out_head_stride;
@@ -509,15 +518,18 @@ mla_status linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t 
     a.rows = rows;
     a.n = w->n;
     a.k = w->k;
+    a.blocks_n = (int)l.blocks_n;
+    a.blocks_k = (int)l.blocks_k;
     a.early = early;
-    a.packed = w->k % 128 == 0 && is_aligned(w->scale, 8) && is_aligned(w->zero, 4);
-    // blocks of a cluster over k: doubled while there are too few tiles for two blocks per SM and
-    // every block keeps two stages
+    // As many of a block's warps over k as have two blocks each; the others over n.
+    a.k_warps = 1;
+    while (a.k_warps < kWarps && a.blocks_k >= 2 * a.k_warps) a.k_warps *= 2;
+    // Blocks of a cluster over k: doubled while there are too few for three per SM and every warp
+    // keeps two of the packed blocks.
     const int64_t row_blocks = (rows + kMaxRowTiles * kRowTile - 1) / (kMaxRowTiles * kRowTile);
-    const int64_t tiles = (int64_t)((w->n + kTileN - 1) / kTileN) * w->heads * row_blocks;
-    const int stages = (w->k + kStageK - 1) / kStageK;
+    const int64_t tiles = l.blocks_n * a.k_warps / kWarps * w->heads * row_blocks;
     a.splits = 1;
-    while (a.splits < 8 && tiles * a.splits < 2 * 152 && stages >= 4 * a.splits) a.splits *= 2;
+    while (a.splits < 8 && tiles * a.splits < 3 * 152 && a.blocks_k >= 4 * a.k_warps * a.splits) a.splits *= 2;
     switch (w->group) {
         case 16: return launch_rows<16>(a, w->heads, stream);
         case 32: return launch_rows<32>(a, w->heads, stream);
@@ -556,4 +568,36 @@ extern "C" MLA_API mla_status mla_out_proj_w4(const void* o_lat, const mla_w4_we
 {
     const mla::NvtxRange nvtx_range("mla_out_proj_w4");
     return head_product(batch, o_lat, w_uv, MLA_HEAD_DIM, MLA_LATENT_DIM, out, stream);
+}
+
+extern "C" MLA_API size_t mla_w4_packed_bytes(const mla_w4_weight* w)
+{
+    return check_shape(w) == MLA_OK ? (size_t)mla::w4::layout_of(*w).bytes : 0;
+}
+
+extern "C" MLA_API mla_status mla_w4_pack(const mla_w4_weight* w, const void* codes, const void* scale,
+                                          const void* zero, void* packed, void* stream)
+{
+    const mla::NvtxRange nvtx_range("mla_w4_pack");
+    const mla_status shape = check_shape(w);
+    if (shape != MLA_OK) return shape;
+    if (!codes || !scale || !packed || (w->has_zero != 0) != (zero != nullptr)) return MLA_ERR_INVALID_ARG;
+    if (!is_aligned(codes, 16) || !is_aligned(packed, 16) || (w->format == MLA_W4_INT4 && !is_aligned(scale, 2)))
+        return MLA_ERR_ALIGNMENT;
+    const mla::w4::Layout l = mla::w4::layout_of(*w);
+    mla::w4::PackArgs a = {};
+    a.codes = static_cast<const uint8_t*>(codes);
+    a.scale = scale;
+    a.zero = static_cast<const uint8_t*>(zero);
+    a.packed = static_cast<uint8_t*>(packed);
+    a.scale_off = l.scale_off;
+    a.zero_off = l.zero_off;
+    a.n = w->n;
+    a.k = w->k;
+    a.group = w->group;
+    a.blocks_n = (int)l.blocks_n;
+    a.blocks_k = (int)l.blocks_k;
+    const dim3 grid((unsigned)((l.blocks_n * l.blocks_k + 7) / 8), (unsigned)w->heads);
+    mla::w4::pack_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return mla::cuda_status(cudaGetLastError(), "4-bit pack kernel launch");
 }

@@ -25,7 +25,7 @@ DEV = "cuda:0"
 E2M1 = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64)
 
 
-def _weight(heads, n, k, fmt, group, zero, seed):
+def _weight(heads, n, k, fmt, group, zero, seed, change=None):
     """(W4Weight, its values in 64 bits [heads, n, k])."""
     g = torch.Generator().manual_seed(seed)
     codes = torch.randint(0, 256, (heads, n, k // 2), generator=g, dtype=torch.uint8)
@@ -34,6 +34,8 @@ def _weight(heads, n, k, fmt, group, zero, seed):
     if fmt == "int4":
         scale = (torch.randn(heads, n, k // group, generator=g) * 2 / k ** 0.5).bfloat16()
         scale[0, 0, 0] = 0.0
+        if change is not None:
+            change(scale)
         if zero:
             z = torch.randint(0, 16, (heads, n, k // group), generator=g, dtype=torch.uint8)
         value = (both.double() - (8.0 if z is None else z.double()[..., None])) * scale.double()[..., None]
@@ -160,7 +162,11 @@ def test_linear_special_values():
     assert torch.equal(out[keep], clean[keep]) and out[3].isnan().all() and not out[9].isfinite().all()
     binding.mla_linear_w4(torch.zeros_like(x), w, out)
     assert (out == 0).all()
-    w.scale[0, 20, 1] = float("inf")
+
+    def infinite(scale):
+        scale[0, 20, 1] = float("inf")
+
+    w, _ = _weight(1, 50, 256, "int4", 64, False, 9, infinite)
     binding.mla_linear_w4(x, w, out)
     keep = [c for c in range(50) if c != 20]
     assert torch.equal(out[:, keep], clean[:, keep]) and not out[:, 20].isfinite().any()
@@ -226,9 +232,14 @@ def test_linear_empty_and_refusals():
     with pytest.raises(ValueError):
         binding.mla_absorb_q_w4(torch.zeros(1, 128, 128, dtype=torch.bfloat16, device=DEV), w,
                                 torch.zeros(1, 128, 512, dtype=torch.bfloat16, device=DEV))
-    cpu = binding.W4Weight(w.codes.cpu(), w.scale.cpu())
-    with pytest.raises(ValueError):
-        binding.mla_linear_w4(x, cpu, out)
+    codes = torch.zeros(2, 3, 32, dtype=torch.uint8, device=DEV)
+    ones = torch.ones(2, 3, 2, dtype=torch.bfloat16, device=DEV)
+    for args, kw in (((codes.cpu(), ones), {}), ((codes, ones.cpu()), {}), ((codes[:, :, ::2], ones[:, :, :1]), {}),
+                     ((codes, ones[:, :2]), {}), ((codes, ones), dict(zero=codes[:, :, :2]))):
+        with pytest.raises(ValueError):
+            binding.W4Weight(*args, **kw)
+    with pytest.raises(TypeError):
+        binding.W4Weight(codes.int(), ones)
 
 
 def _attention(inp, q_c, q_r, k_val, v_val):
@@ -253,7 +264,7 @@ def test_step_with_4_bit_weights(fmt, group, zero):
     # absolute bounds of the step's tolerance are for outputs of about 1: weights of unit rows
     for w, v in ((uk, k_val), (uv, v_val)):
         s = 1.0 / float(v.square().sum(-1).mean().sqrt()) * (0.5 if w is uk else 1.0)
-        w.struct.tensor_scale = s * w.tensor_scale
+        w.struct.tensor_scale = s * w.tensor_scale   # a float of the struct, read at each call
         v *= w.struct.tensor_scale / w.tensor_scale
     step = binding.DecodeStep(inp.seq_lens, w_uk=uk, w_uv=uv, block_table=bt, min_pages_per_split=2, **kv)
     out = step.run(q_c, q_r).clone()

@@ -157,75 +157,82 @@ def test_rope_append_of_nothing_and_of_another_dim(L):
     assert _append(L, binding.Rope(128)) == INV
 
 
-def _w4(L, rows=4, x=0x100000, xs=(128, 128), out=0x800000, os_=(512, 512), **kw):
-    f = dict(format=0, heads=1, n=512, k=128, group=32, tensor_scale=1.0, codes=0x200000, scale=0x300000, zero=None)
+def _weight(**kw):
+    f = dict(format=0, heads=1, n=512, k=128, group=32, has_zero=0, tensor_scale=1.0, packed=0x200000)
     f.update(kw)
-    w = binding.W4Struct(*[f[n] for n, _ in binding.W4Struct._fields_])
+    return binding.W4Struct(*[f[n] for n, _ in binding.W4Struct._fields_])
+
+
+def _w4(L, rows=4, x=0x100000, xs=(128, 128), out=0x800000, os_=(512, 512), **kw):
+    w = _weight(**kw)
     return L.mla_linear_w4(rows, P(x) if x else None, xs[0], xs[1], ctypes.byref(w), P(out) if out else None, os_[0],
                            os_[1], None)
 
 
-@pytest.mark.parametrize("kw,status", [
-    (dict(rows=-1), INV), (dict(format=2), INV), (dict(heads=0), INV), (dict(n=0), INV), (dict(k=0), INV),
-    (dict(group=16), INV), (dict(group=48), INV), (dict(k=144), INV), (dict(k=96, group=64), INV),
-    (dict(format=1), INV), (dict(format=1, group=16, zero=0x400000), INV), (dict(format=1, group=16, k=48), INV),
-    (dict(tensor_scale=float("nan")), INV), (dict(tensor_scale=float("inf")), INV),
-    (dict(x=0), INV), (dict(out=0), INV), (dict(codes=None), INV), (dict(scale=None), INV), (dict(out=0x100000), INV),
+SHAPES = [(dict(format=2), INV), (dict(heads=0), INV), (dict(n=0), INV), (dict(k=0), INV), (dict(group=16), INV),
+          (dict(group=48), INV), (dict(k=144), INV), (dict(k=96, group=64), INV), (dict(format=1), INV),
+          (dict(format=1, group=16, has_zero=1), INV), (dict(format=1, group=16, k=48), INV), (dict(has_zero=2), INV),
+          (dict(tensor_scale=float("nan")), INV), (dict(tensor_scale=float("inf")), INV), (dict(heads=65536), UNSUP),
+          (dict(heads=65535, n=40000), UNSUP), (dict(k=(1 << 30) + 128), UNSUP), (dict(n=1 << 30, k=1 << 14), UNSUP)]
+
+
+@pytest.mark.parametrize("kw,status", SHAPES + [
+    (dict(rows=-1), INV), (dict(x=0), INV), (dict(out=0), INV), (dict(packed=None), INV), (dict(out=0x100000), INV),
     (dict(xs=(-8, 128)), INV), (dict(os_=(-8, 512)), INV), (dict(os_=(256, 512)), INV), (dict(os_=(0, 512)), INV),
-    (dict(heads=2, os_=(512, 512)), INV), (dict(heads=2, os_=(1024, 256)), INV),
-    (dict(x=0x100008), ALIGN), (dict(codes=0x200008), ALIGN), (dict(out=0x800001), ALIGN),
-    (dict(scale=0x300001), ALIGN), (dict(xs=(132, 128)), ALIGN), (dict(heads=2, xs=(256, 132), os_=(1024, 512)), ALIGN),
-    (dict(heads=65536, os_=(512 * 65536, 512)), UNSUP),
-    (dict(heads=65535, n=40000, os_=(40000 * 65535, 40000)), UNSUP)])
+    (dict(heads=2, os_=(512, 512)), INV), (dict(heads=2, os_=(1024, 256)), INV), (dict(xs=(1 << 41, 128)), INV),
+    (dict(x=0x100008), ALIGN), (dict(packed=0x200008), ALIGN), (dict(out=0x800001), ALIGN),
+    (dict(xs=(132, 128)), ALIGN), (dict(heads=2, xs=(256, 132), os_=(1024, 512)), ALIGN)])
 def test_w4_refuses(L, kw, status):
     assert _w4(L, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", SHAPES + [
+    (dict(codes=0), INV), (dict(scale=0), INV), (dict(to=0), INV), (dict(zero=0x400000), INV), (dict(has_zero=1), INV),
+    (dict(codes=0x200008), ALIGN), (dict(scale=0x300001), ALIGN), (dict(to=0x500008), ALIGN)])
+def test_w4_pack_refuses(L, kw, status):
+    p = dict(codes=0x200000, scale=0x300000, zero=0, to=0x500000)
+    p.update({k: v for k, v in kw.items() if k in p})
+    w = _weight(**{k: v for k, v in kw.items() if k not in p})
+    f = lambda v: P(v) if v else None  # noqa: E731
+    assert L.mla_w4_pack(ctypes.byref(w), f(p["codes"]), f(p["scale"]), f(p["zero"]), f(p["to"]), None) == status
+
+
+def test_w4_packed_bytes(L):
+    """Blocks of 32 n x 128 k: 2,048 bytes of codes, and 32 scales and zeros per group of k."""
+    size = lambda **kw: L.mla_w4_packed_bytes(ctypes.byref(_weight(**kw)))  # noqa: E731
+    assert size(n=512, k=128, group=128) == 16 * (2048 + 64)
+    assert size(n=33, k=160, group=32, has_zero=1, heads=3) == 3 * 2 * 2 * (2048 + 256 + 128)
+    assert size(n=1, k=64, group=64, has_zero=1) == 2048 + 128 + 64
+    assert size(n=32, k=128, group=16, format=1) == 2048 + 256
+    assert all(size(**kw) == 0 for kw, _ in SHAPES)
+    assert L.mla_w4_packed_bytes(None) == 0
 
 
 def test_w4_of_no_rows_and_head_shapes(L):
     assert _w4(L, rows=0, x=0, out=0) == binding.MLA_OK
     assert L.mla_linear_w4(1, P(16), 8, 8, None, P(4096), 8, 8, None) == INV
-    w = binding.W4Struct(0, 128, 512, 128, 32, 1.0, 0x200000, 0x300000, None)
-    for fn, bad in ((L.mla_absorb_q_w4, (0, 128, 128, 512, 32)), (L.mla_out_proj_w4, (0, 128, 512, 128, 32)),
-                    (L.mla_absorb_q_w4, (0, 1, 512, 128, 32))):
-        v = binding.W4Struct(*bad, 1.0, 0x200000, 0x300000, None)
+    w = _weight(heads=128)
+    for fn, bad in ((L.mla_absorb_q_w4, dict(heads=128, n=128, k=512)), (L.mla_out_proj_w4, dict(heads=128)),
+                    (L.mla_absorb_q_w4, {})):
+        v = _weight(**bad)
         assert fn(P(0x100000), ctypes.byref(v), P(0x800000), 1, None) == INV
         assert fn(P(0x100000), None, P(0x800000), 1, None) == INV
     assert L.mla_absorb_q_w4(P(0x100000), ctypes.byref(w), P(0x800000), 0, None) == INV
     assert L.mla_absorb_q_w4(P(0x100008), ctypes.byref(w), P(0x800000), 1, None) == ALIGN
 
 
-def _weight(heads=2, n=3, k=64, group=32, **kw):
-    codes = torch.zeros(heads, n, k // 2, dtype=torch.uint8)
-    return binding.W4Weight(codes, torch.ones(heads, n, k // group, dtype=torch.bfloat16), **kw)
-
-
 def test_w4_weight_checks():
-    w = _weight()
-    assert (w.heads, w.n, w.k, w.group, w.format) == (2, 3, 64, 32, binding.MLA_W4_INT4)
-    v = binding.W4Weight(torch.zeros(5, 16, dtype=torch.uint8), torch.zeros(5, 2, dtype=torch.uint8))
-    assert (v.heads, v.n, v.k, v.group, v.format) == (1, 5, 32, 16, binding.MLA_W4_NVFP4)
-    f8 = torch.zeros(5, 2, dtype=torch.uint8).view(torch.float8_e4m3fn)
-    assert binding.W4Weight(torch.zeros(5, 16, dtype=torch.uint8), f8).format == binding.MLA_W4_NVFP4
+    """Shapes and types are refused before anything is asked of a GPU."""
     codes = torch.zeros(2, 3, 32, dtype=torch.uint8)
     ones = torch.ones(2, 3, 2, dtype=torch.bfloat16)
-    with pytest.raises(ValueError):
-        binding.W4Weight(codes, ones, group=64)
-    with pytest.raises(ValueError):
-        binding.W4Weight(codes, torch.ones(2, 3, 3, dtype=torch.bfloat16))           # 3 groups of k = 64
-    with pytest.raises(ValueError):
-        binding.W4Weight(codes, torch.ones(2, 3, 4, dtype=torch.bfloat16))           # int4 in groups of 16
-    with pytest.raises(ValueError):
-        binding.W4Weight(codes, torch.ones(2, 4, 2, dtype=torch.bfloat16))           # another n
-    with pytest.raises(ValueError):
-        binding.W4Weight(codes[:, :, ::2], torch.ones(2, 3, 1, dtype=torch.bfloat16))  # not contiguous
-    with pytest.raises(ValueError):
-        binding.W4Weight(codes[:, :, :24].contiguous(), torch.zeros(2, 3, 3, dtype=torch.uint8),
-                         zero=torch.zeros(2, 3, 3, dtype=torch.uint8))               # k = 48
-    with pytest.raises(ValueError):
-        binding.W4Weight(codes, torch.zeros(2, 3, 4, dtype=torch.uint8), zero=torch.zeros(2, 3, 4, dtype=torch.uint8))
-    with pytest.raises(TypeError):
-        binding.W4Weight(codes, ones.float())
-    with pytest.raises(TypeError):
-        binding.W4Weight(codes.int(), ones)
-    with pytest.raises(TypeError):
-        binding.W4Weight(codes, ones, zero=torch.zeros(2, 3, 2))
+    for args, kw in (((codes, ones), dict(group=64)),
+                     ((codes, torch.ones(2, 3, 3, dtype=torch.bfloat16)), {}),     # 3 groups of k = 64
+                     ((codes, torch.ones(2, 3, 4, dtype=torch.bfloat16)), {}),     # int4 in groups of 16
+                     ((codes, ones[0]), {}),                                       # another number of dimensions
+                     ((codes[:, :, :24], torch.zeros(2, 3, 3, dtype=torch.uint8)), {}),   # k = 48
+                     ((codes, torch.zeros(2, 3, 4, dtype=torch.uint8)), dict(zero=torch.zeros(2, 3, 4, dtype=torch.uint8)))):
+        with pytest.raises(ValueError):
+            binding.W4Weight(*args, **kw)
+    for args, kw in (((codes, ones.float()), {}), ((codes, None), {}), ((codes, ones), dict(zero=7))):
+        with pytest.raises(TypeError):
+            binding.W4Weight(*args, **kw)
