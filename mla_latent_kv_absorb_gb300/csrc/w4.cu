@@ -6,14 +6,14 @@
 // would want the unpacked weights in shared memory and a group's scale cannot be applied inside its
 // accumulator; at these row counts the product is bound by the weights' bytes, then by unpacking.
 //
-// A warp works on blocks of 32 n x 128 k, which the packed layout keeps in 2 KB: lane 4 g + t finds
-// its words (q, t), the eight k from 32 q + 8 t, q = 0..3, of rows g, g + 8, g + 16 and g + 24 in four
-// 16-byte pieces, so that the codes go from memory to the registers that unpack them, the next
-// block's while this one's are worked on, and no barrier is in the loop.  (Codes by cp.async through
-// shared memory with a barrier a stage took 34 us where this takes TIME1, at one row, N 8192, K
-// 16384.)  Unpacking is bound by the integer pipe, which runs at half the rate of the FMA pipes, so
-// it is built from as few integer operations as there are.  A word has k 2 i and 2 i + 1 in nibbles i
-// and i + 4:
+// A warp works on blocks of 32 n x 128 k: lane 4 g + t has the words (q, t), the eight k from 32 q + 8 t,
+// q = 0..3, of rows g, g + 8, g + 16 and g + 24.  The packed layout keeps a block's 2 KB of codes in
+// that order, its scales and zeros behind them, and the blocks of a thread block's four warps side by
+// side, so that one bulk copy brings a step of all four (8 to 10 KB) and a lane reads its part in
+// 16-byte pieces.  A ring of four or five steps covers the latency of HBM; x comes by cp.async, two
+// steps at a time.  Unpacking is bound by the integer pipe, which runs at half the rate of the FMA
+// pipes, so it is built from as few integer operations as there are.  A word has k 2 i and 2 i + 1 in
+// nibbles i and i + 4:
 //   int4: the bits (w & 0x000F000F) are, as a pair of bf16, code 2^-133 (subnormal bf16 is linear in
 //         its bits, and still is one binade up, so (w & 0x00F000F0) is 16 code 2^-133); one bf16 FMA
 //         with 2^127 or 2^123 and -zero / 64 makes (code - zero) / 64 exactly.  Five integer
@@ -21,10 +21,9 @@
 //         sums are scaled into the output's (the scale times a weight would round in bf16).
 //   NVFP4: the code's bits moved to bf16's sign, two exponent bits and one mantissa bit are its value
 //         times 2^-126; times scale 2^118 it is exact in bf16 (two times four significant bits).
-// The powers of two left over, 2^6 and 2^8, go into the end's product.  x is read as it lies, through
-// L1, where the warps of an SM find each other's pieces.  The warps of a block split k (and n, when
-// there is little k), and so do the blocks of a cluster when there are few output tiles; the sums are
-// joined in a fixed order through (distributed) shared memory.
+// The powers of two left over, 2^6 and 2^8, go into the end's product.  Thread blocks of a cluster
+// split k when there are few output tiles; the sums are joined in a fixed order through (distributed)
+// shared memory, four outputs a thread.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,10 +37,11 @@
 
 namespace mla::w4 {
 
+constexpr uint64_t kTimeoutNs = 2000000000ull;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlockN = 32, kBlockK = 128;          // of a packed block
-constexpr int kBlockBytes = kBlockN * kBlockK / 2;  // its codes
+constexpr int kCodeBytes = kBlockN * kBlockK / 2;   // its codes
 constexpr int kRowTile = 8;                         // rows of x per MMA
 constexpr int kMaxRowTiles = 8;
 constexpr int kRedPitch = kBlockN + 4;  // floats; the four lanes of a row hit different banks
@@ -49,22 +49,41 @@ constexpr int kRedPitch = kBlockN + 4;  // floats; the four lanes of a row hit d
 // Bytes of a block's scales (int4: bf16 [g][j][group], NVFP4: e4m3 [g][t / 2][j][q]) and of its zeros
 // (uint8 [g][j][group]), row 8 j + g of the block.
 __host__ __device__ constexpr int scale_bytes(int group) { return group == 16 ? kBlockN * 8 : kBlockN * (kBlockK / group) * 2; }
-__host__ __device__ constexpr int zero_bytes(int group) { return kBlockN * (kBlockK / group); }
+__host__ __device__ constexpr int zero_bytes(int group) { return group == 16 ? 0 : kBlockN * (kBlockK / group); }
 
-// The packed image: all blocks' codes [h][n / 32][k / 128], then their scales, then their zeros.
+// How the four warps of a thread block share its outputs: all over n, so that x is brought for 128
+// outputs at a time; two or all four over k where that leaves too few thread blocks for the SMs even
+// with clusters of eight over k.  Goes by the weights alone, since they are packed for it.
+__host__ inline int k_warps_of(const mla_w4_weight& w)
+{
+    const int64_t blocks_n = ((int64_t)w.n + kBlockN - 1) / kBlockN, blocks_k = ((int64_t)w.k + kBlockK - 1) / kBlockK;
+    int k_warps = 1;
+    while (k_warps < kWarps && blocks_k >= 4 * k_warps) {
+        const int64_t tiles = (blocks_n * k_warps + kWarps - 1) / kWarps * w.heads, splits = blocks_k / k_warps / 2;
+        if (tiles * (splits < 8 ? splits : 8) >= 2 * 152) break;
+        k_warps *= 2;
+    }
+    return k_warps;
+}
+
+// The packed image: steps [h][n / (32 kWarps / k_warps)][k / (128 k_warps)] of four blocks, one for each
+// warp of a thread block (warp w: w / k_warps over n, w % k_warps over k), each its codes, its scales
+// and (has_zero) its zeros, a multiple of 16 bytes.
 struct Layout {
-    int64_t blocks_n, blocks_k;  // of one head
-    int64_t scale_off, zero_off, bytes;
+    int k_warps;
+    int64_t panels, steps;  // of one head
+    int block_bytes;
+    int64_t bytes;
 };
 __host__ inline Layout layout_of(const mla_w4_weight& w)
 {
     Layout l;
-    l.blocks_n = ((int64_t)w.n + kBlockN - 1) / kBlockN;
-    l.blocks_k = ((int64_t)w.k + kBlockK - 1) / kBlockK;
-    const int64_t blocks = l.blocks_n * l.blocks_k * w.heads;
-    l.scale_off = blocks * kBlockBytes;
-    l.zero_off = l.scale_off + blocks * scale_bytes(w.group);
-    l.bytes = l.zero_off + (w.has_zero ? blocks * zero_bytes(w.group) : 0);
+    l.k_warps = k_warps_of(w);
+    const int64_t panel_n = kBlockN * kWarps / l.k_warps, step_k = kBlockK * l.k_warps;
+    l.panels = (w.n + panel_n - 1) / panel_n;
+    l.steps = (w.k + step_k - 1) / step_k;
+    l.block_bytes = kCodeBytes + scale_bytes(w.group) + (w.has_zero ? zero_bytes(w.group) : 0);
+    l.bytes = l.panels * l.steps * w.heads * kWarps * l.block_bytes;
     return l;
 }
 
@@ -73,19 +92,21 @@ struct PackArgs {
     const void* scale;
     const uint8_t* zero;
     uint8_t* packed;
-    int64_t scale_off, zero_off;
     int n, k, group;
-    int blocks_n, blocks_k;
+    int panels, steps, k_warps, block_bytes;
 };
 
 // One warp per packed block; n and k past the weights' are filled with zeros of scale zero.
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, h = blockIdx.y;
-    const int64_t b = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (b >= (int64_t)a.blocks_n * a.blocks_k) return;
-    const int n0 = (int)(b / a.blocks_k) * kBlockN, k0 = (int)(b % a.blocks_k) * kBlockK;
-    const int64_t block = (int64_t)h * a.blocks_n * a.blocks_k + b;
+    const int64_t b = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);  // of the head
+    if (b >= (int64_t)a.panels * a.steps * kWarps) return;
+    const int w = (int)(b % kWarps), step = (int)(b / kWarps % a.steps), panel = (int)(b / kWarps / a.steps);
+    const int n0 = (panel * (kWarps / a.k_warps) + w / a.k_warps) * kBlockN, k0 = (step * a.k_warps + w % a.k_warps) * kBlockK;
+    uint8_t* block = a.packed + ((int64_t)h * a.panels * a.steps * kWarps + b) * a.block_bytes;
+    uint8_t* scales = block + kCodeBytes;
+    uint8_t* zeros = scales + scale_bytes(a.group);
     const int groups = a.k / a.group;  // of a row
     const bool nv = a.group == 16;
     for (int j = 0; j < 4; ++j) {
@@ -94,18 +115,17 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackA
         uint32_t word[4];
         for (int q = 0; q < 4; ++q) {
             const int k = k0 + 32 * q + 8 * t;
-            uint32_t w = 0;
+            uint32_t to = 0;
             if (n < a.n && k < a.k) {
                 const uint32_t v = *reinterpret_cast<const uint32_t*>(a.codes + row * (a.k / 2) + k / 2);
                 for (int i = 0; i < 4; ++i)  // nibbles 2 i and 2 i + 1 to i and i + 4
-                    w |= ((v >> (8 * i)) & 15u) << (4 * i) | ((v >> (8 * i + 4)) & 15u) << (4 * i + 16);
+                    to |= ((v >> (8 * i)) & 15u) << (4 * i) | ((v >> (8 * i + 4)) & 15u) << (4 * i + 16);
                 // a negative scale's sign goes into its codes
-                if (nv && (static_cast<const uint8_t*>(a.scale)[row * groups + k / 16] & 0x80u)) w ^= 0x88888888u;
+                if (nv && (static_cast<const uint8_t*>(a.scale)[row * groups + k / 16] & 0x80u)) to ^= 0x88888888u;
             }
-            word[q] = w;
+            word[q] = to;
         }
-        *reinterpret_cast<uint4*>(a.packed + block * kBlockBytes + j * 512 + lane * 16) =
-            make_uint4(word[0], word[1], word[2], word[3]);
+        *reinterpret_cast<uint4*>(block + j * 512 + lane * 16) = make_uint4(word[0], word[1], word[2], word[3]);
         if (nv) {
             if (t & 1) continue;
             uint32_t s = 0;
@@ -114,18 +134,16 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackA
                 if (n < a.n && k < a.k)
                     s |= (uint32_t)(static_cast<const uint8_t*>(a.scale)[row * groups + k / 16] & 0x7Fu) << (8 * q);
             }
-            *reinterpret_cast<uint32_t*>(a.packed + a.scale_off + block * scale_bytes(16) + (g * 2 + (t >> 1)) * 16 + j * 4) = s;
+            *reinterpret_cast<uint32_t*>(scales + (g * 2 + (t >> 1)) * 16 + j * 4) = s;
         } else {
             const int count = kBlockK / a.group;
             if (t >= count) continue;
             const int k = k0 + t * a.group;
             const bool in = n < a.n && k < a.k;
             const int at = (g * 4 + j) * count + t;
-            reinterpret_cast<uint16_t*>(a.packed + a.scale_off + block * scale_bytes(a.group))[at] =
+            reinterpret_cast<uint16_t*>(scales)[at] =
                 in ? static_cast<const uint16_t*>(a.scale)[row * groups + k / a.group] : (uint16_t)0;
-            if (a.zero)
-                (a.packed + a.zero_off + block * zero_bytes(a.group))[at] =
-                    in ? a.zero[row * groups + k / a.group] : (uint8_t)8;
+            if (a.zero) zeros[at] = in ? a.zero[row * groups + k / a.group] : (uint8_t)8;
         }
     }
 }
@@ -133,34 +151,51 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackA
 struct Args {
     const __nv_bfloat16* x;
     int64_t x_row, x_head;
-    const uint8_t* codes;
-    const uint8_t* scale;
-    const uint8_t* zero;  // NULL: 8
+    const uint8_t* packed;
+    int block_bytes;
+    uint32_t zero_mask;  // all ones, or 0: every zero is 8
     __nv_bfloat16* out;
     int64_t out_row, out_head;
     float tensor_scale;
     int rows, n, k;
-    int blocks_n, blocks_k;
+    int steps;    // of 128 k_warps k
     int k_warps;  // warps of a thread block over k; the others over n
     int splits;   // thread blocks of a cluster, over k
-    bool early;   // kernels behind this one may start before it ends (they wait for `out` themselves)
+    int ring_off, bars_off;  // in shared memory
+    bool out_quads;  // four outputs are one aligned 8-byte store
+    bool early;      // kernels behind this one may start before it ends (they wait for `out` themselves)
 };
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool valid)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Four floats of a block of the cluster (after a cluster barrier; not volatile, so that loads from
+// several blocks are under way at once).
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr)
+{
+    float4 v;
+    asm("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
     return v;
 }
 
-__device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes)
+// `bytes` (a multiple of 16) from global to this block's shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -218,7 +253,7 @@ __device__ __forceinline__ uint32_t e4m3_scale(uint32_t bytes, int i)
     return mul_bf16x2(mul_bf16x2(b << 4, k2p127), k2p111);
 }
 
-// What a lane holds of a block: the codes of its four rows, and their scales and zeros.
+// What a lane holds of a block: the codes of its four rows, their scales and zeros.
 template <int kGroup>
 struct Held {
     static constexpr int kScale = kGroup == 128 ? 2 : kGroup == 32 ? 8 : 4;  // 32-bit words
@@ -227,43 +262,30 @@ struct Held {
     uint32_t s[kScale];
     uint32_t z[kZero];
 
-    // Through L2 only what is read once; the scales' sectors are shared by the four lanes of a row.
-    __device__ __forceinline__ void load(const Args& a, int64_t block, int lane)
+    template <int N>
+    static __device__ __forceinline__ void words(uint32_t (&to)[N], const uint8_t* from)
     {
-        const uint4* p = reinterpret_cast<const uint4*>(a.codes + block * kBlockBytes) + lane;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = __ldcg(p + 32 * j);
-        const int g = lane >> 2;
-        const uint8_t* ps = a.scale + block * scale_bytes(kGroup);
-        if constexpr (kGroup == 16) {
-            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(ps) + (lane >> 1));
-            s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
-        } else if constexpr (kGroup == 128) {
-            const uint2 v = __ldcg(reinterpret_cast<const uint2*>(ps) + g);
-            s[0] = v.x, s[1] = v.y;
+        if constexpr (N == 1) {
+            to[0] = *reinterpret_cast<const uint32_t*>(from);
+        } else if constexpr (N == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(from);
+            to[0] = v.x, to[1] = v.y;
         } else {
 #pragma unroll
-            for (int i = 0; i < kScale / 4; ++i) {
-                const uint4 v = __ldcg(reinterpret_cast<const uint4*>(ps) + g * (kScale / 4) + i);
-                s[4 * i] = v.x, s[4 * i + 1] = v.y, s[4 * i + 2] = v.z, s[4 * i + 3] = v.w;
+            for (int i = 0; i < N / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(from)[i];
+                to[4 * i] = v.x, to[4 * i + 1] = v.y, to[4 * i + 2] = v.z, to[4 * i + 3] = v.w;
             }
         }
-        if constexpr (kGroup >= 32) {
+    }
+    // from the block's image in shared memory; without zeros the bytes read for them are not used
+    __device__ __forceinline__ void load(const uint8_t* image, int lane)
+    {
 #pragma unroll
-            for (int i = 0; i < kZero; ++i) z[i] = 0x08080808u;
-            if (a.zero) {
-                const uint8_t* pz = a.zero + block * zero_bytes(kGroup);
-                if constexpr (kZero == 1) {
-                    z[0] = __ldcg(reinterpret_cast<const uint32_t*>(pz) + g);
-                } else if constexpr (kZero == 2) {
-                    const uint2 v = __ldcg(reinterpret_cast<const uint2*>(pz) + g);
-                    z[0] = v.x, z[1] = v.y;
-                } else {
-                    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(pz) + g);
-                    z[0] = v.x, z[1] = v.y, z[2] = v.z, z[3] = v.w;
-                }
-            }
-        }
+        for (int j = 0; j < 4; ++j) c[j] = reinterpret_cast<const uint4*>(image)[32 * j + lane];
+        const uint8_t* scales = image + kCodeBytes;
+        words(s, scales + (kGroup == 16 ? lane >> 1 : lane >> 2) * (4 * kScale));
+        if constexpr (kGroup >= 32) words(z, scales + scale_bytes(kGroup) + (lane >> 2) * (4 * kZero));
     }
     // int4: scale and zero of group i of row 8 j + g
     __device__ __forceinline__ float scale(int j, int i) const
@@ -271,17 +293,11 @@ struct Held {
         const int e = j * (kBlockK / kGroup) + i;
         return e & 1 ? dev::bf16_hi(s[e / 2]) : dev::bf16_lo(s[e / 2]);
     }
-    __device__ __forceinline__ uint32_t zero64(int j, int i) const
+    __device__ __forceinline__ uint32_t zero64(const Args& a, int j, int i) const
     {
         const int e = j * (kBlockK / kGroup) + i;
-        return minus_zero(z[e / 4], e & 3);
+        return minus_zero((z[e / 4] & a.zero_mask) | (~a.zero_mask & 0x08080808u), e & 3);
     }
-};
-
-// x of a block's k: piece (q, t) of rows g + 8 rt
-template <int RT>
-struct XPieces {
-    uint4 v[RT];
 };
 
 template <int RT>
@@ -290,6 +306,36 @@ __host__ __device__ constexpr int blocks_per_sm()
     return RT <= 2 ? 4 : RT <= 5 ? 3 : 2;
 }
 
+// Shared memory: x's two stages of kStageSteps steps of k_warps pieces of 128 k; a ring of steps'
+// packed blocks, with a barrier a slot; afterwards, in the same place, the sums.  A step is one bulk
+// copy of 8 to 10 KB: an SM's copy engine takes about the same time for any size (2 KB blocks, a copy
+// each, stopped at 5 TB/s with nothing done to them).
+constexpr int kStageSteps = 2;
+constexpr int kXPiece = kRowTile * kBlockK * 2;  // bytes of 128 k of one row tile
+template <int kGroup, int RT>
+struct Shared {
+    static constexpr int kBlock = kCodeBytes + scale_bytes(kGroup) + zero_bytes(kGroup);
+    static constexpr int kSlots = (RT == 1 && kGroup != 32) || RT == 3 ? 5 : 4;
+    static constexpr int kBars = (kSlots + 1) * 8;
+    // of a thread block that takes `steps` steps
+    static __host__ constexpr int x_bytes(int k_warps, int steps)
+    {
+        return (steps < 2 * kStageSteps ? steps : 2 * kStageSteps) * k_warps * RT * kXPiece;
+    }
+    static __host__ constexpr int bytes(int k_warps, int steps)
+    {
+        const int sums = kWarps * RT * kRowTile * kRedPitch * 4;
+        const int rings = x_bytes(k_warps, steps) + kWarps * (steps < kSlots ? steps : kSlots) * kBlock;
+        return (sums > rings ? sums : rings) + kBars;
+    }
+    // thread blocks that an SM holds
+    static __host__ constexpr int resident(int k_warps, int steps)
+    {
+        const int fit = 228 * 1024 / (bytes(k_warps, steps) + 1024);
+        return fit < blocks_per_sm<RT>() ? fit : blocks_per_sm<RT>();
+    }
+};
+
 // kGroup 32, 64, 128: int4; 16: NVFP4.
 template <int kGroup, int RT>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<RT>()) linear_w4_kernel(const __grid_constant__ Args a)
@@ -297,44 +343,56 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<RT>()) linear_w4_kerne
     using namespace dev;
     constexpr bool kInt4 = kGroup >= 32;
     constexpr int kQ = kInt4 ? kGroup / 32 : 1;  // q's of a group
-    extern __shared__ __align__(16) float red[];  // [warp][row][kRedPitch]
+    using S = Shared<kGroup, RT>;
+    extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int n_warps = kWarps / a.k_warps, wk = warp % a.k_warps, wn = warp / a.k_warps;
     const int rank = (int)blockIdx.x % a.splits, tile = (int)blockIdx.x / a.splits;
-    const int bn = tile * n_warps + wn;
     const int h = blockIdx.y, r0 = (int)blockIdx.z * (RT * kRowTile);
-    const int first = (int)((int64_t)a.blocks_k * rank / a.splits) + wk;
-    const int last = bn < a.blocks_n ? (int)((int64_t)a.blocks_k * (rank + 1) / a.splits) : 0;
-    const int64_t row_blocks = ((int64_t)h * a.blocks_n + bn) * a.blocks_k;
+    const int begin = (int)((int64_t)a.steps * rank / a.splits), end = (int)((int64_t)a.steps * (rank + 1) / a.splits);
+    const int steps = end - begin, stages = (steps + kStageSteps - 1) / kStageSteps;
 
-    constexpr int kFar = 4;  // blocks of this warp from HBM to L2 ahead
-    // Bringing the weights to L2 is no read of them: it may come before the kernel ahead has ended.
-    if (lane < kFar && first + lane * a.k_warps < last)
-        prefetch_l2_bulk(a.codes + (row_blocks + first + lane * a.k_warps) * kBlockBytes, kBlockBytes);
-    griddep_wait();
-    if (a.early) griddep_launch_dependents();
-
-    const __nv_bfloat16* xsrc = a.x + (int64_t)(r0 + g) * a.x_row + (int64_t)h * a.x_head + 8 * t;
-    const auto load_x = [&](int block, int q, XPieces<RT>& p) {
-        const int k = block * kBlockK + 32 * q;
-        const bool k_ok = k + 8 * t < a.k;
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            p.v[rt] = make_uint4(0u, 0u, 0u, 0u);
-            if (k_ok && r0 + g + 8 * rt < a.rows)
-                p.v[rt] = __ldca(reinterpret_cast<const uint4*>(xsrc + (int64_t)rt * 8 * a.x_row + k));
-        }
+    // the ring of steps
+    const uint32_t sbase = smem_u32(smem);
+    const int ring_off = a.ring_off, bars_off = a.bars_off;
+    const uint32_t bars = sbase + bars_off;
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + bars_off + S::kSlots * 8);
+    const WaitCtx wait{kTimeoutNs, abort, nullptr};
+    const int step_bytes = kWarps * a.block_bytes;
+    const uint8_t* source = a.packed + (((int64_t)h * (gridDim.x / a.splits) + tile) * a.steps + begin) * step_bytes;
+    const auto bring = [&](int i) {  // thread 0: step i of this thread block
+        const int slot = i % S::kSlots;
+        mbar_arrive_expect_tx(bars + 8 * slot, step_bytes);
+        bulk_load(sbase + ring_off + slot * (kWarps * S::kBlock), source + (int64_t)i * step_bytes, step_bytes, bars + 8 * slot);
     };
+    const auto fill = [&]() {
+        if (tid == 0)
+            for (int i = 0; i < S::kSlots && i < steps; ++i) bring(i);
+    };
+    if (tid == 0) {
+        *abort = 0;
+        for (int i = 0; i < S::kSlots; ++i) mbar_init(bars + 8 * i, 1);
+        fence_barrier_init();
+    }
+    if (a.early) fill();  // the step's weights do not depend on the kernel before this one
+    griddep_wait();
+    if (a.early)
+        griddep_launch_dependents();
+    else
+        fill();
 
+    const __nv_bfloat16* xhead = a.x + (int64_t)h * a.x_head;
     float acc[2][RT][4] = {};
-    const auto work = [&](const Held<kGroup>& w, int block, int after) {
-        if (lane == 0 && block + kFar * a.k_warps < last)
-            prefetch_l2_bulk(a.codes + (row_blocks + block + kFar * a.k_warps) * kBlockBytes, kBlockBytes);
+    // a block in w, its x at `ring`
+    const auto work = [&](const Held<kGroup>& w, const uint8_t* ring) {
         float part[2][RT][4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            XPieces<RT> b;
-            load_x(block, q, b);
+            uint4 b[RT];  // piece (q, t) of rows g + 8 rt
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+                b[rt] = *reinterpret_cast<const uint4*>(ring + rt * kXPiece + g * (kBlockK * 2) +
+                                                        (((4 * q + t) ^ ((g & 1) << 2)) << 4));
             if (kInt4 && q % kQ == 0) {
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
@@ -351,15 +409,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<RT>()) linear_w4_kerne
                     const int j = 2 * m + half;
                     const uint32_t word = q == 0 ? w.c[j].x : q == 1 ? w.c[j].y : q == 2 ? w.c[j].z : w.c[j].w;
                     if constexpr (kInt4)
-                        unpack_int4(word, w.zero64(j, q / kQ), v[half]);
+                        unpack_int4(word, w.zero64(a, j, q / kQ), v[half]);
                     else
                         unpack_e2m1(word, e4m3_scale(w.s[j], q), v[half]);
                 }
                 const uint32_t a0[4] = {v[0][0], v[1][0], v[0][1], v[1][1]}, a1[4] = {v[0][2], v[1][2], v[0][3], v[1][3]};
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    mma(kInt4 ? part[m][rt] : acc[m][rt], a0, b.v[rt].x, b.v[rt].y);
-                    mma(kInt4 ? part[m][rt] : acc[m][rt], a1, b.v[rt].z, b.v[rt].w);
+                    mma(kInt4 ? part[m][rt] : acc[m][rt], a0, b[rt].x, b[rt].y);
+                    mma(kInt4 ? part[m][rt] : acc[m][rt], a1, b[rt].z, b[rt].w);
                 }
             }
             if (kInt4 && q % kQ == kQ - 1) {
@@ -374,18 +432,52 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<RT>()) linear_w4_kerne
             }
         }
     };
-    if (first < last) {
-        Held<kGroup> even, odd;  // the block worked on and the next one
-        even.load(a, row_blocks + first, lane);
-        for (int block = first; block < last; block += 2 * a.k_warps) {
-            const int second = block + a.k_warps, third = second + a.k_warps;
-            if (second < last) odd.load(a, row_blocks + second, lane);
-            work(even, block, second);
-            if (third < last) even.load(a, row_blocks + third, lane);
-            if (second < last) work(odd, second, third);
+    // x: this thread brings 16 bytes, piece tid % 16 of rows tid / 16 + 8 rt; what is not there is zero
+    const int xrow = tid >> 4, xpiece = tid & 15;
+    const uint32_t xdst = sbase + xrow * (kBlockK * 2) + ((xpiece ^ ((xrow & 1) << 2)) << 4);
+    const __nv_bfloat16* xsrc = xhead + (int64_t)(r0 + xrow) * a.x_row + xpiece * 8;
+    const auto load_x = [&](int stage) {
+        const int left = steps - stage * kStageSteps, pieces = (left < kStageSteps ? left : kStageSteps) * a.k_warps;
+        const uint32_t dst = xdst + (stage & 1) * (kStageSteps * a.k_warps) * (RT * kXPiece);
+        for (int i = 0; i < pieces; ++i) {
+            const int k = ((begin + stage * kStageSteps) * a.k_warps + i) * kBlockK;
+            const bool k_ok = k + xpiece * 8 < a.k;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const bool ok = k_ok && r0 + xrow + 8 * rt < a.rows;
+                cp_async16_or_zero(dst + (i * RT + rt) * kXPiece, ok ? xsrc + (int64_t)rt * 8 * a.x_row + k : a.x, ok);
+            }
+        }
+        cp_async_commit();
+    };
+    load_x(0);
+    int slot = 0, phase = 0, taken = 0;
+    bool ok = true;
+    for (int stage = 0; stage < stages; ++stage) {
+        cp_async_wait<0>();
+        __syncthreads();  // the stage's x has landed, and every warp has left the stage before
+        if (stage + 1 < stages) load_x(stage + 1);
+        if (tid == 0 && stage > 0 && ok)  // the slots of the stage before take other steps
+            for (int i = taken - kStageSteps + S::kSlots; i < taken + S::kSlots && i < steps; ++i) bring(i);
+        const uint8_t* xat = smem + ((stage & 1) * kStageSteps * a.k_warps + wk) * (RT * kXPiece);
+#pragma unroll
+        for (int sub = 0; sub < kStageSteps; ++sub) {
+            if (taken >= steps || !ok) break;
+            ok = wait_warp(bars + 8 * slot, phase, wait);
+            if (!ok) break;
+            Held<kGroup> w;
+            w.load(smem + ring_off + slot * (kWarps * S::kBlock) + warp * a.block_bytes, lane);
+            ++taken;
+            if (++slot == S::kSlots) slot = 0, phase ^= 1;
+            work(w, xat + sub * a.k_warps * (RT * kXPiece));
         }
     }
-
+    if (!ok && tid == 0)  // given up: what is in flight lands first
+        for (int i = taken; i < steps && i < taken + S::kSlots; ++i)
+            drain_phase(bars + 8 * (i % S::kSlots), i / S::kSlots, kTimeoutNs);
+    cp_async_wait<0>();
+    __syncthreads();  // every warp has left the rings: their memory takes the sums, [warp][row][kRedPitch]
+    float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -399,43 +491,72 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<RT>()) linear_w4_kerne
         cluster_sync();
     else
         __syncthreads();
+    // Four outputs a thread; the sums of the k warps and of the cluster's blocks are added in the order
+    // of k.
     const int rows = a.rows - r0 < RT * kRowTile ? a.rows - r0 : RT * kRowTile;
-    const int width = n_warps * kBlockN, n0 = tile * width;
-    const uint32_t rbase = smem_u32(red);
-    for (int e = rank * kThreads + tid; e < rows * width; e += a.splits * kThreads) {
-        const int r = e / width, c = e % width, n = n0 + c;
+    const int quads = n_warps * (kBlockN / 4);
+    const int n0 = tile * n_warps * kBlockN;
+    constexpr int kWarpSums = RT * kRowTile * kRedPitch;
+    for (int e = rank * kThreads + tid; e < rows * quads; e += a.splits * kThreads) {
+        const int r = e / quads, c = e % quads * 4, n = n0 + c;
         if (n >= a.n) continue;
         const int at = ((c / kBlockN) * a.k_warps * RT * kRowTile + r) * kRedPitch + c % kBlockN;
-        float sum = 0.f;
-        for (int p = 0; p < a.splits; ++p) {
-            const uint32_t peer = a.splits > 1 ? map_to_cta(rbase + at * 4, p) : 0u;
-            for (int i = 0; i < a.k_warps; ++i)
-                sum += a.splits > 1 ? ld_cluster_f32(peer + i * (RT * kRowTile * kRedPitch * 4))
-                                    : red[at + i * (RT * kRowTile * kRedPitch)];
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        const auto add = [&](const float4& v) { sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w; };
+        if (a.splits > 1) {
+            for (int i = 0; i < a.k_warps; ++i) {
+                float4 v[8];
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+                    if (p < a.splits) v[p] = ld_cluster_f32x4(map_to_cta(sbase + (at + i * kWarpSums) * 4, p));
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+                    if (p < a.splits) add(v[p]);
+            }
+        } else {
+            for (int i = 0; i < a.k_warps; ++i) add(*reinterpret_cast<const float4*>(red + at + i * kWarpSums));
         }
-        a.out[(int64_t)(r0 + r) * a.out_row + (int64_t)h * a.out_head + n] =
-            __float2bfloat16_rn(sum * (kInt4 ? 64.f : 256.f) * a.tensor_scale);
+        const float scale = kInt4 ? 64.f : 256.f;
+        const auto to_bf16 = [&](float f) { return __float2bfloat16_rn(f * scale * a.tensor_scale); };
+        alignas(8) const __nv_bfloat16 v[4] = {to_bf16(sum.x), to_bf16(sum.y), to_bf16(sum.z), to_bf16(sum.w)};
+        __nv_bfloat16* out = a.out + (int64_t)(r0 + r) * a.out_row + (int64_t)h * a.out_head + n;
+        if (a.out_quads && n + 4 <= a.n) {
+            *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(v);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (n + i < a.n) out[i] = v[i];
+        }
     }
     __syncwarp();
     if (a.splits > 1) cluster_sync();  // no block leaves while another reads its sums
 }
 
 template <int kGroup, int RT>
-mla_status launch(const Args& a, int heads, void* stream)
+mla_status launch(Args a, int heads, int64_t panels, void* stream)
 {
+    using S = Shared<kGroup, RT>;
     const auto kernel = linear_w4_kernel<kGroup, RT>;
-    constexpr int kBytes = kWarps * RT * kRowTile * kRedPitch * 4;
-    if (kBytes > 48 * 1024) {
-        const mla_status st = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes),
-                                          "cudaFuncSetAttribute(max dynamic shared memory)");
-        if (st != MLA_OK) return st;
+    const int64_t tiles = panels * heads * ((a.rows + RT * kRowTile - 1) / (RT * kRowTile));
+    // Thread blocks of a cluster over k: as many as still start at once (clusters leave some of the
+    // places on the SMs empty: nine tenths are counted on), with four steps or more for each.
+    a.splits = 1;
+    for (const int s : {8, 6, 4, 2}) {
+        if (a.steps < 4 * s || tiles * s * 10 > 9 * 152 * S::resident(a.k_warps, (a.steps + s - 1) / s)) continue;
+        a.splits = s;
+        break;
     }
-    const int n_warps = kWarps / a.k_warps;
+    const int steps = (a.steps + a.splits - 1) / a.splits, bytes = S::bytes(a.k_warps, steps);
+    a.ring_off = S::x_bytes(a.k_warps, steps);
+    a.bars_off = bytes - S::kBars;
+    const mla_status st = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
+                                      "cudaFuncSetAttribute(max dynamic shared memory)");
+    if (st != MLA_OK) return st;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((a.blocks_n + n_warps - 1) / n_warps * a.splits), (unsigned)heads,
+    cfg.gridDim = dim3((unsigned)(panels * a.splits), (unsigned)heads,
                        (unsigned)((a.rows + RT * kRowTile - 1) / (RT * kRowTile)));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kBytes;
+    cfg.dynamicSmemBytes = bytes;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -450,16 +571,16 @@ mla_status launch(const Args& a, int heads, void* stream)
 }
 
 template <int kGroup>
-mla_status launch_rows(const Args& a, int heads, void* stream)
+mla_status launch_rows(const Args& a, int heads, int64_t panels, void* stream)
 {
     switch ((a.rows + kRowTile - 1) / kRowTile) {
-        case 1: return launch<kGroup, 1>(a, heads, stream);
-        case 2: return launch<kGroup, 2>(a, heads, stream);
-        case 3: return launch<kGroup, 3>(a, heads, stream);
-        case 4: return launch<kGroup, 4>(a, heads, stream);
-        case 5: return launch<kGroup, 5>(a, heads, stream);
-        case 6: return launch<kGroup, 6>(a, heads, stream);
-        default: return launch<kGroup, 8>(a, heads, stream);
+        case 1: return launch<kGroup, 1>(a, heads, panels, stream);
+        case 2: return launch<kGroup, 2>(a, heads, panels, stream);
+        case 3: return launch<kGroup, 3>(a, heads, panels, stream);
+        case 4: return launch<kGroup, 4>(a, heads, panels, stream);
+        case 5: return launch<kGroup, 5>(a, heads, panels, stream);
+        case 6: return launch<kGroup, 6>(a, heads, panels, stream);
+        default: return launch<kGroup, 8>(a, heads, panels, stream);
     }
 }
 
@@ -480,7 +601,7 @@ mla_status check_shape(const mla_w4_weight* w)
         return MLA_ERR_INVALID_ARG;
     if (w->heads > 65535 || (int64_t)w->heads * w->n >= ((int64_t)1 << 31) || w->k > (1 << 30)) return MLA_ERR_UNSUPPORTED;
     const mla::w4::Layout l = mla::w4::layout_of(*w);
-    if (l.blocks_n * l.blocks_k >= ((int64_t)1 << 31)) return MLA_ERR_UNSUPPORTED;
+    if (l.panels * l.steps * mla::w4::kWarps >= ((int64_t)1 << 31)) return MLA_ERR_UNSUPPORTED;
     return MLA_OK;
 }
 
@@ -503,14 +624,13 @@ mla_status linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t 
         return MLA_ERR_ALIGNMENT;
     if (rows > 65535 * kMaxRowTiles * kRowTile) return MLA_ERR_UNSUPPORTED;
     const Layout l = layout_of(*w);
-    const uint8_t* packed = static_cast<const uint8_t*>(w->packed);
     Args a = {};
     a.x = static_cast<const __nv_bfloat16*>(x);
     a.x_row = x_row_stride;
     a.x_head = x_head_stride;
-    a.codes = packed;
-    a.scale = packed + l.scale_off;
-    a.zero = w->has_zero ? packed + l.zero_off : nullptr;
+    a.packed = static_cast<const uint8_t*>(w->packed);
+    a.block_bytes = l.block_bytes;
+    a.zero_mask = w->has_zero ? 0xFFFFFFFFu : 0u;
     a.out = static_cast<__nv_bfloat16*>(out);
     a.out_row = out_row_stride;
     a.out_head = out_head_stride;
@@ -518,23 +638,15 @@ mla_status linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t 
     a.rows = rows;
     a.n = w->n;
     a.k = w->k;
-    a.blocks_n = (int)l.blocks_n;
-    a.blocks_k = (int)l.blocks_k;
+    a.steps = (int)l.steps;
+    a.k_warps = l.k_warps;
     a.early = early;
-    // As many of a block's warps over k as have two blocks each; the others over n.
-    a.k_warps = 1;
-    while (a.k_warps < kWarps && a.blocks_k >= 2 * a.k_warps) a.k_warps *= 2;
-    // Blocks of a cluster over k: doubled while there are too few for three per SM and every warp
-    // keeps two of the packed blocks.
-    const int64_t row_blocks = (rows + kMaxRowTiles * kRowTile - 1) / (kMaxRowTiles * kRowTile);
-    const int64_t tiles = l.blocks_n * a.k_warps / kWarps * w->heads * row_blocks;
-    a.splits = 1;
-    while (a.splits < 8 && tiles * a.splits < 3 * 152 && a.blocks_k >= 4 * a.k_warps * a.splits) a.splits *= 2;
+    a.out_quads = is_aligned(out, 8) && (rows == 1 || out_row_stride % 4 == 0) && (w->heads == 1 || out_head_stride % 4 == 0);
     switch (w->group) {
-        case 16: return launch_rows<16>(a, w->heads, stream);
-        case 32: return launch_rows<32>(a, w->heads, stream);
-        case 64: return launch_rows<64>(a, w->heads, stream);
-        default: return launch_rows<128>(a, w->heads, stream);
+        case 16: return launch_rows<16>(a, w->heads, l.panels, stream);
+        case 32: return launch_rows<32>(a, w->heads, l.panels, stream);
+        case 64: return launch_rows<64>(a, w->heads, l.panels, stream);
+        default: return launch_rows<128>(a, w->heads, l.panels, stream);
     }
 }
 
@@ -590,14 +702,14 @@ extern "C" MLA_API mla_status mla_w4_pack(const mla_w4_weight* w, const void* co
     a.scale = scale;
     a.zero = static_cast<const uint8_t*>(zero);
     a.packed = static_cast<uint8_t*>(packed);
-    a.scale_off = l.scale_off;
-    a.zero_off = l.zero_off;
     a.n = w->n;
     a.k = w->k;
     a.group = w->group;
-    a.blocks_n = (int)l.blocks_n;
-    a.blocks_k = (int)l.blocks_k;
-    const dim3 grid((unsigned)((l.blocks_n * l.blocks_k + 7) / 8), (unsigned)w->heads);
+    a.panels = (int)l.panels;
+    a.steps = (int)l.steps;
+    a.k_warps = l.k_warps;
+    a.block_bytes = l.block_bytes;
+    const dim3 grid((unsigned)((l.panels * l.steps * mla::w4::kWarps + 7) / 8), (unsigned)w->heads);
     mla::w4::pack_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(a);
     return mla::cuda_status(cudaGetLastError(), "4-bit pack kernel launch");
 }

@@ -198,12 +198,14 @@ def test_w4_pack_refuses(L, kw, status):
 
 
 def test_w4_packed_bytes(L):
-    """Blocks of 32 n x 128 k: 2,048 bytes of codes, and 32 scales and zeros per group of k."""
+    """Steps of four blocks of 32 n x 128 k: 2,048 bytes of codes, and 32 scales and zeros per group of
+    k; the four side by side over n (128 outputs) or, for few outputs, over k."""
     size = lambda **kw: L.mla_w4_packed_bytes(ctypes.byref(_weight(**kw)))  # noqa: E731
     assert size(n=512, k=128, group=128) == 16 * (2048 + 64)
-    assert size(n=33, k=160, group=32, has_zero=1, heads=3) == 3 * 2 * 2 * (2048 + 256 + 128)
-    assert size(n=1, k=64, group=64, has_zero=1) == 2048 + 128 + 64
-    assert size(n=32, k=128, group=16, format=1) == 2048 + 256
+    assert size(n=33, k=160, group=32, has_zero=1, heads=3) == 3 * 2 * 4 * (2048 + 256 + 128)
+    assert size(n=1, k=64, group=64, has_zero=1) == 4 * (2048 + 128 + 64)
+    assert size(n=32, k=128, group=16, format=1) == 4 * (2048 + 256)
+    assert size(n=64, k=16384, group=128) == 2 * 128 * (2048 + 64)
     assert all(size(**kw) == 0 for kw, _ in SHAPES)
     assert L.mla_w4_packed_bytes(None) == 0
 
