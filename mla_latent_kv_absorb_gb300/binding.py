@@ -529,14 +529,14 @@ def mla_rope_append_kv(rope: Rope, c_kv: torch.Tensor, k_r: torch.Tensor, positi
     c_ptr = _rows(c_kv, "c_kv", bf16, (n, D_C), device)
     k_ptr = _rows(k_r, "k_r", bf16, (n, D_R), device)
     err_ptr = _whole(dev_error, "dev_error", i32, (1,), device)
-    dtype = _kv_dtype(kv_pool, kv_scale, kr_pool)
-    pages = kv_pool.shape[0]
-    scale_ptr = kr_ptr = q_ptr = qc_ptr = qr_ptr = None
-    if dtype != MLA_KV_BF16:
+    pages, scale_ptr, kr_ptr, q_ptr, qc_ptr, qr_ptr = kv_pool.shape[0], None, None, None, None, None
+    if kv_scale is None:
+        dtype, pool_ptr = MLA_KV_BF16, _whole(kv_pool, "kv_pool", bf16, (pages, PAGE, D_ROW), device)
+    else:
+        dtype, width = (MLA_KV_NVFP4, NVFP4_ROW) if kv_pool.shape[-1] == NVFP4_ROW else (MLA_KV_FP8_E4M3, D_C)
+        pool_ptr = _whole(kv_pool, "kv_pool (e4m3 codes or NVFP4 rows)", torch.uint8, (pages, PAGE, width), device)
         scale_ptr = _whole(kv_scale, "kv_scale", torch.float32, (pages, PAGE), device)
         kr_ptr = _whole(kr_pool, "kr_pool", bf16, (pages, PAGE, D_R), device)
-    if kv_pool.get_device() != device:
-        _refuse(kv_pool, "kv_pool", kv_pool.dtype, tuple(kv_pool.shape), device)
     qt = qh = 0
     if q is not None:
         q_ptr, (qt, qh, _) = _rows(q, "q", bf16, (n, NUM_HEADS, D_HC + D_R), device), q.stride()
@@ -545,7 +545,7 @@ def mla_rope_append_kv(rope: Rope, c_kv: torch.Tensor, k_r: torch.Tensor, positi
     elif q_c is not None or q_r is not None:
         raise ValueError("q_c and q_r need q")
     st = lib().mla_rope_append_kv(rope._ref, n, c_ptr, c_kv.stride(0), k_ptr, k_r.stride(0), pos_ptr, slots_ptr, dtype,
-                                  pages, kv_pool.data_ptr(), scale_ptr, kr_ptr, q_ptr, qt, qh, qc_ptr, qr_ptr, err_ptr,
+                                  pages, pool_ptr, scale_ptr, kr_ptr, q_ptr, qt, qh, qc_ptr, qr_ptr, err_ptr,
                                   _stream(stream))
     if st:
         _check("mla_rope_append_kv", st)

@@ -102,7 +102,8 @@ bool config_ok(const mla_rope_config* r)
            r->magnitude > 0.f;
 }
 
-// Four heads a thread share one set of sines when there are blocks enough for every SM that way.
+// Four heads a thread share one set of sines when that leaves four blocks for every SM; with fewer
+// rows than that the launch bounds the call and one head a thread spreads them widest.
 bool four_heads(int64_t tokens, int32_t heads, int32_t units)
 {
     return heads % 4 == 0 && tokens * heads / 4 * units >= (int64_t)152 * 4 * mla::rope::kThreads;

@@ -2,13 +2,18 @@
 //
 // Angle: turns per position are a 64-bit fraction, so position * step modulo 2^64 is the fraction
 // of a turn exactly, at any position (a product in fp32 would lose it: one ulp of 10^6 radians is
-// 0.06).  Its top 32 bits, as a signed number of half turns in [-1, 1), are within 2^-33 turn of
-// it and go to sincospi in fp32 (another 2^-25 of a half turn).
+// 0.06).  Its top 32 bits are within 2^-33 turn of it.  The nearest quarter turn is taken off in
+// integers, and sine and cosine of what is left, |x| <= pi / 4, are their Taylor series to x^9 and
+// x^10 (the next terms are below 2e-9), so that no range reduction in floats and no special case is
+// left (128 heads of 192, 4,096 tokens: 71 us with sincospi of the half turns, 67 us so).
 //
 // Rows: one unit of a head's row is 16 bytes (or one element or pair, where pointers, strides or
 // sizes do not allow that).  Units of the rotated part come first: an interleaved unit holds whole
 // pairs, a half-layout unit is the two 16-byte pieces i and i + dim / 2; the other units copy.
-// A thread takes the same unit of R heads of one token, so that its sines and cosines serve R rows.
+// A thread takes the same unit of R heads of one token, so that its sines and cosines and its index
+// arithmetic serve R rows (the same 4,096 tokens: 101 us with R = 1, 71 with 2, 60 with 4, 62 with 8
+// and 16), and the copying threads are kept apart from the rotating ones (67 -> 59.7 us: 402 MB at
+// 99.6 % of the measured copy rate).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -25,11 +30,22 @@ constexpr int kThreads = 256;
 // cos and sin (times m) of position * step turns.
 __device__ __forceinline__ void turn(int32_t position, uint64_t step, float m, float& c, float& s)
 {
-    const uint64_t phase = (uint64_t)(int64_t)position * step + 0x80000000ull;  // rounded to 2^-32 turn
-    const float half_turns = __int2float_rn((int32_t)(phase >> 32)) * 0x1p-31f;
-    sincospif(half_turns, &s, &c);
-    c *= m;
-    s *= m;
+    const uint32_t turns = (uint32_t)(((uint64_t)(int64_t)position * step + 0x80000000ull) >> 32);  // 2^-32 turn
+    const uint32_t quarter = (turns + 0x20000000u) >> 30;
+    const float x = __int2float_rn((int32_t)(turns - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi 2^-32
+    const float x2 = x * x;
+    float sn = fmaf(x2, 2.7557319e-6f, -1.9841270e-4f);  // 1 / 9!, -1 / 7!
+    sn = fmaf(sn, x2, 8.3333333e-3f);
+    sn = fmaf(sn, x2, -1.6666667e-1f);
+    sn = fmaf(sn * x2, x, x);
+    float cs = fmaf(x2, -2.7557319e-7f, 2.4801587e-5f);  // -1 / 10!, 1 / 8!
+    cs = fmaf(cs, x2, -1.3888889e-3f);
+    cs = fmaf(cs, x2, 4.1666667e-2f);
+    cs = fmaf(cs, x2, -0.5f);
+    cs = fmaf(cs, x2, 1.0f);
+    const float a = quarter & 1 ? sn : cs, b = quarter & 1 ? cs : sn;
+    c = (quarter + 1) & 2 ? -a * m : a * m;
+    s = quarter & 2 ? -b * m : b * m;
 }
 
 __device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -137,15 +153,25 @@ __device__ __forceinline__ void rotate_group(const Rows& a, const mla_rope_confi
     }
 }
 
-// The groups of block `block`: its threads are a.lanes groups of min(units, kThreads) threads.
+// The groups of block `block`.  The threads of the rotated units come first and the copying ones
+// behind them, so that few warps have both kinds.
 template <typename T, int V, bool kHalf, int R>
 __device__ __forceinline__ void rotate_block(const Rows& a, const mla_rope_config& cfg, int block)
 {
-    const int width = a.units < kThreads ? a.units : kThreads;
-    const int lane = threadIdx.x / width;
+    const int tid = threadIdx.x;
+    int lane = 0, unit = tid, stride = kThreads;
+    if (a.units <= kThreads) {
+        const int copying = a.units - a.rot_units, rotating = a.rot_units * a.lanes, i = tid - rotating;
+        stride = a.units;
+        if (i < 0)
+            lane = tid / a.rot_units, unit = tid - lane * a.rot_units;
+        else if (copying > 0)
+            lane = i / copying, unit = a.rot_units + i - lane * copying;
+        else
+            lane = a.lanes;  // no part
+    }
     const int64_t group = (int64_t)block * a.lanes + lane;
-    if (lane < a.lanes && group < a.groups)
-        rotate_group<T, V, kHalf, R>(a, cfg, (int)group, threadIdx.x - lane * width, width);
+    if (lane < a.lanes && group < a.groups) rotate_group<T, V, kHalf, R>(a, cfg, (int)group, unit, stride);
 }
 
 template <typename T, int V, bool kHalf, int R>
