@@ -487,28 +487,48 @@ def mla_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, out: Optional
     head_dim] (bf16, fp16 or fp32; any strides, the last 1) by positions (int32 [tokens]) into
     out, which it returns: x itself (None: in place), a tensor like x (the other elements copied),
     or, with ``rest`` [tokens, heads, head_dim - dim], one of [tokens, heads, dim]."""
+    device = torch._C._cuda_getDevice()
+    if out is None and rest is None:
+        out = x
+    try:  # the checks in one expression; what it refuses is told by _check_rope
+        dtype, dim, (T, H, D), (xt, xh, xd), (ot, oh, od) = x.dtype, rope.dim, x.shape, x.stride(), out.stride()
+        code = _DTYPES.get(dtype)
+        rest_ptr, rt, rh = None, 0, 0
+        fine = code is not None and xd == 1 and od == 1 and out.dtype is dtype and x.get_device() == device and \
+            out.get_device() == device and positions.dtype is torch.int32 and positions.shape == (T,) and \
+            positions.get_device() == device and positions.is_contiguous()
+        if rest is None:
+            fine = fine and out.shape == x.shape
+        else:
+            rt, rh, rd = rest.stride()
+            rest_ptr = rest.data_ptr()
+            fine = fine and (rd == 1 or D - dim == 1) and rest.dtype is dtype and rest.get_device() == device and \
+                out.shape == (T, H, dim) and rest.shape == (T, H, D - dim)
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _check_rope(rope, x, positions, out, rest, device)
+    st = lib().mla_rope(rope._ref, code, T, H, D, rot_offset, x.data_ptr(), xt, xh, out.data_ptr(), ot, oh, rest_ptr, rt,
+                        rh, positions.data_ptr(), _stream(stream))
+    if st:
+        _check("mla_rope", st)
+    return out
+
+
+def _check_rope(rope, x, positions, out, rest, device: int) -> None:
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("x must be [tokens, heads, head_dim]")
     if x.dtype not in _DTYPES:
         raise TypeError(f"x: expected bfloat16, float16 or float32, got {x.dtype}")
     T, H, D = x.shape
-    device, dtype, dim = torch._C._cuda_getDevice(), x.dtype, rope.dim
-    x_ptr, (xt, xh, _) = _rows(x, "x", dtype, (T, H, D), device), x.stride()
-    if rest is None:
-        if out is None:
-            out, out_ptr, ot, oh = x, x_ptr, xt, xh
-        else:
-            out_ptr, (ot, oh, _) = _rows(out, "out", dtype, (T, H, D), device), out.stride()
-        rest_ptr, rt, rh = None, 0, 0
-    else:
-        out_ptr, (ot, oh, _) = _rows(out, "out", dtype, (T, H, dim), device), out.stride()
-        rest_ptr, (rt, rh, _) = _rows(rest, "rest", dtype, (T, H, D - dim), device), rest.stride()
-    p_ptr = _whole(positions, "positions", torch.int32, (T,), device)
-    st = lib().mla_rope(rope._ref, _DTYPES[dtype], T, H, D, rot_offset, x_ptr, xt, xh, out_ptr, ot, oh, rest_ptr, rt,
-                        rh, p_ptr, _stream(stream))
-    if st:
-        _check("mla_rope", st)
-    return out
+    if out is None:
+        raise ValueError("rest needs out")
+    _rows(x, "x", x.dtype, (T, H, D), device)
+    _rows(out, "out", x.dtype, (T, H, D if rest is None else rope.dim), device)
+    if rest is not None:
+        _rows(rest, "rest", x.dtype, (T, H, D - rope.dim), device)
+    _whole(positions, "positions", torch.int32, (T,), device)
+    raise ValueError("mla_rope: arguments that do not fit together")
 
 
 def mla_rope_append_kv(rope: Rope, c_kv: torch.Tensor, k_r: torch.Tensor, positions: torch.Tensor,
@@ -520,35 +540,70 @@ def mla_rope_append_kv(rope: Rope, c_kv: torch.Tensor, k_r: torch.Tensor, positi
     [n, 64] may be columns of a wider row.  With q [n, 128, 192] (content, then un-rotated part;
     any strides, the last 1), q_c [n, 128, 128] and q_r [n, 128, 64] receive the split and rotated
     queries in the same launch."""
+    bf16, i32, device = torch.bfloat16, torch.int32, torch._C._cuda_getDevice()
+    scale_ptr = kr_ptr = q_ptr = qc_ptr = qr_ptr = None
+    qt = qh = 0
+    try:  # the checks in one expression; what it refuses is told by _check_rope_append
+        n, (pages, _, width) = slots.numel(), kv_pool.shape
+        (cs, c1), (ks, k1) = c_kv.stride(), k_r.stride()
+        fine = slots.dtype is i32 and slots.shape == (n,) and slots.is_contiguous() and slots.get_device() == device and \
+            positions.dtype is i32 and positions.shape == (n,) and positions.is_contiguous() and \
+            positions.get_device() == device and c_kv.dtype is bf16 and c_kv.shape == (n, D_C) and c1 == 1 and \
+            c_kv.get_device() == device and k_r.dtype is bf16 and k_r.shape == (n, D_R) and k1 == 1 and \
+            k_r.get_device() == device and dev_error.dtype is i32 and dev_error.shape == (1,) and \
+            dev_error.get_device() == device and kv_pool.is_contiguous() and kv_pool.get_device() == device and \
+            kv_pool.shape[1] == PAGE
+        if kv_scale is None:
+            dtype = MLA_KV_BF16
+            fine = fine and kv_pool.dtype is bf16 and width == D_ROW
+        else:
+            dtype = MLA_KV_NVFP4 if width == NVFP4_ROW else MLA_KV_FP8_E4M3
+            fine = fine and kv_pool.dtype is torch.uint8 and (width == D_C or width == NVFP4_ROW) and \
+                kv_scale.dtype is torch.float32 and kv_scale.shape == (pages, PAGE) and kv_scale.is_contiguous() and \
+                kv_scale.get_device() == device and kr_pool.dtype is bf16 and kr_pool.shape == (pages, PAGE, D_R) and \
+                kr_pool.is_contiguous() and kr_pool.get_device() == device
+            scale_ptr, kr_ptr = kv_scale.data_ptr(), kr_pool.data_ptr()
+        if q is not None:
+            qt, qh, q1 = q.stride()
+            fine = fine and q.dtype is bf16 and q.shape == (n, NUM_HEADS, D_HC + D_R) and q1 == 1 and \
+                q.get_device() == device and q_c.dtype is bf16 and q_c.shape == (n, NUM_HEADS, D_HC) and \
+                q_c.is_contiguous() and q_c.get_device() == device and q_r.dtype is bf16 and \
+                q_r.shape == (n, NUM_HEADS, D_R) and q_r.is_contiguous() and q_r.get_device() == device
+            q_ptr, qc_ptr, qr_ptr = q.data_ptr(), q_c.data_ptr(), q_r.data_ptr()
+        else:
+            fine = fine and q_c is None and q_r is None
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _check_rope_append(c_kv, k_r, positions, slots, kv_pool, dev_error, kv_scale, kr_pool, q, q_c, q_r, device)
+    st = lib().mla_rope_append_kv(rope._ref, n, c_kv.data_ptr(), cs, k_r.data_ptr(), ks, positions.data_ptr(),
+                                  slots.data_ptr(), dtype, pages, kv_pool.data_ptr(), scale_ptr, kr_ptr, q_ptr, qt, qh,
+                                  qc_ptr, qr_ptr, dev_error.data_ptr(), _stream(stream))
+    if st:
+        _check("mla_rope_append_kv", st)
+
+
+def _check_rope_append(c_kv, k_r, positions, slots, kv_pool, dev_error, kv_scale, kr_pool, q, q_c, q_r,
+                       device: int) -> None:
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be a 1-d tensor")
     n, bf16, i32 = slots.shape[0], torch.bfloat16, torch.int32
-    device = torch._C._cuda_getDevice()
-    slots_ptr = _whole(slots, "slots", i32, (n,), device)
-    pos_ptr = _whole(positions, "positions", i32, (n,), device)
-    c_ptr = _rows(c_kv, "c_kv", bf16, (n, D_C), device)
-    k_ptr = _rows(k_r, "k_r", bf16, (n, D_R), device)
-    err_ptr = _whole(dev_error, "dev_error", i32, (1,), device)
-    pages, scale_ptr, kr_ptr, q_ptr, qc_ptr, qr_ptr = kv_pool.shape[0], None, None, None, None, None
-    if kv_scale is None:
-        dtype, pool_ptr = MLA_KV_BF16, _whole(kv_pool, "kv_pool", bf16, (pages, PAGE, D_ROW), device)
-    else:
-        dtype, width = (MLA_KV_NVFP4, NVFP4_ROW) if kv_pool.shape[-1] == NVFP4_ROW else (MLA_KV_FP8_E4M3, D_C)
-        pool_ptr = _whole(kv_pool, "kv_pool (e4m3 codes or NVFP4 rows)", torch.uint8, (pages, PAGE, width), device)
-        scale_ptr = _whole(kv_scale, "kv_scale", torch.float32, (pages, PAGE), device)
-        kr_ptr = _whole(kr_pool, "kr_pool", bf16, (pages, PAGE, D_R), device)
-    qt = qh = 0
+    _whole(slots, "slots", i32, (n,), device)
+    _whole(positions, "positions", i32, (n,), device)
+    _rows(c_kv, "c_kv", bf16, (n, D_C), device)
+    _rows(k_r, "k_r", bf16, (n, D_R), device)
+    _whole(dev_error, "dev_error", i32, (1,), device)
+    _kv_dtype(kv_pool, kv_scale, kr_pool)
+    for name, t in (("kv_pool", kv_pool), ("kv_scale", kv_scale), ("kr_pool", kr_pool)):
+        if t is not None:
+            _whole(t, name, t.dtype, tuple(t.shape), device)
     if q is not None:
-        q_ptr, (qt, qh, _) = _rows(q, "q", bf16, (n, NUM_HEADS, D_HC + D_R), device), q.stride()
-        qc_ptr = _whole(q_c, "q_c", bf16, (n, NUM_HEADS, D_HC), device)
-        qr_ptr = _whole(q_r, "q_r", bf16, (n, NUM_HEADS, D_R), device)
+        _rows(q, "q", bf16, (n, NUM_HEADS, D_HC + D_R), device)
+        _whole(q_c, "q_c", bf16, (n, NUM_HEADS, D_HC), device)
+        _whole(q_r, "q_r", bf16, (n, NUM_HEADS, D_R), device)
     elif q_c is not None or q_r is not None:
         raise ValueError("q_c and q_r need q")
-    st = lib().mla_rope_append_kv(rope._ref, n, c_ptr, c_kv.stride(0), k_ptr, k_r.stride(0), pos_ptr, slots_ptr, dtype,
-                                  pages, pool_ptr, scale_ptr, kr_ptr, q_ptr, qt, qh, qc_ptr, qr_ptr, err_ptr,
-                                  _stream(stream))
-    if st:
-        _check("mla_rope_append_kv", st)
+    raise ValueError("mla_rope_append_kv: arguments that do not fit together")
 
 
 # --------------------------------------------------------------------------- 4-bit weights
@@ -610,12 +665,13 @@ def mla_linear_w4(x: torch.Tensor, w: W4Weight, out: torch.Tensor, stream=None) 
     expanded over the heads."""
     if not isinstance(x, torch.Tensor) or not isinstance(out, torch.Tensor):
         raise TypeError("x and out: expected tensors")
-    if w.heads == 1:
+    heads, device = w.heads, torch._C._cuda_getDevice()
+    if heads == 1:
         x = x.unsqueeze(1) if x.dim() == 2 else x
         out = out.unsqueeze(1) if out.dim() == 2 else out
-    rows, heads, device = x.shape[0], w.heads, torch._C._cuda_getDevice()
-    x_ptr = _rows(x, "x", torch.bfloat16, (rows, heads, w.k), device)
-    out_ptr = _rows(out, "out", torch.bfloat16, (rows, heads, w.n), device)
+    rows, bf16 = x.shape[0], torch.bfloat16
+    x_ptr = _rows(x, "x", bf16, (rows, heads, w.k), device)
+    out_ptr = _rows(out, "out", bf16, (rows, heads, w.n), device)
     if w.device_index != device:
         raise ValueError(f"w: must be on the current CUDA device ({device})")
     (xr, xh, _), (o_r, oh, _) = x.stride(), out.stride()
