@@ -193,6 +193,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm(
@@ -365,21 +370,18 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<RT>()) linear_w4_kerne
         mbar_arrive_expect_tx(bars + 8 * slot, step_bytes);
         bulk_load(sbase + ring_off + slot * (kWarps * S::kBlock), source + (int64_t)i * step_bytes, step_bytes, bars + 8 * slot);
     };
-    const auto fill = [&]() {
-        if (tid == 0)
-            for (int i = 0; i < S::kSlots && i < steps; ++i) bring(i);
-    };
     if (tid == 0) {
         *abort = 0;
         for (int i = 0; i < S::kSlots; ++i) mbar_init(bars + 8 * i, 1);
         fence_barrier_init();
+        // Bringing weights to L2 is no read of them: it may come before the kernel ahead has ended,
+        // even one that writes them.
+        prefetch_l2(source, (steps < S::kSlots ? steps : S::kSlots) * step_bytes);
     }
-    if (a.early) fill();  // the step's weights do not depend on the kernel before this one
     griddep_wait();
-    if (a.early)
-        griddep_launch_dependents();
-    else
-        fill();
+    if (a.early) griddep_launch_dependents();
+    if (tid == 0)
+        for (int i = 0; i < S::kSlots && i < steps; ++i) bring(i);
 
     const __nv_bfloat16* xhead = a.x + (int64_t)h * a.x_head;
     float acc[2][RT][4] = {};
