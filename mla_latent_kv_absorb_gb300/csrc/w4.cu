@@ -305,10 +305,13 @@ struct Held {
     }
 };
 
-template <int RT>
+// Thread blocks per SM, which sets the registers of a thread: 128, 168 or 255.  Three at four and five
+// row tiles only where the sums of a group fit without spilling (33 rows, groups of 64: 46 us with
+// three and spills, 42 with two; groups of 128: 40 with three, 41 with two).
+template <int kGroup, int RT>
 __host__ __device__ constexpr int blocks_per_sm()
 {
-    return RT <= 2 ? 4 : RT <= 5 ? 3 : 2;
+    return RT <= 2 ? 4 : RT == 3 || (RT == 4 && kGroup != 32) || (RT == 5 && (kGroup == 128 || kGroup == 16)) ? 3 : 2;
 }
 
 // Shared memory: x's two stages of kStageSteps steps of k_warps pieces of 128 k; a ring of steps'
@@ -320,6 +323,7 @@ constexpr int kXPiece = kRowTile * kBlockK * 2;  // bytes of 128 k of one row ti
 template <int kGroup, int RT>
 struct Shared {
     static constexpr int kBlock = kCodeBytes + scale_bytes(kGroup) + zero_bytes(kGroup);
+    // as many as leave room for those thread blocks
     static constexpr int kSlots = (RT == 1 && kGroup != 32) || RT == 3 ? 5 : 4;
     static constexpr int kBars = (kSlots + 1) * 8;
     // of a thread block that takes `steps` steps
@@ -337,13 +341,13 @@ struct Shared {
     static __host__ constexpr int resident(int k_warps, int steps)
     {
         const int fit = 228 * 1024 / (bytes(k_warps, steps) + 1024);
-        return fit < blocks_per_sm<RT>() ? fit : blocks_per_sm<RT>();
+        return fit < blocks_per_sm<kGroup, RT>() ? fit : blocks_per_sm<kGroup, RT>();
     }
 };
 
 // kGroup 32, 64, 128: int4; 16: NVFP4.
 template <int kGroup, int RT>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm<RT>()) linear_w4_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<kGroup, RT>()) linear_w4_kernel(const __grid_constant__ Args a)
 {
     using namespace dev;
     constexpr bool kInt4 = kGroup >= 32;

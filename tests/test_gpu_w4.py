@@ -88,6 +88,55 @@ def test_linear_sizes(fmt, group, zero, heads, n, k):
         _assert_product(out, x, value)
 
 
+@pytest.mark.parametrize("fmt,group,zero", FORMATS)
+@pytest.mark.parametrize("heads,n,k,rows", [
+    (1, 20000, 512, 17),
+    (1, 8200, 1312, 33),      # k ends inside a step, two thread blocks of a cluster
+    (1, 8192, 2560, 64),      # clusters of four
+    (5, 1400, 2048, 65),      # heads, a second block of rows with one row
+    (1, 20100, 640, 130),
+])
+def test_linear_many_rows(fmt, group, zero, heads, n, k, rows):
+    """More rows and outputs than the cases above: all warps of a thread block over the outputs."""
+    k -= k % max(group, 32)
+    w, value = _weight(heads, n, k, fmt, group, zero, n + rows)
+    x = torch.randn(rows, heads, k, generator=torch.Generator().manual_seed(rows)).bfloat16().to(DEV)
+    out = torch.full((rows, heads, n), float("nan"), dtype=torch.bfloat16, device=DEV)
+    binding.mla_linear_w4(x, w, out)
+    _assert_product(out, x, value)
+
+
+def test_linear_many_rows_strides():
+    """Rows of a wider tensor, one row for all heads, odd strides of the outputs, not-finite rows."""
+    w, value = _weight(6, 1400, 2048, "int4", 64, True, 5)
+    g = torch.Generator().manual_seed(6)
+    wide = torch.randn(40, 6 * 2048 + 8, generator=g).bfloat16().to(DEV)
+    x = wide[:, 8:].unflatten(1, (6, 2048))
+    want = torch.empty(40, 6, 1400, dtype=torch.bfloat16, device=DEV)
+    binding.mla_linear_w4(x.contiguous(), w, want)
+    _assert_product(want, x, value)
+    buf = torch.full((40 * 6 * 1401 + 1,), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[1:].view(40, 6, 1401)[:, :, :1400]
+    binding.mla_linear_w4(x, w, out)
+    assert torch.equal(out, want) and (buf[1:].view(40, 6, 1401)[:, :, 1400] == 7.0).all() and buf[0] == 7.0
+    swapped = torch.empty(6, 40, 1400, dtype=torch.bfloat16, device=DEV)
+    binding.mla_linear_w4(x.transpose(0, 1).contiguous().transpose(0, 1), w, swapped.transpose(0, 1))
+    assert torch.equal(swapped.transpose(0, 1), want)
+    out = torch.empty_like(want)
+    shared = x[:, :1].expand(40, 6, 2048)
+    binding.mla_linear_w4(shared, w, out)
+    _assert_product(out, shared, value)
+    binding.mla_linear_w4(x[:1].expand(40, 6, 2048), w, out)     # one row for all: every row the same bits
+    assert torch.equal(out, out[:1].expand(40, 6, 1400))
+    _assert_product(out, x[:1].expand(40, 6, 2048), value)
+    y = x.clone()
+    y[3, 2, 100], y[39, 5, 2047] = float("nan"), float("inf")
+    binding.mla_linear_w4(y, w, out)
+    keep = torch.ones(40, 6, dtype=torch.bool, device=DEV)
+    keep[3, 2], keep[39, 5] = False, False
+    assert torch.equal(out[keep], want[keep]) and out[3, 2].isnan().all() and not out[39, 5].isfinite().all()
+
+
 @pytest.mark.parametrize("k", [32, 64, 96, 160, 2016])
 def test_linear_groups_of_32_at_any_multiple(k):
     w, value = _weight(1, 40, k, "int4", 32, True, k)
