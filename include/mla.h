@@ -420,10 +420,12 @@ MLA_API mla_status mla_rope(const mla_rope_config* rope, mla_dtype dtype, int32_
  *              either's).
  *   q          device bf16 [num_tokens][128][192], 128 content then 64 un-rotated values per
  *              head, strides q_token_stride and q_head_stride; q_c [num_tokens][128][128] receives
- *              the content, q_r [num_tokens][128][64] the rotated part, both contiguous.  Tokens
- *              whose slot is negative or past the pool have their queries written all the same.
- * All bf16 pointers 16-byte aligned, all strides multiples of 8 elements in [0, 2^40]; num_tokens
- * at most 2^23 (else MLA_ERR_UNSUPPORTED).  num_tokens 0 enqueues nothing. */
+ *              the content, q_r [num_tokens][128][64] the rotated part, both contiguous; the three
+ *              share no element.  Tokens whose slot is negative or past the pool have their queries
+ *              written all the same.
+ * All bf16 pointers 16-byte aligned, all strides in [0, 2^40] and multiples of 8 elements (those
+ * from token to token only with more than one token); num_tokens at most 2^23 (else
+ * MLA_ERR_UNSUPPORTED).  num_tokens 0 enqueues nothing. */
 MLA_API mla_status mla_rope_append_kv(const mla_rope_config* rope, int32_t num_tokens, const void* c_kv,
                                       int64_t c_kv_stride, const void* k_r, int64_t k_r_stride,
                                       const int32_t* positions, const int32_t* slots, mla_kv_dtype kv_dtype,
@@ -468,7 +470,8 @@ MLA_API mla_status mla_w4_pack(const mla_w4_weight* w, const void* codes, const 
  *   out  device bf16, element strides out_row_stride and out_head_stride, distinct elements, sharing
  *        none with x; 2-byte aligned
  * Strides lie in [0, 2^40].  Products are exact and summed in fp32; out is rounded once.  rows 0
- * enqueues nothing. */
+ * enqueues nothing.  Weights that do not arrive within 2 s (the kernel's waits are bounded) make the
+ * outputs that need them NaN. */
 MLA_API mla_status mla_linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t x_head_stride,
                                  const mla_w4_weight* w, void* out, int64_t out_row_stride, int64_t out_head_stride,
                                  void* stream);

@@ -618,7 +618,7 @@ class W4Weight:
     For the decode step: W_UK as [128, 512, 128] (c, then d) and W_UV as [128, 128, 512]."""
 
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor, *, zero: Optional[torch.Tensor] = None,
-                 group: Optional[int] = None, tensor_scale: float = 1.0, stream=None):
+                 group: Optional[int] = None, tensor_scale: float = 1.0):
         for name, t in (("codes", codes), ("scale", scale)) + ((("zero", zero),) if zero is not None else ()):
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{name}: expected a tensor")
@@ -655,7 +655,7 @@ class W4Weight:
             raise MlaError("mla_w4_packed_bytes", MLA_ERR_UNSUPPORTED, "sizes past the limits")
         self.packed = torch.empty(size, dtype=torch.uint8, device=codes.device)
         _check("mla_w4_pack", lib().mla_w4_pack(self._ref, codes_ptr, scale_ptr, zero_ptr, self.packed.data_ptr(),
-                                                _stream(stream)))
+                                                _stream(None)))
         self.struct.packed = self.packed.data_ptr()
 
 

@@ -273,12 +273,12 @@ extern "C" MLA_API mla_status mla_rope_append_kv(const mla_rope_config* rope, in
     if (!c_kv || !k_r || !positions || !slots || !kv_pool || !dev_error) return MLA_ERR_INVALID_ARG;
     const bool quant = kv_dtype != MLA_KV_BF16;
     if (quant && (!kv_scale || !kr_pool)) return MLA_ERR_INVALID_ARG;
-    if (q && (!q_c || !q_r)) return MLA_ERR_INVALID_ARG;
+    if (q && (!q_c || !q_r || q_c == q || q_r == q || q_c == q_r)) return MLA_ERR_INVALID_ARG;
     if (!is_aligned(c_kv, 16) || !is_aligned(k_r, 16) || !is_aligned(kv_pool, 16) || !is_aligned(slots, 4) ||
-        !is_aligned(positions, 4) || !is_aligned(dev_error, 4) || c_kv_stride % 8 || k_r_stride % 8 ||
+        !is_aligned(positions, 4) || !is_aligned(dev_error, 4) ||
+        (num_tokens > 1 && (c_kv_stride % 8 || k_r_stride % 8 || (q && q_token_stride % 8))) ||
         (quant && (!is_aligned(kr_pool, 16) || !is_aligned(kv_scale, 4))) ||
-        (q && (!is_aligned(q, 16) || !is_aligned(q_c, 16) || !is_aligned(q_r, 16) || q_token_stride % 8 ||
-               q_head_stride % 8)))
+        (q && (!is_aligned(q, 16) || !is_aligned(q_c, 16) || !is_aligned(q_r, 16) || q_head_stride % 8)))
         return MLA_ERR_ALIGNMENT;
     if (num_tokens > (1 << 23)) return MLA_ERR_UNSUPPORTED;
 

@@ -478,7 +478,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kGroup, RT>()) linear_
             work(w, xat + sub * a.k_warps * (RT * kXPiece));
         }
     }
-    if (!ok && tid == 0)  // given up: what is in flight lands first
+    if (!ok) {  // given up: the outputs say so
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][rt][e] = __uint_as_float(0x7FFFFFFFu);
+    }
+    if (!ok && tid == 0)  // and what is in flight lands first
         for (int i = taken; i < steps && i < taken + S::kSlots; ++i)
             drain_phase(bars + 8 * (i % S::kSlots), i / S::kSlots, kTimeoutNs);
     cp_async_wait<0>();

@@ -2,10 +2,11 @@
 (mla_rope_append_kv) against the formulas in 64 bits.
 
 Tolerance of one rotated element, y = m (x0 cos a -+ x1 sin a), counted from the roundings of the
-path: the angle's half turns in fp32 (2^-25 of a half turn, and 2^-32 from the phase's top word:
-pi (2^-25 + 2^-32) < 9.5e-8 rad), sincospi (1 ulp: 6.0e-8), m and its product (2 * 6.0e-8), two
-products and their sum (2 * 6.0e-8 each against |x0| + |x1|): less than 4e-7 m (|x0| + |x1|); the
-frequency's own roundings (pow, 1 / 2 pi, their quotient: 2^-51 of the angle, for the kernel and the
+path: the angle's rest r, at most a quarter of a half turn, in fp32 and in radians (r (2 * 6.0e-8 +
+2.8e-8) < 1.2e-7 rad, against sines and cosines that are 0.71 where r is that large: 8.3e-8), sine
+and cosine (series 2e-9, one ulp and a part: 7e-8), m and its product (2 * 6.0e-8), two products and
+their sum (2 * 6.0e-8 against |x0| + |x1|): less than 4e-7 m (|x0| + |x1|); the frequency's own
+roundings (pow, 1 / 2 pi, their quotient: 2^-51 of the angle, for the kernel and the
 reference together); then the output type's half step.  Copied elements are equal.
 """
 import os
@@ -388,6 +389,21 @@ def test_run_tokens_is_the_step_on_rotated_inputs(kind, lens, q):
     stream.synchronize()
     assert torch.equal(two.out, wants[0])
     assert one.device_error() == 0 and two.device_error() == 0
+
+
+def test_one_token_of_any_token_stride():
+    """The stride from token to token of a single token is never used, so it may be anything."""
+    rope, err = binding.Rope(64), torch.zeros(1, dtype=torch.int32, device=DEV)
+    c_kv, k_r, pos, slots, q = _tokens(1, 8)
+    pools = [_cache("bf16") for _ in range(2)]
+    outs = [[torch.zeros(1, 128, d, dtype=torch.bfloat16, device=DEV) for d in (128, 64)] for _ in range(2)]
+    odd = [c_kv.as_strided(c_kv.shape, (577, 1)), k_r.as_strided(k_r.shape, (1, 1)),
+           q.as_strided(q.shape, (3, q.stride(1), 1))]
+    for (c, k, qq), kv, (q_c, q_r) in zip(([c_kv, k_r, q], odd), pools, outs):
+        kv["kv_pool"].zero_()
+        binding.mla_rope_append_kv(rope, c, k, pos, slots, dev_error=err, q=qq, q_c=q_c, q_r=q_r, **kv)
+    assert torch.equal(pools[0]["kv_pool"], pools[1]["kv_pool"]) and int(err) == 0
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
 
 
 def test_run_tokens_refusals():

@@ -147,6 +147,9 @@ def _append(L, r=None, n=4, c=0x100000, cs=576, k=0x100400, ks=576, pos=0x200000
     (dict(q=0x600008, qc=0x700000, qr=0x800000), ALIGN), (dict(q=0x600000, qc=0x700008, qr=0x800000), ALIGN),
     (dict(q=0x600000, qc=0x700000, qr=0x800008), ALIGN),
     (dict(q=0x600000, qc=0x700000, qr=0x800000, qs=(24576, 196)), ALIGN),
+    (dict(q=0x600000, qc=0x700000, qr=0x800000, qs=(24577, 192)), ALIGN),
+    (dict(q=0x600000, qc=0x600000, qr=0x800000), INV), (dict(q=0x600000, qc=0x700000, qr=0x600000), INV),
+    (dict(q=0x600000, qc=0x700000, qr=0x700000), INV),           # queries over themselves
     (dict(n=(1 << 23) + 1), UNSUP)])
 def test_rope_append_refuses(L, kw, status):
     assert _append(L, **kw) == status
