@@ -587,7 +587,10 @@ mla_status launch(Args a, int heads, int64_t panels, void* stream)
 template <int kGroup>
 mla_status launch_rows(const Args& a, int heads, int64_t panels, void* stream)
 {
-    switch ((a.rows + kRowTile - 1) / kRowTile) {
+    int row_tiles = (a.rows + kRowTile - 1) / kRowTile;
+    // with four warps over k, x of more than 40 rows does not fit the shared memory: two thread blocks
+    if (a.k_warps == kWarps && row_tiles > 5) row_tiles = row_tiles <= 6 ? 3 : 4;
+    switch (row_tiles) {
         case 1: return launch<kGroup, 1>(a, heads, panels, stream);
         case 2: return launch<kGroup, 2>(a, heads, panels, stream);
         case 3: return launch<kGroup, 3>(a, heads, panels, stream);

@@ -106,6 +106,17 @@ def test_linear_many_rows(fmt, group, zero, heads, n, k, rows):
     _assert_product(out, x, value)
 
 
+@pytest.mark.parametrize("fmt,group,zero", FORMATS)
+@pytest.mark.parametrize("rows", [41, 48, 49, 64, 90])
+def test_linear_many_rows_of_few_outputs(fmt, group, zero, rows):
+    """Four warps over k: x of so many rows is more than a thread block's shared memory holds."""
+    w, value = _weight(1, 576, 8192, fmt, group, zero, rows)
+    x = torch.randn(rows, 1, 8192, generator=torch.Generator().manual_seed(rows)).bfloat16().to(DEV)
+    out = torch.full((rows, 1, 576), float("nan"), dtype=torch.bfloat16, device=DEV)
+    binding.mla_linear_w4(x, w, out)
+    _assert_product(out, x, value)
+
+
 def test_linear_many_rows_strides():
     """Rows of a wider tensor, one row for all heads, odd strides of the outputs, not-finite rows."""
     w, value = _weight(6, 1400, 2048, "int4", 64, True, 5)
