@@ -579,6 +579,11 @@ extern "C" const char* mla_last_error_string(void) { return t_last_error; }
 namespace mla {
 // For the library's other translation units: replace this thread's last-error text.
 void set_last_error_text(const char* text) { snprintf(t_last_error, sizeof t_last_error, "%s", text); }
+bool make_bf16_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                   const cuuint32_t* box)
+{
+    return make_map_bf16(m, base, rank, dims, strides, box);
+}
 }  // namespace mla
 
 extern "C" mla_status mla_read_device_error(const uint32_t* dev_error, uint32_t* host_bits, void* stream)

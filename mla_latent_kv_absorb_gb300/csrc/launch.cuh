@@ -1,6 +1,7 @@
 // launch.cuh -- host helpers of the translation units beside api.cu: pointer checks, programmatic
 // dependent launches and the record of a failed launch.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -12,6 +13,11 @@
 namespace mla {
 
 void set_last_error_text(const char* text);
+
+// A tiled map of bf16 with 128-byte swizzle; dims and strides innermost first, strides in bytes for dims
+// 1.. (defined in api.cu).
+bool make_bf16_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                   const cuuint32_t* box);
 
 inline bool is_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 

@@ -2,9 +2,9 @@
 // group of k, and mla_w4_pack, which lays such weights out once (declared in include/mla.h).
 //
 // The weights are the M side of mma.sync m16n8k16 and eight rows of x its N side, so that a decode
-// batch fills the instruction and every weight is unpacked once for all rows (up to 64).  tcgen05
-// would want the unpacked weights in shared memory and a group's scale cannot be applied inside its
-// accumulator; at these row counts the product is bound by the weights' bytes, then by unpacking.
+// batch fills the instruction and every weight is unpacked once for all rows (up to 64).  At a few rows
+// the product is bound by the weights' bytes and by unpacking; from some 25 to 40 rows on, where the
+// MMAs take longer, the kernel of w4_rows.cuh, on tcgen05, is the faster one for weights of some size.
 //
 // A warp works on blocks of 32 n x 128 k: lane 4 g + t has the words (q, t), the eight k from 32 q + 8 t,
 // q = 0..3, of rows g, g + 8, g + 16 and g + 24.  The packed layout keeps a block's 2 KB of codes in
@@ -87,6 +87,10 @@ __host__ inline Layout layout_of(const mla_w4_weight& w)
     return l;
 }
 
+// Where lane 4 g + t's 16 bytes of 32 are: lanes in order, and the four t of one g, or one t of eight g,
+// hit different banks.
+__device__ __forceinline__ int piece_of(int lane) { return lane ^ ((lane >> 3) & 3); }
+
 struct PackArgs {
     const uint8_t* codes;
     const void* scale;
@@ -125,7 +129,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackA
             }
             word[q] = to;
         }
-        *reinterpret_cast<uint4*>(block + j * 512 + lane * 16) = make_uint4(word[0], word[1], word[2], word[3]);
+        *reinterpret_cast<uint4*>(block + j * 512 + piece_of(lane) * 16) = make_uint4(word[0], word[1], word[2], word[3]);
         if (nv) {
             if (t & 1) continue;
             uint32_t s = 0;
@@ -287,7 +291,7 @@ struct Held {
     __device__ __forceinline__ void load(const uint8_t* image, int lane)
     {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[j] = reinterpret_cast<const uint4*>(image)[32 * j + lane];
+        for (int j = 0; j < 4; ++j) c[j] = reinterpret_cast<const uint4*>(image)[32 * j + piece_of(lane)];
         const uint8_t* scales = image + kCodeBytes;
         words(s, scales + (kGroup == 16 ? lane >> 1 : lane >> 2) * (4 * kScale));
         if constexpr (kGroup >= 32) words(z, scales + scale_bytes(kGroup) + (lane >> 2) * (4 * kZero));
@@ -302,6 +306,54 @@ struct Held {
     {
         const int e = j * (kBlockK / kGroup) + i;
         return minus_zero((z[e / 4] & a.zero_mask) | (~a.zero_mask & 0x08080808u), e & 3);
+    }
+};
+
+// What a thread holds of one row of a block, row 8 j + g for lane 8 j + g.
+template <int kGroup>
+struct RowOfBlock {
+    static constexpr int kCount = kGroup == 16 ? 1 : kBlockK / kGroup;  // groups
+    uint4 c[4];     // [t], its words q
+    uint32_t s[2];  // NVFP4: scales [t / 2], byte q; int4: zeros in s[0]
+
+    __device__ __forceinline__ void load(const uint8_t* block, int lane)
+    {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            c[t] = *reinterpret_cast<const uint4*>(block + lane * 64 + ((t ^ ((lane >> 1) & 3)) << 4));
+        const int j = lane >> 3, g = lane & 7;
+        const uint8_t* scales = block + kCodeBytes;
+        if constexpr (kGroup == 16) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) s[i] = *reinterpret_cast<const uint32_t*>(scales + (g * 2 + i) * 16 + j * 4);
+        } else {
+            const uint8_t* z = scales + scale_bytes(kGroup) + (g * 4 + j) * kCount;
+            s[0] = kCount == 1 ? *z : kCount == 2 ? *reinterpret_cast<const uint16_t*>(z) : *reinterpret_cast<const uint32_t*>(z);
+        }
+    }
+    static __device__ __forceinline__ void scales(float (&to)[kCount], const uint8_t* block, int lane)
+    {
+        const uint16_t* at = reinterpret_cast<const uint16_t*>(block + kCodeBytes) + ((lane & 7) * 4 + (lane >> 3)) * kCount;
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) to[i] = __uint_as_float((uint32_t)at[i] << 16);
+    }
+    // The 32 k of q, in pairs.
+    __device__ __forceinline__ void unpack(uint32_t zero_mask, int q, uint32_t (&v)[16]) const
+    {
+        uint32_t zero = 0u;
+        if constexpr (kGroup >= 32)
+            zero = minus_zero((s[0] & zero_mask) | (~zero_mask & 0x08080808u), q / (kGroup / 32));
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint32_t word = q == 0 ? c[t].x : q == 1 ? c[t].y : q == 2 ? c[t].z : c[t].w;
+            uint32_t o[4];
+            if constexpr (kGroup >= 32)
+                unpack_int4(word, zero, o);
+            else
+                unpack_e2m1(word, e4m3_scale(s[t >> 1], q), o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * t + i] = o[i];
+        }
     }
 };
 
@@ -355,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kGroup, RT>()) linear_
     using S = Shared<kGroup, RT>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int n_warps = kWarps / a.k_warps, wk = warp % a.k_warps, wn = warp / a.k_warps;
+    const int n_warps = kWarps / a.k_warps, wk = warp % a.k_warps;
     const int rank = (int)blockIdx.x % a.splits, tile = (int)blockIdx.x / a.splits;
     const int h = blockIdx.y, r0 = (int)blockIdx.z * (RT * kRowTile);
     const int begin = (int)((int64_t)a.steps * rank / a.splits), end = (int)((int64_t)a.steps * (rank + 1) / a.splits);
@@ -561,6 +613,7 @@ mla_status launch(Args a, int heads, int64_t panels, void* stream)
         break;
     }
     const int steps = (a.steps + a.splits - 1) / a.splits, bytes = S::bytes(a.k_warps, steps);
+    if (bytes > 227 * 1024) return MLA_ERR_UNSUPPORTED;
     a.ring_off = S::x_bytes(a.k_warps, steps);
     a.bars_off = bytes - S::kBars;
     const mla_status st = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
@@ -584,9 +637,18 @@ mla_status launch(Args a, int heads, int64_t panels, void* stream)
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, a), "4-bit product kernel launch");
 }
 
+}  // namespace mla::w4
+
+#include "w4_rows.cuh"
+
+namespace mla::w4 {
+
 template <int kGroup>
-mla_status launch_rows(const Args& a, int heads, int64_t panels, void* stream)
+mla_status launch_rows(const Args& a, const mla_w4_weight& w, const Layout& l, void* stream)
 {
+    const int heads = w.heads;
+    const int64_t panels = l.panels;
+    if (rows::faster<kGroup>(a, w, l)) return rows::launch<kGroup>(a, w, l, stream);
     int row_tiles = (a.rows + kRowTile - 1) / kRowTile;
     // with four warps over k, x of more than 40 rows does not fit the shared memory: two thread blocks
     if (a.k_warps == kWarps && row_tiles > 5) row_tiles = row_tiles <= 6 ? 3 : 4;
@@ -660,10 +722,10 @@ mla_status linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t 
     a.early = early;
     a.out_quads = is_aligned(out, 8) && (rows == 1 || out_row_stride % 4 == 0) && (w->heads == 1 || out_head_stride % 4 == 0);
     switch (w->group) {
-        case 16: return launch_rows<16>(a, w->heads, l.panels, stream);
-        case 32: return launch_rows<32>(a, w->heads, l.panels, stream);
-        case 64: return launch_rows<64>(a, w->heads, l.panels, stream);
-        default: return launch_rows<128>(a, w->heads, l.panels, stream);
+        case 16: return launch_rows<16>(a, *w, l, stream);
+        case 32: return launch_rows<32>(a, *w, l, stream);
+        case 64: return launch_rows<64>(a, *w, l, stream);
+        default: return launch_rows<128>(a, *w, l, stream);
     }
 }
 

@@ -107,6 +107,28 @@ def test_linear_many_rows(fmt, group, zero, heads, n, k, rows):
 
 
 @pytest.mark.parametrize("fmt,group,zero", FORMATS)
+@pytest.mark.parametrize("heads,n,k,rows", [
+    (1, 16500, 2112, 57),     # outputs and k end inside a tile and a step, an odd number of steps
+    (1, 8200, 4096, 64),      # clusters of four, four of 256 outputs are there
+    (1, 4096, 4096, 192),     # two warps over k in the packed layout, three blocks of rows
+    (1, 2048, 8192, 250),     # four warps over k
+    (128, 512, 128, 30),      # two pairs of tiles in turn, one step each
+    (64, 384, 192, 60),       # half a pair
+    (3, 3000, 1024, 100),
+    (1, 40000, 64, 64),       # less than a step
+    (1, 65000, 320, 49),
+])
+def test_linear_rows_in_tensor_memory(fmt, group, zero, heads, n, k, rows):
+    """Sizes where the rows are the columns of tensor memory."""
+    k = max(k - k % max(group, 32), group)
+    w, value = _weight(heads, n, k, fmt, group, zero, n + rows)
+    x = torch.randn(rows, heads, k, generator=torch.Generator().manual_seed(rows)).bfloat16().to(DEV)
+    out = torch.full((rows, heads, n), float("nan"), dtype=torch.bfloat16, device=DEV)
+    binding.mla_linear_w4(x, w, out)
+    _assert_product(out, x, value)
+
+
+@pytest.mark.parametrize("fmt,group,zero", FORMATS)
 @pytest.mark.parametrize("rows", [41, 48, 49, 64, 90])
 def test_linear_many_rows_of_few_outputs(fmt, group, zero, rows):
     """Four warps over k: x of so many rows is more than a thread block's shared memory holds."""
@@ -115,6 +137,48 @@ def test_linear_many_rows_of_few_outputs(fmt, group, zero, rows):
     out = torch.full((rows, 1, 576), float("nan"), dtype=torch.bfloat16, device=DEV)
     binding.mla_linear_w4(x, w, out)
     _assert_product(out, x, value)
+
+
+def test_many_rows_in_a_chain_in_graphs_and_on_streams():
+    """The step's two products for 40 rows, one reading what the other wrote: in one stream, captured and
+    replayed, and on three streams at once, the same bits as calls waited for one by one."""
+    uk, _ = _weight(128, 512, 128, "int4", 32, False, 31)
+    uv, _ = _weight(128, 128, 512, "nvfp4", 16, False, 32)
+    for w in (uk, uv):
+        w.struct.tensor_scale *= 0.02
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(40, 128, 128, generator=g).bfloat16().to(DEV)
+
+    def buffers():
+        return torch.empty(40, 128, 512, dtype=torch.bfloat16, device=DEV), torch.empty_like(x)
+
+    def chain(first, bufs, stream=None, wait=False):
+        q, (lat, back) = first, bufs
+        for _ in range(3):
+            for fn, a, w, b in ((binding.mla_absorb_q_w4, q, uk, lat), (binding.mla_out_proj_w4, lat, uv, back)):
+                fn(a, w, b, stream)
+                if wait:
+                    torch.cuda.synchronize()
+            q = back
+        return back
+
+    want = chain(x, buffers(), wait=True).clone()
+    assert want.isfinite().all()
+    assert torch.equal(chain(x, buffers()), want)
+    torch.cuda.synchronize()
+    streams, sets = [torch.cuda.Stream() for _ in range(3)], [buffers() for _ in range(3)]
+    torch.cuda.synchronize()
+    for s, b in zip(streams, sets):
+        chain(x, b, s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(b[1], want) for b in sets)
+    static, bufs, graph = torch.zeros_like(x), buffers(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(static, bufs)
+    static.copy_(x)
+    for _ in range(2):
+        graph.replay()
+    assert torch.equal(bufs[1], want)
 
 
 def test_linear_many_rows_strides():
@@ -340,6 +404,30 @@ def test_step_with_4_bit_weights(fmt, group, zero):
     mixed = binding.DecodeStep(inp.seq_lens, w_uk=uk, w_uv=w_uv, block_table=bt, fused_tail=True, **kv)
     got = mixed.run(q_c, q_r)
     assert_close(got, _attention(inp, q_c, q_r, k_val, w_uv.double()), TOL_BF16, "out (bf16 projection)")
+
+
+def test_step_with_4_bit_weights_and_many_sequences():
+    """48 sequences: the step's kernels one behind the other against calls waited for one by one."""
+    lens = [1 + (37 * i) % 300 for i in range(48)]
+    inp = synth.make_inputs(lens, seed=73)
+    q_c, q_r, _, _, kv, bt = binding.inputs_to_device(inp, DEV)
+    uk, _ = _weight(128, 512, 128, "int4", 128, True, 3)
+    uv, _ = _weight(128, 128, 512, "int4", 64, False, 4)
+    uk.struct.tensor_scale *= 0.05
+    step = binding.DecodeStep(inp.seq_lens, w_uk=uk, w_uv=uv, block_table=bt, **kv)
+    out = step.run(q_c, q_r).clone()
+    assert step.device_error() == 0
+    q_abs, proj = torch.empty_like(step.q_abs), torch.empty_like(out)
+    binding.mla_absorb_q_w4(q_c, uk, q_abs)
+    torch.cuda.synchronize()
+    assert torch.equal(q_abs, step.q_abs)
+    binding.mla_out_proj_w4(step.o_lat, uv, proj)
+    assert torch.equal(proj, out) and out.isfinite().all()
+    graph = step.capture(q_c, q_r)
+    for _ in range(3):
+        step.out.zero_()
+        graph.replay()
+        assert torch.equal(step.out, out)
 
 
 def test_4_bit_step_refusals():
