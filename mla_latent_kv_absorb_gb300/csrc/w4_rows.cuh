@@ -12,13 +12,14 @@
 //   1 thread      of each half issues the MMAs (16 k: 45 cycles for up to 64 rows)
 //   4 warps       of each half add up the groups in registers, and at the end of a tile write the
 //                 outputs through shared memory, 16 bytes a thread
-// A step of the two halves takes 0.85 us at groups of 128 (33 rows of 16384 -> 8192: 33.7 us, 2.1 TB/s;
+// A step of the two halves takes 0.7 us at groups of 128 (33 rows of 16384 -> 8192: 31.8 us, 2.3 TB/s;
 // the weights' bytes alone 10.4 us, the MMAs 12): nothing in it is busy throughout, the chain of codes,
-// unpacking, MMAs and sums through two buffers each is what it waits for (with the unpacking taken
-// out 31 us, the sums as well 30).  What it took to get there, same case: one tile of 128 outputs a
-// thread block and x for each, 48 us; the rings counted without divisions, 37; two halves over one x,
-// 36; codes two steps a copy and x one, 33.5 (an SM takes about 0.1 us for a copy of any size).  Codes
-// fetched a step ahead into registers spill: 39.
+// unpacking, MMAs and sums through two buffers each is what it waits for (two microseconds less with
+// the unpacking taken out, none with the sums).  What it took to get there, same case: one tile of 128
+// outputs a thread block and x for each, 48 us; the rings counted without divisions, 37; two halves over
+// one x, 36; codes two steps a copy and x one, 33.5 (an SM takes about 0.1 us for a copy of any size);
+// the sums' registers kept from the other warps, which spilled, and one barrier less, 31.8.  Codes
+// fetched a step ahead into registers: no gain.
 #pragma once
 
 namespace mla::w4::rows {
@@ -163,10 +164,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     if (a.early) griddep_launch_dependents();
     const uint32_t tmem_d = *tmem_holder, tmem_a = tmem_d + kHalves * kBufs * kRows;
     const WaitCtx wait{kTimeoutNs, abort, nullptr};
+    float* sums = reinterpret_cast<float*>(smem);  // [row][kSumPitch], at the end
     bool ok = true;
-    float acc[kRows];  // of a scaler: the rows of output 32 quarter + lane
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) acc[i] = 0.f;
     const int quarter = warp & 3, half = warp >> 2 & 1;
 
     // (rings are counted through: divisions by what is known at run time only take longer than a copy)
@@ -241,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     }
                     mma_commit(d_full + 8 * buf);
                 }
-                mma_commit(a_empty + 8 * ab);
+                if constexpr (kPerStep > 1) mma_commit(a_empty + 8 * ab);
                 mma_commit(x_empty + 8 * slot);
                 if (++slot == a.x_slots) slot = 0, ++turn;
             }
@@ -249,6 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         }
     } else if (warp >= kScalers) {
         const uint32_t to = tmem_a + ((uint32_t)(32 * quarter) << 16) + half * kBufs * kACols;
+        // that the MMAs of a step are done; one group a step: its sums say so
+        const uint32_t a_left = kPerStep > 1 ? a_empty : d_full;
         const uint8_t* block = smem + C::kCodes + half * tile_off + quarter * row_bytes;
         int slot = 0, turn = 0, kb = begin;
         for (int s = 0; s < all && ok; ) {
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     __syncwarp();
                     if (lane == 0) mbar_arrive(codes_empty + 8 * slot);
                 }
-                ok = s < kBufs || wait_warp(a_empty + 8 * (half * kBufs + ab), s / kBufs - 1, wait);
+                ok = s < kBufs || wait_warp(a_left + 8 * (half * kBufs + ab), s / kBufs - 1, wait);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -285,6 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         const int rows = a.rows - r0 < kRows ? a.rows - r0 : kRows;
         __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(smem + C::kOut) + half * kRows * kPitch;
         const uint8_t* block = smem + C::kCodes + half * tile_off + quarter * row_bytes;
+        float acc[kRows];  // the rows of output 32 quarter + lane
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) acc[i] = 0.f;
         int s = 0, slot = 0, turn = 0;
         for (int pair = pair0; pair < pair0 + pairs; ++pair) {
             for (int ks = 0; ks < ksteps && ok; ++ks, ++s) {
@@ -325,7 +329,12 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) acc[i] = __uint_as_float(0x7FFFFFFFu);
             }
-            if (a.splits > 1) break;  // one pair, joined below
+            if (a.splits > 1) {  // one pair: its sums are joined below
+                barrier_sync(1, 32 * kScalers);  // the MMAs of both halves have left x, whose place they take
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) sums[i * kSumPitch + half * kTileN + 32 * quarter + lane] = acc[i];
+                break;
+            }
             barrier_sync(1 + half, 128);  // the tile before has left
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
@@ -355,11 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     __syncthreads();
     if (a.splits > 1) {
         // the sums of the cluster's blocks, added in the order of k, four outputs a thread
-        float* sums = reinterpret_cast<float*>(smem);  // [row][kSumPitch]
-        if (warp < kScalers) {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) sums[i * kSumPitch + half * kTileN + 32 * quarter + lane] = acc[i];
-        }
+        if (*abort)  // x that came late may have overwritten them
+            for (int i = tid; i < kRows * kSumPitch; i += kThreads) sums[i] = __uint_as_float(0x7FFFFFFFu);
         __syncwarp();
         cluster_sync();
         constexpr int kQuads = kHalves * kTileN / 4;
@@ -428,11 +434,11 @@ inline Spread spread_of(int rows, const mla_w4_weight& w)
 
 // Whether this kernel is the faster one.  Either takes a fixed time and a time for its work: w4.cu's for
 // every 32 outputs x 128 k x 8 rows of an SM (0.033 us, more where a thread block has few steps), this
-// one for every step of 256 outputs x 128 k of a thread block, whatever number of rows up to 64 (0.85 us,
-// with more groups of a step to add up 1 and 1.45 us, NVFP4 1.05 us).  In units of 0.033 us, fitted to
+// one for every step of 256 outputs x 128 k of a thread block, whatever number of rows up to 64 (0.8 us,
+// with more groups of a step to add up 0.9 and 1.35 us, NVFP4 0.85 us).  In units of 0.033 us, fitted to
 // measurements of 13 shapes with 17 to 128 rows; us of w4.cu's and of this kernel, groups of 128:
-//   16384 -> 8192   25 rows 34.4 / 32.9   33: 40.2 / 33.8   64: 56.6 / 35.1   128: 107 / 60
-//   4096 -> 4096    25 rows  9.0 / 13.5   33: 11.3 / 13.8   64: 14.1 / 14.7   128: 20.7 / 14.9
+//   16384 -> 8192   25 rows 34.4 / 31.2   33: 40.2 / 31.7   64: 56.6 / 33.2   128: 107 / 57
+//   4096 -> 4096    25 rows  9.0 / 13.3   33: 11.3 / 13.6   64: 14.1 / 14.5   128: 20.7 / 14.7
 //   128 heads, 128 -> 512  17 rows 9.1 / 7.6   33: 11.7 / 8.2   64: 17.3 / 9.1   128: 32.4 / 17.1
 // Not for 128 outputs or fewer, which leave a half idle (128 heads, 512 -> 128, 64 rows: 9.5 / 10.5 us),
 // nor where x does not suit the tensor map: rows and heads apart from each other, k in whole 64.
@@ -446,7 +452,7 @@ bool faster(const w4::Args& a, const mla_w4_weight& w, const Layout& l)
     const double tiles = (double)l.panels * l.steps * kWarps * w.heads * ((a.rows + kRowTile - 1) / kRowTile) / 152;
     const Spread p = spread_of(a.rows, w);
     const double steps = (double)p.pairs_each * ((p.steps + p.splits - 1) / p.splits) * ((p.blocks + 151) / 152);
-    constexpr double kStep = kGroup == 128 ? 26 : kGroup == 64 ? 30 : kGroup == 16 ? 32 : 44;
+    constexpr double kStep = kGroup == 128 ? 24 : kGroup == 64 ? 28 : kGroup == 16 ? 26 : 41;
     return tiles * (1 + 1.5 / l.steps) > 45 + kStep * steps;
 }
 
