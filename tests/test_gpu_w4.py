@@ -181,35 +181,36 @@ def test_many_rows_in_a_chain_in_graphs_and_on_streams():
     assert torch.equal(bufs[1], want)
 
 
-def test_linear_many_rows_strides():
+@pytest.mark.parametrize("rows", [40, 60])
+def test_linear_many_rows_strides(rows):
     """Rows of a wider tensor, one row for all heads, odd strides of the outputs, not-finite rows."""
     w, value = _weight(6, 1400, 2048, "int4", 64, True, 5)
     g = torch.Generator().manual_seed(6)
-    wide = torch.randn(40, 6 * 2048 + 8, generator=g).bfloat16().to(DEV)
+    wide = torch.randn(rows, 6 * 2048 + 8, generator=g).bfloat16().to(DEV)
     x = wide[:, 8:].unflatten(1, (6, 2048))
-    want = torch.empty(40, 6, 1400, dtype=torch.bfloat16, device=DEV)
+    want = torch.empty(rows, 6, 1400, dtype=torch.bfloat16, device=DEV)
     binding.mla_linear_w4(x.contiguous(), w, want)
     _assert_product(want, x, value)
-    buf = torch.full((40 * 6 * 1401 + 1,), 7.0, dtype=torch.bfloat16, device=DEV)
-    out = buf[1:].view(40, 6, 1401)[:, :, :1400]
+    buf = torch.full((rows * 6 * 1401 + 1,), 7.0, dtype=torch.bfloat16, device=DEV)
+    out = buf[1:].view(rows, 6, 1401)[:, :, :1400]
     binding.mla_linear_w4(x, w, out)
-    assert torch.equal(out, want) and (buf[1:].view(40, 6, 1401)[:, :, 1400] == 7.0).all() and buf[0] == 7.0
-    swapped = torch.empty(6, 40, 1400, dtype=torch.bfloat16, device=DEV)
+    assert torch.equal(out, want) and (buf[1:].view(rows, 6, 1401)[:, :, 1400] == 7.0).all() and buf[0] == 7.0
+    swapped = torch.empty(6, rows, 1400, dtype=torch.bfloat16, device=DEV)
     binding.mla_linear_w4(x.transpose(0, 1).contiguous().transpose(0, 1), w, swapped.transpose(0, 1))
     assert torch.equal(swapped.transpose(0, 1), want)
     out = torch.empty_like(want)
-    shared = x[:, :1].expand(40, 6, 2048)
+    shared = x[:, :1].expand(rows, 6, 2048)
     binding.mla_linear_w4(shared, w, out)
     _assert_product(out, shared, value)
-    binding.mla_linear_w4(x[:1].expand(40, 6, 2048), w, out)     # one row for all: every row the same bits
-    assert torch.equal(out, out[:1].expand(40, 6, 1400))
-    _assert_product(out, x[:1].expand(40, 6, 2048), value)
+    binding.mla_linear_w4(x[:1].expand(rows, 6, 2048), w, out)     # one row for all: every row the same bits
+    assert torch.equal(out, out[:1].expand(rows, 6, 1400))
+    _assert_product(out, x[:1].expand(rows, 6, 2048), value)
     y = x.clone()
-    y[3, 2, 100], y[39, 5, 2047] = float("nan"), float("inf")
+    y[3, 2, 100], y[rows - 1, 5, 2047] = float("nan"), float("inf")
     binding.mla_linear_w4(y, w, out)
-    keep = torch.ones(40, 6, dtype=torch.bool, device=DEV)
-    keep[3, 2], keep[39, 5] = False, False
-    assert torch.equal(out[keep], want[keep]) and out[3, 2].isnan().all() and not out[39, 5].isfinite().all()
+    keep = torch.ones(rows, 6, dtype=torch.bool, device=DEV)
+    keep[3, 2], keep[rows - 1, 5] = False, False
+    assert torch.equal(out[keep], want[keep]) and out[3, 2].isnan().all() and not out[rows - 1, 5].isfinite().all()
 
 
 @pytest.mark.parametrize("k", [32, 64, 96, 160, 2016])
