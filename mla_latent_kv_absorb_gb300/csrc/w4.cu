@@ -598,6 +598,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<kGroup, RT>()) linear_
     if (a.splits > 1) cluster_sync();  // no block leaves while another reads its sums
 }
 
+constexpr int kLimit = 227 * 1024;  // shared memory of a thread block
+
 template <int kGroup, int RT>
 mla_status launch(Args a, int heads, int64_t panels, void* stream)
 {
@@ -613,10 +615,13 @@ mla_status launch(Args a, int heads, int64_t panels, void* stream)
         break;
     }
     const int steps = (a.steps + a.splits - 1) / a.splits, bytes = S::bytes(a.k_warps, steps);
-    if (bytes > 227 * 1024) return MLA_ERR_UNSUPPORTED;
+    if (bytes > kLimit) return MLA_ERR_UNSUPPORTED;
     a.ring_off = S::x_bytes(a.k_warps, steps);
     a.bars_off = bytes - S::kBars;
-    const mla_status st = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes),
+    // The kernel's limit is the process's: set to the same value by every call, the most that any asks
+    // for (full rings, four warps over k), so that no thread lowers it between another's set and launch.
+    constexpr int kFull = S::bytes(kWarps, 2 * kStageSteps + S::kSlots), kMost = kFull < kLimit ? kFull : kLimit;
+    const mla_status st = cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost),
                                       "cudaFuncSetAttribute(max dynamic shared memory)");
     if (st != MLA_OK) return st;
     cudaLaunchConfig_t cfg = {};
