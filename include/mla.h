@@ -470,7 +470,8 @@ MLA_API mla_status mla_w4_pack(const mla_w4_weight* w, const void* codes, const 
  *   out  device bf16, element strides out_row_stride and out_head_stride, distinct elements, sharing
  *        none with x; 2-byte aligned
  * Strides lie in [0, 2^40].  Products are exact and summed in fp32; out is rounded once.  rows 0
- * enqueues nothing.  Weights that do not arrive within 2 s (the kernel's waits are bounded) make the
+ * enqueues nothing; more than 4,194,240 rows, or 2,097,120 where few outputs and a long k make a thread
+ * block take 32 at a time, are refused (MLA_ERR_UNSUPPORTED).  Weights that do not arrive within 2 s (the kernel's waits are bounded) make the
  * outputs that need them NaN. */
 MLA_API mla_status mla_linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t x_head_stride,
                                  const mla_w4_weight* w, void* out, int64_t out_row_stride, int64_t out_head_stride,

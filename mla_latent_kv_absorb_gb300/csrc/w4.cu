@@ -44,6 +44,7 @@ constexpr int kBlockN = 32, kBlockK = 128;          // of a packed block
 constexpr int kCodeBytes = kBlockN * kBlockK / 2;   // its codes
 constexpr int kRowTile = 8;                         // rows of x per MMA
 constexpr int kMaxRowTiles = 8;
+constexpr int kMaxGridZ = 65535;  // blocks of rows
 constexpr int kRedPitch = kBlockN + 4;  // floats; the four lanes of a row hit different banks
 
 // Bytes of a block's scales (int4: bf16 [g][j][group], NVFP4: e4m3 [g][t / 2][j][q]) and of its zeros
@@ -605,7 +606,9 @@ mla_status launch(Args a, int heads, int64_t panels, void* stream)
 {
     using S = Shared<kGroup, RT>;
     const auto kernel = linear_w4_kernel<kGroup, RT>;
-    const int64_t tiles = panels * heads * ((a.rows + RT * kRowTile - 1) / (RT * kRowTile));
+    const int row_blocks = (a.rows + RT * kRowTile - 1) / (RT * kRowTile);
+    if (row_blocks > kMaxGridZ) return MLA_ERR_UNSUPPORTED;
+    const int64_t tiles = panels * heads * row_blocks;
     // Thread blocks of a cluster over k: as many as still start at once (clusters leave some of the
     // places on the SMs empty: nine tenths are counted on), with four steps or more for each.
     a.splits = 1;
@@ -625,8 +628,7 @@ mla_status launch(Args a, int heads, int64_t panels, void* stream)
                                       "cudaFuncSetAttribute(max dynamic shared memory)");
     if (st != MLA_OK) return st;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(panels * a.splits), (unsigned)heads,
-                       (unsigned)((a.rows + RT * kRowTile - 1) / (RT * kRowTile)));
+    cfg.gridDim = dim3((unsigned)(panels * a.splits), (unsigned)heads, (unsigned)row_blocks);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = bytes;
     cfg.stream = static_cast<cudaStream_t>(stream);
@@ -706,7 +708,7 @@ mla_status linear_w4(int32_t rows, const void* x, int64_t x_row_stride, int64_t 
     if (!is_aligned(x, 16) || !is_aligned(w->packed, 16) || !is_aligned(out, 2) || (rows > 1 && x_row_stride % 8) ||
         (w->heads > 1 && x_head_stride % 8))
         return MLA_ERR_ALIGNMENT;
-    if (rows > 65535 * kMaxRowTiles * kRowTile) return MLA_ERR_UNSUPPORTED;
+    if (rows > kMaxGridZ * kMaxRowTiles * kRowTile) return MLA_ERR_UNSUPPORTED;  // of 64 rows a thread block
     const Layout l = layout_of(*w);
     Args a = {};
     a.x = static_cast<const __nv_bfloat16*>(x);
