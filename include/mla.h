@@ -448,7 +448,7 @@ MLA_API mla_status mla_rope_append_kv(const mla_rope_config* rope, int32_t num_t
  *          scale  device uint8 [heads][n][k / 16], finite e4m3 codes (not 0x7F or 0xFF); zero NULL
  *   packed device, mla_w4_packed_bytes(w) bytes, 16-byte aligned, sharing none with the others, which
  *          are not needed afterwards (w->packed is not read by mla_w4_pack)
- *   k is a multiple of group and of 32; heads <= 65535, n * heads < 2^31, k <= 2^30. */
+ *   k is a multiple of group and of 32; heads <= 65535, n * heads <= 2^31 - 256, k <= 2^30. */
 typedef enum mla_w4_format { MLA_W4_INT4 = 0, MLA_W4_NVFP4 = 1 } mla_w4_format;
 typedef struct mla_w4_weight {
     int32_t format; /* mla_w4_format */

@@ -685,7 +685,8 @@ mla_status check_shape(const mla_w4_weight* w)
     if (int4 ? (w->group != 32 && w->group != 64 && w->group != 128) : w->group != 16) return MLA_ERR_INVALID_ARG;
     if (w->k % w->group || w->k % 32 || (w->has_zero != 0 && w->has_zero != 1) || (!int4 && w->has_zero))
         return MLA_ERR_INVALID_ARG;
-    if (w->heads > 65535 || (int64_t)w->heads * w->n >= ((int64_t)1 << 31) || w->k > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+    // outputs fit 32 bits with those that fill up a pair of tiles (256)
+    if (w->heads > 65535 || (int64_t)w->heads * w->n > ((int64_t)1 << 31) - 256 || w->k > (1 << 30)) return MLA_ERR_UNSUPPORTED;
     const mla::w4::Layout l = mla::w4::layout_of(*w);
     if (l.panels * l.steps * mla::w4::kWarps >= ((int64_t)1 << 31)) return MLA_ERR_UNSUPPORTED;
     return MLA_OK;

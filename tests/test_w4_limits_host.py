@@ -35,3 +35,17 @@ def test_rows_past_the_grid_are_refused(L, group, fmt):
     for n, k in ((128, 1024), (128, 128), (8192, 1024)):
         assert _product(L, 65535 * 64 + 1, n, k, **kw) == binding.MLA_ERR_UNSUPPORTED
         assert _product(L, 2 ** 31 - 1, n, k, **kw) == binding.MLA_ERR_UNSUPPORTED
+
+
+def test_outputs_that_do_not_fit_32_bits_when_filled_up_are_refused(L):
+    """The kernels round the outputs up to 4, 8 or 256 at a time in 32 bits."""
+    most = 2 ** 31 - 256
+    for n in (most + 1, 2 ** 31 - 4, 2 ** 31 - 1):
+        w = _weight(n, 32)
+        assert L.mla_w4_packed_bytes(ctypes.byref(w)) == 0
+        assert _product(L, 1, n, 32) == binding.MLA_ERR_UNSUPPORTED
+        assert L.mla_w4_pack(ctypes.byref(w), P(0x100000), P(0x200000), None, P(0x300000), None) == binding.MLA_ERR_UNSUPPORTED
+    assert L.mla_w4_packed_bytes(ctypes.byref(_weight(most // 2 + 1, 32, heads=2))) == 0
+    # 32 outputs x 128 k a block: 2,048 bytes of codes and 32 x 4 scales
+    assert L.mla_w4_packed_bytes(ctypes.byref(_weight(most, 32))) == most // 32 * (2048 + 256)
+    assert L.mla_w4_packed_bytes(ctypes.byref(_weight(most // 2, 32, heads=2))) == most // 32 * (2048 + 256)
