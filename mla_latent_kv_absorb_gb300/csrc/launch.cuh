@@ -50,14 +50,15 @@ mla_status launch_dependent(const char* where, void (*kernel)(KArgs...), dim3 gr
 }
 
 // True when the elements [a][b][0..width) at a * sa + b * sb are all distinct (strides in elements):
-// one of the two outer dimensions steps over the other's whole extent.
+// one of the two outer dimensions steps over the other's whole extent (up to 2^31 x 2^40 elements: more
+// than 64 bits hold).
 inline bool distinct_elements(int64_t na, int64_t sa, int64_t nb, int64_t sb, int64_t width)
 {
     if (sa < 0 || sb < 0) return false;
     const bool inner_b = nb <= 1 || sb >= width, inner_a = na <= 1 || sa >= width;
     if (!inner_a || !inner_b) return false;
     if (na <= 1 || nb <= 1) return true;
-    return sa >= (nb - 1) * sb + width || sb >= (na - 1) * sa + width;
+    return sa >= (__int128)(nb - 1) * sb + width || sb >= (__int128)(na - 1) * sa + width;
 }
 
 }  // namespace mla
