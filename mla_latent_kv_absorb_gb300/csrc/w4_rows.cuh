@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     const WaitCtx wait{kTimeoutNs, abort, nullptr};
     float* sums = reinterpret_cast<float*>(smem);  // [row][kSumPitch], at the end
     bool ok = true;
+    int issued = 0;  // copies, by the two threads that bring codes and x
     const int quarter = warp & 3, half = warp >> 2 & 1;
 
     // (rings are counted through: divisions by what is known at run time only take longer than a copy)
@@ -194,9 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 if ((kb += 2) >= end) kb = begin, ++pair;
                 if (++slot == code_slots) slot = 0, ++turn;
             }
-            if (*abort)  // given up: what is in flight lands first
-                for (int i = s < code_slots ? 0 : s - code_slots; i < s; ++i)
-                    drain_phase(codes_full + 8 * (i % code_slots), i / code_slots, wait.timeout_ns);
+            issued = s;
         }
     } else if (warp == kXWarp) {
         if (lane == 0) {
@@ -211,9 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 if (++kb == end) kb = begin;
                 if (++slot == a.x_slots) slot = 0, ++turn;
             }
-            if (*abort)
-                for (int i = s < a.x_slots ? 0 : s - a.x_slots; i < s; ++i)
-                    drain_phase(x_full + 8 * (i % a.x_slots), i / a.x_slots, wait.timeout_ns);
+            issued = s;
         }
     } else if (warp >= kMmaWarp) {
         if (lane == 0) {
@@ -362,6 +359,15 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    // Given up, which no thread finds out later than here: copies that nobody has waited for land before
+    // their memory takes sums or goes to another thread block.
+    if (*abort) {
+        const bool codes = warp == kCodesWarp;
+        const int slots = codes ? code_slots : a.x_slots;
+        for (int i = issued < slots ? 0 : issued - slots; i < issued; ++i)
+            drain_phase((codes ? codes_full : x_full) + 8 * (i % slots), i / slots, wait.timeout_ns);
+        __syncthreads();
+    }
     if (a.splits > 1) {
         // the sums of the cluster's blocks, added in the order of k, four outputs a thread
         if (*abort)  // x that came late may have overwritten them
