@@ -165,14 +165,17 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     const uint32_t tmem_d = *tmem_holder, tmem_a = tmem_d + kHalves * kBufs * kRows;
     const WaitCtx wait{kTimeoutNs, abort, nullptr};
     float* sums = reinterpret_cast<float*>(smem);  // [row][kSumPitch], at the end
-    bool ok = true;
+    // The swizzled tiles need a base of whole 1,024 bytes (uniform over the thread block).  Without it
+    // nothing is brought and the outputs say so, as where a wait runs out.
+    const bool aligned = (sbase & 1023u) == 0;
+    bool ok = aligned;
     int issued = 0;  // copies, by the two threads that bring codes and x
     const int quarter = warp & 3, half = warp >> 2 & 1;
 
     // (rings are counted through: divisions by what is known at run time only take longer than a copy)
     if (warp == kCodesWarp) {
         if (lane == 0) {
-            const int count = pairs * ((ksteps + 1) / 2);
+            const int count = aligned ? pairs * ((ksteps + 1) / 2) : 0;
             int s = 0, slot = 0, turn = 0, pair = pair0, kb = begin;
             for (; s < count; ++s) {
                 if (turn > 0 && !wait_phase(codes_empty + 8 * slot, turn - 1, wait)) break;
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             const uint64_t keep = l2_policy_evict_last();  // x is read by every tile
             const int bytes = a.cols * 128;
             int s = 0, slot = 0, turn = 0, kb = begin;
-            for (; s < all; ++s) {
+            for (; aligned && s < all; ++s) {
                 if (turn > 0 && !wait_phase(x_empty + 8 * slot, turn - 1, wait)) break;
                 const uint32_t to = sbase + C::kX + slot * 2 * bytes, bar = x_full + 8 * slot;
                 mbar_arrive_expect_tx(bar, 2 * bytes);
