@@ -844,7 +844,6 @@ class DecodeStep:
             self.q_r = torch.empty(B, NUM_HEADS, D_R, dtype=torch.bfloat16, device=self.device)
         self._h_stage = self._d_stage = None  # pinned host / device staging of run_host
         self._host_graph = None  # (mla_step_graph handle, key of the buffers and lengths it was made for)
-        self._old_graph = None   # the handle before it, kept until the next is made, so that the two differ
 
     def run(self, q_c: torch.Tensor, q_r: torch.Tensor, stream=None) -> torch.Tensor:
         kv = dict(kv_pool=self.kv_pool, block_table=self.block_table, o_lat=self.o_lat, lse=self.lse,
@@ -889,18 +888,9 @@ class DecodeStep:
                 out.data_ptr(), out.numel(), out.dtype)
 
     def _drop_host_graph(self) -> None:
-        if self._old_graph is not None:
-            handle, self._old_graph = self._old_graph, None
-            lib().mla_step_graph_destroy(handle)
         if self._host_graph is not None:
             handle, self._host_graph = self._host_graph[0], None
             lib().mla_step_graph_destroy(handle)
-
-    def _retire_host_graph(self) -> None:
-        if self._host_graph is not None:
-            new, self._host_graph = self._host_graph[0], None
-            self._drop_host_graph()
-            self._old_graph = new
 
     def __del__(self):
         try:
@@ -929,6 +919,16 @@ class DecodeStep:
             if self._host_key(q_c, q_r, block_table, lens, out) == self._host_graph[1]:
                 _check("mla_step_graph_run", lib().mla_step_graph_run(self._host_graph[0], 1, _stream(stream)))
                 return out
+        before = self._host_graph
+        try:
+            return self._run_host(q_c, q_r, block_table, lens, out, stream)
+        finally:  # a graph that was replaced, or that no later call can use, goes behind its successor
+            if before is not None and self._host_graph is not before:
+                lib().mla_step_graph_destroy(before[0])
+
+    def _run_host(self, q_c, q_r, block_table, lens, out, stream) -> torch.Tensor:
+        """run_host where no captured step fits; the graph that was there is let go of (None) once its
+        lengths or buffers are not the step's any more."""
         B = self.batch
         _need(q_c, "q_c", torch.bfloat16, (B, NUM_HEADS, D_HC), device=False)
         _need(q_r, "q_r", torch.bfloat16, (B, NUM_HEADS, D_R), device=False)
@@ -940,7 +940,7 @@ class DecodeStep:
                 raise ValueError("block_table must be [sequences, max_pages]")
         if not np.array_equal(lens, self.seq_lens) or self._h_stage is None:
             # new lengths: size the workspace for their plan (the library plans again itself)
-            self._retire_host_graph()
+            self._host_graph = None
             self.seq_lens = lens.copy()
             _, info = mla_plan_splits(lens, self._num_sms, **self._plan_opts)
             ws = int(info.workspace_bytes)
@@ -954,7 +954,7 @@ class DecodeStep:
                 self._q_r_dev = torch.empty(B, NUM_HEADS, D_R, dtype=torch.bfloat16, device=self.device)
         if block_table is not None and (getattr(self, "_bt_dev", None) is None or
                                         tuple(self._bt_dev.shape) != tuple(block_table.shape)):
-            self._retire_host_graph()
+            self._host_graph = None
             self._bt_dev = torch.empty(tuple(block_table.shape), dtype=torch.int32, device=self.device)
         bt_dev = self._bt_dev if block_table is not None else self.block_table
         _check_table_rows(lens, bt_dev)
@@ -978,10 +978,9 @@ class DecodeStep:
                 _ptr(self.kv_scale), _ptr(self.kr_pool), int(self.kv_pool.shape[0]), float(self.softmax_scale),
                 ctypes.byref(bufs), _ptr(out), ctypes.byref(info), _stream(stream))
         if use_graph:
-            self._retire_host_graph()
+            self._host_graph = None
             handle = ctypes.c_void_p()
             _check("mla_step_graph_create", lib().mla_step_graph_create(*args, ctypes.byref(handle)))
-            self._drop_host_graph()
             self._host_graph = (handle, self._host_key(q_c, q_r, block_table, lens, out))
             self.info = info
             _check("mla_step_graph_run", lib().mla_step_graph_run(handle, 1, _stream(stream)))
