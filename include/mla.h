@@ -356,7 +356,11 @@ typedef enum mla_rope_scaling {
                             beta_fast times over original_len positions keep their frequency, those
                             that turn fewer than beta_slow times have it divided by factor, with a
                             linear ramp over the pair index between the two (both ends rounded
-                            outwards to whole indexes); m = 0.1 ln(factor) + 1 unless given */
+                            outwards to whole indexes); m = 0.1 ln(factor) + 1 unless given.
+                            That m is YaRN's attention temperature where the whole head is rotated:
+                            it multiplies q and k.  Where a part is, as in this library's step (64
+                            of 192), give magnitude 1 and put m^2 into the softmax scale instead,
+                            so that the content part of the scores has it too */
 } mla_rope_scaling;
 typedef struct mla_rope_options {
     int32_t dim;            /* even, 2 .. MLA_ROPE_MAX_DIM */

@@ -428,7 +428,10 @@ class Rope:
     head, ``layout`` "interleaved" (pairs 2i, 2i + 1) or "half" (pairs i, i + dim / 2), frequencies
     base^(-2i / dim) with ``scaling`` "none", "linear" (divided by ``factor``) or "yarn" (``factor``
     over ``original_len`` trained positions), or the caller's ``inv_freq`` [dim / 2] as they are.
-    ``magnitude`` multiplies cos and sin (0: the scaling's own)."""
+    ``magnitude`` multiplies cos and sin (0: the scaling's own, for "yarn" m = 0.1 ln(factor) + 1,
+    which is the attention temperature of a head that is rotated as a whole).  For DecodeStep, whose
+    heads are rotated in 64 of 192 elements, YaRN is magnitude=1.0 here and softmax_scale = m^2 /
+    sqrt(192) there."""
 
     def __init__(self, dim: int = D_R, *, base: float = 10000.0, layout: str = "interleaved", scaling: str = "none",
                  factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
