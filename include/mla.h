@@ -420,6 +420,7 @@ MLA_API mla_status mla_rope(const mla_rope_config* rope, mla_dtype dtype, int32_
  *              the e4m3 nearest (max|c| of the block / sigma) * fp32(1 / 6), where mla_append_kv has
  *              quotients by 2688 and 6; the values differ only where a quotient lies at the border
  *              of two codes (about 1 in 700 of N(0,1) latents, by one step of the format).
+ *              mla_rope on the keys, then mla_append_kv, gives the quotients' bytes.
  *              No two tokens have the same slot (of two that do, each element of the row is
  *              either's).
  *   q          device bf16 [num_tokens][128][192], 128 content then 64 un-rotated values per

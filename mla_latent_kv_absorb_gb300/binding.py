@@ -800,7 +800,8 @@ class DecodeStep:
     the bf16 decode kernel's prologue (mla_absorb_decode_paged); fused_tail runs merge and
     projection as one kernel (mla_merge_out_proj).  All buffers are allocated here, by torch, once.
     w_uk and w_uv may be 4-bit weights (W4Weight): the absorb and the projection are then
-    mla_absorb_q_w4 and mla_out_proj_w4 (not with the fused kernels, nor from host memory).  With
+    mla_absorb_q_w4 and mla_out_proj_w4 (not with the fused kernels, nor from host memory; faster
+    than bf16 up to some 30 rows of the batch, slower beyond 64).  With
     ``rope``, run_tokens takes the new tokens as their projections give them.
     """
 

@@ -9,10 +9,11 @@
 //   1 thread      brings the packed codes, steps of 128 k (bulk copies)
 //   1 thread      brings x (TMA, 128-byte swizzle)
 //   4 warps       of each half unpack, into one of two buffers of 64 columns
-//   1 thread      of each half issues the MMAs (16 k: 45 cycles for up to 64 rows)
+//   1 thread      of each half issues the MMAs (16 k: 45 cycles for up to 64 rows; one thread for both
+//                 halves waits for either in turn: 40.9 us where two take 31.3)
 //   4 warps       of each half add up the groups in registers, and at the end of a tile write the
 //                 outputs through shared memory, 16 bytes a thread
-// A step of the two halves takes 0.7 us at groups of 128 (33 rows of 16384 -> 8192: 31.8 us, 2.3 TB/s;
+// A step of the two halves takes 0.7 us at groups of 128 (33 rows of 16384 -> 8192: 31.3 us, 2.2 TB/s;
 // the weights' bytes alone 10.4 us, the MMAs 12): nothing in it is busy throughout, the chain of codes,
 // unpacking, MMAs and sums through two buffers each is what it waits for (two microseconds less with
 // the unpacking taken out, none with the sums).  What it took to get there, same case: one tile of 128
@@ -446,10 +447,11 @@ inline Spread spread_of(int rows, const mla_w4_weight& w)
 // one for every step of 256 outputs x 128 k of a thread block, whatever number of rows up to 64 (0.8 us,
 // with more groups of a step to add up 0.9 and 1.35 us, NVFP4 0.85 us).  In units of 0.033 us, fitted to
 // measurements of 13 shapes with 17 to 128 rows; us of w4.cu's and of this kernel, groups of 128:
-//   16384 -> 8192   25 rows 34.4 / 31.2   33: 40.2 / 31.7   64: 56.6 / 33.2   128: 107 / 57
-//   4096 -> 4096    25 rows  9.0 / 13.3   33: 11.3 / 13.6   64: 14.1 / 14.5   128: 20.7 / 14.7
-//   128 heads, 128 -> 512  17 rows 9.1 / 7.6   33: 11.7 / 8.2   64: 17.3 / 9.1   128: 32.4 / 17.1
-// Not for 128 outputs or fewer, which leave a half idle (128 heads, 512 -> 128, 64 rows: 9.5 / 10.5 us),
+//   16384 -> 8192   25 rows 34.3 / 30.7   33: 40.5 / 31.3   64: 56.2 / 33.0   128: 106 / 56.2
+//   4096 -> 4096    25 rows  8.2 / 12.1   33: 10.9 / 12.4   64: 13.6 / 13.3   128: 20.4 / 13.8
+//   128 heads, 128 -> 512  17 rows 7.7 / 6.6   33: 10.5 / 7.2   64: 15.7 / 8.1   128: 30.9 / 15.4
+// Not for 128 outputs or fewer, which leave a half idle (128 heads, 512 -> 128, 33 rows: 6.2 / 7.8 us,
+// 64: 8.4 / 8.4, 128: 15.4 / 16.0),
 // nor where x does not suit the tensor map: rows and heads apart from each other, k in whole 64.
 template <int kGroup>
 bool faster(const w4::Args& a, const mla_w4_weight& w, const Layout& l)
