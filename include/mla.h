@@ -108,6 +108,12 @@ typedef struct mla_plan_options {
                                     (q_c, q_R, q_abs, o_lat, lse, out) then has batch * q rows of
                                     128 heads; the block table keeps one row per sequence.  Each
                                     query row scans its pages on its own (no shared scan). */
+    int32_t window;              /* sliding window W (0 = none): a query row that sees the first L
+                                    cached tokens sees only the last W of them ... */
+    int32_t sinks;               /* ... and the first `sinks` (>= 0; W = 0: 0).  Pages without a token
+                                    that some row sees are not read and their table entries may hold
+                                    anything, so that a sequence can give them back; in the other pages
+                                    the tokens that no row sees may hold anything, NaN included */
 } mla_plan_options;
 #define MLA_MAX_QUERIES_PER_SEQ 4096
 
@@ -118,11 +124,14 @@ typedef struct mla_plan_info {
     int32_t num_partials;    /* items that write a split partial into the workspace */
     int32_t num_combine;     /* sequences with more than one item */
     int32_t max_splits;      /* most items any one sequence has */
-    int32_t total_pages;     /* sum over query rows of ceil(visible length / 64) */
+    int32_t total_pages;     /* sum over query rows of the pages they read: ceil(visible length / 64)
+                                without a window */
     int32_t queries_per_seq; /* q of the plan (1 for ordinary decode) */
     int64_t plan_bytes;      /* bytes of the plan image written to plan_host */
     int64_t workspace_bytes; /* bytes mla_decode_paged needs in `workspace` */
     int64_t wait_timeout_ns;
+    int32_t window;          /* as planned */
+    int32_t sinks;
 } mla_plan_info;
 
 /* Upper bound on the plan image size for `batch` query rows (sequences x queries_per_seq) on
@@ -518,6 +527,79 @@ MLA_API mla_status mla_prefill_decompressed(mla_kv_dtype kv_dtype, const void* k
                                             int32_t chunk_len, const void* q_c, const void* q_r, const void* w_uk,
                                             const void* w_uv, float softmax_scale, void* workspace,
                                             size_t workspace_bytes, void* out, uint32_t* dev_error, void* stream);
+
+/* ---------------------------------------------------------------- a prefix that a batch shares
+ *
+ * Sequences that begin with the same tokens (a system prompt, samples of one prompt) share the pages of
+ * that prefix.  Decoded with block tables that list those pages, every sequence scans them on its own, in
+ * the absorbed form: 278,528 FLOP for each sequence and prefix token.  Here the prefix is decompressed
+ * once (P1 section 4, path A) and kept, and each step's query rows attend to it together: 81,920 FLOP for
+ * each row and token, and 64 KB of keys and values read for each token whatever the number of rows.  That
+ * is faster from about 40 query rows on (256 rows: several times), and takes 66.7 KB of memory for each
+ * prefix token.
+ *
+ * mla_prefix_open makes the prefix's keys and values from its cache pages:
+ *   kv_dtype, kv_pool, kv_scale, kr_pool, num_pool_pages   the cache, as mla_gather_kv
+ *   block_table_row  device int32 [max_pages]: the pages of tokens 0 .. prefix_len - 1
+ *                    (ceil(prefix_len / 64) <= max_pages; the last may be partly filled)
+ *   w_uk, w_uv       device bf16 [128][128][512]
+ *   rows             device bf16 [prefix_len][576], receives the cache rows as mla_gather_kv writes them
+ *                    (columns 512..575 are k_R)
+ *   k, v             device bf16 [128 heads][prefix_len][128], receive W_UK[h] c and W_UV[h] c, fp32
+ *                    sums rounded once
+ *   dev_error        MLA_DEVERR_BAD_PAGE for an entry outside the pool (the rows of that page hold what
+ *                    they held before)
+ * All but block_table_row, kv_scale and dev_error 16-byte aligned.  1 <= prefix_len <= 65535 * 128 (above:
+ * MLA_ERR_UNSUPPORTED). */
+MLA_API mla_status mla_prefix_open(mla_kv_dtype kv_dtype, const void* kv_pool, const float* kv_scale,
+                                   const void* kr_pool, int32_t num_pool_pages, const int32_t* block_table_row,
+                                   int32_t max_pages, int32_t prefix_len, const void* w_uk, const void* w_uv,
+                                   void* rows, void* k, void* v, uint32_t* dev_error, void* stream);
+
+/* Attention of num_rows query rows to the prefix, merged with each row's attention over its sequence's own
+ * tokens (mla_out_proj's output and the lse of mla_decode_paged / mla_combine_splits):
+ *   s_j = (q_c[r,h] . k[h,j] + q_R[r,h] . k_R[j]) * softmax_scale over all prefix tokens j,
+ *   lse = logaddexp(own_lse, logsumexp_j s_j),
+ *   out = exp(own_lse - lse) own_out + sum_j exp(s_j - lse) v[h,j].
+ *   q_c, q_r    device bf16 [num_rows][128][128] / [num_rows][128][64] (already rotated: the prefix is
+ *               positions 0 .. prefix_len - 1, the rows' own tokens lie behind it)
+ *   k, v        device bf16 [128][prefix_len][128]; k_r device bf16, token j's 64 values at
+ *               k_r + j * k_r_stride (elements, a multiple of 8, 64 .. 2^32)
+ *   own_out     device bf16 [num_rows][128][128], own_lse device fp32 [num_rows][128] (natural log; -inf:
+ *               no own tokens, that row of own_out is not read), or both NULL: the prefix alone
+ *   workspace   device, >= mla_prefix_attend_workspace_bytes(num_rows, prefix_len, num_sms); calls that
+ *               may overlap need one each
+ *   out         device bf16 [num_rows][128][128], may be own_out; otherwise shares no byte with the rest
+ *   lse         device fp32 [num_rows][128] or NULL, may be own_lse
+ *   num_sms     SMs of the device: the number of thread blocks, and so how the sums are split
+ *   dev_error   MLA_DEVERR_TIMEOUT for a bounded wait that ran out
+ * bf16 and workspace pointers 16-byte aligned.  num_rows 0 enqueues nothing; more than 65,536 rows,
+ * a prefix of more than 65535 * 128 tokens or more than 4,096 SMs are refused (MLA_ERR_UNSUPPORTED).
+ * Results do not depend on the rows around them, and are the same from call to call. */
+MLA_API size_t mla_prefix_attend_workspace_bytes(int32_t num_rows, int32_t prefix_len, int32_t num_sms);
+MLA_API mla_status mla_prefix_attend(int32_t num_rows, int32_t prefix_len, int32_t num_sms, const void* q_c,
+                                     const void* q_r, const void* k, const void* v, const void* k_r,
+                                     int64_t k_r_stride, float softmax_scale, const void* own_out,
+                                     const float* own_lse, void* workspace, size_t workspace_bytes, void* out,
+                                     float* lse, uint32_t* dev_error, void* stream);
+
+/* ---------------------------------------------------------------- a prefill chunk under a sliding window
+ *
+ * mla_prefill_decompressed with the window and sinks of mla_plan_options: the query at position p
+ * (seq_len - chunk_len .. seq_len - 1) sees the positions j <= p with j > p - window or j < sinks.  Only
+ * tokens that some query sees are read and decompressed: the first `sinks` and those from the first query's
+ * window on; table entries of pages without such a token may hold anything.
+ *   window >= 1, sinks >= 0; the other arguments as mla_prefill_decompressed, with
+ *   workspace of mla_prefill_window_workspace_bytes(seq_len, chunk_len, window, sinks) bytes (0 if the
+ *   sizes are not valid)
+ * A token that some query of the chunk sees has to be finite. */
+MLA_API size_t mla_prefill_window_workspace_bytes(int32_t seq_len, int32_t chunk_len, int32_t window, int32_t sinks);
+MLA_API mla_status mla_prefill_window(mla_kv_dtype kv_dtype, const void* kv_pool, const float* kv_scale,
+                                      const void* kr_pool, int32_t num_pool_pages, const int32_t* block_table_row,
+                                      int32_t max_pages, int32_t seq_len, int32_t chunk_len, int32_t window,
+                                      int32_t sinks, const void* q_c, const void* q_r, const void* w_uk,
+                                      const void* w_uv, float softmax_scale, void* workspace, size_t workspace_bytes,
+                                      void* out, uint32_t* dev_error, void* stream);
 
 /* ---- the whole step from host memory in one call ------------------------------------------
  * For callers whose queries, block table and lengths live in host memory: plans the step for

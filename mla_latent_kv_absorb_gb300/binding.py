@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from functools import partial
 from typing import Optional
 
 import numpy as np
@@ -45,14 +46,15 @@ class MlaError(RuntimeError):
 class PlanOptions(ctypes.Structure):
     _fields_ = [("min_pages_per_split", ctypes.c_int32), ("max_clusters", ctypes.c_int32),
                 ("wait_timeout_ns", ctypes.c_int64), ("item_cost_pages", ctypes.c_int32),
-                ("queries_per_seq", ctypes.c_int32)]
+                ("queries_per_seq", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
 
 
 class PlanInfo(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("num_clusters", ctypes.c_int32), ("num_items", ctypes.c_int32),
                 ("num_partials", ctypes.c_int32), ("num_combine", ctypes.c_int32), ("max_splits", ctypes.c_int32),
                 ("total_pages", ctypes.c_int32), ("queries_per_seq", ctypes.c_int32), ("plan_bytes", ctypes.c_int64),
-                ("workspace_bytes", ctypes.c_int64), ("wait_timeout_ns", ctypes.c_int64)]
+                ("workspace_bytes", ctypes.c_int64), ("wait_timeout_ns", ctypes.c_int64), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32)]
 
 
 EXPORTS = ("mla_status_string", "mla_last_error_string", "mla_plan_bytes_max", "mla_plan_splits", "mla_absorb_q", "mla_decode_paged",
@@ -61,7 +63,8 @@ EXPORTS = ("mla_status_string", "mla_last_error_string", "mla_plan_bytes_max", "
            "mla_absorb_decode_paged", "mla_gather_kv", "mla_step_graph_create", "mla_step_graph_run",
            "mla_step_graph_destroy", "mla_prefill_workspace_bytes", "mla_prefill_decompressed",
            "mla_rope_init", "mla_rope", "mla_rope_append_kv", "mla_w4_packed_bytes", "mla_w4_pack",
-           "mla_linear_w4", "mla_absorb_q_w4", "mla_out_proj_w4")
+           "mla_linear_w4", "mla_absorb_q_w4", "mla_out_proj_w4", "mla_prefix_open", "mla_prefix_attend_workspace_bytes",
+           "mla_prefix_attend", "mla_prefill_window_workspace_bytes", "mla_prefill_window")
 
 # capacity of the library's fixed split-partial array (mla_decode_paged_static_ws)
 MLA_STATIC_WS_MAX_PARTIALS = 128
@@ -168,6 +171,18 @@ def lib() -> ctypes.CDLL:
     L.mla_absorb_q_w4.argtypes = [P, P, P, i32, P]
     L.mla_out_proj_w4.restype = ctypes.c_int
     L.mla_out_proj_w4.argtypes = [P, P, P, i32, P]
+    f32 = ctypes.c_float
+    L.mla_prefix_open.restype = ctypes.c_int
+    L.mla_prefix_open.argtypes = [ctypes.c_int, P, P, P, i32, P, i32, i32, P, P, P, P, P, P, P]
+    L.mla_prefix_attend_workspace_bytes.restype = sz
+    L.mla_prefix_attend_workspace_bytes.argtypes = [i32, i32, i32]
+    L.mla_prefix_attend.restype = ctypes.c_int
+    L.mla_prefix_attend.argtypes = [i32, i32, i32, P, P, P, P, P, i64, f32, P, P, P, sz, P, P, P, P]
+    L.mla_prefill_window_workspace_bytes.restype = sz
+    L.mla_prefill_window_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.mla_prefill_window.restype = ctypes.c_int
+    L.mla_prefill_window.argtypes = [ctypes.c_int, P, P, P, i32, P, i32, i32, i32, i32, i32, P, P, P, P, f32, P, sz, P,
+                                     P, P]
     L.mla_read_device_error.restype = ctypes.c_int
     L.mla_read_device_error.argtypes = [u32p, ctypes.POINTER(ctypes.c_uint32), P]
     L.mla_debug_wait_timeout.restype = ctypes.c_int
@@ -218,10 +233,12 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None, device=True):
 # --------------------------------------------------------------------------- C ABI, same names
 
 def mla_plan_splits(seq_lens, num_sms: int, *, min_pages_per_split: int = 0, max_clusters: int = 0,
-                    wait_timeout_ns: int = 0, item_cost_pages: int = 0, queries_per_seq: int = 0):
+                    wait_timeout_ns: int = 0, item_cost_pages: int = 0, queries_per_seq: int = 0, window: int = 0,
+                    sinks: int = 0):
     """Host planning. Returns (plan image as an int32 numpy array, PlanInfo).  With
     queries_per_seq = q > 1 the plan covers len(seq_lens) * q query rows (token t of sequence b
-    is row b * q + t and sees the first S_b - q + 1 + t cached tokens)."""
+    is row b * q + t and sees the first S_b - q + 1 + t cached tokens); with window = W > 0 a row
+    sees the last W of its tokens and the first ``sinks``."""
     lens = np.ascontiguousarray(np.asarray(seq_lens, dtype=np.int32))
     B = int(lens.size)
     cap = int(lib().mla_plan_bytes_max(B * max(1, int(queries_per_seq)), int(num_sms)))
@@ -229,7 +246,7 @@ def mla_plan_splits(seq_lens, num_sms: int, *, min_pages_per_split: int = 0, max
         raise MlaError("mla_plan_splits", MLA_ERR_INVALID_ARG, "bad batch or SM count")
     buf = np.zeros(cap // 4, dtype=np.int32)
     opts = PlanOptions(int(min_pages_per_split), int(max_clusters), int(wait_timeout_ns), int(item_cost_pages),
-                       int(queries_per_seq))
+                       int(queries_per_seq), int(window), int(sinks))
     info = PlanInfo()
     st = lib().mla_plan_splits(lens.ctypes.data_as(ctypes.c_void_p), B, int(num_sms), ctypes.byref(opts),
                                buf.ctypes.data_as(ctypes.c_void_p), cap, ctypes.byref(info))
@@ -740,26 +757,179 @@ def mla_prefill_decompressed(*, kv_pool: torch.Tensor, block_table_row: torch.Te
 def prefill_chunk(seq_len: int, q_c: torch.Tensor, q_r: torch.Tensor, *, w_uk: torch.Tensor, w_uv: torch.Tensor,
                   kv_pool: torch.Tensor, block_table_row: torch.Tensor, kv_scale: Optional[torch.Tensor] = None,
                   kr_pool: Optional[torch.Tensor] = None, threshold: int = PREFILL_THRESHOLD,
-                  softmax_scale: float = SOFTMAX_SCALE, stream=None):
+                  softmax_scale: float = SOFTMAX_SCALE, window: int = 0, sinks: int = 0, stream=None):
     """A chunk of T = q_c.shape[0] new tokens at the end of one sequence of seq_len cached
     tokens (the chunk's cache rows included): chunks shorter than `threshold` run the absorbed
     decode with T query rows (DecodeStep, queries_per_seq = T), longer ones the decompressed
-    form (mla_prefill_decompressed).  Returns (out [T, 128, 128], device error word)."""
+    form (mla_prefill_decompressed; with a ``window`` mla_prefill_window).  Returns
+    (out [T, 128, 128], device error word)."""
     T = int(q_c.shape[0])
     bt = block_table_row.reshape(1, -1)
     if T < threshold:
         step = DecodeStep(np.array([seq_len], np.int32), w_uk=w_uk, w_uv=w_uv, kv_pool=kv_pool, block_table=bt,
                           kv_scale=kv_scale, kr_pool=kr_pool, device=q_c.device, queries_per_seq=T,
-                          softmax_scale=softmax_scale)
+                          softmax_scale=softmax_scale, window=window, sinks=sinks)
         return step.run(q_c, q_r, stream), step.dev_error
     if isinstance(w_uk, W4Weight) or isinstance(w_uv, W4Weight):
         raise ValueError(f"prefill_chunk: chunks of {threshold} or more new tokens read bf16 weights")
     out = torch.empty(T, NUM_HEADS, D_HC, dtype=torch.bfloat16, device=q_c.device)
     err = torch.zeros(1, dtype=torch.int32, device=q_c.device)
-    mla_prefill_decompressed(kv_pool=kv_pool, block_table_row=bt[0], seq_len=seq_len, q_c=q_c, q_r=q_r, w_uk=w_uk,
-                             w_uv=w_uv, out=out, dev_error=err, kv_scale=kv_scale, kr_pool=kr_pool,
-                             softmax_scale=softmax_scale, stream=stream)
+    if sinks and not window:
+        raise ValueError("sinks need a window")
+    attend = partial(mla_prefill_window, window=window, sinks=sinks) if window else mla_prefill_decompressed
+    attend(kv_pool=kv_pool, block_table_row=bt[0], seq_len=seq_len, q_c=q_c, q_r=q_r, w_uk=w_uk, w_uv=w_uv, out=out,
+           dev_error=err, kv_scale=kv_scale, kr_pool=kr_pool, softmax_scale=softmax_scale, stream=stream)
     return out, err
+
+
+# --------------------------------------------------------------------------- windows and shared prefixes
+
+def mla_prefill_window_workspace_bytes(seq_len: int, chunk_len: int, window: int, sinks: int = 0) -> int:
+    size = int(lib().mla_prefill_window_workspace_bytes(int(seq_len), int(chunk_len), int(window), int(sinks)))
+    if size == 0:
+        raise MlaError("mla_prefill_window_workspace_bytes", MLA_ERR_INVALID_ARG, "invalid sizes")
+    return size
+
+
+def mla_prefill_window(*, kv_pool: torch.Tensor, block_table_row: torch.Tensor, seq_len: int, window: int,
+                       q_c: torch.Tensor, q_r: torch.Tensor, w_uk: torch.Tensor, w_uv: torch.Tensor, out: torch.Tensor,
+                       dev_error: torch.Tensor, sinks: int = 0, workspace: Optional[torch.Tensor] = None,
+                       kv_scale: Optional[torch.Tensor] = None, kr_pool: Optional[torch.Tensor] = None,
+                       softmax_scale: float = SOFTMAX_SCALE, stream=None) -> None:
+    """mla_prefill_decompressed under a sliding window: the query at position p sees the last
+    ``window`` positions up to its own and the first ``sinks``.  workspace: a uint8 tensor of at least
+    mla_prefill_window_workspace_bytes(seq_len, chunk, window, sinks) (allocated here when None)."""
+    device = torch._C._cuda_getDevice()
+    if not isinstance(q_c, torch.Tensor) or q_c.dim() != 3:
+        raise ValueError("q_c must be [chunk, 128, 128]")
+    T, bf16 = int(q_c.shape[0]), torch.bfloat16
+    ptrs = [_whole(t, name, bf16, shape, device) for t, name, shape in (
+        (q_c, "q_c", (T, NUM_HEADS, D_HC)), (q_r, "q_r", (T, NUM_HEADS, D_R)), (w_uk, "w_uk", (NUM_HEADS, D_HC, D_C)),
+        (w_uv, "w_uv", (NUM_HEADS, D_HC, D_C)))]
+    out_ptr = _whole(out, "out", bf16, (T, NUM_HEADS, D_HC), device)
+    cache = _cache(kv_pool, kv_scale, kr_pool, device)
+    table, pages = _table_row(block_table_row, device)
+    err = _whole(dev_error, "dev_error", torch.int32, (1,), device)
+    if workspace is None:
+        workspace = torch.empty(mla_prefill_window_workspace_bytes(seq_len, T, window, sinks), dtype=torch.uint8,
+                                device=q_c.device)
+    ws = _whole(workspace, "workspace", workspace.dtype, tuple(workspace.shape), device)
+    st = lib().mla_prefill_window(*cache, table, pages, int(seq_len), T, int(window), int(sinks), *ptrs,
+                                  float(softmax_scale), ws, workspace.numel() * workspace.element_size(), out_ptr, err,
+                                  _stream(stream))
+    if st:
+        _check("mla_prefill_window", st)
+
+
+def _cache(kv_pool, kv_scale, kr_pool, device: int):
+    """The leading arguments of a call that reads a cache of any of the three kinds."""
+    dtype = _kv_dtype(kv_pool, kv_scale, kr_pool)
+    for name, t in (("kv_pool", kv_pool), ("kv_scale", kv_scale), ("kr_pool", kr_pool)):
+        if t is not None:
+            _whole(t, name, t.dtype, tuple(t.shape), device)
+    return dtype, kv_pool.data_ptr(), _ptr(kv_scale), _ptr(kr_pool), int(kv_pool.shape[0])
+
+
+def _table_row(row, device: int):
+    if not isinstance(row, torch.Tensor) or row.dim() != 1:
+        raise ValueError("block_table_row must be a 1-d tensor")
+    return _whole(row, "block_table_row", torch.int32, tuple(row.shape), device), int(row.shape[0])
+
+
+class SharedPrefix:
+    """A prefix that the sequences of a batch share, decompressed once (``mla_prefix_open``, on the
+    current stream) and kept: keys ``k`` and values ``v`` [128 heads, tokens, 128] and rotary keys
+    ``k_r`` [tokens, 64], 66.7 KB for each token.  ``block_table_row`` lists the prefix's pages, whose
+    last may be partly filled.  For mla_prefix_attend, and for DecodeStep(prefix=...), whose sequences
+    are then the tokens behind the prefix.  Worth it from about 40 query rows on; fewer are faster
+    with block tables that list the shared pages themselves."""
+
+    def __init__(self, prefix_len: int, *, w_uk: torch.Tensor, w_uv: torch.Tensor, kv_pool: torch.Tensor,
+                 block_table_row: torch.Tensor, kv_scale: Optional[torch.Tensor] = None,
+                 kr_pool: Optional[torch.Tensor] = None, dev_error: Optional[torch.Tensor] = None):
+        device, bf16, P = torch._C._cuda_getDevice(), torch.bfloat16, int(prefix_len)
+        if P < 1:
+            raise ValueError(f"prefix_len: expected at least one token, got {P}")
+        weights = [_whole(t, name, bf16, (NUM_HEADS, D_HC, D_C), device) for t, name in ((w_uk, "w_uk"), (w_uv, "w_uv"))]
+        cache = _cache(kv_pool, kv_scale, kr_pool, device)
+        table, pages = _table_row(block_table_row, device)
+        where = dict(device=kv_pool.device)
+        err = torch.zeros(1, dtype=torch.int32, **where) if dev_error is None else dev_error
+        err_ptr = _whole(err, "dev_error", torch.int32, (1,), device)
+        if (P + PAGE - 1) // PAGE > pages:
+            raise ValueError(f"block_table_row holds {pages} pages, the prefix needs {(P + PAGE - 1) // PAGE}")
+        rows = torch.empty(P, D_ROW, dtype=bf16, **where)
+        k, v = (torch.empty(NUM_HEADS, P, D_HC, dtype=bf16, **where) for _ in range(2))
+        _check("mla_prefix_open", lib().mla_prefix_open(*cache, table, pages, P, *weights, rows.data_ptr(), k.data_ptr(),
+                                                        v.data_ptr(), err_ptr, _stream(None)))
+        self._set(k, v, rows[:, D_C:], err, device)
+
+    @classmethod
+    def of(cls, k: torch.Tensor, v: torch.Tensor, k_r: torch.Tensor, dev_error: Optional[torch.Tensor] = None):
+        """The prefix of keys and values that are there already (bf16; k_r's rows may be columns of wider
+        ones, in steps of 8).  The tensors are kept, not copied."""
+        device = torch._C._cuda_getDevice()
+        P = int(k.shape[1]) if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
+        if P < 1:
+            raise ValueError("k must be [128, tokens, 128] with at least one token")
+        for name, t in (("k", k), ("v", v)):
+            _whole(t, name, torch.bfloat16, (NUM_HEADS, P, D_HC), device)
+        _rows(k_r, "k_r", torch.bfloat16, (P, D_R), device)
+        self = cls.__new__(cls)
+        self._set(k, v, k_r, torch.zeros(1, dtype=torch.int32, device=k.device) if dev_error is None else dev_error, device)
+        return self
+
+    def _set(self, k, v, k_r, err, device: int) -> None:
+        self.k, self.v, self.k_r, self.dev_error, self.device_index = k, v, k_r, err, device
+        self.prefix_len = int(k.shape[1])
+        self._num_sms = num_sms(device)
+        # one token: any stride is that token's
+        stride = int(k_r.stride(0)) if self.prefix_len > 1 else D_R
+        self._args = (self.prefix_len, self._num_sms), (k.data_ptr(), v.data_ptr(), k_r.data_ptr(), stride)
+
+    def workspace_bytes(self, rows: int) -> int:
+        return int(lib().mla_prefix_attend_workspace_bytes(int(rows), self.prefix_len, self._num_sms))
+
+    def workspace(self, rows: int) -> torch.Tensor:
+        """A workspace for mla_prefix_attend with that many query rows."""
+        return torch.empty(max(16, self.workspace_bytes(rows)), dtype=torch.uint8, device=self.k.device)
+
+
+def mla_prefix_attend(prefix: SharedPrefix, q_c: torch.Tensor, q_r: torch.Tensor, out: torch.Tensor, *,
+                      lse: Optional[torch.Tensor] = None, own_out: Optional[torch.Tensor] = None,
+                      own_lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      dev_error: Optional[torch.Tensor] = None, softmax_scale: float = SOFTMAX_SCALE,
+                      stream=None) -> None:
+    """Attention of all query rows q_c [rows, 128, 128], q_r [rows, 128, 64] to the prefix, merged with
+    their attention over their own tokens (own_out [rows, 128, 128] and own_lse [rows, 128]; None: the
+    prefix alone) into out and lse, which may be own_out and own_lse themselves.  workspace: a tensor of
+    prefix.workspace_bytes(rows) bytes (allocated here when None)."""
+    device, bf16 = torch._C._cuda_getDevice(), torch.bfloat16
+    if not isinstance(q_c, torch.Tensor) or q_c.dim() != 3:
+        raise ValueError("q_c must be [rows, 128, 128]")
+    R = int(q_c.shape[0])
+    q_c_ptr = _whole(q_c, "q_c", bf16, (R, NUM_HEADS, D_HC), device)
+    q_r_ptr = _whole(q_r, "q_r", bf16, (R, NUM_HEADS, D_R), device)
+    out_ptr = _whole(out, "out", bf16, (R, NUM_HEADS, D_HC), device)
+    lse_ptr = None if lse is None else _whole(lse, "lse", torch.float32, (R, NUM_HEADS), device)
+    if (own_out is None) != (own_lse is None):
+        raise ValueError("own_out and own_lse: both or neither")
+    own_ptr = own_lse_ptr = None
+    if own_out is not None:
+        own_ptr = _whole(own_out, "own_out", bf16, (R, NUM_HEADS, D_HC), device)
+        own_lse_ptr = _whole(own_lse, "own_lse", torch.float32, (R, NUM_HEADS), device)
+    if prefix.device_index != device:
+        raise ValueError(f"prefix: must be on the current CUDA device ({device})")
+    if workspace is None:
+        workspace = prefix.workspace(R)
+    ws = _whole(workspace, "workspace", workspace.dtype, tuple(workspace.shape), device)
+    err = prefix.dev_error if dev_error is None else dev_error
+    sizes, keys = prefix._args
+    st = lib().mla_prefix_attend(R, *sizes, q_c_ptr, q_r_ptr, *keys, softmax_scale, own_ptr, own_lse_ptr, ws,
+                                 workspace.numel() * workspace.element_size(), out_ptr, lse_ptr,
+                                 _whole(err, "dev_error", torch.int32, (1,), device), _stream(stream))
+    if st:
+        _check("mla_prefix_attend", st)
 
 
 def mla_read_device_error(dev_error: torch.Tensor, stream=None) -> int:
@@ -802,7 +972,12 @@ class DecodeStep:
     w_uk and w_uv may be 4-bit weights (W4Weight): the absorb and the projection are then
     mla_absorb_q_w4 and mla_out_proj_w4 (not with the fused kernels, nor from host memory; faster
     than bf16 up to some 30 rows of the batch, slower beyond 64).  With
-    ``rope``, run_tokens takes the new tokens as their projections give them.
+    ``rope``, run_tokens takes the new tokens as their projections give them.  With ``window`` = W > 0
+    a token sees the last W tokens up to itself and the first ``sinks``; pages without such a token
+    are not read, and their table entries may hold anything.  With ``prefix`` the sequences begin
+    with that shared prefix: seq_lens, block_table and the cache's rows are those of their own tokens
+    behind it (at least one each; positions count the prefix), and the step ends with
+    mla_prefix_attend, which joins both parts in out and lse (o_lat is the own tokens' alone).
     """
 
     def __init__(self, seq_lens, *, w_uk, w_uv, kv_pool: torch.Tensor,
@@ -810,7 +985,10 @@ class DecodeStep:
                  kr_pool: Optional[torch.Tensor] = None, device=None, min_pages_per_split: int = 0,
                  max_clusters: int = 0, wait_timeout_ns: int = 0, item_cost_pages: int = 0,
                  softmax_scale: float = SOFTMAX_SCALE, fused_absorb: bool = False, fused_tail: bool = False,
-                 queries_per_seq: int = 1, rope: Optional[Rope] = None):
+                 queries_per_seq: int = 1, rope: Optional[Rope] = None, window: int = 0, sinks: int = 0,
+                 prefix: Optional[SharedPrefix] = None):
+        if prefix is not None and window:
+            raise ValueError("prefix: a shared prefix is seen whole, a window is not supported with it")
         if (fused_absorb and isinstance(w_uk, W4Weight)) or (fused_tail and isinstance(w_uv, W4Weight)):
             raise ValueError("4-bit weights: the fused kernels read bf16 weights")
         if rope is not None and rope.dim != D_R:
@@ -823,7 +1001,7 @@ class DecodeStep:
         self.batch = self.num_seqs * self.queries_per_seq
         self._plan_opts = dict(min_pages_per_split=min_pages_per_split, max_clusters=max_clusters,
                                wait_timeout_ns=wait_timeout_ns, item_cost_pages=item_cost_pages,
-                               queries_per_seq=self.queries_per_seq)
+                               queries_per_seq=self.queries_per_seq, window=int(window), sinks=int(sinks))
         self._num_sms = num_sms(self.device)
         self.plan_host, self.info = mla_plan_splits(self.seq_lens, self._num_sms, **self._plan_opts)
         self.plan_dev = torch.from_numpy(self.plan_host).to(self.device)
@@ -846,6 +1024,8 @@ class DecodeStep:
         if rope is not None:  # the split and rotated queries of run_tokens
             self.q_c = torch.empty(B, NUM_HEADS, D_HC, dtype=torch.bfloat16, device=self.device)
             self.q_r = torch.empty(B, NUM_HEADS, D_R, dtype=torch.bfloat16, device=self.device)
+        self.prefix = prefix
+        self.prefix_workspace = None if prefix is None else prefix.workspace(B)
         self._h_stage = self._d_stage = None  # pinned host / device staging of run_host
         self._host_graph = None  # (mla_step_graph handle, key of the buffers and lengths it was made for)
 
@@ -866,6 +1046,10 @@ class DecodeStep:
             mla_combine_splits(self.info, self.plan_dev, self.workspace, self.o_lat, self.lse, stream)
             project = mla_out_proj_w4 if isinstance(self.w_uv, W4Weight) else mla_out_proj
             project(self.o_lat, self.w_uv, self.out, stream)
+        if self.prefix is not None:
+            mla_prefix_attend(self.prefix, q_c, q_r, self.out, lse=self.lse, own_out=self.out, own_lse=self.lse,
+                              workspace=self.prefix_workspace, dev_error=self.dev_error,
+                              softmax_scale=self.softmax_scale, stream=stream)
         return self.out
 
     def run_tokens(self, q: torch.Tensor, c_kv: torch.Tensor, k_r: torch.Tensor, positions: torch.Tensor,
@@ -918,6 +1102,8 @@ class DecodeStep:
         the copies and kernels only.  Otherwise each call is one ``mla_decode_step_host``."""
         if isinstance(self.w_uk, W4Weight) or isinstance(self.w_uv, W4Weight):
             raise ValueError("run_host: the step from host memory reads bf16 weights")
+        if self.prefix is not None:
+            raise ValueError("run_host: the step from host memory takes no shared prefix")
         lens = self.seq_lens if seq_lens is None else np.ascontiguousarray(np.asarray(seq_lens, dtype=np.int32))
         if self._host_graph is not None and out is not None:
             if self._host_key(q_c, q_r, block_table, lens, out) == self._host_graph[1]:
@@ -975,7 +1161,7 @@ class DecodeStep:
                            self._h_stage.numel() * 4)
         opts = PlanOptions(int(self._plan_opts["min_pages_per_split"]), int(self._plan_opts["max_clusters"]),
                            int(self._plan_opts["wait_timeout_ns"]), int(self._plan_opts["item_cost_pages"]),
-                           self.queries_per_seq)
+                           self.queries_per_seq, int(self._plan_opts["window"]), int(self._plan_opts["sinks"]))
         info = PlanInfo()
         args = (lens.ctypes.data_as(ctypes.c_void_p), self.num_seqs, self._num_sms, ctypes.byref(opts), _ptr(q_c), _ptr(q_r),
                 _ptr(block_table), int(bt_dev.shape[1]), _ptr(self.w_uk), _ptr(self.w_uv), dtype, _ptr(self.kv_pool),
@@ -1027,6 +1213,7 @@ class DecodeStep:
         # the absorb runs inside the bf16 decode kernel when fused (a kernel of its own with the e4m3
         # cache); the merge is skipped when no sequence is split
         n = 1 if (self.fused_absorb and self.kv_scale is None) else 2
+        n += 2 if self.prefix is not None else 0
         if self.fused_tail:
             return n + 1
         return n + 1 + (1 if self.info.num_combine > 0 else 0)

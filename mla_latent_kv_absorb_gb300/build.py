@@ -31,7 +31,7 @@ def _nvcc() -> str:
 
 def _sources():
     return [os.path.join(CSRC, f) for f in ("api.cu", "static_ws.cu", "append.cu", "gather.cu", "rope.cu", "w4.cu",
-                                           "plan.cpp")]
+                                           "attend.cu", "plan.cpp")]
 
 
 def _deps():

@@ -161,10 +161,22 @@ mla_status launch_head_gemm(const void* act, const void* weight, void* out, int3
     return launch_status();
 }
 
+// The decode kernels, for plans with and without a window.
+auto decode_bf16(bool window)
+{
+    return window ? mla::decode::decode_bf16_kernel<true> : mla::decode::decode_bf16_kernel<false>;
+}
+
+auto decode_fp8(bool window)
+{
+    return window ? mla::decode_fp8::decode_fp8_kernel<true> : mla::decode_fp8::decode_fp8_kernel<false>;
+}
+
 bool plan_header_ok(const mla_plan_info* info)
 {
     return info && info->batch > 0 && info->num_clusters > 0 && info->num_items > 0 && info->num_partials >= 0 &&
-           info->num_combine >= 0 && info->plan_bytes > 0 && info->workspace_bytes >= 0 && info->wait_timeout_ns > 0;
+           info->num_combine >= 0 && info->plan_bytes > 0 && info->workspace_bytes >= 0 && info->wait_timeout_ns > 0 &&
+           info->window >= 0 && info->sinks >= 0;
 }
 
 __global__ void wait_timeout_kernel(uint32_t* dev_error, uint64_t timeout_ns)
@@ -243,6 +255,7 @@ mla_status launch_decode_fp8(const mla_plan_info* info, const void* plan_dev, co
                          : nullptr;
     p.dev_error = dev_error;
     p.timeout_ns = (uint64_t)info->wait_timeout_ns;
+    p.sinks = info->sinks;
     p.kv_scale = kv_scale;
 #ifdef MLA_DECODE_TRACE
     p.trace = g_trace;
@@ -250,8 +263,9 @@ mla_status launch_decode_fp8(const mla_plan_info* info, const void* plan_dev, co
     p.trace = nullptr;
 #endif
 
-    if (!set_smem(mla::decode_fp8::decode_fp8_kernel, mla::decode_fp8::kSmemBytes)) return MLA_ERR_CUDA;
-    return launch_pdl(mla::decode_fp8::decode_fp8_kernel, dim3(2 * info->num_clusters), dim3(mla::decode_fp8::kThreads),
+    const auto kernel = decode_fp8(info->window > 0);
+    if (!set_smem(kernel, mla::decode_fp8::kSmemBytes)) return MLA_ERR_CUDA;
+    return launch_pdl(kernel, dim3(2 * info->num_clusters), dim3(mla::decode_fp8::kThreads),
                       mla::decode_fp8::kSmemBytes, static_cast<cudaStream_t>(stream), tm_c8, tm_kr, tm_q, p);
 }
 
@@ -335,15 +349,17 @@ mla_status launch_decode_bf16(const mla_plan_info* info, const void* plan_dev, c
                          : nullptr;
     p.dev_error = dev_error;
     p.timeout_ns = (uint64_t)info->wait_timeout_ns;
+    p.sinks = info->sinks;
 #ifdef MLA_DECODE_TRACE
     p.trace = g_trace;
 #else
     p.trace = nullptr;
 #endif
 
-    if (!set_smem(mla::decode::decode_bf16_kernel, mla::decode::kSmemBytes)) return MLA_ERR_CUDA;
+    const auto kernel = decode_bf16(info->window > 0);
+    if (!set_smem(kernel, mla::decode::kSmemBytes)) return MLA_ERR_CUDA;
     if (!fused)
-        return launch_pdl(mla::decode::decode_bf16_kernel, dim3(2 * info->num_clusters), dim3(mla::decode::kThreads),
+        return launch_pdl(kernel, dim3(2 * info->num_clusters), dim3(mla::decode::kThreads),
                           mla::decode::kSmemBytes, static_cast<cudaStream_t>(stream), tm_pool, tm_q, tm_qc, tm_wuk, p);
     // enough CTA pairs that no CTA takes more than one absorb job while one fits per SM, and
     // never fewer than the plan's (pairs past the plan's only run absorb jobs)
@@ -352,7 +368,7 @@ mla_status launch_decode_bf16(const mla_plan_info* info, const void* plan_dev, c
         record_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "cudaDeviceGetAttribute") != MLA_OK)
         return MLA_ERR_CUDA;
     const int clusters = std::max(info->num_clusters, std::min(sms / 2, (p.absorb_jobs + 1) / 2));
-    mla::decode::decode_bf16_kernel<<<dim3(2 * clusters), dim3(mla::decode::kThreads), mla::decode::kSmemBytes,
+    kernel<<<dim3(2 * clusters), dim3(mla::decode::kThreads), mla::decode::kSmemBytes,
                                       static_cast<cudaStream_t>(stream)>>>(tm_pool, tm_q, tm_qc, tm_wuk, p);
     return launch_status();
 }
@@ -479,7 +495,15 @@ namespace mla {
 // gather.cu: one sequence's cache rows into contiguous bf16 rows [seq_len][576]
 mla_status gather_one_sequence(mla_kv_dtype kv_dtype, const void* kv_pool, const float* kv_scale, const void* kr_pool,
                                int32_t num_pool_pages, const int32_t* block_table_row, int32_t max_pages,
-                               int32_t seq_len, void* out, uint32_t* dev_error, void* stream);
+                               int32_t seq_len, void* out, uint32_t* dev_error, void* stream, int32_t skip_from = 0,
+                               int32_t skip = 0);
+
+// Per-head keys or values of gathered rows [num_rows][576]: out[h][i][:] = w[h] rows[i][0..512), the
+// out-proj GEMM's shape with one activation row for all heads, head-major.
+mla_status decompress_heads(const void* rows, const void* w, void* out, int32_t num_rows, void* stream)
+{
+    return launch_head_gemm<512, kOutN, false, kOutStages>(rows, w, out, num_rows, 128, kOutN, false, stream, 576, true);
+}
 }  // namespace mla
 
 namespace {
@@ -678,15 +702,15 @@ bool pinned_host(const void* p)
 
 // Loads the step's kernels (and sets their shared-memory limits) outside any stream capture, so
 // that module loading never happens while a graph is being captured.
-mla_status step_load_kernels(mla_kv_dtype kv_dtype)
+mla_status step_load_kernels(mla_kv_dtype kv_dtype, bool window)
 {
     using AbsK = decltype(&mla::gemm::head_gemm_kernel<128, kAbsorbN, true, kAbsorbStages>);
     const AbsK absorb = mla::gemm::head_gemm_kernel<128, kAbsorbN, true, kAbsorbStages>;
     const AbsK outp = mla::gemm::head_gemm_kernel<512, kOutN, false, kOutStages>;
     if (!set_smem(absorb, AbsorbCfg::kSmemBytes) || !set_smem(outp, OutCfg::kSmemBytes)) return MLA_ERR_CUDA;
     const bool dec_ok = kv_dtype == MLA_KV_FP8_E4M3
-                            ? set_smem(mla::decode_fp8::decode_fp8_kernel, mla::decode_fp8::kSmemBytes)
-                            : set_smem(mla::decode::decode_bf16_kernel, mla::decode::kSmemBytes);
+                            ? set_smem(decode_fp8(window), mla::decode_fp8::kSmemBytes)
+                            : set_smem(decode_bf16(window), mla::decode::kSmemBytes);
     if (!dec_ok) return MLA_ERR_CUDA;
     cudaFuncAttributes fa;
     return record_cuda(cudaFuncGetAttributes(&fa, mla::combine::combine_kernel), "cudaFuncGetAttributes(combine)");
@@ -748,7 +772,7 @@ extern "C" mla_status mla_step_graph_create(const int32_t* seq_lens, int32_t bat
     if (!pinned_host(q_c_host) || !pinned_host(q_r_host) || !pinned_host(out_host) ||
         (block_table_host && !pinned_host(block_table_host)))
         return MLA_ERR_INVALID_ARG;
-    if ((st = step_load_kernels(kv_dtype)) != MLA_OK) return st;
+    if ((st = step_load_kernels(kv_dtype, info.window > 0)) != MLA_OK) return st;
     int dev = 0;
     if (record_cuda(cudaGetDevice(&dev), "cudaGetDevice") != MLA_OK) return MLA_ERR_CUDA;
     // the plan goes to the device once, outside the graph

@@ -1,0 +1,614 @@
+// attend.cuh -- attention of many query rows over decompressed keys and values, in two forms:
+//
+//   prefix  the rows of a whole decode batch attend to the one prefix that their sequences share
+//           (every row sees every key); the result is a set of normalised partial outputs with
+//           their log-sum-exps, which prefix_merge_kernel joins with each row's attention over its
+//           sequence's own tokens;
+//   chunk   the new tokens of one sequence under a sliding window: the query at position p sees the
+//           keys j <= p with j > p - window or j < sinks.
+//
+// Keys and values are per head (page 1 section 4, path A): k, v [128 heads][keys][128] and k_R
+// [keys][64], so a (row, key) pair costs 2 * (192 + 128) * 128 FLOP where the absorbed form costs
+// 2 * (576 + 512) * 128, and 64 KB of keys and values are read for each prefix token however many
+// rows there are: with up to about 110 rows that is what bounds the prefix form (HBM), beyond it
+// the tensor cores.
+//
+// One CTA holds one or two 128-row query tiles of a head (kQT) and streams 128-key tiles.  It works
+// on two "streams", each with a score buffer S, an output O and a running softmax (m, l) of its own:
+// with two query tiles a stream is a tile, and both use every key tile; with one query tile the even
+// key tiles are one stream and the odd ones the other, and the two are joined at the end, so that one
+// stream's softmax always has the other's products to hide behind and neither waits for the other's
+// running maximum.  Step i belongs to stream i & 1; the MMA order is PV(i), QK(i + 2).
+//   QK:  S[128 x 128] = Q [128 x 192] (q_c | q_R: three 64-column chunks in shared memory)
+//                       x K tile [128 x 192] (k | k_R: three K-major chunks)
+//   PV:  O[128 x 128] += P [128 x 128] (bf16 in TMEM over the first half of S) x V tile (MN-major)
+// Everything that is streamed goes through one ring of 16 KB slots, in the order in which the MMAs
+// first need it: a key chunk [128 keys][64] or 64 keys' values [64][128].  A slot is four MMAs, so
+// the ring is as fine as the tensor core's work and a slot is free as soon as its four are done.
+//
+// Warp 0 streams the ring, warp 2 the query tiles, warp 1 issues the MMAs, warps 3-6 and 7-10 are
+// the streams' softmax, one row per thread, the row's 128 scores in registers.  The running maximum
+// moves only when a tile's exceeds it by more than 8 (log2 units).  P is rounded to bf16 for the
+// PV product (its sum l takes the unrounded values); scores, maxima, sums and O are fp32.
+//
+// The prefix form is persistent: the (head, row group, key tile) units lie in one line that the CTAs
+// cut evenly, so that every SM streams the same number of bytes; a CTA's piece of one (head, group)
+// run is a segment, written as one partial.  Every wait is bounded.
+#pragma once
+#include "ptx.cuh"
+
+namespace mla {
+namespace attend {
+
+constexpr int kTile = 128;                 // query rows of a tile, keys of a tile
+constexpr int kThreads = 32 * 11;
+constexpr int kSoftmaxWarp0 = 3;
+constexpr int kSlotBytes = 16384;
+constexpr uint32_t kTmemCols = 512;        // stream t: S at 256 t, O at 256 t + 128
+constexpr float kRescaleLog2 = 8.f;
+constexpr uint32_t kJoinBarrier = 1;       // named barrier of the eight softmax warps
+
+template <int kQT>
+struct Layout {
+    static constexpr int kSlots = kQT == 1 ? 11 : 8;
+    static constexpr int kOffRing = kQT * 3 * kSlotBytes;
+    static constexpr int kOffXchg = kOffRing + kSlots * kSlotBytes;  // m and l of both streams
+    static constexpr int kOffBar = kOffXchg + 2 * 2 * kTile * 4;
+    static constexpr int kBarFull = 0, kBarEmpty = kSlots;
+    static constexpr int kBarQFull = 2 * kSlots, kBarQEmpty = kBarQFull + 1;
+    static constexpr int kBarSFull = kBarQFull + 2;   // [stream]
+    static constexpr int kBarPReady = kBarSFull + 2;  // [stream], 128 arrivals
+    static constexpr int kBarODone = kBarPReady + 2;  // the segment's last PV has finished
+    static constexpr int kBarOFree = kBarODone + 1;   // 256 arrivals: the segment's O has been read
+    static constexpr int kBarEnd = kBarOFree + 1;     // every MMA of the CTA has finished
+    static constexpr int kBars = kBarEnd + 1;
+    static constexpr int kSmemBytes = kOffBar + 8 * kBars + 16;
+    static_assert(kSmemBytes <= 232448, "a CTA's shared memory");
+};
+// Phase bookkeeping.  A barrier waited by parity must never run two phases ahead of its waiter:
+//   S full [t]   completes once per step of stream t; QK(i + 2) is issued only after the MMA thread
+//                has seen P(i) ready, i.e. after the stream's softmax has finished step i.
+//   P ready [t]  arrives once per step; P(i + 2) needs S(i + 2), issued after that wait.
+//   Q full       one query load per segment, issued after Q empty (the segment's last QK committed).
+//   O done       once per segment; the next one's needs its first PV, which waits for O free, for
+//                which every softmax thread has to have waited for O done.
+//   ring         a slot is refilled only after its empty barrier, waited in order.
+
+struct Params {
+    int rows;            // query rows
+    int keys;            // key rows
+    float scale_log2;    // softmax_scale * log2(e)
+    int groups;          // row groups of kQT tiles
+    uint32_t* dev_error;
+    uint64_t timeout_ns;
+    // prefix
+    int tiles;           // key tiles of a run
+    int rows_cap;        // rows of a partial
+    float* ws_o;         // [slots][rows_cap][128]
+    float* ws_lse;       // [slots][rows_cap]
+    // chunk: query i sees the (compacted) keys c <= hi0 + i with c > hi0 + i - window or c < sinks
+    int hi0, window, sinks;
+    __nv_bfloat16* out;  // [rows][128][128]
+};
+
+// A CTA's piece of one run.
+struct Segment {
+    int head, row0, cnt;  // cnt key tiles
+    int lead, tile0;      // key tile n: n < lead ? n : tile0 + n
+    int slot;             // the prefix's partial
+};
+
+// The first unit of CTA c, of `units` in all shared by g <= units CTAs (each has one at least).
+__host__ __device__ __forceinline__ int64_t first_unit(int64_t c, int64_t units, int64_t g) { return c * units / g; }
+
+// Walks this CTA's segments; every role walks the same ones.
+template <bool kChunk, int kQT>
+struct Walk {
+    int64_t at, end;
+    __device__ __forceinline__ explicit Walk(const Params& p)
+    {
+        if (kChunk) {
+            at = blockIdx.x;
+            end = (int64_t)p.groups * 128;
+        } else {
+            const int64_t units = (int64_t)p.groups * 128 * p.tiles;
+            at = first_unit(blockIdx.x, units, gridDim.x);
+            end = first_unit(blockIdx.x + 1, units, gridDim.x);
+        }
+    }
+    __device__ __forceinline__ bool next(const Params& p, Segment& s)
+    {
+        if (at >= end) return false;
+        if (kChunk) {
+            // a head's groups lie side by side: their windows overlap and are read from L2
+            s.head = (int)(at / p.groups);
+            s.row0 = (int)(at % p.groups) * kQT * kTile;
+            const int last = min(s.row0 + kQT * kTile, p.rows) - 1;
+            const int lo = max(0, p.hi0 + s.row0 - p.window + 1);  // the first key in the first row's window
+            s.lead = (min(p.sinks, lo) + kTile - 1) / kTile;
+            const int first = max(s.lead, lo / kTile);
+            s.tile0 = first - s.lead;
+            s.cnt = s.lead + (p.hi0 + last) / kTile + 1 - first;
+            s.slot = 0;
+            at += gridDim.x;
+        } else {
+            const int run = (int)(at / p.tiles), n0 = (int)(at - (int64_t)run * p.tiles);
+            s.head = run / p.groups;
+            s.row0 = (run % p.groups) * kQT * kTile;
+            s.cnt = (int)min((int64_t)(p.tiles - n0), end - at);
+            s.lead = 0;
+            s.tile0 = n0;
+            s.slot = (int)blockIdx.x + run;
+            at += s.cnt;
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ int key_tile(const Segment& s, int n) { return n < s.lead ? n : s.tile0 + n; }
+
+template <bool kChunk, int kQT>
+// 11 warps: three SM sub-partitions hold three of them, 16K registers each: at most 3 x 32 x 168
+__global__ void __maxnreg__(168)
+attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__ CUtensorMap tm_qr,
+              const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
+              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p)
+{
+    using namespace dev;
+    using L = Layout<kQT>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bars = sbase + L::kOffBar;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 8 * L::kBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    const auto bar = [&](int id) { return bars + 8 * id; };
+
+    if (sbase & 1023u) {
+        if (threadIdx.x == 0) raise_error(p.dev_error, MLA_DEVERR_SMEM_ALIGN);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2 * L::kSlots; ++s) mbar_init(bar(s), 1);
+        mbar_init(bar(L::kBarQFull), 1);
+        mbar_init(bar(L::kBarQEmpty), 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(bar(L::kBarSFull + t), 1);
+            mbar_init(bar(L::kBarPReady + t), 128);
+        }
+        mbar_init(bar(L::kBarODone), 1);
+        mbar_init(bar(L::kBarOFree), 256);
+        mbar_init(bar(L::kBarEnd), 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_holder), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const WaitCtx w{p.timeout_ns, abort_flag, p.dev_error};
+    Walk<kChunk, kQT> walk(p);
+    Segment seg;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_k);
+            tma_prefetch_desc(&tm_kr);
+            tma_prefetch_desc(&tm_v);
+            // the prefix's keys and values are read once by one group of rows, k_R by every head
+            const uint64_t pol_kv = kChunk || p.groups > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+            const uint64_t pol_kr = l2_policy_evict_last();
+            int r = 0, s = 0, phase = 0;
+            bool ok = true;
+            const auto take = [&]() {  // the next slot, free; its full barrier expects a slot's bytes
+                if (r >= L::kSlots && !wait_phase(bar(L::kBarEmpty + s), phase - 1, w)) return ok = false;
+                mbar_arrive_expect_tx(bar(L::kBarFull + s), kSlotBytes);
+                return true;
+            };
+            const auto put = [&]() {
+                ++r;
+                if (++s == L::kSlots) {
+                    s = 0;
+                    ++phase;
+                }
+            };
+            const auto load_k = [&](int j0) {
+#pragma unroll 1
+                for (int c = 0; c < 3; ++c) {
+                    if (!take()) return;
+                    const uint32_t dst = sbase + L::kOffRing + s * kSlotBytes;
+                    if (c < 2)
+                        tma_load_3d(dst, &tm_k, bar(L::kBarFull + s), 64 * c, j0, seg.head, pol_kv);
+                    else
+                        tma_load_2d(dst, &tm_kr, bar(L::kBarFull + s), 0, j0, pol_kr);
+                    put();
+                }
+            };
+            const auto load_v = [&](int j0) {
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    if (!take()) return;
+                    const uint32_t dst = sbase + L::kOffRing + s * kSlotBytes;
+                    tma_load_3d(dst, &tm_v, bar(L::kBarFull + s), 0, j0 + 64 * c, seg.head, pol_kv);
+                    tma_load_3d(dst + kSlotBytes / 2, &tm_v, bar(L::kBarFull + s), 64, j0 + 64 * c, seg.head, pol_kv);
+                    put();
+                }
+            };
+            while (ok && walk.next(p, seg)) {
+                constexpr int kAhead = kQT == 1 ? 2 : 1;  // key tiles ahead of the values
+                for (int n = 0; ok && n < kAhead && n < seg.cnt; ++n) load_k(key_tile(seg, n) * kTile);
+                for (int n = 0; ok && n < seg.cnt; ++n) {
+                    load_v(key_tile(seg, n) * kTile);
+                    if (ok && n + kAhead < seg.cnt) load_k(key_tile(seg, n + kAhead) * kTile);
+                }
+            }
+            // loads in flight land before the CTA can exit
+            for (int k = r > L::kSlots ? r - L::kSlots : 0; k < r; ++k)
+                drain_phase(bar(L::kBarFull + k % L::kSlots), k / L::kSlots, w.timeout_ns);
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_qc);
+            tma_prefetch_desc(&tm_qr);
+            const uint64_t pol = l2_policy_evict_last();
+            int n = 0;
+            while (walk.next(p, seg)) {
+                if (n > 0 && !wait_phase(bar(L::kBarQEmpty), n - 1, w)) break;
+                mbar_arrive_expect_tx(bar(L::kBarQFull), kQT * 3 * kSlotBytes);
+                for (int t = 0; t < kQT; ++t) {
+                    const uint32_t q = sbase + t * 3 * kSlotBytes;
+                    const int row = seg.row0 + kTile * t;
+                    tma_load_3d(q, &tm_qc, bar(L::kBarQFull), 0, seg.head, row, pol);
+                    tma_load_3d(q + kSlotBytes, &tm_qc, bar(L::kBarQFull), 64, seg.head, row, pol);
+                    tma_load_3d(q + 2 * kSlotBytes, &tm_qr, bar(L::kBarQFull), 0, seg.head, row, pol);
+                }
+                ++n;
+            }
+            if (n > 0) drain_phase(bar(L::kBarQFull), n - 1, w.timeout_ns);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc_qk = idesc_bf16(128, kTile, false, false);
+            constexpr uint32_t idesc_pv = idesc_bf16(128, 128, false, true);
+            const uint64_t q_desc = smem_desc(sbase, 16, 1024);
+            const uint64_t k_desc = smem_desc(sbase + L::kOffRing, 16, 1024);
+            const uint64_t v_desc = smem_desc(sbase + L::kOffRing, kSlotBytes / 2, 1024);
+            constexpr uint64_t kSlot16 = kSlotBytes >> 4;  // a slot, in the descriptors' 16-byte units
+            int s = 0, phase = 0;  // the next slot that no MMA has used yet
+            bool ok = true;
+            // Scores of stream t from the three slots at `s0`: waits for them when they are new, frees them
+            // when this is their last use.
+            const auto qk = [&](int t, int& s0, int& ph, bool fresh, bool last) {
+                const uint32_t d = tmem + 256 * t;
+                const uint64_t a0 = q_desc + (kQT == 2 ? t * 3 * kSlot16 : 0);
+#pragma unroll 1
+                for (int c = 0; c < 3; ++c) {
+                    if (fresh && !wait_phase(bar(L::kBarFull + s0), ph, w)) return ok = false;
+                    tc_fence_after();
+                    const uint64_t a = a0 + c * kSlot16, b = k_desc + s0 * kSlot16;
+                    mma_ss(d, a, b, idesc_qk, c != 0 ? 1u : 0u);
+                    mma_ss(d, a + 2, b + 2, idesc_qk, 1u);
+                    mma_ss(d, a + 4, b + 4, idesc_qk, 1u);
+                    mma_ss(d, a + 6, b + 6, idesc_qk, 1u);
+                    if (last) mma_commit(bar(L::kBarEmpty + s0));
+                    if (++s0 == L::kSlots) {
+                        s0 = 0;
+                        ++ph;
+                    }
+                }
+                mma_commit(bar(L::kBarSFull + t));
+                return true;
+            };
+            const auto pv = [&](int t, int& s0, int& ph, bool fresh, bool last, bool first_of_stream) {
+                const uint32_t pt = tmem + 256 * t, d = pt + 128;
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    if (fresh && !wait_phase(bar(L::kBarFull + s0), ph, w)) return ok = false;
+                    tc_fence_after();
+                    const uint64_t b = v_desc + s0 * kSlot16;
+                    const uint32_t a = pt + 32 * c;
+                    mma_ts(d, a, b, idesc_pv, first_of_stream && c == 0 ? 0u : 1u);
+                    mma_ts(d, a + 8, b + (2048 >> 4), idesc_pv, 1u);
+                    mma_ts(d, a + 16, b + (4096 >> 4), idesc_pv, 1u);
+                    mma_ts(d, a + 24, b + (6144 >> 4), idesc_pv, 1u);
+                    if (last) mma_commit(bar(L::kBarEmpty + s0));
+                    if (++s0 == L::kSlots) {
+                        s0 = 0;
+                        ++ph;
+                    }
+                }
+                return true;
+            };
+            int n_seg = 0;
+            int done[2] = {0, 0};  // steps of each stream
+            while (ok && walk.next(p, seg)) {
+                if (!(ok = wait_phase(bar(L::kBarQFull), n_seg, w))) break;
+                tc_fence_after();
+                const int steps = kQT == 1 ? seg.cnt : 2 * seg.cnt;
+                if (kQT == 1) {
+                    qk(0, s, phase, true, true);
+                    if (ok && steps > 1) qk(1, s, phase, true, true);
+                } else {
+                    int s1 = s, ph1 = phase;
+                    qk(0, s1, ph1, true, false);
+                    if (ok) qk(1, s, phase, false, true);
+                }
+                if (!ok) break;
+                if (steps <= 2) mma_commit(bar(L::kBarQEmpty));
+                int sv = 0, pv_ph = 0, sk = 0, pk_ph = 0;  // kQT == 2: the slots of stream 0's values and keys
+                for (int i = 0; i < steps; ++i) {
+                    const int t = i & 1;
+                    if (!(ok = wait_phase(bar(L::kBarPReady + t), done[t], w))) break;
+                    ++done[t];
+                    tc_fence_after();
+                    if (i == 0 && n_seg > 0) {
+                        if (!(ok = wait_phase(bar(L::kBarOFree), n_seg - 1, w))) break;
+                        tc_fence_after();
+                    }
+                    if (kQT == 1) {
+                        if (!pv(t, s, phase, true, true, i < 2)) break;
+                        if (i + 2 < steps && !qk(t, s, phase, true, true)) break;
+                    } else if (t == 0) {
+                        sv = s;
+                        pv_ph = phase;
+                        if (!pv(0, s, phase, true, false, i < 2)) break;
+                        sk = s;
+                        pk_ph = phase;
+                        if (i + 2 < steps && !qk(0, s, phase, true, false)) break;
+                    } else {
+                        if (!pv(1, sv, pv_ph, false, true, i < 2)) break;
+                        if (i + 2 < steps && !qk(1, sk, pk_ph, false, true)) break;
+                    }
+                    if (i + 3 == steps) mma_commit(bar(L::kBarQEmpty));  // the segment's last QK
+                }
+                if (!ok) break;
+                mma_commit(bar(L::kBarODone));
+                ++n_seg;
+            }
+            mma_commit(bar(L::kBarEnd));  // arrives when every MMA issued here has finished
+        }
+    } else {
+        // softmax of stream t: warp (3..10) & 3 selects the TMEM lane quarter, one row per thread
+        const int t = (warp - kSoftmaxWarp0) >> 2;
+        const int q4 = warp & 3, row = 32 * q4 + lane;
+        const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
+        const uint32_t t_s = tmem + lane_base + 256 * t, t_o = t_s + 128;
+        float* xchg = reinterpret_cast<float*>(smem + L::kOffXchg);  // [stream][m, l][128]
+        int n_seg = 0, n_step = 0;
+        bool ok = true;
+        while (ok && walk.next(p, seg)) {
+            const int tile_row = seg.row0 + (kQT == 2 ? kTile * t : 0);
+            const int i = tile_row + row;                                 // this thread's query row
+            const bool any_row = tile_row + 32 * q4 < p.rows;             // the warp has a row at all
+            const int hi = p.hi0 + min(i, p.rows - 1), lo = hi - p.window + 1;  // chunk: the row's window
+            const int mine = kQT == 1 ? (seg.cnt + 1 - t) >> 1 : seg.cnt;
+            float m = -INFINITY, l = 0.f;
+            for (int k = 0; k < mine; ++k, ++n_step) {
+                if (!(ok = wait_warp(bar(L::kBarSFull + t), n_step, w))) break;
+                tc_fence_after();
+                if (any_row) {
+                    const int j0 = key_tile(seg, kQT == 1 ? 2 * k + t : k) * kTile;
+                    uint32_t sr[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, sr[c]);
+                    tmem_wait_ld();
+                    // keys that the row does not see get -infinity
+                    if (kChunk) {
+                        const bool whole = j0 + kTile - 1 <= hi && (j0 >= lo || j0 + kTile <= p.sinks);
+                        if (__any_sync(0xffffffffu, !whole)) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) {
+                                    const int j = j0 + 32 * c + x;
+                                    if (j > hi || (j < lo && j >= p.sinks)) sr[c][x] = 0xff800000u;
+                                }
+                        }
+                    } else if (j0 + kTile > p.keys) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                if (j0 + 32 * c + x >= p.keys) sr[c][x] = 0xff800000u;
+                    }
+                    float m4[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        m4[c] = __uint_as_float(sr[c][0]);
+#pragma unroll
+                        for (int x = 1; x < 32; ++x) m4[c] = fmaxf(m4[c], __uint_as_float(sr[c][x]));
+                    }
+                    const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+                    // The running maximum: set by the stream's first tile, moved later only by more than the
+                    // threshold.  While a row has seen no key it stays at -infinity and f is 0 times 0.
+                    const bool grow = mt > m + kRescaleLog2 || m == -INFINITY;
+                    const float f = grow && m != -INFINITY ? ex2_approx(m - mt) : 1.f;
+                    if (grow) m = mt;
+                    if (k > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                        // O's earlier PVs have finished: S(i) complete implies it (QK(i) was issued after
+                        // PV(i - 2), and a commit covers every earlier MMA of the thread)
+#pragma unroll 1
+                        for (int c = 0; c < 8; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(t_o + 16 * c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                            tmem_st16(t_o + 16 * c, o);
+                        }
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const float a = ex2_approx(fmaf(__uint_as_float(sr[c][2 * x]), p.scale_log2, -base));
+                            const float b = ex2_approx(fmaf(__uint_as_float(sr[c][2 * x + 1]), p.scale_log2, -base));
+                            sum[(2 * x) & 3] += a;
+                            sum[(2 * x + 1) & 3] += b;
+                            pk[x] = pack_bf16x2(a, b);
+                        }
+                        tmem_st16(t_s + 16 * c, pk);
+                    }
+                    l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(bar(L::kBarPReady + t));
+            }
+            ok = ok && wait_warp(bar(L::kBarODone), n_seg, w);
+            tc_fence_after();
+            if (kQT == 2) {
+                if (!ok) break;
+                if (any_row) {
+                    const float inv = 1.f / l;
+                    const bool real = i < p.rows;
+                    float* part = kChunk ? nullptr : p.ws_o + ((int64_t)seg.slot * p.rows_cap + (i - seg.row0)) * 128;
+                    __nv_bfloat16* dst = kChunk ? p.out + ((int64_t)i * 128 + seg.head) * 128 : nullptr;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(t_o + 32 * c, o);
+                        tmem_wait_ld();
+                        if (!real) continue;
+#pragma unroll
+                        for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * inv);
+                        if (kChunk) {
+#pragma unroll
+                            for (int v = 0; v < 4; ++v)
+                                reinterpret_cast<uint4*>(dst + 32 * c)[v] = make_uint4(
+                                    pack_bf16x2(__uint_as_float(o[8 * v + 0]), __uint_as_float(o[8 * v + 1])),
+                                    pack_bf16x2(__uint_as_float(o[8 * v + 2]), __uint_as_float(o[8 * v + 3])),
+                                    pack_bf16x2(__uint_as_float(o[8 * v + 4]), __uint_as_float(o[8 * v + 5])),
+                                    pack_bf16x2(__uint_as_float(o[8 * v + 6]), __uint_as_float(o[8 * v + 7])));
+                        } else {
+#pragma unroll
+                            for (int v = 0; v < 8; ++v)
+                                reinterpret_cast<uint4*>(part + 32 * c)[v] =
+                                    make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                        }
+                    }
+                    if (!kChunk && real)
+                        p.ws_lse[(int64_t)seg.slot * p.rows_cap + (i - seg.row0)] = (m + log2f(l)) * 0.69314718055994531f;
+                }
+            } else {
+                // join the two streams: each four warps write half of the columns
+                xchg[(2 * t) * kTile + row] = m;
+                xchg[(2 * t + 1) * kTile + row] = l;
+                if (named_barrier_or(kJoinBarrier, 256, !ok || *w.abort)) break;
+                if (any_row) {
+                    const bool two = seg.cnt > 1;  // else stream 1 had no tile and its O holds nothing
+                    const float m0 = xchg[row], l0 = xchg[kTile + row], m1 = xchg[2 * kTile + row],
+                                l1 = xchg[3 * kTile + row];
+                    const float top = two ? fmaxf(m0, m1) : m0;
+                    float f0 = ex2_approx(m0 - top), f1 = two ? ex2_approx(m1 - top) : 0.f;
+                    const float total = l0 * f0 + (two ? l1 * f1 : 0.f);
+                    f0 /= total;
+                    f1 /= total;
+                    const bool real = i < p.rows;
+                    float* part = p.ws_o + ((int64_t)seg.slot * p.rows_cap + (i - seg.row0)) * 128 + 64 * t;
+                    const uint32_t o_col = tmem + lane_base + 128 + 64 * t;
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t a[32], b[32];
+                        tmem_ld32(o_col + 32 * c, a);
+                        if (two) tmem_ld32(o_col + 256 + 32 * c, b);
+                        tmem_wait_ld();
+                        if (!real) continue;
+#pragma unroll
+                        for (int v = 0; v < 32; ++v) {
+                            float x = __uint_as_float(a[v]) * f0;
+                            if (two) x = fmaf(__uint_as_float(b[v]), f1, x);
+                            a[v] = __float_as_uint(x);
+                        }
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            reinterpret_cast<uint4*>(part + 32 * c)[v] =
+                                make_uint4(a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]);
+                    }
+                    if (t == 0 && real)
+                        p.ws_lse[(int64_t)seg.slot * p.rows_cap + (i - seg.row0)] = (top + log2f(total)) * 0.69314718055994531f;
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(bar(L::kBarOFree));
+            ++n_seg;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        if (lane == 0) drain_phase(bar(L::kBarEnd), 0, w.timeout_ns);
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+struct Merge {
+    const float* ws_o;
+    const float* ws_lse;
+    int rows, rows_cap, groups, group_rows, tiles, ctas;  // as the attend kernel cut the units
+    const __nv_bfloat16* own_out;  // [rows][128][128] or NULL
+    const float* own_lse;          // [rows][128]
+    __nv_bfloat16* out;            // may be own_out
+    float* lse;                    // may be own_lse, or NULL
+};
+
+constexpr int kMergeWarps = 8;
+
+// Joins the partials of the prefix (at most a few for one head and group) with the row's attention over
+// its own tokens by log-sum-exp.  One warp per (row, head), four columns a lane: bound by HBM and L2 (own
+// outputs in, outputs out, partials from L2).
+__global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __grid_constant__ Merge a)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t id = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    if (id >= (int64_t)a.rows * 128) return;
+    const int row = (int)(id >> 7), head = (int)(id & 127);
+    const int group = row / a.group_rows, run = head * a.groups + group;
+    const int64_t units = (int64_t)a.groups * 128 * a.tiles, u0 = (int64_t)run * a.tiles, u1 = u0 + a.tiles;
+    // the CTAs with a unit of the run: c0 has the first, which lies at or after the quotient's
+    int c0 = (int)(u0 * a.ctas / units);
+    while (c0 + 1 < a.ctas && first_unit(c0 + 1, units, a.ctas) <= u0) ++c0;
+    int c1 = c0;
+    while (c1 + 1 < a.ctas && first_unit(c1 + 1, units, a.ctas) < u1) ++c1;
+    const int64_t at = row - group * a.group_rows;
+    const float own = a.own_lse ? a.own_lse[id] : -INFINITY;
+    float top = own;
+    for (int c = c0; c <= c1; ++c) top = fmaxf(top, a.ws_lse[(int64_t)(c + run) * a.rows_cap + at]);
+    float total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c = c0; c <= c1; ++c) {
+        const int64_t part = (int64_t)(c + run) * a.rows_cap + at;
+        const float wgt = __expf(a.ws_lse[part] - top);
+        const float4 o = reinterpret_cast<const float4*>(a.ws_o + part * 128)[lane];
+        total += wgt;
+        x[0] = fmaf(wgt, o.x, x[0]);
+        x[1] = fmaf(wgt, o.y, x[1]);
+        x[2] = fmaf(wgt, o.z, x[2]);
+        x[3] = fmaf(wgt, o.w, x[3]);
+    }
+    const float wgt = own == -INFINITY ? 0.f : __expf(own - top);
+    if (wgt != 0.f) {  // a row without own tokens may hold anything
+        const uint2 o = reinterpret_cast<const uint2*>(a.own_out + id * 128)[lane];
+        total += wgt;
+        x[0] = fmaf(wgt, dev::bf16_lo(o.x), x[0]);
+        x[1] = fmaf(wgt, dev::bf16_hi(o.x), x[1]);
+        x[2] = fmaf(wgt, dev::bf16_lo(o.y), x[2]);
+        x[3] = fmaf(wgt, dev::bf16_hi(o.y), x[3]);
+    }
+    const float inv = 1.f / total;
+    reinterpret_cast<uint2*>(a.out + id * 128)[lane] =
+        make_uint2(dev::pack_bf16x2(x[0] * inv, x[1] * inv), dev::pack_bf16x2(x[2] * inv, x[3] * inv));
+    __syncwarp();
+    if (lane == 0 && a.lse) a.lse[id] = top + logf(total);
+}
+
+}  // namespace attend
+}  // namespace mla

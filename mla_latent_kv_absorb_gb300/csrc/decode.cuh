@@ -201,19 +201,44 @@ struct Params {
     float* ws_lse;               // [partials][128]
     uint32_t* dev_error;
     uint64_t timeout_ns;
+    int32_t sinks;               // with a window: the first tokens that stay visible
     long long* trace;            // wait-cycle accounting (MLA_DECODE_TRACE builds only), else null
 };
 
 struct Item {
-    int seq, page_begin, page_end, seq_len, slot, table_row;
+    int seq, page_begin, page_end, seq_len, slot, table_row, skip, hole_end;
 };
 
 __device__ __forceinline__ Item load_item(const int32_t* plan, int items_off, int i)
 {
     const int4 a = *reinterpret_cast<const int4*>(plan + items_off + kItemWords * i);
     const int4 b = *reinterpret_cast<const int4*>(plan + items_off + kItemWords * i + 4);
-    return Item{a.x, a.y, a.z, a.w, b.x, b.y};
+    return Item{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
+
+// Which tokens of an item's pages its row sees.  Under a window page v of the item is another page of the
+// sequence (see plan.h), and beside the slots past the sequence's end those of the tokens
+// [sinks, hole_end) are masked: at most part of the last sink page and of the window's first page (or
+// the middle of one page that is both).
+template <bool kWindow>
+struct Seen {
+    int seq_len, sinks, skip, hole_end;
+    __device__ __forceinline__ Seen(const Item& it, int sinks_)
+        : seq_len(it.seq_len), sinks(sinks_), skip(it.skip), hole_end(it.hole_end)
+    {
+    }
+    __device__ __forceinline__ int page(int v) const { return !kWindow || v < ((sinks + 63) >> 6) ? v : v + skip; }
+    // slots [0, valid) of page v belong to the sequence; of them [hole_lo, hole_hi) are not seen
+    __device__ __forceinline__ int valid(int v) const { return min(64, seq_len - 64 * page(v)); }
+    __device__ __forceinline__ int hole_lo(int v) const { return kWindow ? max(0, min(64, sinks - 64 * page(v))) : 0; }
+    __device__ __forceinline__ int hole_hi(int v) const { return kWindow ? max(0, min(64, hole_end - 64 * page(v))) : 0; }
+    __device__ __forceinline__ bool partial(int v) const { return valid(v) < 64 || (kWindow && hole_hi(v) > hole_lo(v)); }
+    __device__ __forceinline__ bool sees(int v, int slot) const
+    {
+        const int pos = 64 * page(v) + slot;
+        return pos < seq_len && !(kWindow && pos >= sinks && pos < hole_end);
+    }
+};
 
 // ---------------------------------------------------------------------------- absorb prologue
 
@@ -339,6 +364,7 @@ __device__ __forceinline__ bool absorb_wait(const Params& p, const dev::WaitCtx&
 
 // Streams the pages of this cluster's items into a `stages`-deep ring; `boxes` 64-column boxes
 // per page (9 for the score CTA: latent + RoPE key, 8 for the value CTA: latent only).
+template <bool kWindow>
 __device__ __forceinline__ void run_producer(const CUtensorMap* tm, const Params& p, int item_begin, int item_end,
                                              int items_off, uint32_t sbase, uint32_t bars, int boxes, int stages,
                                              int stage_bytes, uint64_t policy, const dev::WaitCtx& w, int lane)
@@ -350,12 +376,14 @@ __device__ __forceinline__ void run_producer(const CUtensorMap* tm, const Params
     bool ok = true;
     for (int i = item_begin; i < item_end && ok; ++i) {
         const Item it = load_item(p.plan, items_off, i);
+        const Seen<kWindow> seen(it, p.sinks);
         const int32_t* bt = p.block_table + (int64_t)it.table_row * p.max_pages;
         for (int pg0 = it.page_begin; pg0 < it.page_end && ok; pg0 += 32) {
             const int n = min(32, it.page_end - pg0);
             int page = 0;
             if (lane < n) {
-                page = pg0 + lane < p.max_pages ? __ldg(bt + pg0 + lane) : -1;  // past the row: bad page
+                const int at = seen.page(pg0 + lane);
+                page = at < p.max_pages ? __ldg(bt + at) : -1;  // past the row: bad page
                 if (page < 0 || page >= p.num_pool_pages) raise_error(p.dev_error, MLA_DEVERR_BAD_PAGE);
             }
             for (int j = 0; j < n; ++j) {
@@ -389,6 +417,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap* tm, const Params
 
 // Streams this cluster's pages as K-chunks: chunk j of a four-page group holds 64-column box j
 // (boxes 0-7: c_KV, box 8: k_R) of the group's pages in rows 0-63, 64-127, 128-191, 192-255.
+template <bool kWindow>
 __device__ __forceinline__ void score_producer(const CUtensorMap* tm, const CUtensorMap* tm_q, const Params& p,
                                                int item_begin, int item_end, int items_off, uint32_t sbase,
                                                uint32_t bars, const dev::WaitCtx& w, int lane)
@@ -406,6 +435,7 @@ __device__ __forceinline__ void score_producer(const CUtensorMap* tm, const CUte
     ok = __shfl_sync(0xffffffffu, ok, 0);
     for (int i = item_begin; i < item_end && ok; ++i) {
         const Item it = load_item(p.plan, items_off, i);
+        const Seen<kWindow> seen(it, p.sinks);
         const int32_t* bt = p.block_table + (int64_t)it.table_row * p.max_pages;
         if (lane == 0) {
             // the item's q_abs rows (128 heads x 512 dims) as four ring entries of two 64-dim
@@ -430,7 +460,8 @@ __device__ __forceinline__ void score_producer(const CUtensorMap* tm, const CUte
             const int n = min(32, it.page_end - pg0);  // a multiple of 4 unless it ends the item
             int page = 0;
             if (lane < n) {
-                page = pg0 + lane < p.max_pages ? __ldg(bt + pg0 + lane) : -1;  // past the row: bad page
+                const int at = seen.page(pg0 + lane);
+                page = at < p.max_pages ? __ldg(bt + at) : -1;  // past the row: bad page
                 if (page < 0 || page >= p.num_pool_pages) raise_error(p.dev_error, MLA_DEVERR_BAD_PAGE);
             }
             for (int j = 0; j < n && ok; j += kGroupPages) {
@@ -568,13 +599,19 @@ __device__ __forceinline__ void load_query_rope(const Params& p, int seq, int ro
 
 // Slots past the sequence end read as -infinity (the raw score there may be anything, NaN
 // included): then the page maximum skips them and their p is 2^-inf = 0.  Only a sequence's
-// last page has such slots.
-__device__ __forceinline__ void page_mask(uint32_t (&sr)[64], int valid)
+// last page has such slots, and under a window the pages at its hole's ends.
+template <bool kWindow>
+__device__ __forceinline__ void page_mask(uint32_t (&sr)[64], int valid, int hole_lo, int hole_hi)
 {
     if (valid < 64) {
 #pragma unroll
         for (int j = 0; j < 64; ++j)
             if (j >= valid) sr[j] = __float_as_uint(-INFINITY);
+    }
+    if (kWindow && hole_hi > hole_lo) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+            if (j >= hole_lo && j < hole_hi) sr[j] = __float_as_uint(-INFINITY);
     }
 }
 
@@ -705,6 +742,7 @@ __device__ __forceinline__ bool wait_freed(const uint32_t* freed, uint32_t targe
     return __all_sync(0xffffffffu, ok);
 }
 
+template <bool kWindow>
 __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, int item_end, int items_off,
                                               uint8_t* smem, uint32_t sbase, uint32_t bars, uint32_t tmem,
                                               const dev::WaitCtx& w, int warp, int lane)
@@ -721,6 +759,7 @@ __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, i
     int g = 0, G = 0;  // pages (messages) and four-page groups
     for (int i = item_begin; i < item_end; ++i) {
         const Item it = load_item(p.plan, items_off, i);
+        const Seen<kWindow> seen(it, p.sinks);
         [[maybe_unused]] const long long tq0 = MLA_TRACE_NOW();
         if (set == 0) load_query_rope(p, it.seq, row, smem + kOffQR);
         __syncwarp();
@@ -740,7 +779,7 @@ __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, i
             [[maybe_unused]] const long long tc0 = MLA_TRACE_NOW();
             uint32_t sr[2][64];
             const int t0 = pg + 2 * set;
-            const int valid0 = min(64, it.seq_len - 64 * t0), valid1 = min(64, it.seq_len - 64 * (t0 + 1));
+            const bool partial0 = seen.partial(t0), partial1 = seen.partial(t0 + 1);
             float mx = -INFINITY;
             if (ok) {
                 tc_fence_after();
@@ -760,11 +799,11 @@ __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, i
                 if (lane == 0 && warp == 2) MLA_EV(5, G);
                 MLA_TRACE_ADD(14, MLA_TRACE_NOW() - tc0);
                 if (n_mine > 0) {
-                    page_mask(sr[0], valid0);
+                    page_mask<kWindow>(sr[0], seen.valid(t0), seen.hole_lo(t0), seen.hole_hi(t0));
                     mx = page_max(sr[0]);
                 }
                 if (n_mine > 1) {
-                    page_mask(sr[1], valid1);
+                    page_mask<kWindow>(sr[1], seen.valid(t0 + 1), seen.hole_lo(t0 + 1), seen.hole_hi(t0 + 1));
                     mx = fmaxf(mx, page_max(sr[1]));
                 }
             }
@@ -807,7 +846,7 @@ __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, i
                 if (t0 + j == it.page_end - 1)
                     hold_last = true;
                 else
-                    stage_message(smem, bars, slot, q4, lane, f_page, 0.f, false, (j ? valid1 : valid0) < 64);
+                    stage_message(smem, bars, slot, q4, lane, f_page, 0.f, false, j ? partial1 : partial0);
                 MLA_TRACE_ADD(10, MLA_TRACE_NOW() - tw0);
             }
             if (last_group) {  // 1/l for the item's last page needs both sets' sums
@@ -818,7 +857,7 @@ __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, i
                     const int j = n_mine - 1;
                     const int slot = (g + 2 * set + j) % kStagingSlots;
                     const float f_page = (set == 0 && j == 0) ? factor : 1.f;
-                    stage_message(smem, bars, slot, q4, lane, f_page, 1.f / l_total, true, (j ? valid1 : valid0) < 64);
+                    stage_message(smem, bars, slot, q4, lane, f_page, 1.f / l_total, true, j ? partial1 : partial0);
                 }
             }
             if (lane == 0 && (warp == 2 || warp == 6)) MLA_EV(warp == 2 ? 7 : 14, G);
@@ -973,6 +1012,7 @@ __device__ __forceinline__ void write_output(const KernelParams& p, const Item& 
     }
 }
 
+template <bool kWindow>
 __device__ __forceinline__ void value_correction(const Params& p, int item_begin, int item_end, int items_off,
                                                  uint8_t* smem, uint32_t bars, uint32_t tmem, const dev::WaitCtx& w,
                                                  int warp, int lane, int tid128)
@@ -1016,9 +1056,10 @@ __device__ __forceinline__ void value_correction(const Params& p, int item_begin
                 MLA_TRACE_ADD(9, MLA_TRACE_NOW() - te0);
             }
             if (flags & 2u) {
-                // slots past the sequence end may hold anything (NaN): zero them so that
+                // slots that are not seen may hold anything (NaN): zero them so that
                 // p = 0 times them stays 0 in the PV contraction
-                const int valid = min(64, it.seq_len - 64 * t);
+                const Seen<kWindow> seen(it, p.sinks);
+                const int valid = seen.valid(t);
                 const int s = g % kValueStages;
                 if (!wait_warp(bars + 8 * (kFull0 + s), g / kValueStages, w)) goto done;
                 uint8_t* stage = smem + s * kValueStageBytes;
@@ -1026,6 +1067,13 @@ __device__ __forceinline__ void value_correction(const Params& p, int item_begin
                 for (int c = tid128; c < chunks; c += 128) {
                     const int r = valid + (c >> 6), box = (c >> 3) & 7, ch = c & 7;
                     *reinterpret_cast<uint4*>(stage + box * kBoxBytes + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+                }
+                if (kWindow) {
+                    const int lo = seen.hole_lo(t), holes = (min(seen.hole_hi(t), valid) - lo) * 64;
+                    for (int c = tid128; c < holes; c += 128) {
+                        const int r = lo + (c >> 6), box = (c >> 3) & 7, ch = c & 7;
+                        *reinterpret_cast<uint4*>(stage + box * kBoxBytes + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+                    }
                 }
                 fence_proxy_async_cta();
             }
@@ -1067,6 +1115,7 @@ done:
 
 // 11 warps: three SM sub-partitions hold three of them, and a sub-partition's 16K registers then
 // allow at most 3 x 32 x 168.
+template <bool kWindow>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
 decode_bf16_kernel(const __grid_constant__ CUtensorMap tm_pool, const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__ CUtensorMap tm_wuk, const Params p)
@@ -1139,24 +1188,24 @@ decode_bf16_kernel(const __grid_constant__ CUtensorMap tm_pool, const __grid_con
         const int item_end = cluster < n_clusters ? p.plan[cl_off + cluster + 1] : 0;
         if (rank == 0) {
             if (warp == 0)
-                score_producer(&tm_pool, &tm_q, p, item_begin, item_end, items_off, sbase, bars, w, lane);
+                score_producer<kWindow>(&tm_pool, &tm_q, p, item_begin, item_end, items_off, sbase, bars, w, lane);
             else if (warp == 1) {
                 if (lane == 0) score_mma(p, item_begin, item_end, items_off, sbase, bars, tmem, w);
             } else if (warp == kShipperWarp) {
                 if (lane == 0) score_shipper(p, item_begin, item_end, items_off, smem, sbase, bars, w);
                 else if (lane == 1) score_tracker(p, item_begin, item_end, items_off, smem, bars, w);
             } else if (warp >= 2 && warp < 10)
-                score_softmax(p, item_begin, item_end, items_off, smem, sbase, bars, tmem, w, warp, lane);
+                score_softmax<kWindow>(p, item_begin, item_end, items_off, smem, sbase, bars, tmem, w, warp, lane);
         } else {
             if (warp == 0)
-                run_producer(&tm_pool, p, item_begin, item_end, items_off, sbase, bars, 8, kValueStages,
+                run_producer<kWindow>(&tm_pool, p, item_begin, item_end, items_off, sbase, bars, 8, kValueStages,
                              kValueStageBytes, l2_policy_evict_first(), w, lane);
             else if (warp == 1) {
                 if (lane == 0) value_mma(p, item_begin, item_end, items_off, smem, sbase, bars, tmem, w);
             } else if (warp == kAckWarp) {
                 if (lane == 0) value_ack(p, item_begin, item_end, items_off, bars, w);
             } else if (warp >= 2 && warp < 6)
-                value_correction(p, item_begin, item_end, items_off, smem, bars, tmem, w, warp, lane,
+                value_correction<kWindow>(p, item_begin, item_end, items_off, smem, bars, tmem, w, warp, lane,
                                  threadIdx.x - 64);
         }
     }

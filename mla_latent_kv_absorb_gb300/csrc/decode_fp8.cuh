@@ -61,6 +61,7 @@ namespace decode_fp8 {
 using decode::Item;
 using decode::kTraceSlots;
 using decode::load_item;
+using decode::Seen;
 using decode::wait_freed;
 using decode::write_output;
 using decode::kOutTileBytes;
@@ -170,6 +171,7 @@ struct Params {
     float* ws_lse;               // [partials][128]
     uint32_t* dev_error;
     uint64_t timeout_ns;
+    int32_t sinks;               // with a window: the first tokens that stay visible
     const float* kv_scale;       // [pages][64] per-token scale of the e4m3 latent rows
     long long* trace;            // instrumented builds only, else null
 };
@@ -251,6 +253,7 @@ __device__ __forceinline__ float exp2i(int e)
 // ---------------------------------------------------------------------------- TMA producers
 
 // Value CTA: each page's 512 c8 columns as four 128-byte-wide boxes into a four-stage ring.
+template <bool kWindow>
 __device__ __forceinline__ void value_producer(const CUtensorMap* tm_c8, const Params& p, int item_begin,
                                                int item_end, int items_off, uint32_t sbase, uint32_t bars,
                                                const dev::WaitCtx& w, int lane)
@@ -262,12 +265,14 @@ __device__ __forceinline__ void value_producer(const CUtensorMap* tm_c8, const P
     bool ok = true;
     for (int i = item_begin; i < item_end && ok; ++i) {
         const Item it = load_item(p.plan, items_off, i);
+        const Seen<kWindow> seen(it, p.sinks);
         const int32_t* bt = p.block_table + (int64_t)it.table_row * p.max_pages;
         for (int pg0 = it.page_begin; pg0 < it.page_end && ok; pg0 += 32) {
             const int n = min(32, it.page_end - pg0);
             int page = 0;
             if (lane < n) {
-                page = pg0 + lane < p.max_pages ? __ldg(bt + pg0 + lane) : -1;  // past the row: bad page
+                const int at = seen.page(pg0 + lane);
+                page = at < p.max_pages ? __ldg(bt + at) : -1;  // past the row: bad page
                 if (page < 0 || page >= p.num_pool_pages) raise_error(p.dev_error, MLA_DEVERR_BAD_PAGE);
             }
             for (int j = 0; j < n; ++j) {
@@ -300,6 +305,7 @@ __device__ __forceinline__ void value_producer(const CUtensorMap* tm_c8, const P
 // Score CTA: chunk j of a four-page group holds c8 box j (128 columns) of the group's pages in
 // rows 0-63, 64-127, 128-191, 192-255, through a three-slot ring; the k_R box has a buffer of
 // its own that warp 11 fills (see kr_convert).
+template <bool kWindow>
 __device__ __forceinline__ void score_producer(const CUtensorMap* tm_c8, const CUtensorMap* tm_q, const Params& p,
                                                int item_begin, int item_end, int items_off, uint32_t sbase,
                                                uint32_t bars, const dev::WaitCtx& w, int lane)
@@ -314,6 +320,7 @@ __device__ __forceinline__ void score_producer(const CUtensorMap* tm_c8, const C
     bool ok = true;
     for (int i = item_begin; i < item_end && ok; ++i) {
         const Item it = load_item(p.plan, items_off, i);
+        const Seen<kWindow> seen(it, p.sinks);
         const int32_t* bt = p.block_table + (int64_t)it.table_row * p.max_pages;
         if (lane == 0) {
             // the item's q_abs rows (128 heads x 512 dims) as four ring entries of two 64-dim
@@ -338,7 +345,8 @@ __device__ __forceinline__ void score_producer(const CUtensorMap* tm_c8, const C
             const int n = min(32, it.page_end - pg0);  // a multiple of 4 unless it ends the item
             int page = 0;
             if (lane < n) {
-                page = pg0 + lane < p.max_pages ? __ldg(bt + pg0 + lane) : -1;  // past the row: bad page
+                const int at = seen.page(pg0 + lane);
+                page = at < p.max_pages ? __ldg(bt + at) : -1;  // past the row: bad page
                 if (page < 0 || page >= p.num_pool_pages) raise_error(p.dev_error, MLA_DEVERR_BAD_PAGE);
             }
             for (int j = 0; j < n && ok; j += kGroupPages) {
@@ -385,6 +393,7 @@ __device__ __forceinline__ void score_producer(const CUtensorMap* tm_c8, const C
 // does after s_free of group G - 2; every softmax warp had finished group G - 3 then, and slot
 // G % 4 last held group G - 4.  Owning the k_R loads keeps them off the c8 ring: the load for
 // group G + 1 starts as soon as the MMA has taken group G's k_R.
+template <bool kWindow>
 __device__ __forceinline__ void kr_convert(const CUtensorMap* tm_kr, const Params& p, int item_begin, int item_end,
                                            int items_off, uint8_t* smem, uint32_t sbase, uint32_t bars,
                                            const dev::WaitCtx& w, int lane)
@@ -396,29 +405,31 @@ __device__ __forceinline__ void kr_convert(const CUtensorMap* tm_kr, const Param
     int G = 0;
     for (int i = item_begin; i < item_end; ++i) {
         const Item it = load_item(p.plan, items_off, i);
+        const Seen<kWindow> seen(it, p.sinks);
         const int32_t* bt = p.block_table + (int64_t)it.table_row * p.max_pages;
         // largest scale over the item's tokens: lane k takes pages k, k + 32, ...; a page's
         // sixteen scale loads are in flight together, and the next page id is loaded before them,
         // so each page costs one memory round trip
         const auto page_at = [&](int pg) {
-            return (pg < it.page_end && pg < p.max_pages) ? __ldg(bt + pg) : -1;
+            return (pg < it.page_end && seen.page(pg) < p.max_pages) ? __ldg(bt + seen.page(pg)) : -1;
         };
         float smax = 0.f;
         int page = page_at(it.page_begin + lane);
         for (int pg = it.page_begin + lane; pg < it.page_end; pg += 32) {
             const int next = page_at(pg + 32);
             if (page >= 0 && page < p.num_pool_pages) {  // a bad id is reported by the producers
-                const int valid = min(64, it.seq_len - 64 * pg);
+                const int valid = seen.valid(pg), lo = seen.hole_lo(pg), hi = seen.hole_hi(pg);
+                const auto seen_slot = [&](int k) { return k < valid && !(kWindow && k >= lo && k < hi); };
                 const float4* sc = reinterpret_cast<const float4*>(p.kv_scale + (int64_t)page * 64);
                 float4 x[16];
 #pragma unroll
                 for (int v = 0; v < 16; ++v) x[v] = __ldg(sc + v);
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
-                    if (4 * v + 0 < valid) smax = fmaxf(smax, x[v].x);
-                    if (4 * v + 1 < valid) smax = fmaxf(smax, x[v].y);
-                    if (4 * v + 2 < valid) smax = fmaxf(smax, x[v].z);
-                    if (4 * v + 3 < valid) smax = fmaxf(smax, x[v].w);
+                    if (seen_slot(4 * v + 0)) smax = fmaxf(smax, x[v].x);
+                    if (seen_slot(4 * v + 1)) smax = fmaxf(smax, x[v].y);
+                    if (seen_slot(4 * v + 2)) smax = fmaxf(smax, x[v].z);
+                    if (seen_slot(4 * v + 3)) smax = fmaxf(smax, x[v].w);
                 }
             }
             page = next;
@@ -439,7 +450,8 @@ __device__ __forceinline__ void kr_convert(const CUtensorMap* tm_kr, const Param
             // is used, so the group costs two memory round trips.
             int page_mine = 0;
             if (lane < npg) {
-                page_mine = pg + lane < p.max_pages ? __ldg(bt + pg + lane) : -1;
+                const int at = seen.page(pg + lane);
+                page_mine = at < p.max_pages ? __ldg(bt + at) : -1;
                 if (page_mine < 0 || page_mine >= p.num_pool_pages) page_mine = -1;  // reported by the producers
             }
             int pages[kGroupPages];
@@ -461,11 +473,11 @@ __device__ __forceinline__ void kr_convert(const CUtensorMap* tm_kr, const Param
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int t = lane + 32 * k, q = k >> 1;
-                const bool in_seq = q < npg && 64 * (pg + q) + (t & 63) < it.seq_len;
+                const bool in_seq = q < npg && seen.sees(pg + q, t & 63);
                 const bool valid = in_seq && pages[q] >= 0;
                 // a zero scale (a zero latent row) enters the score side as 2^-64, so that k_R /
                 // sigma stays finite and sigma (q . c8 + q_R . k_R / sigma) is still q_R . k_R;
-                // a slot past the sequence end gets NaN, which the softmax's maximum skips
+                // a slot that is not seen (past the sequence end) gets NaN, which the softmax's maximum skips
                 // (fmaxf returns the other operand), so the maximum needs no mask
                 sig[t] = valid ? fmaxf(sigma[k], 5.421011e-20f) * p.scale_log2 : (in_seq ? 0.f : __int_as_float(0x7fc00000));
                 sig[256 + t] = valid ? sigma[k] * g : 0.f;
@@ -784,6 +796,7 @@ __device__ __forceinline__ void score_shipper(const Params& p, int item_begin, i
         if (!wait_phase<true>(bars + 8 * (kMsgFree0 + k % kMsgSlots), k / kMsgSlots, w)) break;
 }
 
+template <bool kWindow>
 __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, int item_end, int items_off,
                                               uint8_t* smem, uint32_t bars, uint32_t tmem, const dev::WaitCtx& w,
                                               int warp, int lane)
@@ -799,6 +812,7 @@ __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, i
     int g = 0, G = 0;  // pages (messages) and four-page groups
     for (int i = item_begin, n_item = 0; i < item_end; ++i, ++n_item) {
         const Item it = load_item(p.plan, items_off, i);
+        const Seen<kWindow> seen(it, p.sinks);
         // The exchange slot of the query maxima: the group-max slot that the next group does not
         // use.  Group G - 1 (the previous item's last group, which also ran the l barrier) read it
         // before every softmax thread passed that barrier; group G + 1 writes it only after the
@@ -829,7 +843,7 @@ __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, i
             uint32_t sr[64];
             const uint32_t scol = tmem + lane_off + kSCol + 128 * set;
             const int t0 = pg + 2 * set;
-            const int valid0 = min(64, it.seq_len - 64 * t0), valid1 = min(64, it.seq_len - 64 * (t0 + 1));
+            const bool partial0 = seen.partial(t0), partial1 = seen.partial(t0 + 1);
             float mx = -INFINITY;
             if (ok) ok = wait_freed(sig_ready, (uint32_t)(G + 1), w);  // this group's token factors
             if (ok) {
@@ -886,7 +900,7 @@ __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, i
                 if (t0 + j == it.page_end - 1)
                     hold_last = true;
                 else
-                    stage_message(smem, bars, slot, q4, lane, f_page, 0.f, false, (j ? valid1 : valid0) < 64,
+                    stage_message(smem, bars, slot, q4, lane, f_page, 0.f, false, j ? partial1 : partial0,
                                   sig + 256 + 64 * (2 * set + j));
             }
             if (last_group) {  // 1/(g l) for the item's last page needs both sets' sums
@@ -898,7 +912,7 @@ __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, i
                     const int slot = (g + 2 * set + j) % kStagingSlots;
                     const float f_page = (set == 0 && j == 0) ? factor : 1.f;
                     stage_message(smem, bars, slot, q4, lane, f_page, 1.f / (g_item * l_total), true,
-                                  (j ? valid1 : valid0) < 64, sig + 256 + 64 * (2 * set + j));
+                                  j ? partial1 : partial0, sig + 256 + 64 * (2 * set + j));
                 }
             }
             if (lane == 0 && warp == 2) MLA_EV(7, G);
@@ -1045,6 +1059,7 @@ __device__ __forceinline__ void value_pconvert(const Params& p, int item_begin, 
 // The normalised output of an item, O / (g l), leaves through decode.cuh's write_output (its
 // inv_l here carries the item's token-factor normaliser g as well).
 
+template <bool kWindow>
 __device__ __forceinline__ void value_correction(const Params& p, int item_begin, int item_end, int items_off,
                                                  uint8_t* smem, uint32_t bars, uint32_t tmem, const dev::WaitCtx& w,
                                                  int warp, int lane, int tid128)
@@ -1084,9 +1099,10 @@ __device__ __forceinline__ void value_correction(const Params& p, int item_begin
                 have_prev = false;
             }
             if (flags & 2u) {
-                // slots past the sequence end may hold anything (NaN codes): zero them so that
+                // slots that are not seen may hold anything (NaN codes): zero them so that
                 // P~ = 0 times them stays 0 in the PV contraction
-                const int valid = min(64, it.seq_len - 64 * t);
+                const Seen<kWindow> seen(it, p.sinks);
+                const int valid = seen.valid(t);
                 const int s = g % kValueStages;
                 if (!wait_warp_ool(bars + 8 * (kFull0 + s), g / kValueStages, w)) goto done;
                 uint8_t* stage = smem + s * kValueStageBytes;
@@ -1094,6 +1110,13 @@ __device__ __forceinline__ void value_correction(const Params& p, int item_begin
                 for (int c = tid128; c < chunks; c += 128) {
                     const int r = valid + (c >> 5), box = (c >> 3) & 3, ch = c & 7;
                     *reinterpret_cast<uint4*>(stage + box * kBoxBytes + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+                }
+                if (kWindow) {
+                    const int lo = seen.hole_lo(t), holes = (min(seen.hole_hi(t), valid) - lo) * 32;
+                    for (int c = tid128; c < holes; c += 128) {
+                        const int r = lo + (c >> 5), box = (c >> 3) & 3, ch = c & 7;
+                        *reinterpret_cast<uint4*>(stage + box * kBoxBytes + r * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+                    }
                 }
                 fence_proxy_async_cta();
             }
@@ -1134,6 +1157,7 @@ done:
 // a 163 KB build).  So the per-chunk and per-row loops stay rolled, barrier polling runs out of
 // line, and the query load (once per item) is a separate function.
 // 12 warps: each SM sub-partition holds three, and its 16K registers allow 3 x 32 x 168.
+template <bool kWindow>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(168)
 decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_c8, const __grid_constant__ CUtensorMap tm_kr,
                   const __grid_constant__ CUtensorMap tm_q, const Params p)
@@ -1202,23 +1226,23 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_c8, const __grid_consta
         const int item_end = cluster < n_clusters ? p.plan[cl_off + cluster + 1] : 0;
         if (rank == 0) {
             if (warp == 0)
-                score_producer(&tm_c8, &tm_q, p, item_begin, item_end, items_off, sbase, bars, w, lane);
+                score_producer<kWindow>(&tm_c8, &tm_q, p, item_begin, item_end, items_off, sbase, bars, w, lane);
             else if (warp == 1) {
                 if (lane == 0) score_mma(p, item_begin, item_end, items_off, sbase, bars, tmem, w);
             } else if (warp >= 2 && warp < 10)
-                score_softmax(p, item_begin, item_end, items_off, smem, bars, tmem, w, warp, lane);
+                score_softmax<kWindow>(p, item_begin, item_end, items_off, smem, bars, tmem, w, warp, lane);
             else if (warp == kShipperWarp) {
                 if (lane == 0) score_shipper(p, item_begin, item_end, items_off, smem, sbase, bars, w);
                 else if (lane == 1) score_tracker(p, item_begin, item_end, items_off, smem, bars, w);
             } else if (warp == kKrWarp)
-                kr_convert(&tm_kr, p, item_begin, item_end, items_off, smem, sbase, bars, w, lane);
+                kr_convert<kWindow>(&tm_kr, p, item_begin, item_end, items_off, smem, sbase, bars, w, lane);
         } else {
             if (warp == 0)
-                value_producer(&tm_c8, p, item_begin, item_end, items_off, sbase, bars, w, lane);
+                value_producer<kWindow>(&tm_c8, p, item_begin, item_end, items_off, sbase, bars, w, lane);
             else if (warp == 1) {
                 if (lane == 0) value_mma(p, item_begin, item_end, items_off, smem, sbase, bars, tmem, w);
             } else if (warp >= 2 && warp < 6)
-                value_correction(p, item_begin, item_end, items_off, smem, bars, tmem, w, warp, lane,
+                value_correction<kWindow>(p, item_begin, item_end, items_off, smem, bars, tmem, w, warp, lane,
                                  threadIdx.x - 64);
             else if (warp == kAckWarp) {
                 if (lane == 0) value_ack(p, item_begin, item_end, items_off, bars, w);

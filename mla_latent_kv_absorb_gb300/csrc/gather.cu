@@ -66,6 +66,7 @@ struct Args {
     const int32_t* seq_lens;      // [B], or NULL: one sequence of one_len tokens (cu_seqlens unused)
     const int32_t* cu_seqlens;    // [B + 1]
     int32_t one_len;
+    int32_t skip_from, skip;      // one sequence: row t is token t below skip_from, token t + skip behind it
     uint4* out;                   // bf16 [total][576]
     uint32_t* dev_error;
 };
@@ -76,13 +77,14 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kv_kernel(const Args a)
     const int lane = threadIdx.x & 31, b = blockIdx.y;
     const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (t >= (a.seq_lens ? __ldg(a.seq_lens + b) : a.one_len)) return;
-    const int64_t pg = t / 64;
+    const int64_t pos = a.seq_lens || t < a.skip_from ? t : t + a.skip;
+    const int64_t pg = pos / 64;
     const int32_t page = pg < a.max_pages ? __ldg(a.block_table + (int64_t)b * a.max_pages + pg) : -1;
     if (page < 0 || page >= a.num_pool_pages) {
         if (lane == 0) atomicOr(a.dev_error, MLA_DEVERR_BAD_PAGE);
         return;
     }
-    const int64_t tok = (int64_t)page * 64 + t % 64;
+    const int64_t tok = (int64_t)page * 64 + pos % 64;
     uint4* dst = a.out + ((a.seq_lens ? (int64_t)__ldg(a.cu_seqlens + b) : 0) + t) * 72;  // 72 x 16 bytes per row
     if (a.kv_dtype == MLA_KV_BF16) {
         const uint4* src = reinterpret_cast<const uint4*>(a.pool) + tok * 72;
@@ -176,17 +178,19 @@ extern "C" MLA_API mla_status mla_gather_kv(mla_kv_dtype kv_dtype, const void* k
     a.seq_lens = seq_lens;
     a.cu_seqlens = cu_seqlens;
     a.one_len = 0;
+    a.skip_from = a.skip = 0;
     a.out = static_cast<uint4*>(out);
     a.dev_error = dev_error;
     return launch(a, max_pages_per_seq, batch, stream);
 }
 
 namespace mla {
-// One sequence of seq_len tokens (its block-table row given), rows to out [seq_len][576]; the
-// caller has checked the arguments as mla_gather_kv does.
+// `seq_len` tokens of one sequence (its block-table row given), rows to out [seq_len][576]: the first
+// ones up to skip_from, then, `skip` tokens left out, those behind; the caller has checked the arguments
+// as mla_gather_kv does.
 mla_status gather_one_sequence(mla_kv_dtype kv_dtype, const void* kv_pool, const float* kv_scale, const void* kr_pool,
                                int32_t num_pool_pages, const int32_t* block_table_row, int32_t max_pages,
-                               int32_t seq_len, void* out, uint32_t* dev_error, void* stream)
+                               int32_t seq_len, void* out, uint32_t* dev_error, void* stream, int32_t skip_from, int32_t skip)
 {
     using namespace mla::gather;
     Args a;
@@ -200,6 +204,8 @@ mla_status gather_one_sequence(mla_kv_dtype kv_dtype, const void* kv_pool, const
     a.seq_lens = nullptr;
     a.cu_seqlens = nullptr;
     a.one_len = seq_len;
+    a.skip_from = skip_from;
+    a.skip = skip;
     a.out = static_cast<uint4*>(out);
     a.dev_error = dev_error;
     return launch(a, (seq_len + 63) / 64, 1, stream);

@@ -90,12 +90,15 @@ extern "C" mla_status mla_plan_splits(const int32_t* seq_lens, int32_t batch, in
                                       mla_plan_info* info)
 {
     if (!seq_lens || !plan_host || !info || batch <= 0 || num_sms < 2) return MLA_ERR_INVALID_ARG;
-    int32_t min_pages = 8, max_clusters = num_sms / 2, item_cost = kDefaultItemCostPages, qps = 1;
+    int32_t min_pages = 8, max_clusters = num_sms / 2, item_cost = kDefaultItemCostPages, qps = 1, window = 0, sinks = 0;
     int64_t timeout_ns = 2000000000LL;
     if (opts) {
         if (opts->min_pages_per_split < 0 || opts->max_clusters < 0 || opts->wait_timeout_ns < 0 ||
-            opts->queries_per_seq < 0 || opts->queries_per_seq > MLA_MAX_QUERIES_PER_SEQ)
+            opts->queries_per_seq < 0 || opts->queries_per_seq > MLA_MAX_QUERIES_PER_SEQ || opts->window < 0 ||
+            opts->sinks < 0 || (opts->sinks > 0 && opts->window == 0))
             return MLA_ERR_INVALID_ARG;
+        window = opts->window;
+        sinks = opts->sinks;
         if (opts->item_cost_pages != 0) item_cost = std::max(0, opts->item_cost_pages);  // < 0: equal page runs
         if (opts->min_pages_per_split > 0) min_pages = opts->min_pages_per_split;
         if (opts->max_clusters > 0) max_clusters = std::min(max_clusters, opts->max_clusters);
@@ -117,10 +120,16 @@ extern "C" mla_status mla_plan_splits(const int32_t* seq_lens, int32_t batch, in
     seq_lens = row_len.data();
 
     // pages of each query row and where each starts in the concatenated page list
+    // (with a window: of the pages that hold a token which the row sees)
     std::vector<int64_t> pages(batch), start(batch + 1);
+    std::vector<int32_t> skip(batch, 0), hole_end(batch, 0);
     start[0] = 0;
     for (int b = 0; b < batch; ++b) {
-        pages[b] = (seq_lens[b] + 63) / 64;
+        if (window > 0 && seq_lens[b] - window > sinks) {  // tokens [sinks, hole_end) are not seen
+            hole_end[b] = seq_lens[b] - window;
+            skip[b] = std::max(0, hole_end[b] / 64 - (int32_t)(((int64_t)sinks + 63) / 64));
+        }
+        pages[b] = (seq_lens[b] + 63) / 64 - skip[b];
         start[b + 1] = start[b] + pages[b];
     }
     const int64_t total = start[batch];
@@ -183,6 +192,8 @@ extern "C" mla_status mla_plan_splits(const int32_t* seq_lens, int32_t batch, in
             it.seq_len = seq_lens[ss];
             it.partial_slot = -1;
             it.table_row = ss / qps;
+            it.skip = skip[ss];
+            it.hole_end = hole_end[ss];
             items.push_back(it);
             ++items_per_seq[ss];
             g = e;
@@ -230,6 +241,7 @@ extern "C" mla_status mla_plan_splits(const int32_t* seq_lens, int32_t batch, in
     w[kHdrTimeoutLo] = (int32_t)(uint32_t)(timeout_ns & 0xffffffffu);
     w[kHdrTimeoutHi] = (int32_t)(uint32_t)((uint64_t)timeout_ns >> 32);
     w[kHdrQueriesPerSeq] = qps;
+    w[kHdrSinks] = sinks;
     for (int64_t k = 0; k <= C; ++k) w[cl_off + k] = cluster_begin[k];
     std::memcpy(w + it_off, items.data(), (size_t)n_items * sizeof(PlanItem));
     if (n_comb) std::memcpy(w + cb_off, combine.data(), (size_t)n_comb * sizeof(PlanCombine));
@@ -245,5 +257,7 @@ extern "C" mla_status mla_plan_splits(const int32_t* seq_lens, int32_t batch, in
     info->plan_bytes = words * 4;
     info->workspace_bytes = (int64_t)next_slot * (kPartialOBytes + kPartialLseBytes);
     info->wait_timeout_ns = timeout_ns;
+    info->window = window;
+    info->sinks = sinks;
     return MLA_OK;
 }

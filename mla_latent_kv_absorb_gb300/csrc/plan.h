@@ -30,6 +30,7 @@ enum PlanHeader : int {
     kHdrTimeoutLo = 12,
     kHdrTimeoutHi = 13,
     kHdrQueriesPerSeq = 14,  // query tokens per sequence (1: ordinary decode)
+    kHdrSinks = 15,          // with a window: the first tokens that stay visible
 };
 
 // One work item: pages [page_begin, page_end) of query row `seq` (its visible context length
@@ -38,8 +39,11 @@ enum PlanHeader : int {
 // token t of sequence b (table row b).  partial_slot < 0: the item covers the whole row and
 // writes o_lat / lse directly; otherwise it writes split partial number partial_slot of the
 // workspace.
+// With a window the tokens [sinks, hole_end) are not seen.  The pages of which every token lies there
+// are left out of the count: page v of the item is page v of the sequence below ceil(sinks / 64) and
+// page v + skip behind it.  Without such tokens skip and hole_end are 0.
 struct PlanItem {
-    int32_t seq, page_begin, page_end, seq_len, partial_slot, table_row, pad1, pad2;
+    int32_t seq, page_begin, page_end, seq_len, partial_slot, table_row, skip, hole_end;
 };
 
 // A sequence cut into n_parts items whose partials are the consecutive slots
