@@ -196,6 +196,8 @@ extern "C" MLA_API mla_status mla_prefix_attend(int32_t num_rows, int32_t prefix
     p.groups = c.groups;
     p.dev_error = dev_error;
     p.timeout_ns = kTimeoutNs;
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
     p.tiles = c.tiles;
     p.rows_cap = c.rows_cap;
     p.ws_o = static_cast<float*>(workspace);
@@ -268,6 +270,8 @@ extern "C" MLA_API mla_status mla_prefill_window(mla_kv_dtype kv_dtype, const vo
     p.groups = (chunk_len + 255) / 256;
     p.dev_error = dev_error;
     p.timeout_ns = kTimeoutNs;
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
     p.hi0 = seq_len - chunk_len - s.skip;
     p.window = std::min(window, seq_len);
     p.sinks = std::min(sinks, seq_len);

@@ -40,12 +40,100 @@
 namespace mla {
 namespace attend {
 
+using dev::WaitCtx;
+
+// ---- The MMA warp runs as a whole, on values that are the same in all its lanes, and one elected lane
+// issues: descriptors then live in uniform registers and an MMA is an instruction or two.  A single lane that
+// computes them takes some ten instructions for each MMA, and waits for every one of them behind the two
+// softmax warps of its SM sub-partition (measured beside eight warps that issue FMAs all the time: 134 cycles
+// for an MMA of 64, against 71 this way).
+
+__device__ __forceinline__ void mma_ss_one(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts_one(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit_one(uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+
+// A wait whose answer is the same in all lanes (a vote), with the polling out of line.
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t phase, const WaitCtx& w)
+{
+    if (__all_sync(0xffffffffu, dev::mbar_try_wait(bar, phase & 1u))) return true;
+    return __all_sync(0xffffffffu, dev::wait_phase_slow<false>(bar, phase, w.abort, w.timeout_ns, w.dev_error));
+}
+
+// ---- Two floats at a time (one instruction each on sm_103a), and the largest of three.
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// `bytes` (a multiple of 16) from `p` into L2, without waiting.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 constexpr int kTile = 128;                 // query rows of a tile, keys of a tile
 constexpr int kThreads = 32 * 11;
 constexpr int kSoftmaxWarp0 = 3;
 constexpr int kSlotBytes = 16384;
 constexpr uint32_t kTmemCols = 512;        // stream t: S at 256 t, O at 256 t + 128
 constexpr float kRescaleLog2 = 8.f;
+constexpr int kFetch = 4;                  // key tiles ahead that are brought into L2
 constexpr uint32_t kJoinBarrier = 1;       // named barrier of the eight softmax warps
 
 template <int kQT>
@@ -57,9 +145,9 @@ struct Layout {
     static constexpr int kBarFull = 0, kBarEmpty = kSlots;
     static constexpr int kBarQFull = 2 * kSlots, kBarQEmpty = kBarQFull + 1;
     static constexpr int kBarSFull = kBarQFull + 2;   // [stream]
-    static constexpr int kBarPReady = kBarSFull + 2;  // [stream], 128 arrivals
+    static constexpr int kBarPReady = kBarSFull + 2;  // [stream], four warps' arrivals
     static constexpr int kBarODone = kBarPReady + 2;  // the segment's last PV has finished
-    static constexpr int kBarOFree = kBarODone + 1;   // 256 arrivals: the segment's O has been read
+    static constexpr int kBarOFree = kBarODone + 1;   // eight warps' arrivals: the segment's O has been read
     static constexpr int kBarEnd = kBarOFree + 1;     // every MMA of the CTA has finished
     static constexpr int kBars = kBarEnd + 1;
     static constexpr int kSmemBytes = kOffBar + 8 * kBars + 16;
@@ -88,6 +176,7 @@ struct Params {
     float* ws_lse;       // [slots][rows_cap]
     // chunk: query i sees the (compacted) keys c <= hi0 + i with c > hi0 + i - window or c < sinks
     int hi0, window, sinks;
+    const __nv_bfloat16 *k, *v;  // [128][keys][128]
     __nv_bfloat16* out;  // [rows][128][128]
 };
 
@@ -157,7 +246,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
     using namespace dev;
     using L = Layout<kQT>;
     extern __shared__ __align__(1024) uint8_t smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (through a shuffle, so that the compiler sees a value that is the warp's)
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bars = sbase + L::kOffBar;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 8 * L::kBars);
@@ -174,10 +264,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         mbar_init(bar(L::kBarQEmpty), 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar(L::kBarSFull + t), 1);
-            mbar_init(bar(L::kBarPReady + t), 128);
+            mbar_init(bar(L::kBarPReady + t), 4);  // one arrive per softmax warp
         }
         mbar_init(bar(L::kBarODone), 1);
-        mbar_init(bar(L::kBarOFree), 256);
+        mbar_init(bar(L::kBarOFree), 8);
         mbar_init(bar(L::kBarEnd), 1);
         *abort_flag = 0;
         fence_barrier_init();
@@ -189,7 +279,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     const WaitCtx w{p.timeout_ns, abort_flag, p.dev_error};
     Walk<kChunk, kQT> walk(p);
     Segment seg;
@@ -202,6 +292,16 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             // the prefix's keys and values are read once by one group of rows, k_R by every head
             const uint64_t pol_kv = kChunk || p.groups > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
             const uint64_t pol_kr = l2_policy_evict_last();
+            // keys and values of the tile kFetch ahead go into L2, so that a slot, which is free only a step
+            // before it is needed, is filled from there
+            const auto fetch = [&](int n) {
+                if (n >= seg.cnt) return;
+                const int j0 = key_tile(seg, n) * kTile;
+                const uint32_t bytes = (uint32_t)min(kTile, p.keys - j0) * 256;
+                const int64_t at = ((int64_t)seg.head * p.keys + j0) * 128;
+                prefetch_l2(p.k + at, bytes);
+                prefetch_l2(p.v + at, bytes);
+            };
             int r = 0, s = 0, phase = 0;
             bool ok = true;
             const auto take = [&]() {  // the next slot, free; its full barrier expects a slot's bytes
@@ -241,7 +341,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             while (ok && walk.next(p, seg)) {
                 constexpr int kAhead = kQT == 1 ? 2 : 1;  // key tiles ahead of the values
                 for (int n = 0; ok && n < kAhead && n < seg.cnt; ++n) load_k(key_tile(seg, n) * kTile);
+                for (int n = kAhead; n < kFetch; ++n) fetch(n);
                 for (int n = 0; ok && n < seg.cnt; ++n) {
+                    fetch(n + kFetch);
                     load_v(key_tile(seg, n) * kTile);
                     if (ok && n + kAhead < seg.cnt) load_k(key_tile(seg, n + kAhead) * kTile);
                 }
@@ -271,106 +373,104 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             if (n > 0) drain_phase(bar(L::kBarQFull), n - 1, w.timeout_ns);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = idesc_bf16(128, kTile, false, false);
-            constexpr uint32_t idesc_pv = idesc_bf16(128, 128, false, true);
-            const uint64_t q_desc = smem_desc(sbase, 16, 1024);
-            const uint64_t k_desc = smem_desc(sbase + L::kOffRing, 16, 1024);
-            const uint64_t v_desc = smem_desc(sbase + L::kOffRing, kSlotBytes / 2, 1024);
-            constexpr uint64_t kSlot16 = kSlotBytes >> 4;  // a slot, in the descriptors' 16-byte units
-            int s = 0, phase = 0;  // the next slot that no MMA has used yet
-            bool ok = true;
-            // Scores of stream t from the three slots at `s0`: waits for them when they are new, frees them
-            // when this is their last use.
-            const auto qk = [&](int t, int& s0, int& ph, bool fresh, bool last) {
-                const uint32_t d = tmem + 256 * t;
-                const uint64_t a0 = q_desc + (kQT == 2 ? t * 3 * kSlot16 : 0);
+        constexpr uint32_t idesc_qk = idesc_bf16(128, kTile, false, false);
+        constexpr uint32_t idesc_pv = idesc_bf16(128, 128, false, true);
+        const uint64_t q_desc = smem_desc(sbase, 16, 1024);
+        const uint64_t k_desc = smem_desc(sbase + L::kOffRing, 16, 1024);
+        const uint64_t v_desc = smem_desc(sbase + L::kOffRing, kSlotBytes / 2, 1024);
+        constexpr uint64_t kSlot16 = kSlotBytes >> 4;  // a slot, in the descriptors' 16-byte units
+        int s = 0, phase = 0;  // the next slot that no MMA has used yet
+        bool ok = true;
+        // Scores of stream t from the three slots at `s0`: waits for them when they are new, frees them
+        // when this is their last use.
+        const auto qk = [&](int t, int& s0, int& ph, bool fresh, bool last) {
+            const uint32_t d = tmem + 256 * t;
+            const uint64_t a0 = q_desc + (kQT == 2 ? t * 3 * kSlot16 : 0);
 #pragma unroll 1
-                for (int c = 0; c < 3; ++c) {
-                    if (fresh && !wait_phase(bar(L::kBarFull + s0), ph, w)) return ok = false;
-                    tc_fence_after();
-                    const uint64_t a = a0 + c * kSlot16, b = k_desc + s0 * kSlot16;
-                    mma_ss(d, a, b, idesc_qk, c != 0 ? 1u : 0u);
-                    mma_ss(d, a + 2, b + 2, idesc_qk, 1u);
-                    mma_ss(d, a + 4, b + 4, idesc_qk, 1u);
-                    mma_ss(d, a + 6, b + 6, idesc_qk, 1u);
-                    if (last) mma_commit(bar(L::kBarEmpty + s0));
-                    if (++s0 == L::kSlots) {
-                        s0 = 0;
-                        ++ph;
-                    }
-                }
-                mma_commit(bar(L::kBarSFull + t));
-                return true;
-            };
-            const auto pv = [&](int t, int& s0, int& ph, bool fresh, bool last, bool first_of_stream) {
-                const uint32_t pt = tmem + 256 * t, d = pt + 128;
-#pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    if (fresh && !wait_phase(bar(L::kBarFull + s0), ph, w)) return ok = false;
-                    tc_fence_after();
-                    const uint64_t b = v_desc + s0 * kSlot16;
-                    const uint32_t a = pt + 32 * c;
-                    mma_ts(d, a, b, idesc_pv, first_of_stream && c == 0 ? 0u : 1u);
-                    mma_ts(d, a + 8, b + (2048 >> 4), idesc_pv, 1u);
-                    mma_ts(d, a + 16, b + (4096 >> 4), idesc_pv, 1u);
-                    mma_ts(d, a + 24, b + (6144 >> 4), idesc_pv, 1u);
-                    if (last) mma_commit(bar(L::kBarEmpty + s0));
-                    if (++s0 == L::kSlots) {
-                        s0 = 0;
-                        ++ph;
-                    }
-                }
-                return true;
-            };
-            int n_seg = 0;
-            int done[2] = {0, 0};  // steps of each stream
-            while (ok && walk.next(p, seg)) {
-                if (!(ok = wait_phase(bar(L::kBarQFull), n_seg, w))) break;
+            for (int c = 0; c < 3; ++c) {
+                if (fresh && !wait_all(bar(L::kBarFull + s0), ph, w)) return ok = false;
                 tc_fence_after();
-                const int steps = kQT == 1 ? seg.cnt : 2 * seg.cnt;
-                if (kQT == 1) {
-                    qk(0, s, phase, true, true);
-                    if (ok && steps > 1) qk(1, s, phase, true, true);
-                } else {
-                    int s1 = s, ph1 = phase;
-                    qk(0, s1, ph1, true, false);
-                    if (ok) qk(1, s, phase, false, true);
+                const uint64_t a = a0 + c * kSlot16, b = k_desc + s0 * kSlot16;
+                mma_ss_one(d, a, b, idesc_qk, c != 0 ? 1u : 0u);
+                mma_ss_one(d, a + 2, b + 2, idesc_qk, 1u);
+                mma_ss_one(d, a + 4, b + 4, idesc_qk, 1u);
+                mma_ss_one(d, a + 6, b + 6, idesc_qk, 1u);
+                if (last) mma_commit_one(bar(L::kBarEmpty + s0));
+                if (++s0 == L::kSlots) {
+                    s0 = 0;
+                    ++ph;
                 }
-                if (!ok) break;
-                if (steps <= 2) mma_commit(bar(L::kBarQEmpty));
-                int sv = 0, pv_ph = 0, sk = 0, pk_ph = 0;  // kQT == 2: the slots of stream 0's values and keys
-                for (int i = 0; i < steps; ++i) {
-                    const int t = i & 1;
-                    if (!(ok = wait_phase(bar(L::kBarPReady + t), done[t], w))) break;
-                    ++done[t];
-                    tc_fence_after();
-                    if (i == 0 && n_seg > 0) {
-                        if (!(ok = wait_phase(bar(L::kBarOFree), n_seg - 1, w))) break;
-                        tc_fence_after();
-                    }
-                    if (kQT == 1) {
-                        if (!pv(t, s, phase, true, true, i < 2)) break;
-                        if (i + 2 < steps && !qk(t, s, phase, true, true)) break;
-                    } else if (t == 0) {
-                        sv = s;
-                        pv_ph = phase;
-                        if (!pv(0, s, phase, true, false, i < 2)) break;
-                        sk = s;
-                        pk_ph = phase;
-                        if (i + 2 < steps && !qk(0, s, phase, true, false)) break;
-                    } else {
-                        if (!pv(1, sv, pv_ph, false, true, i < 2)) break;
-                        if (i + 2 < steps && !qk(1, sk, pk_ph, false, true)) break;
-                    }
-                    if (i + 3 == steps) mma_commit(bar(L::kBarQEmpty));  // the segment's last QK
-                }
-                if (!ok) break;
-                mma_commit(bar(L::kBarODone));
-                ++n_seg;
             }
-            mma_commit(bar(L::kBarEnd));  // arrives when every MMA issued here has finished
+            mma_commit_one(bar(L::kBarSFull + t));
+            return true;
+        };
+        const auto pv = [&](int t, int& s0, int& ph, bool fresh, bool last, bool first_of_stream) {
+            const uint32_t pt = tmem + 256 * t, d = pt + 128;
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+                if (fresh && !wait_all(bar(L::kBarFull + s0), ph, w)) return ok = false;
+                tc_fence_after();
+                const uint64_t b = v_desc + s0 * kSlot16;
+                const uint32_t a = pt + 32 * c;
+                mma_ts_one(d, a, b, idesc_pv, first_of_stream && c == 0 ? 0u : 1u);
+                mma_ts_one(d, a + 8, b + (2048 >> 4), idesc_pv, 1u);
+                mma_ts_one(d, a + 16, b + (4096 >> 4), idesc_pv, 1u);
+                mma_ts_one(d, a + 24, b + (6144 >> 4), idesc_pv, 1u);
+                if (last) mma_commit_one(bar(L::kBarEmpty + s0));
+                if (++s0 == L::kSlots) {
+                    s0 = 0;
+                    ++ph;
+                }
+            }
+            return true;
+        };
+        int n_seg = 0;
+        int done[2] = {0, 0};  // steps of each stream
+        while (ok && walk.next(p, seg)) {
+            if (!(ok = wait_all(bar(L::kBarQFull), n_seg, w))) break;
+            tc_fence_after();
+            const int steps = kQT == 1 ? seg.cnt : 2 * seg.cnt;
+            if (kQT == 1) {
+                qk(0, s, phase, true, true);
+                if (ok && steps > 1) qk(1, s, phase, true, true);
+            } else {
+                int s1 = s, ph1 = phase;
+                qk(0, s1, ph1, true, false);
+                if (ok) qk(1, s, phase, false, true);
+            }
+            if (!ok) break;
+            if (steps <= 2) mma_commit_one(bar(L::kBarQEmpty));
+            int sv = 0, pv_ph = 0, sk = 0, pk_ph = 0;  // kQT == 2: the slots of stream 0's values and keys
+            for (int i = 0; i < steps; ++i) {
+                const int t = i & 1;
+                if (!(ok = wait_all(bar(L::kBarPReady + t), done[t], w))) break;
+                ++done[t];
+                tc_fence_after();
+                if (i == 0 && n_seg > 0) {
+                    if (!(ok = wait_all(bar(L::kBarOFree), n_seg - 1, w))) break;
+                    tc_fence_after();
+                }
+                if (kQT == 1) {
+                    if (!pv(t, s, phase, true, true, i < 2)) break;
+                    if (i + 2 < steps && !qk(t, s, phase, true, true)) break;
+                } else if (t == 0) {
+                    sv = s;
+                    pv_ph = phase;
+                    if (!pv(0, s, phase, true, false, i < 2)) break;
+                    sk = s;
+                    pk_ph = phase;
+                    if (i + 2 < steps && !qk(0, s, phase, true, false)) break;
+                } else {
+                    if (!pv(1, sv, pv_ph, false, true, i < 2)) break;
+                    if (i + 2 < steps && !qk(1, sk, pk_ph, false, true)) break;
+                }
+                if (i + 3 == steps) mma_commit_one(bar(L::kBarQEmpty));  // the segment's last QK
+            }
+            if (!ok) break;
+            mma_commit_one(bar(L::kBarODone));
+            ++n_seg;
         }
+        mma_commit_one(bar(L::kBarEnd));  // arrives when every MMA issued here has finished
     } else {
         // softmax of stream t: warp (3..10) & 3 selects the TMEM lane quarter, one row per thread
         const int t = (warp - kSoftmaxWarp0) >> 2;
@@ -418,9 +518,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     float m4[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        m4[c] = __uint_as_float(sr[c][0]);
+                        m4[c] = fmaxf(__uint_as_float(sr[c][0]), __uint_as_float(sr[c][1]));
 #pragma unroll
-                        for (int x = 1; x < 32; ++x) m4[c] = fmaxf(m4[c], __uint_as_float(sr[c][x]));
+                        for (int x = 2; x < 32; x += 2)
+                            m4[c] = max3(m4[c], __uint_as_float(sr[c][x]), __uint_as_float(sr[c][x + 1]));
                     }
                     const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
                     // The running maximum: set by the stream's first tile, moved later only by more than the
@@ -442,25 +543,31 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                         }
                     }
                     const float base = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), base2 = pair(-base, -base);
+                    uint64_t sum[2] = {0, 0};  // pairs of zeros
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
-                            const float a = ex2_approx(fmaf(__uint_as_float(sr[c][2 * x]), p.scale_log2, -base));
-                            const float b = ex2_approx(fmaf(__uint_as_float(sr[c][2 * x + 1]), p.scale_log2, -base));
-                            sum[(2 * x) & 3] += a;
-                            sum[(2 * x + 1) & 3] += b;
+                            float a, b;
+                            unpair(fma2(pair(__uint_as_float(sr[c][2 * x]), __uint_as_float(sr[c][2 * x + 1])), scale2, base2),
+                                   a, b);
+                            a = ex2_approx(a);
+                            b = ex2_approx(b);
+                            sum[x & 1] = add2(sum[x & 1], pair(a, b));
                             pk[x] = pack_bf16x2(a, b);
                         }
                         tmem_st16(t_s + 16 * c, pk);
                     }
-                    l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    float s0, s1;
+                    unpair(add2(sum[0], sum[1]), s0, s1);
+                    l = l * f + (s0 + s1);
                     tmem_wait_st();
                 }
                 tc_fence_before();
-                mbar_arrive(bar(L::kBarPReady + t));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::kBarPReady + t));
             }
             ok = ok && wait_warp(bar(L::kBarODone), n_seg, w);
             tc_fence_after();
@@ -537,7 +644,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 }
             }
             tc_fence_before();
-            mbar_arrive(bar(L::kBarOFree));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::kBarOFree));
             ++n_seg;
         }
     }
