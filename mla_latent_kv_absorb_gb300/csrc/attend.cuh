@@ -17,8 +17,8 @@
 // on two "streams", each with a score buffer S, an output O and a running softmax (m, l) of its own:
 // with two query tiles a stream is a tile, and both use every key tile; with one query tile the even
 // key tiles are one stream and the odd ones the other, and the two are joined at the end, so that one
-// stream's softmax always has the other's products to hide behind and neither waits for the other's
-// running maximum.  Step i belongs to stream i & 1; the MMA order is PV(i), QK(i + 2).
+// stream's softmax always has the other's products to hide behind.  Step i belongs to stream i & 1; the
+// MMA order is PV(i), QK(i + 2).
 //   QK:  S[128 x 128] = Q [128 x 192] (q_c | q_R: three 64-column chunks in shared memory)
 //                       x K tile [128 x 192] (k | k_R: three K-major chunks)
 //   PV:  O[128 x 128] += P [128 x 128] (bf16 in TMEM over the first half of S) x V tile (MN-major)
@@ -26,10 +26,13 @@
 // first need it: a key chunk [128 keys][64] or 64 keys' values [64][128].  A slot is four MMAs, so
 // the ring is as fine as the tensor core's work and a slot is free as soon as its four are done.
 //
-// Warp 0 streams the ring, warp 2 the query tiles, warp 1 issues the MMAs, warps 3-6 and 7-10 are
-// the streams' softmax, one row per thread, the row's 128 scores in registers.  The running maximum
-// moves only when a tile's exceeds it by more than 8 (log2 units).  P is rounded to bf16 for the
-// PV product (its sum l takes the unrounded values); scores, maxima, sums and O are fp32.
+// Warp 0 streams the ring, warp 2 the query tiles, warp 1 issues the MMAs, warps 3-10 are the softmax
+// of every step: a thread has half of a row, 64 scores in registers, and the two halves of a row agree on
+// its maximum through shared memory.  (What bounds a CTA with two query tiles is the chain QK -> softmax ->
+// PV of a stream against the other stream's products: with four warps to a stream and whole rows a step's
+// softmax took 1,530 cycles of that chain, twice as many as a step's MMAs.)  The running maximum moves only
+// when a tile's exceeds it by more than 8 (log2 units).  P is rounded to bf16 for the PV product (its sum l
+// takes the unrounded values); scores, maxima, sums and O are fp32.
 //
 // The prefix form is persistent: the (head, row group, key tile) units lie in one line that the CTAs
 // cut evenly, so that every SM streams the same number of bytes; a CTA's piece of one (head, group)
@@ -79,11 +82,36 @@ __device__ __forceinline__ void mma_commit_one(uint32_t bar)
         : "memory");
 }
 
-// A wait whose answer is the same in all lanes (a vote), with the polling out of line.
+// A bounded wait (as dev::wait_phase) that looks at the timer, which is slow to read, once in many polls.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns,
+                                       uint32_t* dev_error)
+{
+    const uint64_t t0 = dev::globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int k = 0; k < 64; ++k)
+            if (dev::mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if (dev::globaltimer_ns() - t0 > timeout_ns) {
+            *abort = 1;
+            dev::raise_error(dev_error, MLA_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// The whole warp waits; the answer is a vote, the same in all lanes.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t phase, const WaitCtx& w)
 {
     if (__all_sync(0xffffffffu, dev::mbar_try_wait(bar, phase & 1u))) return true;
-    return __all_sync(0xffffffffu, dev::wait_phase_slow<false>(bar, phase, w.abort, w.timeout_ns, w.dev_error));
+    return __all_sync(0xffffffffu, wait_slow(bar, phase & 1u, w.abort, w.timeout_ns, w.dev_error));
+}
+
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(one));
+    return one != 0;
 }
 
 // ---- Two floats at a time (one instruction each on sm_103a), and the largest of three.
@@ -121,6 +149,13 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
+__device__ __forceinline__ void prefetch_tile_3d(const void* map, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 // `bytes` (a multiple of 16) from `p` into L2, without waiting.
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes)
 {
@@ -138,14 +173,15 @@ constexpr uint32_t kJoinBarrier = 1;       // named barrier of the eight softmax
 
 template <int kQT>
 struct Layout {
-    static constexpr int kSlots = kQT == 1 ? 11 : 8;
-    static constexpr int kOffRing = kQT * 3 * kSlotBytes;
-    static constexpr int kOffXchg = kOffRing + kSlots * kSlotBytes;  // m and l of both streams
+    static constexpr int kSlots = 8;
+    static constexpr int kQBufs = 2 / kQT;  // with one query tile the next segment's is loaded beside it
+    static constexpr int kOffRing = 2 * 3 * kSlotBytes;
+    static constexpr int kOffXchg = kOffRing + kSlots * kSlotBytes;  // [slot 2][half 2][128]
     static constexpr int kOffBar = kOffXchg + 2 * 2 * kTile * 4;
     static constexpr int kBarFull = 0, kBarEmpty = kSlots;
-    static constexpr int kBarQFull = 2 * kSlots, kBarQEmpty = kBarQFull + 1;
-    static constexpr int kBarSFull = kBarQFull + 2;   // [stream]
-    static constexpr int kBarPReady = kBarSFull + 2;  // [stream], four warps' arrivals
+    static constexpr int kBarQFull = 2 * kSlots, kBarQEmpty = kBarQFull + 2;  // [buffer]
+    static constexpr int kBarSFull = kBarQEmpty + 2;  // [stream]
+    static constexpr int kBarPReady = kBarSFull + 2;  // [stream], eight warps' arrivals
     static constexpr int kBarODone = kBarPReady + 2;  // the segment's last PV has finished
     static constexpr int kBarOFree = kBarODone + 1;   // eight warps' arrivals: the segment's O has been read
     static constexpr int kBarEnd = kBarOFree + 1;     // every MMA of the CTA has finished
@@ -157,7 +193,7 @@ struct Layout {
 //   S full [t]   completes once per step of stream t; QK(i + 2) is issued only after the MMA thread
 //                has seen P(i) ready, i.e. after the stream's softmax has finished step i.
 //   P ready [t]  arrives once per step; P(i + 2) needs S(i + 2), issued after that wait.
-//   Q full       one query load per segment, issued after Q empty (the segment's last QK committed).
+//   Q full       a query load into a buffer is issued after its Q empty (the last QK of the segment before).
 //   O done       once per segment; the next one's needs its first PV, which waits for O free, for
 //                which every softmax thread has to have waited for O done.
 //   ring         a slot is refilled only after its empty barrier, waited in order.
@@ -234,6 +270,25 @@ struct Walk {
     }
 };
 
+// 32 columns of a row.
+__device__ __forceinline__ void store_fp32(float* dst, const uint32_t (&o)[32])
+{
+#pragma unroll
+    for (int v = 0; v < 8; ++v)
+        reinterpret_cast<uint4*>(dst)[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+}
+
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const uint32_t (&o)[32])
+{
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+        reinterpret_cast<uint4*>(dst)[v] =
+            make_uint4(dev::pack_bf16x2(__uint_as_float(o[8 * v + 0]), __uint_as_float(o[8 * v + 1])),
+                       dev::pack_bf16x2(__uint_as_float(o[8 * v + 2]), __uint_as_float(o[8 * v + 3])),
+                       dev::pack_bf16x2(__uint_as_float(o[8 * v + 4]), __uint_as_float(o[8 * v + 5])),
+                       dev::pack_bf16x2(__uint_as_float(o[8 * v + 6]), __uint_as_float(o[8 * v + 7])));
+}
+
 __device__ __forceinline__ int key_tile(const Segment& s, int n) { return n < s.lead ? n : s.tile0 + n; }
 
 template <bool kChunk, int kQT>
@@ -260,11 +315,11 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2 * L::kSlots; ++s) mbar_init(bar(s), 1);
-        mbar_init(bar(L::kBarQFull), 1);
-        mbar_init(bar(L::kBarQEmpty), 1);
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(bar(L::kBarSFull + t), 1);
-            mbar_init(bar(L::kBarPReady + t), 4);  // one arrive per softmax warp
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(L::kBarQFull + b), 1);
+            mbar_init(bar(L::kBarQEmpty + b), 1);
+            mbar_init(bar(L::kBarSFull + b), 1);
+            mbar_init(bar(L::kBarPReady + b), 8);  // one arrive per softmax warp
         }
         mbar_init(bar(L::kBarODone), 1);
         mbar_init(bar(L::kBarOFree), 8);
@@ -285,93 +340,115 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
     Segment seg;
 
     if (warp == 0) {
-        if (lane == 0) {
+        const bool leader = elect_lane();
+        // the prefix's keys and values are read once by one group of rows, k_R by every head
+        const uint64_t pol_kv = kChunk || p.groups > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
+        const uint64_t pol_kr = l2_policy_evict_last();
+        // Keys and values of the tile kFetch ahead go into L2, so that a slot, which is free only a step
+        // before it is needed, is filled from there.
+        const auto fetch = [&](int n) {
+            if (n >= seg.cnt) return;
+            const int j0 = key_tile(seg, n) * kTile;
+            const uint32_t bytes = (uint32_t)min(kTile, p.keys - j0) * 256;
+            const int64_t at = ((int64_t)seg.head * p.keys + j0) * 128;
+            if (leader) {
+                prefetch_l2(p.k + at, bytes);
+                prefetch_l2(p.v + at, bytes);
+            }
+        };
+        int r = 0, s = 0, phase = 0;
+        bool ok = true;
+        const auto take = [&]() {  // the next slot, free
+            return ok = r < L::kSlots || wait_all(bar(L::kBarEmpty + s), phase - 1, w);
+        };
+        const auto put = [&]() {
+            ++r;
+            if (++s == L::kSlots) {
+                s = 0;
+                ++phase;
+            }
+        };
+        const auto load_k = [&](int j0) {
+#pragma unroll 1
+            for (int c = 0; c < 3; ++c) {
+                if (!take()) return;
+                const uint32_t dst = sbase + L::kOffRing + s * kSlotBytes, full = bar(L::kBarFull + s);
+                if (leader) {
+                    mbar_arrive_expect_tx(full, kSlotBytes);
+                    if (c < 2)
+                        tma_load_3d(dst, &tm_k, full, 64 * c, j0, seg.head, pol_kv);
+                    else
+                        tma_load_2d(dst, &tm_kr, full, 0, j0, pol_kr);
+                }
+                put();
+            }
+        };
+        const auto load_v = [&](int j0) {
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+                if (!take()) return;
+                const uint32_t dst = sbase + L::kOffRing + s * kSlotBytes, full = bar(L::kBarFull + s);
+                if (leader) {
+                    mbar_arrive_expect_tx(full, kSlotBytes);
+                    tma_load_3d(dst, &tm_v, full, 0, j0 + 64 * c, seg.head, pol_kv);
+                    tma_load_3d(dst + kSlotBytes / 2, &tm_v, full, 64, j0 + 64 * c, seg.head, pol_kv);
+                }
+                put();
+            }
+        };
+        if (leader) {
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_kr);
             tma_prefetch_desc(&tm_v);
-            // the prefix's keys and values are read once by one group of rows, k_R by every head
-            const uint64_t pol_kv = kChunk || p.groups > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-            const uint64_t pol_kr = l2_policy_evict_last();
-            // keys and values of the tile kFetch ahead go into L2, so that a slot, which is free only a step
-            // before it is needed, is filled from there
-            const auto fetch = [&](int n) {
-                if (n >= seg.cnt) return;
-                const int j0 = key_tile(seg, n) * kTile;
-                const uint32_t bytes = (uint32_t)min(kTile, p.keys - j0) * 256;
-                const int64_t at = ((int64_t)seg.head * p.keys + j0) * 128;
-                prefetch_l2(p.k + at, bytes);
-                prefetch_l2(p.v + at, bytes);
-            };
-            int r = 0, s = 0, phase = 0;
-            bool ok = true;
-            const auto take = [&]() {  // the next slot, free; its full barrier expects a slot's bytes
-                if (r >= L::kSlots && !wait_phase(bar(L::kBarEmpty + s), phase - 1, w)) return ok = false;
-                mbar_arrive_expect_tx(bar(L::kBarFull + s), kSlotBytes);
-                return true;
-            };
-            const auto put = [&]() {
-                ++r;
-                if (++s == L::kSlots) {
-                    s = 0;
-                    ++phase;
-                }
-            };
-            const auto load_k = [&](int j0) {
-#pragma unroll 1
-                for (int c = 0; c < 3; ++c) {
-                    if (!take()) return;
-                    const uint32_t dst = sbase + L::kOffRing + s * kSlotBytes;
-                    if (c < 2)
-                        tma_load_3d(dst, &tm_k, bar(L::kBarFull + s), 64 * c, j0, seg.head, pol_kv);
-                    else
-                        tma_load_2d(dst, &tm_kr, bar(L::kBarFull + s), 0, j0, pol_kr);
-                    put();
-                }
-            };
-            const auto load_v = [&](int j0) {
-#pragma unroll 1
-                for (int c = 0; c < 2; ++c) {
-                    if (!take()) return;
-                    const uint32_t dst = sbase + L::kOffRing + s * kSlotBytes;
-                    tma_load_3d(dst, &tm_v, bar(L::kBarFull + s), 0, j0 + 64 * c, seg.head, pol_kv);
-                    tma_load_3d(dst + kSlotBytes / 2, &tm_v, bar(L::kBarFull + s), 64, j0 + 64 * c, seg.head, pol_kv);
-                    put();
-                }
-            };
-            while (ok && walk.next(p, seg)) {
-                constexpr int kAhead = kQT == 1 ? 2 : 1;  // key tiles ahead of the values
-                for (int n = 0; ok && n < kAhead && n < seg.cnt; ++n) load_k(key_tile(seg, n) * kTile);
-                for (int n = kAhead; n < kFetch; ++n) fetch(n);
-                for (int n = 0; ok && n < seg.cnt; ++n) {
-                    fetch(n + kFetch);
-                    load_v(key_tile(seg, n) * kTile);
-                    if (ok && n + kAhead < seg.cnt) load_k(key_tile(seg, n + kAhead) * kTile);
-                }
-            }
-            // loads in flight land before the CTA can exit
-            for (int k = r > L::kSlots ? r - L::kSlots : 0; k < r; ++k)
-                drain_phase(bar(L::kBarFull + k % L::kSlots), k / L::kSlots, w.timeout_ns);
         }
+        while (ok && walk.next(p, seg)) {
+            constexpr int kAhead = kQT == 1 ? 2 : 1;  // key tiles ahead of the values
+            for (int n = 0; ok && n < kAhead && n < seg.cnt; ++n) load_k(key_tile(seg, n) * kTile);
+            for (int n = kAhead; n < kFetch; ++n) fetch(n);
+            for (int n = 0; ok && n < seg.cnt; ++n) {
+                fetch(n + kFetch);
+                load_v(key_tile(seg, n) * kTile);
+                if (ok && n + kAhead < seg.cnt) load_k(key_tile(seg, n + kAhead) * kTile);
+            }
+        }
+        // loads in flight land before the CTA can exit
+        for (int k = r > L::kSlots ? r - L::kSlots : 0; k < r; ++k)
+            drain_phase(bar(L::kBarFull + k % L::kSlots), k / L::kSlots, w.timeout_ns);
     } else if (warp == 2) {
-        if (lane == 0) {
+        const bool leader = elect_lane();
+        const uint64_t pol = l2_policy_evict_last();
+        if (leader) {
             tma_prefetch_desc(&tm_qc);
             tma_prefetch_desc(&tm_qr);
-            const uint64_t pol = l2_policy_evict_last();
-            int n = 0;
-            while (walk.next(p, seg)) {
-                if (n > 0 && !wait_phase(bar(L::kBarQEmpty), n - 1, w)) break;
-                mbar_arrive_expect_tx(bar(L::kBarQFull), kQT * 3 * kSlotBytes);
-                for (int t = 0; t < kQT; ++t) {
-                    const uint32_t q = sbase + t * 3 * kSlotBytes;
-                    const int row = seg.row0 + kTile * t;
-                    tma_load_3d(q, &tm_qc, bar(L::kBarQFull), 0, seg.head, row, pol);
-                    tma_load_3d(q + kSlotBytes, &tm_qc, bar(L::kBarQFull), 64, seg.head, row, pol);
-                    tma_load_3d(q + 2 * kSlotBytes, &tm_qr, bar(L::kBarQFull), 0, seg.head, row, pol);
-                }
-                ++n;
-            }
-            if (n > 0) drain_phase(bar(L::kBarQFull), n - 1, w.timeout_ns);
         }
+        int n = 0;
+        bool more = walk.next(p, seg);
+        while (more) {
+            const int b = n % L::kQBufs;
+            if (n >= L::kQBufs && !wait_all(bar(L::kBarQEmpty + b), n / L::kQBufs - 1, w)) break;
+            if (leader) {
+                const uint32_t full = bar(L::kBarQFull + b);
+                mbar_arrive_expect_tx(full, kQT * 3 * kSlotBytes);
+                for (int t = 0; t < kQT; ++t) {
+                    const uint32_t q = sbase + (b + t) * 3 * kSlotBytes;
+                    const int row = seg.row0 + kTile * t;
+                    tma_load_3d(q, &tm_qc, full, 0, seg.head, row, pol);
+                    tma_load_3d(q + kSlotBytes, &tm_qc, full, 64, seg.head, row, pol);
+                    tma_load_3d(q + 2 * kSlotBytes, &tm_qr, full, 0, seg.head, row, pol);
+                }
+            }
+            ++n;
+            more = walk.next(p, seg);
+            if (more && leader && L::kQBufs == 1)  // two tiles have no second buffer: the next ones wait in L2
+                for (int t = 0; t < kQT; ++t) {
+                    const int row = seg.row0 + kTile * t;
+                    prefetch_tile_3d(&tm_qc, 0, seg.head, row);
+                    prefetch_tile_3d(&tm_qc, 64, seg.head, row);
+                    prefetch_tile_3d(&tm_qr, 0, seg.head, row);
+                }
+        }
+        for (int k = n > L::kQBufs ? n - L::kQBufs : 0; k < n; ++k)
+            drain_phase(bar(L::kBarQFull + k % L::kQBufs), k / L::kQBufs, w.timeout_ns);
     } else if (warp == 1) {
         constexpr uint32_t idesc_qk = idesc_bf16(128, kTile, false, false);
         constexpr uint32_t idesc_pv = idesc_bf16(128, 128, false, true);
@@ -380,12 +457,13 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         const uint64_t v_desc = smem_desc(sbase + L::kOffRing, kSlotBytes / 2, 1024);
         constexpr uint64_t kSlot16 = kSlotBytes >> 4;  // a slot, in the descriptors' 16-byte units
         int s = 0, phase = 0;  // the next slot that no MMA has used yet
+        int q_buf = 0;
         bool ok = true;
         // Scores of stream t from the three slots at `s0`: waits for them when they are new, frees them
         // when this is their last use.
         const auto qk = [&](int t, int& s0, int& ph, bool fresh, bool last) {
             const uint32_t d = tmem + 256 * t;
-            const uint64_t a0 = q_desc + (kQT == 2 ? t * 3 * kSlot16 : 0);
+            const uint64_t a0 = q_desc + (kQT == 2 ? t : q_buf) * 3 * kSlot16;
 #pragma unroll 1
             for (int c = 0; c < 3; ++c) {
                 if (fresh && !wait_all(bar(L::kBarFull + s0), ph, w)) return ok = false;
@@ -427,7 +505,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         int n_seg = 0;
         int done[2] = {0, 0};  // steps of each stream
         while (ok && walk.next(p, seg)) {
-            if (!(ok = wait_all(bar(L::kBarQFull), n_seg, w))) break;
+            q_buf = n_seg % L::kQBufs;
+            if (!(ok = wait_all(bar(L::kBarQFull + q_buf), n_seg / L::kQBufs, w))) break;
             tc_fence_after();
             const int steps = kQT == 1 ? seg.cnt : 2 * seg.cnt;
             if (kQT == 1) {
@@ -439,7 +518,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 if (ok) qk(1, s, phase, false, true);
             }
             if (!ok) break;
-            if (steps <= 2) mma_commit_one(bar(L::kBarQEmpty));
+            if (steps <= 2) mma_commit_one(bar(L::kBarQEmpty + q_buf));
             int sv = 0, pv_ph = 0, sk = 0, pk_ph = 0;  // kQT == 2: the slots of stream 0's values and keys
             for (int i = 0; i < steps; ++i) {
                 const int t = i & 1;
@@ -464,7 +543,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     if (!pv(1, sv, pv_ph, false, true, i < 2)) break;
                     if (i + 2 < steps && !qk(1, sk, pk_ph, false, true)) break;
                 }
-                if (i + 3 == steps) mma_commit_one(bar(L::kBarQEmpty));  // the segment's last QK
+                if (i + 3 == steps) mma_commit_one(bar(L::kBarQEmpty + q_buf));  // the segment's last QK
             }
             if (!ok) break;
             mma_commit_one(bar(L::kBarODone));
@@ -472,68 +551,78 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         }
         mma_commit_one(bar(L::kBarEnd));  // arrives when every MMA issued here has finished
     } else {
-        // softmax of stream t: warp (3..10) & 3 selects the TMEM lane quarter, one row per thread
-        const int t = (warp - kSoftmaxWarp0) >> 2;
+        // softmax: warp (3..10) & 3 selects the TMEM lane quarter, a thread has columns 64 half .. of one row
+        const int half = (warp - kSoftmaxWarp0) >> 2;
         const int q4 = warp & 3, row = 32 * q4 + lane;
         const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
-        const uint32_t t_s = tmem + lane_base + 256 * t, t_o = t_s + 128;
-        float* xchg = reinterpret_cast<float*>(smem + L::kOffXchg);  // [stream][m, l][128]
+        float* xchg = reinterpret_cast<float*>(smem + L::kOffXchg);  // [slot][half][128]
         int n_seg = 0, n_step = 0;
-        bool ok = true;
-        while (ok && walk.next(p, seg)) {
-            const int tile_row = seg.row0 + (kQT == 2 ? kTile * t : 0);
-            const int i = tile_row + row;                                 // this thread's query row
-            const bool any_row = tile_row + 32 * q4 < p.rows;             // the warp has a row at all
-            const int hi = p.hi0 + min(i, p.rows - 1), lo = hi - p.window + 1;  // chunk: the row's window
-            const int mine = kQT == 1 ? (seg.cnt + 1 - t) >> 1 : seg.cnt;
-            float m = -INFINITY, l = 0.f;
-            for (int k = 0; k < mine; ++k, ++n_step) {
-                if (!(ok = wait_warp(bar(L::kBarSFull + t), n_step, w))) break;
+        int seen[2] = {0, 0};  // steps of each stream
+        bool out = false;
+        while (!out && walk.next(p, seg)) {
+            const int steps = kQT == 1 ? seg.cnt : 2 * seg.cnt;
+            // this stream's running softmax and the other's, which change places after every step
+            float m = -INFINITY, l = 0.f, m_other = -INFINITY, l_other = 0.f;
+            bool ok = true;
+#pragma unroll 1
+            for (int i = 0; i < steps; ++i, ++n_step) {
+                const int t = i & 1;
+                const int tile_row = seg.row0 + (kQT == 2 ? kTile * t : 0);
+                const bool any_row = tile_row + 32 * q4 < p.rows;  // the warp has a row at all
+                const uint32_t t_s = tmem + lane_base + 256 * t;
+                ok = wait_all(bar(L::kBarSFull + t), seen[t], w);
+                ++seen[t];
                 tc_fence_after();
-                if (any_row) {
-                    const int j0 = key_tile(seg, kQT == 1 ? 2 * k + t : k) * kTile;
-                    uint32_t sr[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, sr[c]);
+                uint32_t sr[2][32];
+                float mt = -INFINITY;
+                if (any_row && ok) {
+                    tmem_ld32(t_s + 64 * half, sr[0]);
+                    tmem_ld32(t_s + 64 * half + 32, sr[1]);
                     tmem_wait_ld();
                     // keys that the row does not see get -infinity
+                    const int j0 = key_tile(seg, kQT == 1 ? i : i >> 1) * kTile + 64 * half;
                     if (kChunk) {
-                        const bool whole = j0 + kTile - 1 <= hi && (j0 >= lo || j0 + kTile <= p.sinks);
+                        const int hi = p.hi0 + min(tile_row + row, p.rows - 1), lo = hi - p.window + 1;
+                        const bool whole = j0 + 63 <= hi && (j0 >= lo || j0 + 64 <= p.sinks);
                         if (__any_sync(0xffffffffu, !whole)) {
 #pragma unroll
-                            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                                for (int x = 0; x < 32; ++x) {
-                                    const int j = j0 + 32 * c + x;
-                                    if (j > hi || (j < lo && j >= p.sinks)) sr[c][x] = 0xff800000u;
-                                }
+                            for (int x = 0; x < 64; ++x)
+                                if (j0 + x > hi || (j0 + x < lo && j0 + x >= p.sinks)) sr[x >> 5][x & 31] = 0xff800000u;
                         }
-                    } else if (j0 + kTile > p.keys) {
+                    } else if (j0 + 64 > p.keys) {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                if (j0 + 32 * c + x >= p.keys) sr[c][x] = 0xff800000u;
+                        for (int x = 0; x < 64; ++x)
+                            if (j0 + x >= p.keys) sr[x >> 5][x & 31] = 0xff800000u;
                     }
                     float m4[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        m4[c] = fmaxf(__uint_as_float(sr[c][0]), __uint_as_float(sr[c][1]));
+                        const uint32_t* v = &sr[c >> 1][16 * (c & 1)];
+                        m4[c] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
 #pragma unroll
-                        for (int x = 2; x < 32; x += 2)
-                            m4[c] = max3(m4[c], __uint_as_float(sr[c][x]), __uint_as_float(sr[c][x + 1]));
+                        for (int x = 2; x < 16; x += 2) m4[c] = max3(m4[c], __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
                     }
-                    const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+                    mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * p.scale_log2;
+                }
+                float* xs = xchg + (n_step & 1) * 2 * kTile;
+                xs[half * kTile + row] = mt;
+                // Both halves reach every barrier equally often: a failed wait only clears `ok`, and each
+                // barrier ORs the abort state so that all leave together.  Behind it both halves' scores have
+                // left TMEM, and P may be written over them.
+                if ((out = named_barrier_or(kJoinBarrier, 256, !ok || *w.abort))) break;
+                if (any_row) {
+                    mt = fmaxf(mt, xs[(half ^ 1) * kTile + row]);
                     // The running maximum: set by the stream's first tile, moved later only by more than the
-                    // threshold.  While a row has seen no key it stays at -infinity and f is 0 times 0.
+                    // threshold.  While a row has seen no key it stays at -infinity and O and l at 0.
                     const bool grow = mt > m + kRescaleLog2 || m == -INFINITY;
                     const float f = grow && m != -INFINITY ? ex2_approx(m - mt) : 1.f;
                     if (grow) m = mt;
-                    if (k > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+                    if (i > 1 && __any_sync(0xffffffffu, f != 1.f)) {
                         // O's earlier PVs have finished: S(i) complete implies it (QK(i) was issued after
                         // PV(i - 2), and a commit covers every earlier MMA of the thread)
+                        const uint32_t t_o = t_s + 128 + 64 * half;
 #pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
+                        for (int c = 0; c < 4; ++c) {
                             uint32_t o[16];
                             tmem_ld16(t_o + 16 * c, o);
                             tmem_wait_ld();
@@ -546,7 +635,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), base2 = pair(-base, -base);
                     uint64_t sum[2] = {0, 0};  // pairs of zeros
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
@@ -558,7 +647,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                             sum[x & 1] = add2(sum[x & 1], pair(a, b));
                             pk[x] = pack_bf16x2(a, b);
                         }
-                        tmem_st16(t_s + 16 * c, pk);
+                        tmem_st16(t_s + 32 * half + 16 * c, pk);
                     }
                     float s0, s1;
                     unpair(add2(sum[0], sum[1]), s0, s1);
@@ -568,79 +657,84 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::kBarPReady + t));
+                float swap = m;
+                m = m_other;
+                m_other = swap;
+                swap = l;
+                l = l_other;
+                l_other = swap;
             }
-            ok = ok && wait_warp(bar(L::kBarODone), n_seg, w);
+            if (out) break;
+            if (steps & 1) {  // stream 0's are in m and l after an even number of steps
+                float swap = m;
+                m = m_other;
+                m_other = swap;
+                swap = l;
+                l = l_other;
+                l_other = swap;
+            }
+            // the two halves' sums: written when the last step's maxima have been read, read before the next
+            // segment's are written
+            ok = wait_all(bar(L::kBarODone), n_seg, w);
+            if ((out = named_barrier_or(kJoinBarrier, 256, !ok || *w.abort))) break;
+            xchg[half * kTile + row] = l;
+            xchg[(2 + half) * kTile + row] = l_other;
+            if ((out = named_barrier_or(kJoinBarrier, 256, *w.abort))) break;
+            l += xchg[(half ^ 1) * kTile + row];
+            l_other += xchg[(2 + (half ^ 1)) * kTile + row];
+            if ((out = named_barrier_or(kJoinBarrier, 256, *w.abort))) break;
             tc_fence_after();
+            const uint32_t t_o = tmem + lane_base + 128 + 64 * half;
             if (kQT == 2) {
-                if (!ok) break;
-                if (any_row) {
-                    const float inv = 1.f / l;
-                    const bool real = i < p.rows;
-                    float* part = kChunk ? nullptr : p.ws_o + ((int64_t)seg.slot * p.rows_cap + (i - seg.row0)) * 128;
-                    __nv_bfloat16* dst = kChunk ? p.out + ((int64_t)i * 128 + seg.head) * 128 : nullptr;
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                for (int t = 0; t < 2; ++t) {
+                    const int tile_row = seg.row0 + kTile * t, i = tile_row + row;
+                    if (tile_row + 32 * q4 >= p.rows) continue;
+                    const float total = t ? l_other : l, top = t ? m_other : m;
+                    const float inv = 1.f / total;
+                    const int64_t at = (int64_t)seg.slot * p.rows_cap + (i - seg.row0);
+#pragma unroll 1
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t o[32];
-                        tmem_ld32(t_o + 32 * c, o);
+                        tmem_ld32(t_o + 256 * t + 32 * c, o);
                         tmem_wait_ld();
-                        if (!real) continue;
+                        if (i >= p.rows) continue;
 #pragma unroll
                         for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * inv);
-                        if (kChunk) {
-#pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                reinterpret_cast<uint4*>(dst + 32 * c)[v] = make_uint4(
-                                    pack_bf16x2(__uint_as_float(o[8 * v + 0]), __uint_as_float(o[8 * v + 1])),
-                                    pack_bf16x2(__uint_as_float(o[8 * v + 2]), __uint_as_float(o[8 * v + 3])),
-                                    pack_bf16x2(__uint_as_float(o[8 * v + 4]), __uint_as_float(o[8 * v + 5])),
-                                    pack_bf16x2(__uint_as_float(o[8 * v + 6]), __uint_as_float(o[8 * v + 7])));
-                        } else {
-#pragma unroll
-                            for (int v = 0; v < 8; ++v)
-                                reinterpret_cast<uint4*>(part + 32 * c)[v] =
-                                    make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-                        }
+                        if (kChunk)
+                            store_bf16(p.out + ((int64_t)i * 128 + seg.head) * 128 + 64 * half + 32 * c, o);
+                        else
+                            store_fp32(p.ws_o + at * 128 + 64 * half + 32 * c, o);
                     }
-                    if (!kChunk && real)
-                        p.ws_lse[(int64_t)seg.slot * p.rows_cap + (i - seg.row0)] = (m + log2f(l)) * 0.69314718055994531f;
+                    if (!kChunk && half == 0 && i < p.rows) p.ws_lse[at] = (top + log2f(total)) * 0.69314718055994531f;
                 }
             } else {
-                // join the two streams: each four warps write half of the columns
-                xchg[(2 * t) * kTile + row] = m;
-                xchg[(2 * t + 1) * kTile + row] = l;
-                if (named_barrier_or(kJoinBarrier, 256, !ok || *w.abort)) break;
-                if (any_row) {
-                    const bool two = seg.cnt > 1;  // else stream 1 had no tile and its O holds nothing
-                    const float m0 = xchg[row], l0 = xchg[kTile + row], m1 = xchg[2 * kTile + row],
-                                l1 = xchg[3 * kTile + row];
-                    const float top = two ? fmaxf(m0, m1) : m0;
-                    float f0 = ex2_approx(m0 - top), f1 = two ? ex2_approx(m1 - top) : 0.f;
-                    const float total = l0 * f0 + (two ? l1 * f1 : 0.f);
+                const int i = seg.row0 + row;
+                if (seg.row0 + 32 * q4 < p.rows) {
+                    // the two streams joined
+                    const bool two = steps > 1;  // else stream 1 had no tile and its O holds nothing
+                    const float top = two ? fmaxf(m, m_other) : m;
+                    float f0 = ex2_approx(m - top), f1 = two ? ex2_approx(m_other - top) : 0.f;
+                    const float total = l * f0 + (two ? l_other * f1 : 0.f);
                     f0 /= total;
                     f1 /= total;
-                    const bool real = i < p.rows;
-                    float* part = p.ws_o + ((int64_t)seg.slot * p.rows_cap + (i - seg.row0)) * 128 + 64 * t;
-                    const uint32_t o_col = tmem + lane_base + 128 + 64 * t;
+                    const int64_t at = (int64_t)seg.slot * p.rows_cap + (i - seg.row0);
 #pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
                         uint32_t a[32], b[32];
-                        tmem_ld32(o_col + 32 * c, a);
-                        if (two) tmem_ld32(o_col + 256 + 32 * c, b);
+                        tmem_ld32(t_o + 32 * c, a);
+                        if (two) tmem_ld32(t_o + 256 + 32 * c, b);
                         tmem_wait_ld();
-                        if (!real) continue;
+                        if (i >= p.rows) continue;
 #pragma unroll
                         for (int v = 0; v < 32; ++v) {
                             float x = __uint_as_float(a[v]) * f0;
                             if (two) x = fmaf(__uint_as_float(b[v]), f1, x);
                             a[v] = __float_as_uint(x);
                         }
-#pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            reinterpret_cast<uint4*>(part + 32 * c)[v] =
-                                make_uint4(a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]);
+                        store_fp32(p.ws_o + at * 128 + 64 * half + 32 * c, a);
                     }
-                    if (t == 0 && real)
-                        p.ws_lse[(int64_t)seg.slot * p.rows_cap + (i - seg.row0)] = (top + log2f(total)) * 0.69314718055994531f;
+                    if (half == 0 && i < p.rows) p.ws_lse[at] = (top + log2f(total)) * 0.69314718055994531f;
                 }
             }
             tc_fence_before();
