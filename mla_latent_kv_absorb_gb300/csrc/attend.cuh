@@ -27,12 +27,14 @@
 // the ring is as fine as the tensor core's work and a slot is free as soon as its four are done.
 //
 // Warp 0 streams the ring, warp 2 the query tiles, warp 1 issues the MMAs, warps 3-10 are the softmax
-// of every step: a thread has half of a row, 64 scores in registers, and the two halves of a row agree on
-// its maximum through shared memory.  (What bounds a CTA with two query tiles is the chain QK -> softmax ->
-// PV of a stream against the other stream's products: with four warps to a stream and whole rows a step's
-// softmax took 1,530 cycles of that chain, twice as many as a step's MMAs.)  The running maximum moves only
-// when a tile's exceeds it by more than 8 (log2 units).  P is rounded to bf16 for the PV product (its sum l
-// takes the unrounded values); scores, maxima, sums and O are fp32.
+// of every step: a warp has 16 rows, a quad of lanes two of them (tcgen05.ld's 16x256b shape: lane l holds
+// columns 8 k + 2 (l & 3), + 1 of rows l / 4 and l / 4 + 8), so that a row's maximum is two shuffles away.
+// What bounds a CTA with two query tiles is the chain QK -> softmax -> PV of a stream against the other
+// stream's products, so all eight warps work on one step: with four warps to a stream and a row a thread a
+// step's softmax took 1,530 cycles of that chain, more than a step's 20 MMAs of 64; with halves of a row that
+// agree through shared memory 1,450, of which the barrier 250.  The running maximum moves only when a
+// tile's exceeds it by more than 8 (log2 units).  P is rounded to bf16 for the PV product (its sum l takes
+// the unrounded values); scores, maxima, sums and O are fp32.
 //
 // The prefix form is persistent: the (head, row group, key tile) units lie in one line that the CTAs
 // cut evenly, so that every SM streams the same number of bytes; a CTA's piece of one (head, group)
@@ -149,6 +151,57 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
+// 16 lanes (rows) x 8 K columns of 32 bits: r[4 k], r[4 k + 1] are columns 8 k + 2 (lane & 3) and the next
+// of row lane / 4, r[4 k + 2], r[4 k + 3] those of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x128(uint32_t taddr, uint32_t (&r)[64])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+        "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+        "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+          "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+          "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+          "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+          "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+
+// 16 rows x 32 columns in the 16x128b shape: r[2 k] is column 4 k + (lane & 3) of row lane / 4, r[2 k + 1] of
+// row lane / 4 + 8: where the bf16 pairs of tmem_ld_16x128's columns go.
+__device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+          "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
+}
+
 __device__ __forceinline__ void prefetch_tile_3d(const void* map, int x, int y, int z)
 {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
@@ -169,15 +222,13 @@ constexpr int kSlotBytes = 16384;
 constexpr uint32_t kTmemCols = 512;        // stream t: S at 256 t, O at 256 t + 128
 constexpr float kRescaleLog2 = 8.f;
 constexpr int kFetch = 4;                  // key tiles ahead that are brought into L2
-constexpr uint32_t kJoinBarrier = 1;       // named barrier of the eight softmax warps
 
 template <int kQT>
 struct Layout {
     static constexpr int kSlots = 8;
     static constexpr int kQBufs = 2 / kQT;  // with one query tile the next segment's is loaded beside it
     static constexpr int kOffRing = 2 * 3 * kSlotBytes;
-    static constexpr int kOffXchg = kOffRing + kSlots * kSlotBytes;  // [slot 2][half 2][128]
-    static constexpr int kOffBar = kOffXchg + 2 * 2 * kTile * 4;
+    static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
     static constexpr int kBarFull = 0, kBarEmpty = kSlots;
     static constexpr int kBarQFull = 2 * kSlots, kBarQEmpty = kBarQFull + 2;  // [buffer]
     static constexpr int kBarSFull = kBarQEmpty + 2;  // [stream]
@@ -270,25 +321,6 @@ struct Walk {
     }
 };
 
-// 32 columns of a row.
-__device__ __forceinline__ void store_fp32(float* dst, const uint32_t (&o)[32])
-{
-#pragma unroll
-    for (int v = 0; v < 8; ++v)
-        reinterpret_cast<uint4*>(dst)[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-}
-
-__device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const uint32_t (&o)[32])
-{
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-        reinterpret_cast<uint4*>(dst)[v] =
-            make_uint4(dev::pack_bf16x2(__uint_as_float(o[8 * v + 0]), __uint_as_float(o[8 * v + 1])),
-                       dev::pack_bf16x2(__uint_as_float(o[8 * v + 2]), __uint_as_float(o[8 * v + 3])),
-                       dev::pack_bf16x2(__uint_as_float(o[8 * v + 4]), __uint_as_float(o[8 * v + 5])),
-                       dev::pack_bf16x2(__uint_as_float(o[8 * v + 6]), __uint_as_float(o[8 * v + 7])));
-}
-
 __device__ __forceinline__ int key_tile(const Segment& s, int n) { return n < s.lead ? n : s.tile0 + n; }
 
 template <bool kChunk, int kQT>
@@ -346,8 +378,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         const uint64_t pol_kr = l2_policy_evict_last();
         // Keys and values of the tile kFetch ahead go into L2, so that a slot, which is free only a step
         // before it is needed, is filled from there.
+        // (Behind the tile's own loads, and at most two tiles a turn: at the start the first tiles come first.)
+        int fetched = 0;
         const auto fetch = [&](int n) {
-            if (n >= seg.cnt) return;
             const int j0 = key_tile(seg, n) * kTile;
             const uint32_t bytes = (uint32_t)min(kTile, p.keys - j0) * 256;
             const int64_t at = ((int64_t)seg.head * p.keys + j0) * 128;
@@ -404,11 +437,11 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         while (ok && walk.next(p, seg)) {
             constexpr int kAhead = kQT == 1 ? 2 : 1;  // key tiles ahead of the values
             for (int n = 0; ok && n < kAhead && n < seg.cnt; ++n) load_k(key_tile(seg, n) * kTile);
-            for (int n = kAhead; n < kFetch; ++n) fetch(n);
+            fetched = kAhead + 1;
             for (int n = 0; ok && n < seg.cnt; ++n) {
-                fetch(n + kFetch);
                 load_v(key_tile(seg, n) * kTile);
                 if (ok && n + kAhead < seg.cnt) load_k(key_tile(seg, n + kAhead) * kTile);
+                for (int two = 0; two < 2 && fetched < min(seg.cnt, n + 1 + kFetch); ++two, ++fetched) fetch(fetched);
             }
         }
         // loads in flight land before the CTA can exit
@@ -503,7 +536,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             return true;
         };
         int n_seg = 0;
-        int done[2] = {0, 0};  // steps of each stream
+        int done0 = 0, done1 = 0;  // steps of each stream
         while (ok && walk.next(p, seg)) {
             q_buf = n_seg % L::kQBufs;
             if (!(ok = wait_all(bar(L::kBarQFull + q_buf), n_seg / L::kQBufs, w))) break;
@@ -522,8 +555,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             int sv = 0, pv_ph = 0, sk = 0, pk_ph = 0;  // kQT == 2: the slots of stream 0's values and keys
             for (int i = 0; i < steps; ++i) {
                 const int t = i & 1;
-                if (!(ok = wait_all(bar(L::kBarPReady + t), done[t], w))) break;
-                ++done[t];
+                if (!(ok = wait_all(bar(L::kBarPReady + t), t ? done1 : done0, w))) break;
+                done0 += t ^ 1;
+                done1 += t;
                 tc_fence_after();
                 if (i == 0 && n_seg > 0) {
                     if (!(ok = wait_all(bar(L::kBarOFree), n_seg - 1, w))) break;
@@ -551,190 +585,208 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         }
         mma_commit_one(bar(L::kBarEnd));  // arrives when every MMA issued here has finished
     } else {
-        // softmax: warp (3..10) & 3 selects the TMEM lane quarter, a thread has columns 64 half .. of one row
-        const int half = (warp - kSoftmaxWarp0) >> 2;
-        const int q4 = warp & 3, row = 32 * q4 + lane;
-        const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
-        float* xchg = reinterpret_cast<float*>(smem + L::kOffXchg);  // [slot][half][128]
-        int n_seg = 0, n_step = 0;
-        int seen[2] = {0, 0};  // steps of each stream
-        bool out = false;
-        while (!out && walk.next(p, seg)) {
+        // softmax: warp (3..10) & 3 selects the TMEM lane quarter, a warp has 16 of its rows, a thread the
+        // columns 8 k + 2 (lane & 3), + 1 of rows `row` and row + 8 (index 0 and 1 below)
+        const int q4 = warp & 3, warp_row = 32 * q4 + 16 * ((warp - kSoftmaxWarp0) >> 2);
+        const int row = warp_row + (lane >> 2), col = 2 * (lane & 3);
+        const uint32_t lane_base = (uint32_t)warp_row << 16;
+        int n_seg = 0, seen0 = 0, seen1 = 0;  // segments, steps of each stream
+        bool ok = true;
+        while (ok && walk.next(p, seg)) {
             const int steps = kQT == 1 ? seg.cnt : 2 * seg.cnt;
-            // this stream's running softmax and the other's, which change places after every step
-            float m = -INFINITY, l = 0.f, m_other = -INFINITY, l_other = 0.f;
-            bool ok = true;
+            // the running softmax of this step's stream and of the other, which change places after every step
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, m_other[2] = {-INFINITY, -INFINITY}, l_other[2] = {0.f, 0.f};
+            const auto change = [&]() {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float a = m[x], b = l[x];
+                    m[x] = m_other[x];
+                    l[x] = l_other[x];
+                    m_other[x] = a;
+                    l_other[x] = b;
+                }
+            };
 #pragma unroll 1
-            for (int i = 0; i < steps; ++i, ++n_step) {
+            for (int i = 0; i < steps; ++i) {
                 const int t = i & 1;
                 const int tile_row = seg.row0 + (kQT == 2 ? kTile * t : 0);
-                const bool any_row = tile_row + 32 * q4 < p.rows;  // the warp has a row at all
                 const uint32_t t_s = tmem + lane_base + 256 * t;
-                ok = wait_all(bar(L::kBarSFull + t), seen[t], w);
-                ++seen[t];
+                if (!(ok = wait_all(bar(L::kBarSFull + t), t ? seen1 : seen0, w))) break;
+                seen0 += t ^ 1;
+                seen1 += t;
                 tc_fence_after();
-                uint32_t sr[2][32];
-                float mt = -INFINITY;
-                if (any_row && ok) {
-                    tmem_ld32(t_s + 64 * half, sr[0]);
-                    tmem_ld32(t_s + 64 * half + 32, sr[1]);
+                if (tile_row + warp_row < p.rows) {  // the warp has a row at all
+                    uint32_t sr[64];
+                    tmem_ld_16x128(t_s, sr);
                     tmem_wait_ld();
-                    // keys that the row does not see get -infinity
-                    const int j0 = key_tile(seg, kQT == 1 ? i : i >> 1) * kTile + 64 * half;
+                    // keys that a row does not see get -infinity
+                    const int j0 = key_tile(seg, kQT == 1 ? i : i >> 1) * kTile;
                     if (kChunk) {
-                        const int hi = p.hi0 + min(tile_row + row, p.rows - 1), lo = hi - p.window + 1;
-                        const bool whole = j0 + 63 <= hi && (j0 >= lo || j0 + 64 <= p.sinks);
+                        int hi[2], lo[2];
+                        bool whole = true;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            hi[x] = p.hi0 + min(tile_row + row + 8 * x, p.rows - 1);
+                            lo[x] = hi[x] - p.window + 1;
+                            whole = whole && j0 + kTile - 1 <= hi[x] && (j0 >= lo[x] || j0 + kTile <= p.sinks);
+                        }
                         if (__any_sync(0xffffffffu, !whole)) {
 #pragma unroll
-                            for (int x = 0; x < 64; ++x)
-                                if (j0 + x > hi || (j0 + x < lo && j0 + x >= p.sinks)) sr[x >> 5][x & 31] = 0xff800000u;
+                            for (int k = 0; k < 64; ++k) {
+                                const int j = j0 + 8 * (k >> 2) + col + (k & 1), x = (k >> 1) & 1;
+                                if (j > hi[x] || (j < lo[x] && j >= p.sinks)) sr[k] = 0xff800000u;
+                            }
                         }
-                    } else if (j0 + 64 > p.keys) {
+                    } else if (j0 + kTile > p.keys) {
 #pragma unroll
-                        for (int x = 0; x < 64; ++x)
-                            if (j0 + x >= p.keys) sr[x >> 5][x & 31] = 0xff800000u;
+                        for (int k = 0; k < 64; ++k)
+                            if (j0 + 8 * (k >> 2) + col + (k & 1) >= p.keys) sr[k] = 0xff800000u;
                     }
-                    float m4[4];
+                    float f[2], neg[2];
+                    bool moved = false;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t* v = &sr[c >> 1][16 * (c & 1)];
-                        m4[c] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+                    for (int x = 0; x < 2; ++x) {
+                        float m2[2];  // two chains
 #pragma unroll
-                        for (int x = 2; x < 16; x += 2) m4[c] = max3(m4[c], __uint_as_float(v[x]), __uint_as_float(v[x + 1]));
+                        for (int c = 0; c < 2; ++c) {
+                            m2[c] = fmaxf(__uint_as_float(sr[4 * c + 2 * x]), __uint_as_float(sr[4 * c + 2 * x + 1]));
+#pragma unroll
+                            for (int k = 2 + c; k < 16; k += 2)
+                                m2[c] = max3(m2[c], __uint_as_float(sr[4 * k + 2 * x]), __uint_as_float(sr[4 * k + 2 * x + 1]));
+                        }
+                        float mt = fmaxf(m2[0], m2[1]);
+                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2)) * p.scale_log2;
+                        // The running maximum: set by the stream's first tile, moved later only by more than the
+                        // threshold.  While a row has seen no key it stays at -infinity and O and l at 0.
+                        const bool first = m[x] == -INFINITY, grow = mt > m[x] + kRescaleLog2 || first;
+                        f[x] = grow && !first ? ex2_approx(m[x] - mt) : 1.f;
+                        if (grow) m[x] = mt;
+                        moved = moved || f[x] != 1.f;
+                        neg[x] = m[x] == -INFINITY ? 0.f : -m[x];
                     }
-                    mt = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * p.scale_log2;
-                }
-                float* xs = xchg + (n_step & 1) * 2 * kTile;
-                xs[half * kTile + row] = mt;
-                // Both halves reach every barrier equally often: a failed wait only clears `ok`, and each
-                // barrier ORs the abort state so that all leave together.  Behind it both halves' scores have
-                // left TMEM, and P may be written over them.
-                if ((out = named_barrier_or(kJoinBarrier, 256, !ok || *w.abort))) break;
-                if (any_row) {
-                    mt = fmaxf(mt, xs[(half ^ 1) * kTile + row]);
-                    // The running maximum: set by the stream's first tile, moved later only by more than the
-                    // threshold.  While a row has seen no key it stays at -infinity and O and l at 0.
-                    const bool grow = mt > m + kRescaleLog2 || m == -INFINITY;
-                    const float f = grow && m != -INFINITY ? ex2_approx(m - mt) : 1.f;
-                    if (grow) m = mt;
-                    if (i > 1 && __any_sync(0xffffffffu, f != 1.f)) {
+                    if (i > 1 && __any_sync(0xffffffffu, moved)) {
                         // O's earlier PVs have finished: S(i) complete implies it (QK(i) was issued after
                         // PV(i - 2), and a commit covers every earlier MMA of the thread)
-                        const uint32_t t_o = t_s + 128 + 64 * half;
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t o[16];
-                            tmem_ld16(t_o + 16 * c, o);
+                            tmem_ld_16x32(t_s + 128 + 32 * c, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                            tmem_st16(t_o + 16 * c, o);
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[(k >> 1) & 1]);
+                            tmem_st_16x32(t_s + 128 + 32 * c, o);
                         }
                     }
-                    const float base = m == -INFINITY ? 0.f : m;
-                    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2), base2 = pair(-base, -base);
+                    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
+                    const uint64_t neg2[2] = {pair(neg[0], neg[0]), pair(neg[1], neg[1])};
                     uint64_t sum[2] = {0, 0};  // pairs of zeros
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t pk[16];
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
+                        for (int k = 0; k < 16; ++k) {
+                            const int at = 32 * c + 2 * k, x = k & 1;
                             float a, b;
-                            unpair(fma2(pair(__uint_as_float(sr[c][2 * x]), __uint_as_float(sr[c][2 * x + 1])), scale2, base2),
-                                   a, b);
+                            unpair(fma2(pair(__uint_as_float(sr[at]), __uint_as_float(sr[at + 1])), scale2, neg2[x]), a, b);
                             a = ex2_approx(a);
                             b = ex2_approx(b);
-                            sum[x & 1] = add2(sum[x & 1], pair(a, b));
-                            pk[x] = pack_bf16x2(a, b);
+                            sum[x] = add2(sum[x], pair(a, b));
+                            pk[k] = pack_bf16x2(a, b);
                         }
-                        tmem_st16(t_s + 32 * half + 16 * c, pk);
+                        tmem_st_pairs(t_s + 32 * c, pk);
                     }
-                    float s0, s1;
-                    unpair(add2(sum[0], sum[1]), s0, s1);
-                    l = l * f + (s0 + s1);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float a, b;
+                        unpair(sum[x], a, b);
+                        l[x] = l[x] * f[x] + (a + b);
+                    }
                     tmem_wait_st();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::kBarPReady + t));
-                float swap = m;
-                m = m_other;
-                m_other = swap;
-                swap = l;
-                l = l_other;
-                l_other = swap;
+                change();
             }
-            if (out) break;
-            if (steps & 1) {  // stream 0's are in m and l after an even number of steps
-                float swap = m;
-                m = m_other;
-                m_other = swap;
-                swap = l;
-                l = l_other;
-                l_other = swap;
-            }
-            // the two halves' sums: written when the last step's maxima have been read, read before the next
-            // segment's are written
-            ok = wait_all(bar(L::kBarODone), n_seg, w);
-            if ((out = named_barrier_or(kJoinBarrier, 256, !ok || *w.abort))) break;
-            xchg[half * kTile + row] = l;
-            xchg[(2 + half) * kTile + row] = l_other;
-            if ((out = named_barrier_or(kJoinBarrier, 256, *w.abort))) break;
-            l += xchg[(half ^ 1) * kTile + row];
-            l_other += xchg[(2 + (half ^ 1)) * kTile + row];
-            if ((out = named_barrier_or(kJoinBarrier, 256, *w.abort))) break;
+            if (steps & 1) change();  // stream 0's are in m and l after an even number of steps
+            if (!(ok = ok && wait_all(bar(L::kBarODone), n_seg, w))) break;
             tc_fence_after();
-            const uint32_t t_o = tmem + lane_base + 128 + 64 * half;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {  // a quad has a row's sum
+                l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+                l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+                l_other[x] += __shfl_xor_sync(0xffffffffu, l_other[x], 1);
+                l_other[x] += __shfl_xor_sync(0xffffffffu, l_other[x], 2);
+            }
+            // The outputs: a quad's lanes write 32 bytes (fp32) of a row side by side.
+            const auto store = [&](int i, float a, float b, int c) {  // columns c, c + 1 of query row i
+                if (i >= p.rows) return;
+                if (kChunk)
+                    *reinterpret_cast<uint32_t*>(p.out + ((int64_t)i * 128 + seg.head) * 128 + c) = pack_bf16x2(a, b);
+                else
+                    *reinterpret_cast<float2*>(p.ws_o + ((int64_t)seg.slot * p.rows_cap + (i - seg.row0)) * 128 + c) =
+                        make_float2(a, b);
+            };
+            const auto store_lse = [&](int i, float top, float total) {
+                if (!kChunk && i < p.rows && (lane & 3) == 0)
+                    p.ws_lse[(int64_t)seg.slot * p.rows_cap + (i - seg.row0)] = (top + log2f(total)) * 0.69314718055994531f;
+            };
+            const uint32_t t_o = tmem + lane_base + 128;
             if (kQT == 2) {
 #pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
-                    const int tile_row = seg.row0 + kTile * t, i = tile_row + row;
-                    if (tile_row + 32 * q4 >= p.rows) continue;
-                    const float total = t ? l_other : l, top = t ? m_other : m;
-                    const float inv = 1.f / total;
-                    const int64_t at = (int64_t)seg.slot * p.rows_cap + (i - seg.row0);
+                    const int i = seg.row0 + kTile * t + row;
+                    if (seg.row0 + kTile * t + warp_row < p.rows) {
+                        const float inv[2] = {1.f / l[0], 1.f / l[1]};
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(t_o + 256 * t + 32 * c, o);
-                        tmem_wait_ld();
-                        if (i >= p.rows) continue;
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[16];
+                            tmem_ld_16x32(t_o + 256 * t + 32 * c, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int v = 0; v < 32; ++v) o[v] = __float_as_uint(__uint_as_float(o[v]) * inv);
-                        if (kChunk)
-                            store_bf16(p.out + ((int64_t)i * 128 + seg.head) * 128 + 64 * half + 32 * c, o);
-                        else
-                            store_fp32(p.ws_o + at * 128 + 64 * half + 32 * c, o);
-                    }
-                    if (!kChunk && half == 0 && i < p.rows) p.ws_lse[at] = (top + log2f(total)) * 0.69314718055994531f;
-                }
-            } else {
-                const int i = seg.row0 + row;
-                if (seg.row0 + 32 * q4 < p.rows) {
-                    // the two streams joined
-                    const bool two = steps > 1;  // else stream 1 had no tile and its O holds nothing
-                    const float top = two ? fmaxf(m, m_other) : m;
-                    float f0 = ex2_approx(m - top), f1 = two ? ex2_approx(m_other - top) : 0.f;
-                    const float total = l * f0 + (two ? l_other * f1 : 0.f);
-                    f0 /= total;
-                    f1 /= total;
-                    const int64_t at = (int64_t)seg.slot * p.rows_cap + (i - seg.row0);
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t a[32], b[32];
-                        tmem_ld32(t_o + 32 * c, a);
-                        if (two) tmem_ld32(t_o + 256 + 32 * c, b);
-                        tmem_wait_ld();
-                        if (i >= p.rows) continue;
-#pragma unroll
-                        for (int v = 0; v < 32; ++v) {
-                            float x = __uint_as_float(a[v]) * f0;
-                            if (two) x = fmaf(__uint_as_float(b[v]), f1, x);
-                            a[v] = __float_as_uint(x);
+                            for (int k = 0; k < 16; k += 2) {
+                                const int x = (k >> 1) & 1;
+                                store(i + 8 * x, __uint_as_float(o[k]) * inv[x], __uint_as_float(o[k + 1]) * inv[x],
+                                      32 * c + 8 * (k >> 2) + col);
+                            }
                         }
-                        store_fp32(p.ws_o + at * 128 + 64 * half + 32 * c, a);
+                        store_lse(i, m[0], l[0]);
+                        store_lse(i + 8, m[1], l[1]);
                     }
-                    if (half == 0 && i < p.rows) p.ws_lse[at] = (top + log2f(total)) * 0.69314718055994531f;
+                    change();
+                }
+            } else if (seg.row0 + warp_row < p.rows) {
+                // the two streams joined
+                const bool two = steps > 1;  // else stream 1 had no tile and its O holds nothing
+                const int i = seg.row0 + row;
+                float f0[2], f1[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float top = two ? fmaxf(m[x], m_other[x]) : m[x];
+                    f0[x] = ex2_approx(m[x] - top);
+                    f1[x] = two ? ex2_approx(m_other[x] - top) : 0.f;
+                    const float total = l[x] * f0[x] + (two ? l_other[x] * f1[x] : 0.f);
+                    f0[x] /= total;
+                    f1[x] /= total;
+                    store_lse(i + 8 * x, top, total);
+                }
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t a[16], b[16];
+                    tmem_ld_16x32(t_o + 32 * c, a);
+                    if (two) tmem_ld_16x32(t_o + 256 + 32 * c, b);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        const int x = (k >> 1) & 1;
+                        float u = __uint_as_float(a[k]) * f0[x], v = __uint_as_float(a[k + 1]) * f0[x];
+                        if (two) {
+                            u = fmaf(__uint_as_float(b[k]), f1[x], u);
+                            v = fmaf(__uint_as_float(b[k + 1]), f1[x], v);
+                        }
+                        store(i + 8 * x, u, v, 32 * c + 8 * (k >> 2) + col);
+                    }
                 }
             }
             tc_fence_before();
