@@ -497,13 +497,6 @@ mla_status gather_one_sequence(mla_kv_dtype kv_dtype, const void* kv_pool, const
                                int32_t num_pool_pages, const int32_t* block_table_row, int32_t max_pages,
                                int32_t seq_len, void* out, uint32_t* dev_error, void* stream, int32_t skip_from = 0,
                                int32_t skip = 0);
-
-// Per-head keys or values of gathered rows [num_rows][576]: out[h][i][:] = w[h] rows[i][0..512), the
-// out-proj GEMM's shape with one activation row for all heads, head-major.
-mla_status decompress_heads(const void* rows, const void* w, void* out, int32_t num_rows, void* stream)
-{
-    return launch_head_gemm<512, kOutN, false, kOutStages>(rows, w, out, num_rows, 128, kOutN, false, stream, 576, true);
-}
 }  // namespace mla
 
 namespace {

@@ -9,6 +9,7 @@
 
 #include "../../include/mla.h"
 #include "attend.cuh"
+#include "expand.cuh"
 #include "launch.cuh"
 #include "nvtx_range.h"
 
@@ -18,8 +19,6 @@ namespace mla {
 mla_status gather_one_sequence(mla_kv_dtype kv_dtype, const void* kv_pool, const float* kv_scale, const void* kr_pool,
                                int32_t num_pool_pages, const int32_t* block_table_row, int32_t max_pages, int32_t len,
                                void* out, uint32_t* dev_error, void* stream, int32_t skip_from = 0, int32_t skip = 0);
-// api.cu: out[h][i][:] = w[h] rows[i][0..512) for w [128][128][512] and rows of 576, head-major
-mla_status decompress_heads(const void* rows, const void* w, void* out, int32_t num_rows, void* stream);
 }  // namespace mla
 
 namespace {
@@ -29,7 +28,7 @@ using mla::is_aligned;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
-constexpr int64_t kMaxKeys = (int64_t)65535 * 128;  // grid z of the decompression
+constexpr int64_t kMaxKeys = (int64_t)65535 * 128;  // as mla_prefill_decompressed
 constexpr int32_t kMaxRows = 65536;
 
 size_t up_1k(size_t x) { return (x + 1023) & ~(size_t)1023; }
@@ -76,8 +75,43 @@ mla_status launch_attend(const Maps& m, const mla::attend::Params& p, int ctas, 
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kQT>::kSmemBytes),
         "cudaFuncSetAttribute(max dynamic shared memory)");
     if (st != MLA_OK) return st;
-    kernel<<<ctas, kThreads, Layout<kQT>::kSmemBytes, static_cast<cudaStream_t>(stream)>>>(m.qc, m.qr, m.k, m.kr, m.v, p);
-    return mla::cuda_status(cudaGetLastError(), "attend kernel launch");
+    return mla::launch_dependent("attend kernel launch", kernel, dim3((unsigned)ctas), dim3(kThreads),
+                                 Layout<kQT>::kSmemBytes, stream, m.qc, m.qr, m.k, m.kr, m.v, p);
+}
+
+mla_status sm_count(int* sms)
+{
+    int dev = 0;
+    const mla_status st = mla::cuda_status(cudaGetDevice(&dev), "cudaGetDevice");
+    if (st != MLA_OK) return st;
+    return mla::cuda_status(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev), "cudaDeviceGetAttribute");
+}
+
+// The keys and values of `num` gathered rows of 576 for all heads: k and v [128][num][128].
+mla_status expand_rows(const void* rows, const void* w_uk, const void* w_uv, void* k, void* v, int32_t num,
+                       uint32_t* dev_error, int sms, void* stream)
+{
+    using namespace mla::expand;
+    CUtensorMap tm_rows, tm_uk, tm_uv;
+    const cuuint64_t r_dims[2] = {512, (cuuint64_t)num}, r_str[1] = {576 * 2};
+    const cuuint64_t w_dims[2] = {512, 128 * 128}, w_str[1] = {512 * 2};
+    const cuuint32_t box[2] = {64, 128};
+    if (!mla::make_bf16_map(&tm_rows, rows, 2, r_dims, r_str, box) || !mla::make_bf16_map(&tm_uk, w_uk, 2, w_dims, w_str, box) ||
+        !mla::make_bf16_map(&tm_uv, w_uv, 2, w_dims, w_str, box))
+        return MLA_ERR_CUDA;
+    const mla_status st = mla::cuda_status(
+        cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes),
+        "cudaFuncSetAttribute(max dynamic shared memory)");
+    if (st != MLA_OK) return st;
+    Params p = {};
+    p.rows = num;
+    p.products = (int64_t)((num + 127) / 128) * kProducts;
+    p.k = static_cast<__nv_bfloat16*>(k);
+    p.v = static_cast<__nv_bfloat16*>(v);
+    p.dev_error = dev_error;
+    p.timeout_ns = kTimeoutNs;
+    return mla::launch_dependent("expand kernel launch", expand_kernel, dim3((unsigned)std::min<int64_t>(sms, p.products)),
+                                 dim3(kThreads), kSmemBytes, stream, tm_rows, tm_uk, tm_uv, p);
 }
 
 // How the prefix form cuts its work: two query tiles a CTA above 128 rows, then each key tile serves both.
@@ -154,11 +188,13 @@ extern "C" MLA_API mla_status mla_prefix_open(mla_kv_dtype kv_dtype, const void*
         !is_aligned(w_uv, 16) || !is_aligned(rows, 16) || !is_aligned(k, 16) || !is_aligned(v, 16) || !is_aligned(dev_error, 4))
         return MLA_ERR_ALIGNMENT;
     if (prefix_len > kMaxKeys) return MLA_ERR_UNSUPPORTED;
-    mla_status st = mla::gather_one_sequence(kv_dtype, kv_pool, kv_scale, kr_pool, num_pool_pages, block_table_row,
+    int sms = 0;
+    mla_status st = sm_count(&sms);
+    if (st != MLA_OK) return st;
+    st = mla::gather_one_sequence(kv_dtype, kv_pool, kv_scale, kr_pool, num_pool_pages, block_table_row,
                                              max_pages, prefix_len, rows, dev_error, stream);
-    if (st == MLA_OK) st = mla::decompress_heads(rows, w_uk, k, prefix_len, stream);
-    if (st == MLA_OK) st = mla::decompress_heads(rows, w_uv, v, prefix_len, stream);
-    return st;
+    if (st != MLA_OK) return st;
+    return expand_rows(rows, w_uk, w_uv, k, v, prefix_len, dev_error, sms, stream);
 }
 
 extern "C" MLA_API size_t mla_prefix_attend_workspace_bytes(int32_t num_rows, int32_t prefix_len, int32_t num_sms)
@@ -220,9 +256,8 @@ extern "C" MLA_API mla_status mla_prefix_attend(int32_t num_rows, int32_t prefix
     a.lse = lse;
     using mla::attend::kMergeWarps;
     const int64_t warps = (int64_t)num_rows * 128;
-    mla::attend::prefix_merge_kernel<<<(unsigned)((warps + kMergeWarps - 1) / kMergeWarps), 32 * kMergeWarps, 0,
-                                       static_cast<cudaStream_t>(stream)>>>(a);
-    return mla::cuda_status(cudaGetLastError(), "prefix merge kernel launch");
+    return mla::launch_dependent("prefix merge kernel launch", mla::attend::prefix_merge_kernel,
+                                 dim3((unsigned)((warps + kMergeWarps - 1) / kMergeWarps)), dim3(32 * kMergeWarps), 0, stream, a);
 }
 
 extern "C" MLA_API size_t mla_prefill_window_workspace_bytes(int32_t seq_len, int32_t chunk_len, int32_t window,
@@ -258,10 +293,12 @@ extern "C" MLA_API mla_status mla_prefill_window(mla_kv_dtype kv_dtype, const vo
     void *k = ws + s.k, *v = ws + s.v;
     Maps m;
     if (!make_maps(&m, q_c, q_r, k, v, ws + 512 * 2, 576, chunk_len, s.keys)) return MLA_ERR_CUDA;
-    mla_status st = mla::gather_one_sequence(kv_dtype, kv_pool, kv_scale, kr_pool, num_pool_pages, block_table_row,
-                                             max_pages, s.keys, ws, dev_error, stream, s.skip_from, s.skip);
-    if (st == MLA_OK) st = mla::decompress_heads(ws, w_uk, k, s.keys, stream);
-    if (st == MLA_OK) st = mla::decompress_heads(ws, w_uv, v, s.keys, stream);
+    int sms = 0;
+    mla_status st = sm_count(&sms);
+    if (st != MLA_OK) return st;
+    st = mla::gather_one_sequence(kv_dtype, kv_pool, kv_scale, kr_pool, num_pool_pages, block_table_row, max_pages, s.keys, ws,
+                                  dev_error, stream, s.skip_from, s.skip);
+    if (st == MLA_OK) st = expand_rows(ws, w_uk, w_uv, k, v, s.keys, dev_error, sms, stream);
     if (st != MLA_OK) return st;
     mla::attend::Params p = {};
     p.rows = chunk_len;
@@ -276,10 +313,5 @@ extern "C" MLA_API mla_status mla_prefill_window(mla_kv_dtype kv_dtype, const vo
     p.window = std::min(window, seq_len);
     p.sinks = std::min(sinks, seq_len);
     p.out = static_cast<__nv_bfloat16*>(out);
-    int dev = 0, sms = 0;
-    if ((st = mla::cuda_status(cudaGetDevice(&dev), "cudaGetDevice")) != MLA_OK ||
-        (st = mla::cuda_status(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev),
-                               "cudaDeviceGetAttribute")) != MLA_OK)
-        return st;
     return launch_attend<true, 2>(m, p, (int)std::min<int64_t>(sms, (int64_t)p.groups * 128), stream);
 }

@@ -372,6 +372,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
     Segment seg;
 
     if (warp == 0) {
+        griddep_wait();  // keys, values and queries may come from the kernel before; nothing is written ahead of them
         const bool leader = elect_lane();
         // the prefix's keys and values are read once by one group of rows, k_R by every head
         const uint64_t pol_kv = kChunk || p.groups > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
@@ -444,10 +445,12 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 for (int two = 0; two < 2 && fetched < min(seg.cnt, n + 1 + kFetch); ++two, ++fetched) fetch(fetched);
             }
         }
+        griddep_launch_dependents();  // the merge may be scheduled; it waits for this kernel's end
         // loads in flight land before the CTA can exit
         for (int k = r > L::kSlots ? r - L::kSlots : 0; k < r; ++k)
             drain_phase(bar(L::kBarFull + k % L::kSlots), k / L::kSlots, w.timeout_ns);
     } else if (warp == 2) {
+        griddep_wait();
         const bool leader = elect_lane();
         const uint64_t pol = l2_policy_evict_last();
         if (leader) {
@@ -834,29 +837,40 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
     int c1 = c0;
     while (c1 + 1 < a.ctas && first_unit(c1 + 1, units, a.ctas) < u1) ++c1;
     const int64_t at = row - group * a.group_rows;
+    dev::griddep_wait();
+    // The row's own part and the first three of the prefix (more only with more CTAs than runs) are requested
+    // together, in one round trip.
+    constexpr int kAtOnce = 3;
     const float own = a.own_lse ? a.own_lse[id] : -INFINITY;
-    float top = own;
-    for (int c = c0; c <= c1; ++c) top = fmaxf(top, a.ws_lse[(int64_t)(c + run) * a.rows_cap + at]);
+    const uint2 own_o = a.own_out ? reinterpret_cast<const uint2*>(a.own_out + id * 128)[lane] : make_uint2(0, 0);
+    float part_lse[kAtOnce];
+    float4 part_o[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+        const int64_t part = (int64_t)(min(c0 + k, c1) + run) * a.rows_cap + at;
+        part_lse[k] = c0 + k <= c1 ? a.ws_lse[part] : -INFINITY;
+        part_o[k] = reinterpret_cast<const float4*>(a.ws_o + part * 128)[lane];
+    }
+    float top = fmaxf(fmaxf(own, part_lse[0]), fmaxf(part_lse[1], part_lse[2]));
+    for (int c = c0 + kAtOnce; c <= c1; ++c) top = fmaxf(top, a.ws_lse[(int64_t)(c + run) * a.rows_cap + at]);
     float total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int c = c0; c <= c1; ++c) {
-        const int64_t part = (int64_t)(c + run) * a.rows_cap + at;
-        const float wgt = __expf(a.ws_lse[part] - top);
-        const float4 o = reinterpret_cast<const float4*>(a.ws_o + part * 128)[lane];
+    const auto add = [&](float part, const float4& o) {
+        const float wgt = __expf(part - top);
         total += wgt;
         x[0] = fmaf(wgt, o.x, x[0]);
         x[1] = fmaf(wgt, o.y, x[1]);
         x[2] = fmaf(wgt, o.z, x[2]);
         x[3] = fmaf(wgt, o.w, x[3]);
+    };
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+        if (c0 + k <= c1) add(part_lse[k], part_o[k]);
+    for (int c = c0 + kAtOnce; c <= c1; ++c) {
+        const int64_t part = (int64_t)(c + run) * a.rows_cap + at;
+        add(a.ws_lse[part], reinterpret_cast<const float4*>(a.ws_o + part * 128)[lane]);
     }
-    const float wgt = own == -INFINITY ? 0.f : __expf(own - top);
-    if (wgt != 0.f) {  // a row without own tokens may hold anything
-        const uint2 o = reinterpret_cast<const uint2*>(a.own_out + id * 128)[lane];
-        total += wgt;
-        x[0] = fmaf(wgt, dev::bf16_lo(o.x), x[0]);
-        x[1] = fmaf(wgt, dev::bf16_hi(o.x), x[1]);
-        x[2] = fmaf(wgt, dev::bf16_lo(o.y), x[2]);
-        x[3] = fmaf(wgt, dev::bf16_hi(o.y), x[3]);
-    }
+    if (own != -INFINITY)  // a row without own tokens may hold anything
+        add(own, make_float4(dev::bf16_lo(own_o.x), dev::bf16_hi(own_o.x), dev::bf16_lo(own_o.y), dev::bf16_hi(own_o.y)));
     const float inv = 1.f / total;
     reinterpret_cast<uint2*>(a.out + id * 128)[lane] =
         make_uint2(dev::pack_bf16x2(x[0] * inv, x[1] * inv), dev::pack_bf16x2(x[2] * inv, x[3] * inv));
