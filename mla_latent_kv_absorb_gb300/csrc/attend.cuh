@@ -84,7 +84,42 @@ __device__ __forceinline__ void mma_commit_one(uint32_t bar)
         : "memory");
 }
 
+// The same for a pair of CTAs (M = 256), issued in the even one.
+__device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Arrives on the barrier at this offset in both CTAs when all earlier MMAs of the pair have finished.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
 // A bounded wait (as dev::wait_phase) that looks at the timer, which is slow to read, once in many polls.
+template <bool kCluster>
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns,
                                        uint32_t* dev_error)
 {
@@ -92,7 +127,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
     while (true) {
 #pragma unroll 1
         for (int k = 0; k < 64; ++k)
-            if (dev::mbar_try_wait(bar, parity)) return true;
+            if (kCluster ? dev::mbar_try_wait_cluster(bar, parity) : dev::mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
         if (dev::globaltimer_ns() - t0 > timeout_ns) {
             *abort = 1;
@@ -102,11 +137,14 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
     }
 }
 
-// The whole warp waits; the answer is a vote, the same in all lanes.
+// The whole warp waits; the answer is a vote, the same in all lanes.  kCluster: the other CTA arrives too.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t phase, const WaitCtx& w)
 {
-    if (__all_sync(0xffffffffu, dev::mbar_try_wait(bar, phase & 1u))) return true;
-    return __all_sync(0xffffffffu, wait_slow(bar, phase & 1u, w.abort, w.timeout_ns, w.dev_error));
+    const uint32_t parity = phase & 1u;
+    if (__all_sync(0xffffffffu, kCluster ? dev::mbar_try_wait_cluster(bar, parity) : dev::mbar_try_wait(bar, parity)))
+        return true;
+    return __all_sync(0xffffffffu, wait_slow<kCluster>(bar, parity, w.abort, w.timeout_ns, w.dev_error));
 }
 
 __device__ __forceinline__ bool elect_lane()
