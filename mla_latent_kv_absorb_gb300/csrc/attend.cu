@@ -92,15 +92,12 @@ mla_status expand_rows(const void* rows, const void* w_uk, const void* w_uv, voi
                        uint32_t* dev_error, int sms, void* stream)
 {
     using namespace mla::expand;
-    CUtensorMap tm_rows, tm_uk, tm_uv, tm_k, tm_v;
-    const cuuint64_t o_dims[3] = {128, (cuuint64_t)num, 128}, o_str[2] = {128 * 2, (cuuint64_t)num * 128 * 2};
-    const cuuint32_t o_box[3] = {64, 32, 1};
+    CUtensorMap tm_rows, tm_uk, tm_uv;
     const cuuint64_t r_dims[2] = {512, (cuuint64_t)num}, r_str[1] = {576 * 2};
     const cuuint64_t w_dims[2] = {512, 128 * 128}, w_str[1] = {512 * 2};
     const cuuint32_t box[2] = {64, 128};
     if (!mla::make_bf16_map(&tm_rows, rows, 2, r_dims, r_str, box) || !mla::make_bf16_map(&tm_uk, w_uk, 2, w_dims, w_str, box) ||
-        !mla::make_bf16_map(&tm_uv, w_uv, 2, w_dims, w_str, box) || !mla::make_bf16_map(&tm_k, k, 3, o_dims, o_str, o_box) ||
-        !mla::make_bf16_map(&tm_v, v, 3, o_dims, o_str, o_box))
+        !mla::make_bf16_map(&tm_uv, w_uv, 2, w_dims, w_str, box))
         return MLA_ERR_CUDA;
     const mla_status st = mla::cuda_status(
         cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes),
@@ -109,11 +106,13 @@ mla_status expand_rows(const void* rows, const void* w_uk, const void* w_uv, voi
     Params p = {};
     p.rows = num;
     p.products = (int64_t)((num + kRowsTile - 1) / kRowsTile) * kProducts;
+    p.k = static_cast<__nv_bfloat16*>(k);
+    p.v = static_cast<__nv_bfloat16*>(v);
     p.dev_error = dev_error;
     p.timeout_ns = kTimeoutNs;
     const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(sms / 2, p.products));
     return mla::launch_dependent("expand kernel launch", expand_kernel, dim3((unsigned)(2 * pairs)),
-                                 dim3(kThreads), kSmemBytes, stream, tm_rows, tm_uk, tm_uv, tm_k, tm_v, p);
+                                 dim3(kThreads), kSmemBytes, stream, tm_rows, tm_uk, tm_uv, p);
 }
 
 // How the prefix form cuts its work: two query tiles a CTA above 128 rows, then each key tile serves both.

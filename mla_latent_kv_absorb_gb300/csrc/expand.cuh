@@ -21,12 +21,10 @@ namespace expand {
 constexpr int kThreads = 32 * 11;
 constexpr int kChunk = 16384;              // [128][64] bf16
 constexpr int kChunks = 8;                 // of a product's 512 k
-constexpr int kSlots = 4;
-constexpr int kStage = 4096;               // an output warp's [32 rows][64] bf16
+constexpr int kSlots = 6;                  // a chunk's way round takes some 2,700 cycles, its MMAs 512
 constexpr int kRowsTile = 256;
 constexpr int kOffRing = kChunks * kChunk;
-constexpr int kOffStage = kOffRing + kSlots * kChunk;
-constexpr int kOffBar = kOffStage + 8 * kStage;
+constexpr int kOffBar = kOffRing + kSlots * kChunk;
 constexpr int kBarWFull = 0, kBarWEmpty = kSlots, kBarAFull = 2 * kSlots, kBarAEmpty = kBarAFull + kChunks,
               kBarDFull = kBarAEmpty + kChunks, kBarEnd = kBarDFull + 2, kBarDFree = kBarEnd + 1, kBars = kBarDFree + 2;
 constexpr int kSmemBytes = kOffBar + 8 * kBars + 16;
@@ -36,6 +34,7 @@ static_assert(kSmemBytes <= 232448, "a CTA's shared memory");
 struct Params {
     int rows;
     int64_t products;  // kProducts x row tiles
+    __nv_bfloat16 *k, *v;  // [128][rows][128]
     uint32_t* dev_error;
     uint64_t timeout_ns;
 };
@@ -47,8 +46,7 @@ struct Params {
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 expand_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_uk,
-              const __grid_constant__ CUtensorMap tm_uv, const __grid_constant__ CUtensorMap tm_k,
-              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p)
+              const __grid_constant__ CUtensorMap tm_uv, const __grid_constant__ Params p)
 {
     using namespace dev;
     using namespace attend;
@@ -171,50 +169,46 @@ expand_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant
     } else if (warp == 1) {
         // the odd CTA's MMAs are issued by the even one
     } else {
-        // A thread has one row; four warps have its keys, four its values.  64 columns at a time go through the
-        // warp's tile in shared memory and out by TMA, in whole lines and clipped at the last row (16 bytes a
-        // lane straight from registers, one row each, took four times a product's MMAs).
-        const int set = (warp - 3) >> 2, q4 = warp & 3, row = 128 * rank + 32 * q4;
+        // Four warps have the keys, four the values of 32 rows each, 16 rows at a time.  Two lanes exchange a pair
+        // of columns, so that a quad writes 32 bytes of a row side by side: whole sectors.  (A row a lane, 16
+        // bytes at a time, took four times a product's MMAs; through shared memory and TMA the smaller ring, or
+        // the wait for the tile, cost more.)
+        const int set = (warp - 3) >> 2, q4 = warp & 3, row = 128 * rank + 32 * q4 + (lane >> 2);
         const uint32_t from = tmem + ((uint32_t)(32 * q4) << 16) + 128 * set;
         const uint32_t r_free = map_to_cta(bar(kBarDFree), 0);
-        const CUtensorMap* map = set == 0 ? &tm_k : &tm_v;
-        uint8_t* stage = smem + kOffStage + (warp - 3) * kStage;
+        const bool odd = lane & 1;
+        const int col = odd ? 8 + 2 * (lane & 2) : 2 * (lane & 2);  // of the 16 columns of two steps
+        __nv_bfloat16* const out = set == 0 ? p.k : p.v;
         int j = 0;
         for (int64_t at = first; at < end; ++at, ++j) {
             if (!wait_all<true>(bar(kBarDFull + (j & 1)), j >> 1, w)) break;
             tc_fence_after();
-            const int i = (int)(at / kProducts) * kRowsTile + row, head = (int)(at % kProducts);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t o[2][32];
-                tmem_ld32(from + 256 * (j & 1) + 64 * c, o[0]);
-                tmem_ld32(from + 256 * (j & 1) + 64 * c + 32, o[1]);
+            __nv_bfloat16* const head = out + (at % kProducts) * p.rows * 128;
+            const int64_t i0 = at / kProducts * kRowsTile + row;
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part) {
+                uint32_t o[64];
+                tmem_ld_16x128(from + ((uint32_t)(16 * part) << 16) + 256 * (j & 1), o);
                 tmem_wait_ld();
-                if (c == 1) {
+                if (part == 1) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(r_free + 8 * (j & 1));
+                    if (lane == 0) mbar_arrive_remote_relaxed(r_free + 8 * (j & 1));
                 }
-                if (lane == 0) bulk_wait_read();  // the store before has read the tile
-                __syncwarp();
 #pragma unroll
-                for (int v = 0; v < 8; ++v) {
-                    const uint32_t* x = &o[v >> 2][8 * (v & 3)];
-                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((v ^ (lane & 7)) << 4)) =
-                        make_uint4(pack_bf16x2(__uint_as_float(x[0]), __uint_as_float(x[1])),
-                                   pack_bf16x2(__uint_as_float(x[2]), __uint_as_float(x[3])),
-                                   pack_bf16x2(__uint_as_float(x[4]), __uint_as_float(x[5])),
-                                   pack_bf16x2(__uint_as_float(x[6]), __uint_as_float(x[7])));
-                }
-                fence_proxy_async_cta();
-                __syncwarp();
-                if (lane == 0 && i < p.rows) {
-                    tma_store_3d(map, smem_u32(stage), 64 * c, i, head);
-                    bulk_commit();
+                for (int x = 0; x < 2; ++x) {
+                    const int64_t i = i0 + 16 * part + 8 * x;
+                    uint2* dst = reinterpret_cast<uint2*>(head + i * 128 + col);
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        const uint32_t a = pack_bf16x2(__uint_as_float(o[4 * k + 2 * x]), __uint_as_float(o[4 * k + 2 * x + 1]));
+                        const uint32_t b = pack_bf16x2(__uint_as_float(o[4 * k + 4 + 2 * x]), __uint_as_float(o[4 * k + 5 + 2 * x]));
+                        const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+                        if (i < p.rows) dst[2 * k] = odd ? make_uint2(other, b) : make_uint2(a, other);
+                    }
                 }
             }
         }
-        if (lane == 0) bulk_wait_all();
     }
     // After a wait that ran out the odd CTA's loads may be in flight without a barrier of its own: they land in
     // microseconds, and it waits a millisecond.
