@@ -957,8 +957,16 @@ def _check_table_rows(seq_lens, block_table) -> None:
                          f"{int(pages.max())}")
 
 
+_sms = {}
+
+
 def num_sms(device=None) -> int:
-    return torch.cuda.get_device_properties(device if device is not None else torch.cuda.current_device()).multi_processor_count
+    index = torch.cuda.current_device() if device is None else device if isinstance(device, int) else torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device()
+    if index not in _sms:
+        _sms[index] = torch.cuda.get_device_properties(index).multi_processor_count
+    return _sms[index]
 
 
 class DecodeStep:

@@ -32,8 +32,10 @@
 // What bounds a CTA with two query tiles is the chain QK -> softmax -> PV of a stream against the other
 // stream's products, so all eight warps work on one step: with four warps to a stream and a row a thread a
 // step's softmax took 1,530 cycles of that chain, more than a step's 20 MMAs of 64; with halves of a row that
-// agree through shared memory 1,450, of which the barrier 250.  The running maximum moves only when a
-// tile's exceeds it by more than 8 (log2 units).  P is rounded to bf16 for the PV product (its sum l takes
+// agree through shared memory 1,450, of which the barrier 250.  The running maximum is the one of the stream's
+// first tile and moves only when a score exceeds it by more than 32 (log2 units), which loses nothing: fp32
+// and bf16 round relative to the value.  So a step takes its exponentials with the maximum that it has, looks
+// at its scores beside that (no exchange between lanes), and does them again in the rare other case.  P is rounded to bf16 for the PV product (its sum l takes
 // the unrounded values); scores, maxima, sums and O are fp32.
 //
 // The prefix form is persistent: the (head, row group, key tile) units lie in one line that the CTAs
@@ -258,7 +260,7 @@ constexpr int kThreads = 32 * 11;
 constexpr int kSoftmaxWarp0 = 3;
 constexpr int kSlotBytes = 16384;
 constexpr uint32_t kTmemCols = 512;        // stream t: S at 256 t, O at 256 t + 128
-constexpr float kRescaleLog2 = 8.f;
+constexpr float kRescaleLog2 = 32.f;       // P up to 2^32, l and O below 2^32 x keys x |v|: far from fp32's 2^127
 constexpr int kFetch = 4;                  // key tiles ahead that are brought into L2
 
 template <int kQT>
@@ -683,8 +685,31 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                         for (int k = 0; k < 64; ++k)
                             if (j0 + 8 * (k >> 2) + col + (k & 1) >= p.keys) sr[k] = 0xff800000u;
                     }
-                    float f[2], neg[2];
-                    bool moved = false;
+                    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
+                    uint32_t pk[2][16];
+                    uint64_t sum[2];
+                    const auto exponentials = [&]() {  // P and its sums with the maxima that there are
+                        uint64_t neg2[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float neg = m[x] == -INFINITY ? 0.f : -m[x];
+                            neg2[x] = pair(neg, neg);
+                            sum[x] = 0;  // a pair of zeros
+                        }
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const int x = k & 1;
+                            float a, b;
+                            unpair(fma2(pair(__uint_as_float(sr[2 * k]), __uint_as_float(sr[2 * k + 1])), scale2, neg2[x]), a, b);
+                            a = ex2_approx(a);
+                            b = ex2_approx(b);
+                            sum[x] = add2(sum[x], pair(a, b));
+                            pk[k >> 4][k & 15] = pack_bf16x2(a, b);
+                        }
+                    };
+                    float mt[2];
+                    bool beyond = i < 2;  // the stream's first tile sets the maximum
+                    if (i >= 2) exponentials();
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         float m2[2];  // two chains
@@ -695,53 +720,42 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                             for (int k = 2 + c; k < 16; k += 2)
                                 m2[c] = max3(m2[c], __uint_as_float(sr[4 * k + 2 * x]), __uint_as_float(sr[4 * k + 2 * x + 1]));
                         }
-                        float mt = fmaxf(m2[0], m2[1]);
-                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-                        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2)) * p.scale_log2;
-                        // The running maximum: set by the stream's first tile, moved later only by more than the
-                        // threshold.  While a row has seen no key it stays at -infinity and O and l at 0.
-                        const bool first = m[x] == -INFINITY, grow = mt > m[x] + kRescaleLog2 || first;
-                        f[x] = grow && !first ? ex2_approx(m[x] - mt) : 1.f;
-                        if (grow) m[x] = mt;
-                        moved = moved || f[x] != 1.f;
-                        neg[x] = m[x] == -INFINITY ? 0.f : -m[x];
+                        mt[x] = fmaxf(m2[0], m2[1]) * p.scale_log2;
+                        beyond = beyond || mt[x] > m[x] + kRescaleLog2;  // -infinity while a row has seen no key
                     }
-                    if (i > 1 && __any_sync(0xffffffffu, moved)) {
-                        // O's earlier PVs have finished: S(i) complete implies it (QK(i) was issued after
-                        // PV(i - 2), and a commit covers every earlier MMA of the thread)
+                    if (__any_sync(0xffffffffu, beyond)) {
+                        float f[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            mt[x] = fmaxf(mt[x], __shfl_xor_sync(0xffffffffu, mt[x], 1));
+                            mt[x] = fmaxf(mt[x], __shfl_xor_sync(0xffffffffu, mt[x], 2));
+                            const bool first = m[x] == -INFINITY, grow = mt[x] > m[x] + kRescaleLog2 || first;
+                            f[x] = grow && !first ? ex2_approx(m[x] - mt[x]) : 1.f;
+                            if (grow) m[x] = mt[x];
+                            l[x] *= f[x];
+                        }
+                        if (i >= 2) {
+                            // O's earlier PVs have finished: S(i) complete implies it (QK(i) was issued after
+                            // PV(i - 2), and a commit covers every earlier MMA of the thread)
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t o[16];
-                            tmem_ld_16x32(t_s + 128 + 32 * c, o);
-                            tmem_wait_ld();
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t o[16];
+                                tmem_ld_16x32(t_s + 128 + 32 * c, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[(k >> 1) & 1]);
-                            tmem_st_16x32(t_s + 128 + 32 * c, o);
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[(k >> 1) & 1]);
+                                tmem_st_16x32(t_s + 128 + 32 * c, o);
+                            }
                         }
+                        exponentials();
                     }
-                    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
-                    const uint64_t neg2[2] = {pair(neg[0], neg[0]), pair(neg[1], neg[1])};
-                    uint64_t sum[2] = {0, 0};  // pairs of zeros
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int at = 32 * c + 2 * k, x = k & 1;
-                            float a, b;
-                            unpair(fma2(pair(__uint_as_float(sr[at]), __uint_as_float(sr[at + 1])), scale2, neg2[x]), a, b);
-                            a = ex2_approx(a);
-                            b = ex2_approx(b);
-                            sum[x] = add2(sum[x], pair(a, b));
-                            pk[k] = pack_bf16x2(a, b);
-                        }
-                        tmem_st_pairs(t_s + 32 * c, pk);
-                    }
+                    tmem_st_pairs(t_s, pk[0]);
+                    tmem_st_pairs(t_s + 32, pk[1]);
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         float a, b;
                         unpair(sum[x], a, b);
-                        l[x] = l[x] * f[x] + (a + b);
+                        l[x] += a + b;
                     }
                     tmem_wait_st();
                 }
