@@ -45,38 +45,38 @@ bool cache_aligned(mla_kv_dtype kv_dtype, const void* kv_pool, const float* kv_s
 }
 
 // The maps of q_c [rows][128][128], q_r [rows][128][64], k and v [128][keys][128] and k_r [keys] rows of
-// `kr_stride` elements: boxes of 128 rows or keys by 64 columns, of 64 keys for the values.
+// `kr_stride` elements: boxes of 64 columns by 128 rows, by 128 keys (64 in a pair), by 64 keys for the values.
 struct Maps {
     CUtensorMap qc, qr, k, kr, v;
 };
 
 bool make_maps(Maps* m, const void* q_c, const void* q_r, const void* k, const void* v, const void* k_r,
-               int64_t kr_stride, int64_t rows, int64_t keys)
+               int64_t kr_stride, int64_t rows, int64_t keys, bool pair)
 {
     using mla::make_bf16_map;
     const cuuint64_t qc_dims[3] = {128, 128, (cuuint64_t)rows}, qc_str[2] = {128 * 2, 128 * 128 * 2};
     const cuuint64_t qr_dims[3] = {64, 128, (cuuint64_t)rows}, qr_str[2] = {64 * 2, 128 * 64 * 2};
     const cuuint32_t q_box[3] = {64, 1, 128};
     const cuuint64_t k_dims[3] = {128, (cuuint64_t)keys, 128}, k_str[2] = {128 * 2, (cuuint64_t)keys * 128 * 2};
-    const cuuint32_t k_box[3] = {64, 128, 1}, v_box[3] = {64, 64, 1};
+    const cuuint32_t k_box[3] = {64, pair ? 64u : 128u, 1}, v_box[3] = {64, 64, 1};
     const cuuint64_t r_dims[2] = {64, (cuuint64_t)keys}, r_str[1] = {(cuuint64_t)kr_stride * 2};
-    const cuuint32_t r_box[2] = {64, 128};
+    const cuuint32_t r_box[2] = {64, pair ? 64u : 128u};
     return make_bf16_map(&m->qc, q_c, 3, qc_dims, qc_str, q_box) && make_bf16_map(&m->qr, q_r, 3, qr_dims, qr_str, q_box) &&
            make_bf16_map(&m->k, k, 3, k_dims, k_str, k_box) && make_bf16_map(&m->v, v, 3, k_dims, k_str, v_box) &&
            make_bf16_map(&m->kr, k_r, 2, r_dims, r_str, r_box);
 }
 
-template <bool kChunk, int kQT>
-mla_status launch_attend(const Maps& m, const mla::attend::Params& p, int ctas, void* stream)
+template <bool kChunk, bool kPair>
+mla_status launch_attend(const Maps& m, const mla::attend::Params& p, int workers, void* stream)
 {
     using namespace mla::attend;
-    const auto kernel = attend_kernel<kChunk, kQT>;
+    const auto kernel = attend_kernel<kChunk, kPair>;
     const mla_status st = mla::cuda_status(
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kQT>::kSmemBytes),
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kPair>::kSmemBytes),
         "cudaFuncSetAttribute(max dynamic shared memory)");
     if (st != MLA_OK) return st;
-    return mla::launch_dependent("attend kernel launch", kernel, dim3((unsigned)ctas), dim3(kThreads),
-                                 Layout<kQT>::kSmemBytes, stream, m.qc, m.qr, m.k, m.kr, m.v, p);
+    return mla::launch_dependent("attend kernel launch", kernel, dim3((unsigned)(kPair ? 2 * workers : workers)), dim3(kThreads),
+                                 Layout<kPair>::kSmemBytes, stream, m.qc, m.qr, m.k, m.kr, m.v, p);
 }
 
 mla_status sm_count(int* sms)
@@ -115,9 +115,10 @@ mla_status expand_rows(const void* rows, const void* w_uk, const void* w_uv, voi
                                  dim3(kThreads), kSmemBytes, stream, tm_rows, tm_uk, tm_uv, p);
 }
 
-// How the prefix form cuts its work: two query tiles a CTA above 128 rows, then each key tile serves both.
+// How the prefix form cuts its work: by CTAs of 128 rows, with more rows by pairs of them.
 struct Cut {
-    int q_tiles, groups, group_rows, rows_cap, tiles, ctas;
+    bool pair;
+    int groups, group_rows, rows_cap, tiles, workers;
     int64_t slots;
     size_t lse_off, total;  // workspace: partials [slots][rows_cap][128] fp32, then [slots][rows_cap] fp32
 };
@@ -125,13 +126,13 @@ struct Cut {
 Cut cut_prefix(int32_t rows, int32_t prefix_len, int32_t num_sms)
 {
     Cut c;
-    c.q_tiles = rows > 128 ? 2 : 1;
-    c.group_rows = 128 * c.q_tiles;
+    c.pair = rows > 128;
+    c.group_rows = c.pair ? 256 : 128;
     c.groups = (rows + c.group_rows - 1) / c.group_rows;
     c.rows_cap = std::min(rows, c.group_rows);
     c.tiles = (prefix_len + 127) / 128;
-    c.ctas = (int)std::min<int64_t>(num_sms, (int64_t)c.groups * 128 * c.tiles);
-    c.slots = (int64_t)c.ctas + (int64_t)c.groups * 128 - 1;
+    c.workers = (int)std::min<int64_t>(c.pair ? std::max(1, num_sms / 2) : num_sms, (int64_t)c.groups * 128 * c.tiles);
+    c.slots = (int64_t)c.workers + (int64_t)c.groups * 128 - 1;
     c.lse_off = (size_t)c.slots * c.rows_cap * 128 * 4;
     c.total = c.lse_off + (size_t)c.slots * c.rows_cap * 4;
     return c;
@@ -225,7 +226,7 @@ extern "C" MLA_API mla_status mla_prefix_attend(int32_t num_rows, int32_t prefix
     const Cut c = cut_prefix(num_rows, prefix_len, num_sms);
     if (workspace_bytes < c.total) return MLA_ERR_WORKSPACE;
     Maps m;
-    if (!make_maps(&m, q_c, q_r, k, v, k_r, k_r_stride, num_rows, prefix_len)) return MLA_ERR_CUDA;
+    if (!make_maps(&m, q_c, q_r, k, v, k_r, k_r_stride, num_rows, prefix_len, c.pair)) return MLA_ERR_CUDA;
     mla::attend::Params p = {};
     p.rows = num_rows;
     p.keys = prefix_len;
@@ -239,8 +240,8 @@ extern "C" MLA_API mla_status mla_prefix_attend(int32_t num_rows, int32_t prefix
     p.rows_cap = c.rows_cap;
     p.ws_o = static_cast<float*>(workspace);
     p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + c.lse_off);
-    const mla_status st = c.q_tiles == 2 ? launch_attend<false, 2>(m, p, c.ctas, stream)
-                                         : launch_attend<false, 1>(m, p, c.ctas, stream);
+    const mla_status st = c.pair ? launch_attend<false, true>(m, p, c.workers, stream)
+                                 : launch_attend<false, false>(m, p, c.workers, stream);
     if (st != MLA_OK) return st;
     mla::attend::Merge a = {};
     a.ws_o = p.ws_o;
@@ -250,7 +251,7 @@ extern "C" MLA_API mla_status mla_prefix_attend(int32_t num_rows, int32_t prefix
     a.groups = c.groups;
     a.group_rows = c.group_rows;
     a.tiles = c.tiles;
-    a.ctas = c.ctas;
+    a.workers = c.workers;
     a.own_out = static_cast<const __nv_bfloat16*>(own_out);
     a.own_lse = own_lse;
     a.out = static_cast<__nv_bfloat16*>(out);
@@ -293,7 +294,7 @@ extern "C" MLA_API mla_status mla_prefill_window(mla_kv_dtype kv_dtype, const vo
     char* ws = static_cast<char*>(workspace);
     void *k = ws + s.k, *v = ws + s.v;
     Maps m;
-    if (!make_maps(&m, q_c, q_r, k, v, ws + 512 * 2, 576, chunk_len, s.keys)) return MLA_ERR_CUDA;
+    if (!make_maps(&m, q_c, q_r, k, v, ws + 512 * 2, 576, chunk_len, s.keys, true)) return MLA_ERR_CUDA;
     int sms = 0;
     mla_status st = sm_count(&sms);
     if (st != MLA_OK) return st;
@@ -314,5 +315,5 @@ extern "C" MLA_API mla_status mla_prefill_window(mla_kv_dtype kv_dtype, const vo
     p.window = std::min(window, seq_len);
     p.sinks = std::min(sinks, seq_len);
     p.out = static_cast<__nv_bfloat16*>(out);
-    return launch_attend<true, 2>(m, p, (int)std::min<int64_t>(sms, (int64_t)p.groups * 128), stream);
+    return launch_attend<true, true>(m, p, (int)std::min<int64_t>(std::max(1, sms / 2), (int64_t)p.groups * 128), stream);
 }

@@ -13,30 +13,30 @@
 // rows there are: with up to about 110 rows that is what bounds the prefix form (HBM), beyond it
 // the tensor cores.
 //
-// One CTA holds one or two 128-row query tiles of a head (kQT) and streams 128-key tiles.  It works
-// on two "streams", each with a score buffer S, an output O and a running softmax (m, l) of its own:
-// with two query tiles a stream is a tile, and both use every key tile; with one query tile the even
-// key tiles are one stream and the odd ones the other, and the two are joined at the end, so that one
-// stream's softmax always has the other's products to hide behind.  Step i belongs to stream i & 1; the
-// MMA order is PV(i), QK(i + 2).
-//   QK:  S[128 x 128] = Q [128 x 192] (q_c | q_R: three 64-column chunks in shared memory)
+// A CTA holds a 128-row query tile of a head and streams 128-key tiles; with more than 128 rows a pair of CTAs
+// (two SMs, MMAs of M = 256) holds 256 rows, and each brings in half of every key tile (64 keys) and of every
+// value tile (64 dims).  Alone a CTA with 256 rows waited for its keys: 80 KB a tile and a ring of 128 KB.
+// It works on two "streams", the even key tiles and the odd ones, each with a score buffer S, an output O and a
+// running softmax (m, l) of its own, joined at the end, so that one stream's softmax always has the other's
+// products to hide behind.  Step i is key tile i, of stream i & 1; the MMA order is PV(i), QK(i + 2).
+//   QK:  S[rows x 128] = Q [rows x 192] (q_c | q_R: three 64-column chunks in shared memory)
 //                       x K tile [128 x 192] (k | k_R: three K-major chunks)
-//   PV:  O[128 x 128] += P [128 x 128] (bf16 in TMEM over the first half of S) x V tile (MN-major)
-// Everything that is streamed goes through one ring of 16 KB slots, in the order in which the MMAs
-// first need it: a key chunk [128 keys][64] or 64 keys' values [64][128].  A slot is four MMAs, so
-// the ring is as fine as the tensor core's work and a slot is free as soon as its four are done.
+//   PV:  O[rows x 128] += P [rows x 128] (bf16 in TMEM over the first half of S) x V tile (MN-major)
+// Everything that is streamed goes through one ring of slots, in the order in which the MMAs need it: a key chunk
+// [128 keys][64] or 64 keys' values [64][128], in a pair half of it.  A slot is four MMAs, so the ring is as fine
+// as the tensor core's work and a slot is free as soon as its four are done.
 //
 // Warp 0 streams the ring, warp 2 the query tiles, warp 1 issues the MMAs, warps 3-10 are the softmax
 // of every step: a warp has 16 rows, a quad of lanes two of them (tcgen05.ld's 16x256b shape: lane l holds
 // columns 8 k + 2 (l & 3), + 1 of rows l / 4 and l / 4 + 8), so that a row's maximum is two shuffles away.
-// What bounds a CTA with two query tiles is the chain QK -> softmax -> PV of a stream against the other
-// stream's products, so all eight warps work on one step: with four warps to a stream and a row a thread a
-// step's softmax took 1,530 cycles of that chain, more than a step's 20 MMAs of 64; with halves of a row that
-// agree through shared memory 1,450, of which the barrier 250.  The running maximum is the one of the stream's
-// first tile and moves only when a score exceeds it by more than 32 (log2 units), which loses nothing: fp32
-// and bf16 round relative to the value.  So a step takes its exponentials with the maximum that it has, looks
-// at its scores beside that (no exchange between lanes), and does them again in the rare other case.  P is rounded to bf16 for the PV product (its sum l takes
-// the unrounded values); scores, maxima, sums and O are fp32.
+// What bounds it with many rows is the chain QK -> softmax -> PV of a stream against the other stream's
+// products, so all eight warps work on one step: with four warps to a stream and a row a thread a step's softmax
+// took 1,530 cycles of that chain, more than a step's 20 MMAs of 64; with halves of a row that agree through
+// shared memory 1,450; this way 1,050.  The running maximum is the one of the stream's first tile and moves only
+// when a score exceeds it by more than 32 (log2 units), which loses nothing: fp32 and bf16 round relative to the
+// value.  So a step takes its exponentials with the maximum that it has, looks at its scores beside that (no
+// exchange between lanes), and does them again in the rare other case.  P is rounded to bf16 for the PV product
+// (its sum l takes the unrounded values); scores, maxima, sums and O are fp32.
 //
 // The prefix form is persistent: the (head, row group, key tile) units lie in one line that the CTAs
 // cut evenly, so that every SM streams the same number of bytes; a CTA's piece of one (head, group)
@@ -242,13 +242,6 @@ __device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, const uint32_t (&r
           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 
-__device__ __forceinline__ void prefetch_tile_3d(const void* map, int x, int y, int z)
-{
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(z)
-                 : "memory");
-}
-
 // `bytes` (a multiple of 16) from `p` into L2, without waiting.
 __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes)
 {
@@ -258,28 +251,30 @@ __device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes)
 constexpr int kTile = 128;                 // query rows of a tile, keys of a tile
 constexpr int kThreads = 32 * 11;
 constexpr int kSoftmaxWarp0 = 3;
-constexpr int kSlotBytes = 16384;
 constexpr uint32_t kTmemCols = 512;        // stream t: S at 256 t, O at 256 t + 128
 constexpr float kRescaleLog2 = 32.f;       // P up to 2^32, l and O below 2^32 x keys x |v|: far from fp32's 2^127
 constexpr int kFetch = 4;                  // key tiles ahead that are brought into L2
 
-template <int kQT>
+template <bool kPair>
 struct Layout {
-    static constexpr int kSlots = 8;
-    static constexpr int kQBufs = 2 / kQT;  // with one query tile the next segment's is loaded beside it
-    static constexpr int kOffRing = 2 * 3 * kSlotBytes;
-    static constexpr int kOffBar = kOffRing + kSlots * kSlotBytes;
-    static constexpr int kBarFull = 0, kBarEmpty = kSlots;
+    static constexpr int kSlot = kPair ? 8192 : 16384;
+    static constexpr int kSlots = 131072 / kSlot;
+    static constexpr int kQ = 3 * 16384;                     // a query tile; the next segment's is loaded beside it
+    static constexpr int kOffRing = 2 * kQ;
+    static constexpr int kOffBar = kOffRing + kSlots * kSlot;
+    static constexpr int kBarFull = 0, kBarEmpty = kSlots;   // [slot]
     static constexpr int kBarQFull = 2 * kSlots, kBarQEmpty = kBarQFull + 2;  // [buffer]
-    static constexpr int kBarSFull = kBarQEmpty + 2;  // [stream]
-    static constexpr int kBarPReady = kBarSFull + 2;  // [stream], eight warps' arrivals
-    static constexpr int kBarODone = kBarPReady + 2;  // the segment's last PV has finished
-    static constexpr int kBarOFree = kBarODone + 1;   // eight warps' arrivals: the segment's O has been read
-    static constexpr int kBarEnd = kBarOFree + 1;     // every MMA of the CTA has finished
+    static constexpr int kBarSFull = kBarQEmpty + 2;         // [stream]
+    static constexpr int kBarPReady = kBarSFull + 2;         // [stream], every softmax warp's arrival
+    static constexpr int kBarODone = kBarPReady + 2;         // the segment's last PV has finished
+    static constexpr int kBarOFree = kBarODone + 1;          // every softmax warp's arrival: the segment's O has been read
+    static constexpr int kBarEnd = kBarOFree + 1;            // every MMA has finished
     static constexpr int kBars = kBarEnd + 1;
     static constexpr int kSmemBytes = kOffBar + 8 * kBars + 16;
     static_assert(kSmemBytes <= 232448, "a CTA's shared memory");
 };
+// In a pair the barriers on which the MMAs wait (full, Q full, P ready, O free) are the even CTA's, by both CTAs'
+// copies and warps; those that MMAs complete (empty, Q empty, S full, O done, end) are in both.
 // Phase bookkeeping.  A barrier waited by parity must never run two phases ahead of its waiter:
 //   S full [t]   completes once per step of stream t; QK(i + 2) is issued only after the MMA thread
 //                has seen P(i) ready, i.e. after the stream's softmax has finished step i.
@@ -293,7 +288,7 @@ struct Params {
     int rows;            // query rows
     int keys;            // key rows
     float scale_log2;    // softmax_scale * log2(e)
-    int groups;          // row groups of kQT tiles
+    int groups;          // row groups of 128, in a pair 256
     uint32_t* dev_error;
     uint64_t timeout_ns;
     // prefix
@@ -307,29 +302,32 @@ struct Params {
     __nv_bfloat16* out;  // [rows][128][128]
 };
 
-// A CTA's piece of one run.
+// A worker's piece of one run.
 struct Segment {
     int head, row0, cnt;  // cnt key tiles
     int lead, tile0;      // key tile n: n < lead ? n : tile0 + n
     int slot;             // the prefix's partial
 };
 
-// The first unit of CTA c, of `units` in all shared by g <= units CTAs (each has one at least).
+// The first unit of worker (CTA or pair) c, of `units` in all shared by g <= units workers (each has one at least).
 __host__ __device__ __forceinline__ int64_t first_unit(int64_t c, int64_t units, int64_t g) { return c * units / g; }
 
-// Walks this CTA's segments; every role walks the same ones.
-template <bool kChunk, int kQT>
+// Walks this worker's segments; every role walks the same ones.
+template <bool kChunk, bool kPair>
 struct Walk {
+    static constexpr int kRows = kPair ? 2 * kTile : kTile;
     int64_t at, end;
+    __device__ __forceinline__ int worker() const { return kPair ? blockIdx.x >> 1 : blockIdx.x; }
+    __device__ __forceinline__ int workers() const { return kPair ? gridDim.x >> 1 : gridDim.x; }
     __device__ __forceinline__ explicit Walk(const Params& p)
     {
         if (kChunk) {
-            at = blockIdx.x;
+            at = worker();
             end = (int64_t)p.groups * 128;
         } else {
             const int64_t units = (int64_t)p.groups * 128 * p.tiles;
-            at = first_unit(blockIdx.x, units, gridDim.x);
-            end = first_unit(blockIdx.x + 1, units, gridDim.x);
+            at = first_unit(worker(), units, workers());
+            end = first_unit(worker() + 1, units, workers());
         }
     }
     __device__ __forceinline__ bool next(const Params& p, Segment& s)
@@ -338,23 +336,23 @@ struct Walk {
         if (kChunk) {
             // a head's groups lie side by side: their windows overlap and are read from L2
             s.head = (int)(at / p.groups);
-            s.row0 = (int)(at % p.groups) * kQT * kTile;
-            const int last = min(s.row0 + kQT * kTile, p.rows) - 1;
+            s.row0 = (int)(at % p.groups) * kRows;
+            const int last = min(s.row0 + kRows, p.rows) - 1;
             const int lo = max(0, p.hi0 + s.row0 - p.window + 1);  // the first key in the first row's window
             s.lead = (min(p.sinks, lo) + kTile - 1) / kTile;
             const int first = max(s.lead, lo / kTile);
             s.tile0 = first - s.lead;
             s.cnt = s.lead + (p.hi0 + last) / kTile + 1 - first;
             s.slot = 0;
-            at += gridDim.x;
+            at += workers();
         } else {
             const int run = (int)(at / p.tiles), n0 = (int)(at - (int64_t)run * p.tiles);
             s.head = run / p.groups;
-            s.row0 = (run % p.groups) * kQT * kTile;
+            s.row0 = (run % p.groups) * kRows;
             s.cnt = (int)min((int64_t)(p.tiles - n0), end - at);
             s.lead = 0;
             s.tile0 = n0;
-            s.slot = (int)blockIdx.x + run;
+            s.slot = worker() + run;
             at += s.cnt;
         }
         return true;
@@ -363,62 +361,73 @@ struct Walk {
 
 __device__ __forceinline__ int key_tile(const Segment& s, int n) { return n < s.lead ? n : s.tile0 + n; }
 
-template <bool kChunk, int kQT>
+template <bool kChunk, bool kPair>
 // 11 warps: three SM sub-partitions hold three of them, 16K registers each: at most 3 x 32 x 168
-__global__ void __maxnreg__(168)
+__global__ void __cluster_dims__(kPair ? 2 : 1, 1, 1) __maxnreg__(168)
 attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__ CUtensorMap tm_qr,
               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
               const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p)
 {
     using namespace dev;
-    using L = Layout<kQT>;
+    using L = Layout<kPair>;
     extern __shared__ __align__(1024) uint8_t smem[];
     // (through a shuffle, so that the compiler sees a value that is the warp's)
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = kPair ? (int)cluster_ctarank() : 0;
     const uint32_t sbase = smem_u32(smem);
     const uint32_t bars = sbase + L::kOffBar;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kOffBar + 8 * L::kBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     const auto bar = [&](int id) { return bars + 8 * id; };
+    // the barrier on which the MMA warp waits: the even CTA's
+    const auto mma_bar = [&](int id) { return kPair ? map_to_cta(bars + 8 * id, 0) : bars + 8 * id; };
 
-    if (sbase & 1023u) {
-        if (threadIdx.x == 0) raise_error(p.dev_error, MLA_DEVERR_SMEM_ALIGN);
-        return;
-    }
     if (threadIdx.x == 0) {
+        constexpr int kWarps = kPair ? 16 : 8;  // softmax warps
         for (int s = 0; s < 2 * L::kSlots; ++s) mbar_init(bar(s), 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar(L::kBarQFull + b), 1);
             mbar_init(bar(L::kBarQEmpty + b), 1);
             mbar_init(bar(L::kBarSFull + b), 1);
-            mbar_init(bar(L::kBarPReady + b), 8);  // one arrive per softmax warp
+            mbar_init(bar(L::kBarPReady + b), kWarps);
         }
         mbar_init(bar(L::kBarODone), 1);
-        mbar_init(bar(L::kBarOFree), 8);
+        mbar_init(bar(L::kBarOFree), kWarps);
         mbar_init(bar(L::kBarEnd), 1);
-        *abort_flag = 0;
+        const bool misaligned = (sbase & 1023u) != 0;
+        if (misaligned) raise_error(p.dev_error, MLA_DEVERR_SMEM_ALIGN);
+        *abort_flag = misaligned;
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_holder), kTmemCols);
-        tmem_relinquish();
+        if (kPair) {
+            tmem_alloc_pair(smem_u32(tmem_holder), kTmemCols);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(tmem_holder), kTmemCols);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    if (kPair)
+        cluster_sync();  // both CTAs' barriers exist before anyone arrives remotely
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     const WaitCtx w{p.timeout_ns, abort_flag, p.dev_error};
-    Walk<kChunk, kQT> walk(p);
+    Walk<kChunk, kPair> walk(p);
     Segment seg;
 
-    if (warp == 0) {
+    if (*abort_flag) {
+    } else if (warp == 0) {
         griddep_wait();  // keys, values and queries may come from the kernel before; nothing is written ahead of them
         const bool leader = elect_lane();
         // the prefix's keys and values are read once by one group of rows, k_R by every head
         const uint64_t pol_kv = kChunk || p.groups > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
         const uint64_t pol_kr = l2_policy_evict_last();
-        // Keys and values of the tile kFetch ahead go into L2, so that a slot, which is free only a step
-        // before it is needed, is filled from there.
+        // Keys and values of the tile kFetch ahead go into L2, so that a slot, which is free only a step or two
+        // before it is needed, is filled from there (the even CTA of a pair fetches the keys, the odd one the values).
         // (Behind the tile's own loads, and at most two tiles a turn: at the start the first tiles come first.)
         int fetched = 0;
         const auto fetch = [&](int n) {
@@ -426,14 +435,17 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             const uint32_t bytes = (uint32_t)min(kTile, p.keys - j0) * 256;
             const int64_t at = ((int64_t)seg.head * p.keys + j0) * 128;
             if (leader) {
-                prefetch_l2(p.k + at, bytes);
-                prefetch_l2(p.v + at, bytes);
+                if (rank == 0) prefetch_l2(p.k + at, bytes);
+                if (!kPair || rank == 1) prefetch_l2(p.v + at, bytes);
             }
         };
         int r = 0, s = 0, phase = 0;
         bool ok = true;
-        const auto take = [&]() {  // the next slot, free
-            return ok = r < L::kSlots || wait_all(bar(L::kBarEmpty + s), phase - 1, w);
+        const uint32_t full0 = mma_bar(L::kBarFull);
+        const auto take = [&]() {  // the next slot, free; its barrier expects the slot's bytes
+            ok = r < L::kSlots || wait_all<kPair>(bar(L::kBarEmpty + s), phase - 1, w);
+            if (ok && leader && rank == 0) mbar_arrive_expect_tx(bar(L::kBarFull + s), (kPair ? 2 : 1) * L::kSlot);
+            return ok;
         };
         const auto put = [&]() {
             ++r;
@@ -446,13 +458,19 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
 #pragma unroll 1
             for (int c = 0; c < 3; ++c) {
                 if (!take()) return;
-                const uint32_t dst = sbase + L::kOffRing + s * kSlotBytes, full = bar(L::kBarFull + s);
+                const uint32_t dst = sbase + L::kOffRing + s * L::kSlot, full = full0 + 8 * s;
                 if (leader) {
-                    mbar_arrive_expect_tx(full, kSlotBytes);
-                    if (c < 2)
-                        tma_load_3d(dst, &tm_k, full, 64 * c, j0, seg.head, pol_kv);
-                    else
-                        tma_load_2d(dst, &tm_kr, full, 0, j0, pol_kr);
+                    if (kPair) {
+                        if (c < 2)
+                            tma_load_3d_pair(dst, &tm_k, full, 64 * c, j0 + 64 * rank, seg.head, pol_kv);
+                        else
+                            tma_load_2d_pair(dst, &tm_kr, full, 0, j0 + 64 * rank, pol_kr);
+                    } else {
+                        if (c < 2)
+                            tma_load_3d(dst, &tm_k, full, 64 * c, j0, seg.head, pol_kv);
+                        else
+                            tma_load_2d(dst, &tm_kr, full, 0, j0, pol_kr);
+                    }
                 }
                 put();
             }
@@ -461,11 +479,14 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
 #pragma unroll 1
             for (int c = 0; c < 2; ++c) {
                 if (!take()) return;
-                const uint32_t dst = sbase + L::kOffRing + s * kSlotBytes, full = bar(L::kBarFull + s);
+                const uint32_t dst = sbase + L::kOffRing + s * L::kSlot, full = full0 + 8 * s;
                 if (leader) {
-                    mbar_arrive_expect_tx(full, kSlotBytes);
-                    tma_load_3d(dst, &tm_v, full, 0, j0 + 64 * c, seg.head, pol_kv);
-                    tma_load_3d(dst + kSlotBytes / 2, &tm_v, full, 64, j0 + 64 * c, seg.head, pol_kv);
+                    if (kPair) {
+                        tma_load_3d_pair(dst, &tm_v, full, 64 * rank, j0 + 64 * c, seg.head, pol_kv);
+                    } else {
+                        tma_load_3d(dst, &tm_v, full, 0, j0 + 64 * c, seg.head, pol_kv);
+                        tma_load_3d(dst + L::kSlot / 2, &tm_v, full, 64, j0 + 64 * c, seg.head, pol_kv);
+                    }
                 }
                 put();
             }
@@ -476,18 +497,17 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             tma_prefetch_desc(&tm_v);
         }
         while (ok && walk.next(p, seg)) {
-            constexpr int kAhead = kQT == 1 ? 2 : 1;  // key tiles ahead of the values
-            for (int n = 0; ok && n < kAhead && n < seg.cnt; ++n) load_k(key_tile(seg, n) * kTile);
-            fetched = kAhead + 1;
+            for (int n = 0; ok && n < 2 && n < seg.cnt; ++n) load_k(key_tile(seg, n) * kTile);
+            fetched = 3;
             for (int n = 0; ok && n < seg.cnt; ++n) {
                 load_v(key_tile(seg, n) * kTile);
-                if (ok && n + kAhead < seg.cnt) load_k(key_tile(seg, n + kAhead) * kTile);
+                if (ok && n + 2 < seg.cnt) load_k(key_tile(seg, n + 2) * kTile);
                 for (int two = 0; two < 2 && fetched < min(seg.cnt, n + 1 + kFetch); ++two, ++fetched) fetch(fetched);
             }
         }
         griddep_launch_dependents();  // the merge may be scheduled; it waits for this kernel's end
-        // loads in flight land before the CTA can exit
-        for (int k = r > L::kSlots ? r - L::kSlots : 0; k < r; ++k)
+        // loads in flight land before the CTA can exit (in a pair both CTAs' complete on the even one's barriers)
+        for (int k = r > L::kSlots ? r - L::kSlots : 0; rank == 0 && k < r; ++k)
             drain_phase(bar(L::kBarFull + k % L::kSlots), k / L::kSlots, w.timeout_ns);
     } else if (warp == 2) {
         griddep_wait();
@@ -498,145 +518,144 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             tma_prefetch_desc(&tm_qr);
         }
         int n = 0;
-        bool more = walk.next(p, seg);
-        while (more) {
-            const int b = n % L::kQBufs;
-            if (n >= L::kQBufs && !wait_all(bar(L::kBarQEmpty + b), n / L::kQBufs - 1, w)) break;
+        while (walk.next(p, seg)) {
+            const int b = n & 1;
+            if (n >= 2 && !wait_all<kPair>(bar(L::kBarQEmpty + b), (n >> 1) - 1, w)) break;
             if (leader) {
-                const uint32_t full = bar(L::kBarQFull + b);
-                mbar_arrive_expect_tx(full, kQT * 3 * kSlotBytes);
-                for (int t = 0; t < kQT; ++t) {
-                    const uint32_t q = sbase + (b + t) * 3 * kSlotBytes;
-                    const int row = seg.row0 + kTile * t;
+                const uint32_t full = mma_bar(L::kBarQFull + b), q = sbase + b * L::kQ;
+                const int row = seg.row0 + kTile * rank;
+                if (rank == 0) mbar_arrive_expect_tx(bar(L::kBarQFull + b), (kPair ? 2 : 1) * L::kQ);
+                if (kPair) {
+                    tma_load_3d_pair(q, &tm_qc, full, 0, seg.head, row, pol);
+                    tma_load_3d_pair(q + 16384, &tm_qc, full, 64, seg.head, row, pol);
+                    tma_load_3d_pair(q + 2 * 16384, &tm_qr, full, 0, seg.head, row, pol);
+                } else {
                     tma_load_3d(q, &tm_qc, full, 0, seg.head, row, pol);
-                    tma_load_3d(q + kSlotBytes, &tm_qc, full, 64, seg.head, row, pol);
-                    tma_load_3d(q + 2 * kSlotBytes, &tm_qr, full, 0, seg.head, row, pol);
+                    tma_load_3d(q + 16384, &tm_qc, full, 64, seg.head, row, pol);
+                    tma_load_3d(q + 2 * 16384, &tm_qr, full, 0, seg.head, row, pol);
                 }
             }
             ++n;
-            more = walk.next(p, seg);
-            if (more && leader && L::kQBufs == 1)  // two tiles have no second buffer: the next ones wait in L2
-                for (int t = 0; t < kQT; ++t) {
-                    const int row = seg.row0 + kTile * t;
-                    prefetch_tile_3d(&tm_qc, 0, seg.head, row);
-                    prefetch_tile_3d(&tm_qc, 64, seg.head, row);
-                    prefetch_tile_3d(&tm_qr, 0, seg.head, row);
-                }
         }
-        for (int k = n > L::kQBufs ? n - L::kQBufs : 0; k < n; ++k)
-            drain_phase(bar(L::kBarQFull + k % L::kQBufs), k / L::kQBufs, w.timeout_ns);
+        for (int k = n > 2 ? n - 2 : 0; rank == 0 && k < n; ++k) drain_phase(bar(L::kBarQFull + (k & 1)), k >> 1, w.timeout_ns);
     } else if (warp == 1) {
-        constexpr uint32_t idesc_qk = idesc_bf16(128, kTile, false, false);
-        constexpr uint32_t idesc_pv = idesc_bf16(128, 128, false, true);
-        const uint64_t q_desc = smem_desc(sbase, 16, 1024);
-        const uint64_t k_desc = smem_desc(sbase + L::kOffRing, 16, 1024);
-        const uint64_t v_desc = smem_desc(sbase + L::kOffRing, kSlotBytes / 2, 1024);
-        constexpr uint64_t kSlot16 = kSlotBytes >> 4;  // a slot, in the descriptors' 16-byte units
-        int s = 0, phase = 0;  // the next slot that no MMA has used yet
-        int q_buf = 0;
-        bool ok = true;
-        // Scores of stream t from the three slots at `s0`: waits for them when they are new, frees them
-        // when this is their last use.
-        const auto qk = [&](int t, int& s0, int& ph, bool fresh, bool last) {
-            const uint32_t d = tmem + 256 * t;
-            const uint64_t a0 = q_desc + (kQT == 2 ? t : q_buf) * 3 * kSlot16;
-#pragma unroll 1
-            for (int c = 0; c < 3; ++c) {
-                if (fresh && !wait_all(bar(L::kBarFull + s0), ph, w)) return ok = false;
-                tc_fence_after();
-                const uint64_t a = a0 + c * kSlot16, b = k_desc + s0 * kSlot16;
-                mma_ss_one(d, a, b, idesc_qk, c != 0 ? 1u : 0u);
-                mma_ss_one(d, a + 2, b + 2, idesc_qk, 1u);
-                mma_ss_one(d, a + 4, b + 4, idesc_qk, 1u);
-                mma_ss_one(d, a + 6, b + 6, idesc_qk, 1u);
-                if (last) mma_commit_one(bar(L::kBarEmpty + s0));
-                if (++s0 == L::kSlots) {
-                    s0 = 0;
-                    ++ph;
+        if (rank == 0) {
+            constexpr uint32_t idesc_qk = idesc_bf16(kPair ? 256 : 128, kTile, false, false);
+            constexpr uint32_t idesc_pv = idesc_bf16(kPair ? 256 : 128, 128, false, true);
+            const uint64_t q_desc = smem_desc(sbase, 16, 1024);
+            const uint64_t k_desc = smem_desc(sbase + L::kOffRing, 16, 1024);
+            const uint64_t v_desc = smem_desc(sbase + L::kOffRing, 8192, 1024);
+            constexpr uint64_t kSlot16 = L::kSlot >> 4, kQChunk16 = 16384 >> 4;  // in the descriptors' 16-byte units
+            const auto ss = [](uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+                if (kPair)
+                    mma_ss_pair(d, a, b, idesc_qk, acc);
+                else
+                    mma_ss_one(d, a, b, idesc_qk, acc);
+            };
+            const auto ts = [](uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+                if (kPair)
+                    mma_ts_pair(d, a, b, idesc_pv, acc);
+                else
+                    mma_ts_one(d, a, b, idesc_pv, acc);
+            };
+            const auto commit = [](uint32_t b) {
+                if (kPair)
+                    mma_commit_pair(b);
+                else
+                    mma_commit_one(b);
+            };
+            int s = 0, phase = 0, q_buf = 0;  // the next slot, the segment's query tile
+            bool ok = true;
+            const auto next_slot = [&]() {
+                commit(bar(L::kBarEmpty + s));
+                if (++s == L::kSlots) {
+                    s = 0;
+                    ++phase;
                 }
-            }
-            mma_commit_one(bar(L::kBarSFull + t));
-            return true;
-        };
-        const auto pv = [&](int t, int& s0, int& ph, bool fresh, bool last, bool first_of_stream) {
-            const uint32_t pt = tmem + 256 * t, d = pt + 128;
+            };
+            // Scores of stream t from the next three slots.
+            const auto qk = [&](int t) {
+                const uint32_t d = tmem + 256 * t;
+                const uint64_t a0 = q_desc + q_buf * 3 * kQChunk16;
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-                if (fresh && !wait_all(bar(L::kBarFull + s0), ph, w)) return ok = false;
-                tc_fence_after();
-                const uint64_t b = v_desc + s0 * kSlot16;
-                const uint32_t a = pt + 32 * c;
-                mma_ts_one(d, a, b, idesc_pv, first_of_stream && c == 0 ? 0u : 1u);
-                mma_ts_one(d, a + 8, b + (2048 >> 4), idesc_pv, 1u);
-                mma_ts_one(d, a + 16, b + (4096 >> 4), idesc_pv, 1u);
-                mma_ts_one(d, a + 24, b + (6144 >> 4), idesc_pv, 1u);
-                if (last) mma_commit_one(bar(L::kBarEmpty + s0));
-                if (++s0 == L::kSlots) {
-                    s0 = 0;
-                    ++ph;
-                }
-            }
-            return true;
-        };
-        int n_seg = 0;
-        int done0 = 0, done1 = 0;  // steps of each stream
-        while (ok && walk.next(p, seg)) {
-            q_buf = n_seg % L::kQBufs;
-            if (!(ok = wait_all(bar(L::kBarQFull + q_buf), n_seg / L::kQBufs, w))) break;
-            tc_fence_after();
-            const int steps = kQT == 1 ? seg.cnt : 2 * seg.cnt;
-            if (kQT == 1) {
-                qk(0, s, phase, true, true);
-                if (ok && steps > 1) qk(1, s, phase, true, true);
-            } else {
-                int s1 = s, ph1 = phase;
-                qk(0, s1, ph1, true, false);
-                if (ok) qk(1, s, phase, false, true);
-            }
-            if (!ok) break;
-            if (steps <= 2) mma_commit_one(bar(L::kBarQEmpty + q_buf));
-            int sv = 0, pv_ph = 0, sk = 0, pk_ph = 0;  // kQT == 2: the slots of stream 0's values and keys
-            for (int i = 0; i < steps; ++i) {
-                const int t = i & 1;
-                if (!(ok = wait_all(bar(L::kBarPReady + t), t ? done1 : done0, w))) break;
-                done0 += t ^ 1;
-                done1 += t;
-                tc_fence_after();
-                if (i == 0 && n_seg > 0) {
-                    if (!(ok = wait_all(bar(L::kBarOFree), n_seg - 1, w))) break;
+                for (int c = 0; c < 3; ++c) {
+                    if (!wait_all<kPair>(bar(L::kBarFull + s), phase, w)) return ok = false;
                     tc_fence_after();
+                    const uint64_t a = a0 + c * kQChunk16, b = k_desc + s * kSlot16;
+                    ss(d, a, b, c != 0 ? 1u : 0u);
+                    ss(d, a + 2, b + 2, 1u);
+                    ss(d, a + 4, b + 4, 1u);
+                    ss(d, a + 6, b + 6, 1u);
+                    next_slot();
                 }
-                if (kQT == 1) {
-                    if (!pv(t, s, phase, true, true, i < 2)) break;
-                    if (i + 2 < steps && !qk(t, s, phase, true, true)) break;
-                } else if (t == 0) {
-                    sv = s;
-                    pv_ph = phase;
-                    if (!pv(0, s, phase, true, false, i < 2)) break;
-                    sk = s;
-                    pk_ph = phase;
-                    if (i + 2 < steps && !qk(0, s, phase, true, false)) break;
-                } else {
-                    if (!pv(1, sv, pv_ph, false, true, i < 2)) break;
-                    if (i + 2 < steps && !qk(1, sk, pk_ph, false, true)) break;
+                commit(bar(L::kBarSFull + t));
+                return true;
+            };
+            // O of stream t from its P and the next two slots.
+            const auto pv = [&](int t, bool first) {
+                const uint32_t pt = tmem + 256 * t, d = pt + 128;
+#pragma unroll 1
+                for (int c = 0; c < 2; ++c) {
+                    if (!wait_all<kPair>(bar(L::kBarFull + s), phase, w)) return ok = false;
+                    tc_fence_after();
+                    const uint64_t b = v_desc + s * kSlot16;
+                    const uint32_t a = pt + 32 * c;
+                    ts(d, a, b, first && c == 0 ? 0u : 1u);
+                    ts(d, a + 8, b + (2048 >> 4), 1u);
+                    ts(d, a + 16, b + (4096 >> 4), 1u);
+                    ts(d, a + 24, b + (6144 >> 4), 1u);
+                    next_slot();
                 }
-                if (i + 3 == steps) mma_commit_one(bar(L::kBarQEmpty + q_buf));  // the segment's last QK
+                return true;
+            };
+            int n_seg = 0, done0 = 0, done1 = 0;  // segments, steps of each stream
+            while (ok && walk.next(p, seg)) {
+                const int steps = seg.cnt;
+                q_buf = n_seg & 1;
+                if (!(ok = wait_all<kPair>(bar(L::kBarQFull + q_buf), n_seg >> 1, w))) break;
+                tc_fence_after();
+                if (!qk(0) || (steps > 1 && !qk(1))) break;
+                if (steps <= 2) commit(bar(L::kBarQEmpty + q_buf));
+                for (int i = 0; i < steps; ++i) {
+                    const int t = i & 1;
+                    if (!(ok = wait_all<kPair>(bar(L::kBarPReady + t), t ? done1 : done0, w))) break;
+                    done0 += t ^ 1;
+                    done1 += t;
+                    tc_fence_after();
+                    if (i == 0 && n_seg > 0) {
+                        if (!(ok = wait_all<kPair>(bar(L::kBarOFree), n_seg - 1, w))) break;
+                        tc_fence_after();
+                    }
+                    if (!pv(t, i < 2) || (i + 2 < steps && !qk(t))) break;
+                    if (i + 3 == steps) commit(bar(L::kBarQEmpty + q_buf));  // the segment's last QK
+                }
+                if (!ok) break;
+                commit(bar(L::kBarODone));
+                ++n_seg;
             }
-            if (!ok) break;
-            mma_commit_one(bar(L::kBarODone));
-            ++n_seg;
+            commit(bar(L::kBarEnd));  // arrives when every MMA issued here has finished
         }
-        mma_commit_one(bar(L::kBarEnd));  // arrives when every MMA issued here has finished
     } else {
         // softmax: warp (3..10) & 3 selects the TMEM lane quarter, a warp has 16 of its rows, a thread the
         // columns 8 k + 2 (lane & 3), + 1 of rows `row` and row + 8 (index 0 and 1 below)
         const int q4 = warp & 3, warp_row = 32 * q4 + 16 * ((warp - kSoftmaxWarp0) >> 2);
         const int row = warp_row + (lane >> 2), col = 2 * (lane & 3);
         const uint32_t lane_base = (uint32_t)warp_row << 16;
+        const uint32_t r_ready = mma_bar(L::kBarPReady), r_free = mma_bar(L::kBarOFree);
+        const auto arrive = [&](uint32_t at) {  // what it orders is in tensor memory
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (kPair)
+                    mbar_arrive_remote_relaxed(at);
+                else
+                    mbar_arrive(at);
+            }
+        };
         int n_seg = 0, seen0 = 0, seen1 = 0;  // segments, steps of each stream
         bool ok = true;
         while (ok && walk.next(p, seg)) {
-            const int steps = kQT == 1 ? seg.cnt : 2 * seg.cnt;
+            const int steps = seg.cnt, tile_row = seg.row0 + kTile * rank;
             // the running softmax of this step's stream and of the other, which change places after every step
             float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, m_other[2] = {-INFINITY, -INFINITY}, l_other[2] = {0.f, 0.f};
             const auto change = [&]() {
@@ -652,9 +671,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
 #pragma unroll 1
             for (int i = 0; i < steps; ++i) {
                 const int t = i & 1;
-                const int tile_row = seg.row0 + (kQT == 2 ? kTile * t : 0);
                 const uint32_t t_s = tmem + lane_base + 256 * t;
-                if (!(ok = wait_all(bar(L::kBarSFull + t), t ? seen1 : seen0, w))) break;
+                if (!(ok = wait_all<kPair>(bar(L::kBarSFull + t), t ? seen1 : seen0, w))) break;
                 seen0 += t ^ 1;
                 seen1 += t;
                 tc_fence_after();
@@ -663,7 +681,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     tmem_ld_16x128(t_s, sr);
                     tmem_wait_ld();
                     // keys that a row does not see get -infinity
-                    const int j0 = key_tile(seg, kQT == 1 ? i : i >> 1) * kTile;
+                    const int j0 = key_tile(seg, i) * kTile;
                     if (kChunk) {
                         int hi[2], lo[2];
                         bool whole = true;
@@ -759,13 +777,11 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     }
                     tmem_wait_st();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::kBarPReady + t));
+                arrive(r_ready + 8 * t);
                 change();
             }
             if (steps & 1) change();  // stream 0's are in m and l after an even number of steps
-            if (!(ok = ok && wait_all(bar(L::kBarODone), n_seg, w))) break;
+            if (!(ok = ok && wait_all<kPair>(bar(L::kBarODone), n_seg, w))) break;
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < 2; ++x) {  // a quad has a row's sum
@@ -774,47 +790,11 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 l_other[x] += __shfl_xor_sync(0xffffffffu, l_other[x], 1);
                 l_other[x] += __shfl_xor_sync(0xffffffffu, l_other[x], 2);
             }
-            // The outputs: a quad's lanes write 32 bytes (fp32) of a row side by side.
-            const auto store = [&](int i, float a, float b, int c) {  // columns c, c + 1 of query row i
-                if (i >= p.rows) return;
-                if (kChunk)
-                    *reinterpret_cast<uint32_t*>(p.out + ((int64_t)i * 128 + seg.head) * 128 + c) = pack_bf16x2(a, b);
-                else
-                    *reinterpret_cast<float2*>(p.ws_o + ((int64_t)seg.slot * p.rows_cap + (i - seg.row0)) * 128 + c) =
-                        make_float2(a, b);
-            };
-            const auto store_lse = [&](int i, float top, float total) {
-                if (!kChunk && i < p.rows && (lane & 3) == 0)
-                    p.ws_lse[(int64_t)seg.slot * p.rows_cap + (i - seg.row0)] = (top + log2f(total)) * 0.69314718055994531f;
-            };
-            const uint32_t t_o = tmem + lane_base + 128;
-            if (kQT == 2) {
-#pragma unroll 1
-                for (int t = 0; t < 2; ++t) {
-                    const int i = seg.row0 + kTile * t + row;
-                    if (seg.row0 + kTile * t + warp_row < p.rows) {
-                        const float inv[2] = {1.f / l[0], 1.f / l[1]};
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t o[16];
-                            tmem_ld_16x32(t_o + 256 * t + 32 * c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 16; k += 2) {
-                                const int x = (k >> 1) & 1;
-                                store(i + 8 * x, __uint_as_float(o[k]) * inv[x], __uint_as_float(o[k + 1]) * inv[x],
-                                      32 * c + 8 * (k >> 2) + col);
-                            }
-                        }
-                        store_lse(i, m[0], l[0]);
-                        store_lse(i + 8, m[1], l[1]);
-                    }
-                    change();
-                }
-            } else if (seg.row0 + warp_row < p.rows) {
-                // the two streams joined
+            if (tile_row + warp_row < p.rows) {
+                // The two streams joined.  A quad's lanes write 32 bytes of a row side by side, whole sectors: fp32 as
+                // they hold them, bf16 after two lanes have exchanged a pair of columns.
                 const bool two = steps > 1;  // else stream 1 had no tile and its O holds nothing
-                const int i = seg.row0 + row;
+                const int i = tile_row + row;
                 float f0[2], f1[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
@@ -824,8 +804,13 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     const float total = l[x] * f0[x] + (two ? l_other[x] * f1[x] : 0.f);
                     f0[x] /= total;
                     f1[x] /= total;
-                    store_lse(i + 8 * x, top, total);
+                    if (!kChunk && i + 8 * x < p.rows && (lane & 3) == 0)
+                        p.ws_lse[(int64_t)seg.slot * p.rows_cap + (i + 8 * x - seg.row0)] =
+                            (top + log2f(total)) * 0.69314718055994531f;
                 }
+                const uint32_t t_o = tmem + lane_base + 128;
+                const bool odd = lane & 1;
+                const int col4 = odd ? 8 + 2 * (lane & 2) : 2 * (lane & 2);  // bf16: of the 16 columns of two steps
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t a[16], b[16];
@@ -833,37 +818,62 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     if (two) tmem_ld_16x32(t_o + 256 + 32 * c, b);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
+                    for (int k = 0; k < 16; ++k) {
                         const int x = (k >> 1) & 1;
-                        float u = __uint_as_float(a[k]) * f0[x], v = __uint_as_float(a[k + 1]) * f0[x];
-                        if (two) {
-                            u = fmaf(__uint_as_float(b[k]), f1[x], u);
-                            v = fmaf(__uint_as_float(b[k + 1]), f1[x], v);
+                        float u = __uint_as_float(a[k]) * f0[x];
+                        if (two) u = fmaf(__uint_as_float(b[k]), f1[x], u);
+                        a[k] = __float_as_uint(u);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int at = i + 8 * x;
+                        if (kChunk) {
+                            uint2* dst = reinterpret_cast<uint2*>(p.out + ((int64_t)at * 128 + seg.head) * 128 + 32 * c + col4);
+#pragma unroll
+                            for (int k = 0; k < 4; k += 2) {
+                                const uint32_t lo = pack_bf16x2(__uint_as_float(a[4 * k + 2 * x]), __uint_as_float(a[4 * k + 2 * x + 1]));
+                                const uint32_t hi = pack_bf16x2(__uint_as_float(a[4 * k + 4 + 2 * x]), __uint_as_float(a[4 * k + 5 + 2 * x]));
+                                const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+                                if (at < p.rows) dst[2 * k] = odd ? make_uint2(other, hi) : make_uint2(lo, other);
+                            }
+                        } else if (at < p.rows) {
+                            float2* dst = reinterpret_cast<float2*>(
+                                p.ws_o + ((int64_t)seg.slot * p.rows_cap + (at - seg.row0)) * 128 + 32 * c + col);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                dst[4 * k] = make_float2(__uint_as_float(a[4 * k + 2 * x]), __uint_as_float(a[4 * k + 2 * x + 1]));
                         }
-                        store(i + 8 * x, u, v, 32 * c + 8 * (k >> 2) + col);
                     }
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(L::kBarOFree));
+            arrive(r_free);
             ++n_seg;
         }
     }
+    // After a wait that ran out an odd CTA's loads may be in flight without a barrier of its own: they land in
+    // microseconds, and it waits a millisecond.
+    if (kPair && threadIdx.x == 0 && *abort_flag)
+        for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) {
+        }
+    // the last MMAs have finished before the tensor memory goes back
+    if (warp == 1 && lane == 0 && rank == 0 && !(sbase & 1023u)) drain_phase(bar(L::kBarEnd), 0, w.timeout_ns);
     tc_fence_before();
     __syncthreads();
+    if (kPair) cluster_sync();
     if (warp == 1) {
-        if (lane == 0) drain_phase(bar(L::kBarEnd), 0, w.timeout_ns);
-        __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        if (kPair)
+            tmem_dealloc_pair(tmem, kTmemCols);
+        else
+            tmem_dealloc(tmem, kTmemCols);
     }
+    if (kPair) cluster_sync();  // no remote arrival at a CTA that has finished
 }
 
 struct Merge {
     const float* ws_o;
     const float* ws_lse;
-    int rows, rows_cap, groups, group_rows, tiles, ctas;  // as the attend kernel cut the units
+    int rows, rows_cap, groups, group_rows, tiles, workers;  // as the attend kernel cut the units
     const __nv_bfloat16* own_out;  // [rows][128][128] or NULL
     const float* own_lse;          // [rows][128]
     __nv_bfloat16* out;            // may be own_out
@@ -884,10 +894,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
     const int group = row / a.group_rows, run = head * a.groups + group;
     const int64_t units = (int64_t)a.groups * 128 * a.tiles, u0 = (int64_t)run * a.tiles, u1 = u0 + a.tiles;
     // the CTAs with a unit of the run: c0 has the first, which lies at or after the quotient's
-    int c0 = (int)(u0 * a.ctas / units);
-    while (c0 + 1 < a.ctas && first_unit(c0 + 1, units, a.ctas) <= u0) ++c0;
+    int c0 = (int)(u0 * a.workers / units);
+    while (c0 + 1 < a.workers && first_unit(c0 + 1, units, a.workers) <= u0) ++c0;
     int c1 = c0;
-    while (c1 + 1 < a.ctas && first_unit(c1 + 1, units, a.ctas) < u1) ++c1;
+    while (c1 + 1 < a.workers && first_unit(c1 + 1, units, a.workers) < u1) ++c1;
     const int64_t at = row - group * a.group_rows;
     dev::griddep_wait();
     // The row's own part and the first three of the prefix (more only with more CTAs than runs) are requested

@@ -216,7 +216,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant
         for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) {
         }
     // the pair's last MMAs have finished before either CTA gives its memory back
-    if (warp == 1 && lane == 0 && rank == 0 && !*abort_flag) drain_phase(bar(kBarEnd), 0, w.timeout_ns);
+    if (warp == 1 && lane == 0 && rank == 0 && !(sbase & 1023u)) drain_phase(bar(kBarEnd), 0, w.timeout_ns);
     tc_fence_before();
     __syncthreads();
     cluster_sync();
