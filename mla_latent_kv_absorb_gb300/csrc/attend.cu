@@ -257,9 +257,9 @@ extern "C" MLA_API mla_status mla_prefix_attend(int32_t num_rows, int32_t prefix
     a.out = static_cast<__nv_bfloat16*>(out);
     a.lse = lse;
     using mla::attend::kMergeWarps;
-    const int64_t warps = (int64_t)num_rows * 128;
+    const int64_t halves = (int64_t)num_rows * 128;  // of warps
     return mla::launch_dependent("prefix merge kernel launch", mla::attend::prefix_merge_kernel,
-                                 dim3((unsigned)((warps + kMergeWarps - 1) / kMergeWarps)), dim3(32 * kMergeWarps), 0, stream, a);
+                                 dim3((unsigned)((halves + 2 * kMergeWarps - 1) / (2 * kMergeWarps))), dim3(32 * kMergeWarps), 0, stream, a);
 }
 
 extern "C" MLA_API size_t mla_prefill_window_workspace_bytes(int32_t seq_len, int32_t chunk_len, int32_t window,

@@ -305,7 +305,7 @@ struct Params {
 // A worker's piece of one run.
 struct Segment {
     int head, row0, cnt;  // cnt key tiles
-    int lead, tile0;      // key tile n: n < lead ? n : tile0 + n
+    int lead, base;       // key tile n begins at key 128 n below lead, at base + 128 (n - lead) behind it
     int slot;             // the prefix's partial
 };
 
@@ -340,9 +340,8 @@ struct Walk {
             const int last = min(s.row0 + kRows, p.rows) - 1;
             const int lo = max(0, p.hi0 + s.row0 - p.window + 1);  // the first key in the first row's window
             s.lead = (min(p.sinks, lo) + kTile - 1) / kTile;
-            const int first = max(s.lead, lo / kTile);
-            s.tile0 = first - s.lead;
-            s.cnt = s.lead + (p.hi0 + last) / kTile + 1 - first;
+            s.base = max(s.lead * kTile, lo);
+            s.cnt = s.lead + (p.hi0 + last - s.base + kTile) / kTile;  // the last key is hi0 + last
             s.slot = 0;
             at += workers();
         } else {
@@ -351,7 +350,7 @@ struct Walk {
             s.row0 = (run % p.groups) * kRows;
             s.cnt = (int)min((int64_t)(p.tiles - n0), end - at);
             s.lead = 0;
-            s.tile0 = n0;
+            s.base = n0 * kTile;
             s.slot = worker() + run;
             at += s.cnt;
         }
@@ -359,7 +358,10 @@ struct Walk {
     }
 };
 
-__device__ __forceinline__ int key_tile(const Segment& s, int n) { return n < s.lead ? n : s.tile0 + n; }
+__device__ __forceinline__ int first_key(const Segment& s, int n)
+{
+    return n < s.lead ? n * kTile : s.base + (n - s.lead) * kTile;
+}
 
 template <bool kChunk, bool kPair>
 // 11 warps: three SM sub-partitions hold three of them, 16K registers each: at most 3 x 32 x 168
@@ -431,7 +433,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         // (Behind the tile's own loads, and at most two tiles a turn: at the start the first tiles come first.)
         int fetched = 0;
         const auto fetch = [&](int n) {
-            const int j0 = key_tile(seg, n) * kTile;
+            const int j0 = first_key(seg, n);
             const uint32_t bytes = (uint32_t)min(kTile, p.keys - j0) * 256;
             const int64_t at = ((int64_t)seg.head * p.keys + j0) * 128;
             if (leader) {
@@ -497,11 +499,11 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             tma_prefetch_desc(&tm_v);
         }
         while (ok && walk.next(p, seg)) {
-            for (int n = 0; ok && n < 2 && n < seg.cnt; ++n) load_k(key_tile(seg, n) * kTile);
+            for (int n = 0; ok && n < 2 && n < seg.cnt; ++n) load_k(first_key(seg, n));
             fetched = 3;
             for (int n = 0; ok && n < seg.cnt; ++n) {
-                load_v(key_tile(seg, n) * kTile);
-                if (ok && n + 2 < seg.cnt) load_k(key_tile(seg, n + 2) * kTile);
+                load_v(first_key(seg, n));
+                if (ok && n + 2 < seg.cnt) load_k(first_key(seg, n + 2));
                 for (int two = 0; two < 2 && fetched < min(seg.cnt, n + 1 + kFetch); ++two, ++fetched) fetch(fetched);
             }
         }
@@ -681,7 +683,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     tmem_ld_16x128(t_s, sr);
                     tmem_wait_ld();
                     // keys that a row does not see get -infinity
-                    const int j0 = key_tile(seg, i) * kTile;
+                    const int j0 = first_key(seg, i);
                     if (kChunk) {
                         int hi[2], lo[2];
                         bool whole = true;
@@ -811,42 +813,46 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 const uint32_t t_o = tmem + lane_base + 128;
                 const bool odd = lane & 1;
                 const int col4 = odd ? 8 + 2 * (lane & 2) : 2 * (lane & 2);  // bf16: of the 16 columns of two steps
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t a[16], b[16];
-                    tmem_ld_16x32(t_o + 32 * c, a);
-                    if (two) tmem_ld_16x32(t_o + 256 + 32 * c, b);
-                    tmem_wait_ld();
+                uint32_t o[64];
+                tmem_ld_16x128(t_o, o);
+                tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int x = (k >> 1) & 1;
-                        float u = __uint_as_float(a[k]) * f0[x];
-                        if (two) u = fmaf(__uint_as_float(b[k]), f1[x], u);
-                        a[k] = __float_as_uint(u);
-                    }
+                for (int k = 0; k < 64; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f0[(k >> 1) & 1]);
+                if (two) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int at = i + 8 * x;
-                        if (kChunk) {
-                            uint2* dst = reinterpret_cast<uint2*>(p.out + ((int64_t)at * 128 + seg.head) * 128 + 32 * c + col4);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t b[16];
+                        tmem_ld_16x32(t_o + 256 + 32 * c, b);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 4; k += 2) {
-                                const uint32_t lo = pack_bf16x2(__uint_as_float(a[4 * k + 2 * x]), __uint_as_float(a[4 * k + 2 * x + 1]));
-                                const uint32_t hi = pack_bf16x2(__uint_as_float(a[4 * k + 4 + 2 * x]), __uint_as_float(a[4 * k + 5 + 2 * x]));
-                                const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
-                                if (at < p.rows) dst[2 * k] = odd ? make_uint2(other, hi) : make_uint2(lo, other);
-                            }
-                        } else if (at < p.rows) {
-                            float2* dst = reinterpret_cast<float2*>(
-                                p.ws_o + ((int64_t)seg.slot * p.rows_cap + (at - seg.row0)) * 128 + 32 * c + col);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                dst[4 * k] = make_float2(__uint_as_float(a[4 * k + 2 * x]), __uint_as_float(a[4 * k + 2 * x + 1]));
-                        }
+                        for (int k = 0; k < 16; ++k)
+                            o[16 * c + k] = __float_as_uint(fmaf(__uint_as_float(b[k]), f1[(k >> 1) & 1], __uint_as_float(o[16 * c + k])));
                     }
                 }
+                arrive(r_free);  // the next segment's products may start
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int at = i + 8 * x;
+                    if (kChunk) {
+                        uint2* dst = reinterpret_cast<uint2*>(p.out + ((int64_t)at * 128 + seg.head) * 128 + col4);
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2) {
+                            const uint32_t lo = pack_bf16x2(__uint_as_float(o[4 * k + 2 * x]), __uint_as_float(o[4 * k + 2 * x + 1]));
+                            const uint32_t hi = pack_bf16x2(__uint_as_float(o[4 * k + 4 + 2 * x]), __uint_as_float(o[4 * k + 5 + 2 * x]));
+                            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+                            if (at < p.rows) dst[2 * k] = odd ? make_uint2(other, hi) : make_uint2(lo, other);
+                        }
+                    } else if (at < p.rows) {
+                        float2* dst =
+                            reinterpret_cast<float2*>(p.ws_o + ((int64_t)seg.slot * p.rows_cap + (at - seg.row0)) * 128 + col);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k)
+                            dst[4 * k] = make_float2(__uint_as_float(o[4 * k + 2 * x]), __uint_as_float(o[4 * k + 2 * x + 1]));
+                    }
+                }
+            } else {
+                arrive(r_free);
             }
-            arrive(r_free);
             ++n_seg;
         }
     }
@@ -883,60 +889,71 @@ struct Merge {
 constexpr int kMergeWarps = 8;
 
 // Joins the partials of the prefix (at most a few for one head and group) with the row's attention over
-// its own tokens by log-sum-exp.  One warp per (row, head), four columns a lane: bound by HBM and L2 (own
+// its own tokens by log-sum-exp.  Half a warp per (row, head), eight columns a lane: bound by HBM and L2 (own
 // outputs in, outputs out, partials from L2).
 __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __grid_constant__ Merge a)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t id = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 15;
+    const int64_t id = (int64_t)blockIdx.x * (2 * kMergeWarps) + (threadIdx.x >> 4);
     if (id >= (int64_t)a.rows * 128) return;
     const int row = (int)(id >> 7), head = (int)(id & 127);
     const int group = row / a.group_rows, run = head * a.groups + group;
     const int64_t units = (int64_t)a.groups * 128 * a.tiles, u0 = (int64_t)run * a.tiles, u1 = u0 + a.tiles;
-    // the CTAs with a unit of the run: c0 has the first, which lies at or after the quotient's
+    // the workers with a unit of the run: c0 has the first, which lies at or after the quotient's
     int c0 = (int)(u0 * a.workers / units);
     while (c0 + 1 < a.workers && first_unit(c0 + 1, units, a.workers) <= u0) ++c0;
     int c1 = c0;
     while (c1 + 1 < a.workers && first_unit(c1 + 1, units, a.workers) < u1) ++c1;
     const int64_t at = row - group * a.group_rows;
     dev::griddep_wait();
-    // The row's own part and the first three of the prefix (more only with more CTAs than runs) are requested
+    // The row's own part and the first three of the prefix (more only with more workers than runs) are requested
     // together, in one round trip.
     constexpr int kAtOnce = 3;
     const float own = a.own_lse ? a.own_lse[id] : -INFINITY;
-    const uint2 own_o = a.own_out ? reinterpret_cast<const uint2*>(a.own_out + id * 128)[lane] : make_uint2(0, 0);
+    const uint4 own_o = a.own_out ? reinterpret_cast<const uint4*>(a.own_out + id * 128)[lane] : make_uint4(0, 0, 0, 0);
     float part_lse[kAtOnce];
-    float4 part_o[kAtOnce];
+    float4 part_o[kAtOnce][2];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
         const int64_t part = (int64_t)(min(c0 + k, c1) + run) * a.rows_cap + at;
-        part_lse[k] = c0 + k <= c1 ? a.ws_lse[part] : -INFINITY;
-        part_o[k] = reinterpret_cast<const float4*>(a.ws_o + part * 128)[lane];
+        part_lse[k] = -INFINITY;
+        if (c0 + k <= c1) {
+            part_lse[k] = a.ws_lse[part];
+            part_o[k][0] = reinterpret_cast<const float4*>(a.ws_o + part * 128)[2 * lane];
+            part_o[k][1] = reinterpret_cast<const float4*>(a.ws_o + part * 128)[2 * lane + 1];
+        }
     }
     float top = fmaxf(fmaxf(own, part_lse[0]), fmaxf(part_lse[1], part_lse[2]));
     for (int c = c0 + kAtOnce; c <= c1; ++c) top = fmaxf(top, a.ws_lse[(int64_t)(c + run) * a.rows_cap + at]);
-    float total = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-    const auto add = [&](float part, const float4& o) {
+    float total = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const auto add = [&](float part, const float4& o, const float4& q) {
         const float wgt = __expf(part - top);
         total += wgt;
         x[0] = fmaf(wgt, o.x, x[0]);
         x[1] = fmaf(wgt, o.y, x[1]);
         x[2] = fmaf(wgt, o.z, x[2]);
         x[3] = fmaf(wgt, o.w, x[3]);
+        x[4] = fmaf(wgt, q.x, x[4]);
+        x[5] = fmaf(wgt, q.y, x[5]);
+        x[6] = fmaf(wgt, q.z, x[6]);
+        x[7] = fmaf(wgt, q.w, x[7]);
     };
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k)
-        if (c0 + k <= c1) add(part_lse[k], part_o[k]);
+        if (c0 + k <= c1) add(part_lse[k], part_o[k][0], part_o[k][1]);
     for (int c = c0 + kAtOnce; c <= c1; ++c) {
         const int64_t part = (int64_t)(c + run) * a.rows_cap + at;
-        add(a.ws_lse[part], reinterpret_cast<const float4*>(a.ws_o + part * 128)[lane]);
+        const float4* o = reinterpret_cast<const float4*>(a.ws_o + part * 128) + 2 * lane;
+        add(a.ws_lse[part], o[0], o[1]);
     }
     if (own != -INFINITY)  // a row without own tokens may hold anything
-        add(own, make_float4(dev::bf16_lo(own_o.x), dev::bf16_hi(own_o.x), dev::bf16_lo(own_o.y), dev::bf16_hi(own_o.y)));
+        add(own, make_float4(dev::bf16_lo(own_o.x), dev::bf16_hi(own_o.x), dev::bf16_lo(own_o.y), dev::bf16_hi(own_o.y)),
+            make_float4(dev::bf16_lo(own_o.z), dev::bf16_hi(own_o.z), dev::bf16_lo(own_o.w), dev::bf16_hi(own_o.w)));
     const float inv = 1.f / total;
-    reinterpret_cast<uint2*>(a.out + id * 128)[lane] =
-        make_uint2(dev::pack_bf16x2(x[0] * inv, x[1] * inv), dev::pack_bf16x2(x[2] * inv, x[3] * inv));
-    __syncwarp();
+    reinterpret_cast<uint4*>(a.out + id * 128)[lane] =
+        make_uint4(dev::pack_bf16x2(x[0] * inv, x[1] * inv), dev::pack_bf16x2(x[2] * inv, x[3] * inv),
+                   dev::pack_bf16x2(x[4] * inv, x[5] * inv), dev::pack_bf16x2(x[6] * inv, x[7] * inv));
+    __syncwarp(__activemask());  // own_lse has been read by the half's lanes before lse, which may be it, is written
     if (lane == 0 && a.lse) a.lse[id] = top + logf(total);
 }
 
