@@ -91,7 +91,8 @@ MLA_API const char* mla_last_error_string(void);
  * pages; sequences cut into several items get a log-sum-exp merge (mla_combine_splits).
  */
 typedef struct mla_plan_options {
-    int32_t min_pages_per_split; /* 0 = default 8: no item boundary closer than this to a sequence edge */
+    int32_t min_pages_per_split; /* 0 = default 8 (under a window 3): no item boundary closer than this to a
+                                    sequence edge */
     int32_t max_clusters;        /* 0 = num_sms / 2; otherwise at most this many CTA pairs */
     int64_t wait_timeout_ns;     /* 0 = default 2e9: bound on every device-side wait */
     int32_t item_cost_pages;     /* balance pages plus this many pages' worth of cost for each item
