@@ -16,9 +16,10 @@
 // A CTA holds a 128-row query tile of a head and streams 128-key tiles; with more than 128 rows a pair of CTAs
 // (two SMs, MMAs of M = 256) holds 256 rows, and each brings in half of every key tile (64 keys) and of every
 // value tile (64 dims).  Alone a CTA with 256 rows waited for its keys: 80 KB a tile and a ring of 128 KB.
-// It works on two "streams", the even key tiles and the odd ones, each with a score buffer S, an output O and a
-// running softmax (m, l) of its own, joined at the end, so that one stream's softmax always has the other's
-// products to hide behind.  Step i is key tile i, of stream i & 1; the MMA order is PV(i), QK(i + 2).
+// It works on two "streams", every other key tile, each with a score buffer S, an output O and a running softmax
+// (m, l) of its own, joined at the end, so that one stream's softmax always has the other's products to hide
+// behind.  Step g is a key tile, of stream g & 1; the MMA order is PV(g), QK(g + 2), from one segment into the
+// next (a segment's own beginning and end took 3,500 of 24,000 cycles a segment of a chunk).
 //   QK:  S[rows x 128] = Q [rows x 192] (q_c | q_R: three 64-column chunks in shared memory)
 //                       x K tile [128 x 192] (k | k_R: three K-major chunks)
 //   PV:  O[rows x 128] += P [rows x 128] (bf16 in TMEM over the first half of S) x V tile (MN-major)
@@ -276,12 +277,12 @@ struct Layout {
 // In a pair the barriers on which the MMAs wait (full, Q full, P ready, O free) are the even CTA's, by both CTAs'
 // copies and warps; those that MMAs complete (empty, Q empty, S full, O done, end) are in both.
 // Phase bookkeeping.  A barrier waited by parity must never run two phases ahead of its waiter:
-//   S full [t]   completes once per step of stream t; QK(i + 2) is issued only after the MMA thread
-//                has seen P(i) ready, i.e. after the stream's softmax has finished step i.
-//   P ready [t]  arrives once per step; P(i + 2) needs S(i + 2), issued after that wait.
+//   S full [t]   completes once per step of stream t; QK(g + 2) is issued only after the MMA warp
+//                has seen P(g) ready, i.e. after the softmax has finished step g.
+//   P ready [t]  arrives once per step; P(g + 2) needs S(g + 2), issued after that wait.
 //   Q full       a query load into a buffer is issued after its Q empty (the last QK of the segment before).
-//   O done       once per segment; the next one's needs its first PV, which waits for O free, for
-//                which every softmax thread has to have waited for O done.
+//   O done       once per segment; the next one's needs that segment's first PV, which waits for O free, for
+//                which every softmax warp has to have waited for O done.
 //   ring         a slot is refilled only after its empty barrier, waited in order.
 
 struct Params {
@@ -335,8 +336,8 @@ struct Walk {
         if (at >= end) return false;
         if (kChunk) {
             // a head's groups lie side by side: their windows overlap and are read from L2
-            s.head = (int)(at / p.groups);
-            s.row0 = (int)(at % p.groups) * kRows;
+            s.head = (int)at / p.groups;  // at most 128 x 32,768
+            s.row0 = ((int)at - s.head * p.groups) * kRows;
             const int last = min(s.row0 + kRows, p.rows) - 1;
             const int lo = max(0, p.hi0 + s.row0 - p.window + 1);  // the first key in the first row's window
             s.lead = (min(p.sinks, lo) + kTile - 1) / kTile;
@@ -431,11 +432,15 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         // Keys and values of the tile kFetch ahead go into L2, so that a slot, which is free only a step or two
         // before it is needed, is filled from there (the even CTA of a pair fetches the keys, the odd one the values).
         // (Behind the tile's own loads, and at most two tiles a turn: at the start the first tiles come first.)
-        int fetched = 0;
+        // Two walks: the keys are two steps ahead of the values.
+        Walk<kChunk, kPair> walk_k(p);
+        Segment seg_k;
+        bool more_k = walk_k.next(p, seg_k);
+        int n_k = 0, fetched = 3;
         const auto fetch = [&](int n) {
-            const int j0 = first_key(seg, n);
+            const int j0 = first_key(seg_k, n);
             const uint32_t bytes = (uint32_t)min(kTile, p.keys - j0) * 256;
-            const int64_t at = ((int64_t)seg.head * p.keys + j0) * 128;
+            const int64_t at = ((int64_t)seg_k.head * p.keys + j0) * 128;
             if (leader) {
                 if (rank == 0) prefetch_l2(p.k + at, bytes);
                 if (!kPair || rank == 1) prefetch_l2(p.v + at, bytes);
@@ -456,7 +461,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 ++phase;
             }
         };
-        const auto load_k = [&](int j0) {
+        const auto load_k = [&]() {  // the next key tile
+            if (!more_k) return;
+            const int j0 = first_key(seg_k, n_k);
 #pragma unroll 1
             for (int c = 0; c < 3; ++c) {
                 if (!take()) return;
@@ -464,17 +471,23 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 if (leader) {
                     if (kPair) {
                         if (c < 2)
-                            tma_load_3d_pair(dst, &tm_k, full, 64 * c, j0 + 64 * rank, seg.head, pol_kv);
+                            tma_load_3d_pair(dst, &tm_k, full, 64 * c, j0 + 64 * rank, seg_k.head, pol_kv);
                         else
                             tma_load_2d_pair(dst, &tm_kr, full, 0, j0 + 64 * rank, pol_kr);
                     } else {
                         if (c < 2)
-                            tma_load_3d(dst, &tm_k, full, 64 * c, j0, seg.head, pol_kv);
+                            tma_load_3d(dst, &tm_k, full, 64 * c, j0, seg_k.head, pol_kv);
                         else
                             tma_load_2d(dst, &tm_kr, full, 0, j0, pol_kr);
                     }
                 }
                 put();
+            }
+            for (int two = 0; two < 2 && fetched < min(seg_k.cnt, n_k - 1 + kFetch); ++two, ++fetched) fetch(fetched);
+            if (++n_k == seg_k.cnt) {
+                n_k = 0;
+                fetched = 3;
+                more_k = walk_k.next(p, seg_k);
             }
         };
         const auto load_v = [&](int j0) {
@@ -498,13 +511,12 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             tma_prefetch_desc(&tm_kr);
             tma_prefetch_desc(&tm_v);
         }
+        load_k();
+        if (ok) load_k();
         while (ok && walk.next(p, seg)) {
-            for (int n = 0; ok && n < 2 && n < seg.cnt; ++n) load_k(first_key(seg, n));
-            fetched = 3;
             for (int n = 0; ok && n < seg.cnt; ++n) {
                 load_v(first_key(seg, n));
-                if (ok && n + 2 < seg.cnt) load_k(first_key(seg, n + 2));
-                for (int two = 0; two < 2 && fetched < min(seg.cnt, n + 1 + kFetch); ++two, ++fetched) fetch(fetched);
+                if (ok) load_k();
             }
         }
         griddep_launch_dependents();  // the merge may be scheduled; it waits for this kernel's end
@@ -610,29 +622,40 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 }
                 return true;
             };
-            int n_seg = 0, done0 = 0, done1 = 0;  // segments, steps of each stream
+            // Two walks: the scores are two steps ahead of the outputs.
+            Walk<kChunk, kPair> walk_q(p);
+            Segment seg_q;
+            bool more_q = walk_q.next(p, seg_q);
+            int n_q = 0, i_q = 0, g_q = 0;  // its segment, step of the segment, step
+            const auto next_qk = [&]() {
+                if (!more_q) return true;
+                if (i_q == 0) {
+                    q_buf = n_q & 1;
+                    if (!(ok = wait_all<kPair>(bar(L::kBarQFull + q_buf), n_q >> 1, w))) return false;
+                }
+                if (!qk(g_q & 1)) return false;
+                ++g_q;
+                if (++i_q == seg_q.cnt) {
+                    commit(bar(L::kBarQEmpty + q_buf));
+                    i_q = 0;
+                    ++n_q;
+                    more_q = walk_q.next(p, seg_q);
+                }
+                return true;
+            };
+            if (next_qk()) next_qk();
+            int n_seg = 0, g = 0;  // segments, steps
             while (ok && walk.next(p, seg)) {
                 const int steps = seg.cnt;
-                q_buf = n_seg & 1;
-                if (!(ok = wait_all<kPair>(bar(L::kBarQFull + q_buf), n_seg >> 1, w))) break;
-                tc_fence_after();
-                if (!qk(0) || (steps > 1 && !qk(1))) break;
-                if (steps <= 2) commit(bar(L::kBarQEmpty + q_buf));
-                for (int i = 0; i < steps; ++i) {
-                    const int t = i & 1;
-                    if (!(ok = wait_all<kPair>(bar(L::kBarPReady + t), t ? done1 : done0, w))) break;
-                    done0 += t ^ 1;
-                    done1 += t;
+                for (int i = 0; i < steps; ++i, ++g) {
+                    const int t = g & 1;
+                    if (!(ok = wait_all<kPair>(bar(L::kBarPReady + t), g >> 1, w))) break;
+                    if (i == 0 && n_seg > 0 && !(ok = wait_all<kPair>(bar(L::kBarOFree), n_seg - 1, w))) break;
                     tc_fence_after();
-                    if (i == 0 && n_seg > 0) {
-                        if (!(ok = wait_all<kPair>(bar(L::kBarOFree), n_seg - 1, w))) break;
-                        tc_fence_after();
-                    }
-                    if (!pv(t, i < 2) || (i + 2 < steps && !qk(t))) break;
-                    if (i + 3 == steps) commit(bar(L::kBarQEmpty + q_buf));  // the segment's last QK
+                    if (!pv(t, i < 2)) break;
+                    if (i + 1 == steps) commit(bar(L::kBarODone));  // ahead of the next segment's scores
+                    if (!next_qk()) break;
                 }
-                if (!ok) break;
-                commit(bar(L::kBarODone));
                 ++n_seg;
             }
             commit(bar(L::kBarEnd));  // arrives when every MMA issued here has finished
@@ -654,7 +677,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     mbar_arrive(at);
             }
         };
-        int n_seg = 0, seen0 = 0, seen1 = 0;  // segments, steps of each stream
+        int n_seg = 0, g = 0;  // segments, steps
         bool ok = true;
         while (ok && walk.next(p, seg)) {
             const int steps = seg.cnt, tile_row = seg.row0 + kTile * rank;
@@ -671,12 +694,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 }
             };
 #pragma unroll 1
-            for (int i = 0; i < steps; ++i) {
-                const int t = i & 1;
+            for (int i = 0; i < steps; ++i, ++g) {
+                const int t = g & 1;
                 const uint32_t t_s = tmem + lane_base + 256 * t;
-                if (!(ok = wait_all<kPair>(bar(L::kBarSFull + t), t ? seen1 : seen0, w))) break;
-                seen0 += t ^ 1;
-                seen1 += t;
+                if (!(ok = wait_all<kPair>(bar(L::kBarSFull + t), g >> 1, w))) break;
                 tc_fence_after();
                 if (tile_row + warp_row < p.rows) {  // the warp has a row at all
                     uint32_t sr[64];
@@ -755,8 +776,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                             l[x] *= f[x];
                         }
                         if (i >= 2) {
-                            // O's earlier PVs have finished: S(i) complete implies it (QK(i) was issued after
-                            // PV(i - 2), and a commit covers every earlier MMA of the thread)
+                            // O's earlier PVs have finished: S(g) complete implies it (QK(g) was issued after
+                            // PV(g - 2), and a commit covers every earlier MMA of the thread)
 #pragma unroll 1
                             for (int c = 0; c < 4; ++c) {
                                 uint32_t o[16];
@@ -782,7 +803,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 arrive(r_ready + 8 * t);
                 change();
             }
-            if (steps & 1) change();  // stream 0's are in m and l after an even number of steps
+            if (steps & 1) change();  // those of the segment's first stream are in m and l after an even number of steps
+            const int t0 = (g - steps) & 1;  // that stream
             if (!(ok = ok && wait_all<kPair>(bar(L::kBarODone), n_seg, w))) break;
             tc_fence_after();
 #pragma unroll
@@ -795,7 +817,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             if (tile_row + warp_row < p.rows) {
                 // The two streams joined.  A quad's lanes write 32 bytes of a row side by side, whole sectors: fp32 as
                 // they hold them, bf16 after two lanes have exchanged a pair of columns.
-                const bool two = steps > 1;  // else stream 1 had no tile and its O holds nothing
+                const bool two = steps > 1;  // else the other stream had no tile and its O holds nothing
                 const int i = tile_row + row;
                 float f0[2], f1[2];
 #pragma unroll
@@ -810,7 +832,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                         p.ws_lse[(int64_t)seg.slot * p.rows_cap + (i + 8 * x - seg.row0)] =
                             (top + log2f(total)) * 0.69314718055994531f;
                 }
-                const uint32_t t_o = tmem + lane_base + 128;
+                const uint32_t t_o = tmem + lane_base + 128 + 256 * t0, t_o_other = tmem + lane_base + 128 + 256 * (t0 ^ 1);
                 const bool odd = lane & 1;
                 const int col4 = odd ? 8 + 2 * (lane & 2) : 2 * (lane & 2);  // bf16: of the 16 columns of two steps
                 uint32_t o[64];
@@ -822,7 +844,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t b[16];
-                        tmem_ld_16x32(t_o + 256 + 32 * c, b);
+                        tmem_ld_16x32(t_o_other + 32 * c, b);
                         tmem_wait_ld();
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
