@@ -47,23 +47,24 @@ bool cache_aligned(mla_kv_dtype kv_dtype, const void* kv_pool, const float* kv_s
 // The maps of q_c [rows][128][128], q_r [rows][128][64], k and v [128][keys][128] and k_r [keys] rows of
 // `kr_stride` elements: boxes of 64 columns by 128 rows, by 128 keys (64 in a pair), by 64 keys for the values.
 struct Maps {
-    CUtensorMap qc, qr, k, kr, v;
+    CUtensorMap qc, qr, k, kr, v, out;  // out: a chunk's, boxes of 16 rows of one head by 64 columns
 };
 
 bool make_maps(Maps* m, const void* q_c, const void* q_r, const void* k, const void* v, const void* k_r,
-               int64_t kr_stride, int64_t rows, int64_t keys, bool pair)
+               int64_t kr_stride, int64_t rows, int64_t keys, bool pair, const void* out)
 {
     using mla::make_bf16_map;
     const cuuint64_t qc_dims[3] = {128, 128, (cuuint64_t)rows}, qc_str[2] = {128 * 2, 128 * 128 * 2};
     const cuuint64_t qr_dims[3] = {64, 128, (cuuint64_t)rows}, qr_str[2] = {64 * 2, 128 * 64 * 2};
-    const cuuint32_t q_box[3] = {64, 1, 128};
+    const cuuint32_t q_box[3] = {64, 1, 128}, o_box[3] = {64, 1, 16};
     const cuuint64_t k_dims[3] = {128, (cuuint64_t)keys, 128}, k_str[2] = {128 * 2, (cuuint64_t)keys * 128 * 2};
     const cuuint32_t k_box[3] = {64, pair ? 64u : 128u, 1}, v_box[3] = {64, 64, 1};
     const cuuint64_t r_dims[2] = {64, (cuuint64_t)keys}, r_str[1] = {(cuuint64_t)kr_stride * 2};
     const cuuint32_t r_box[2] = {64, pair ? 64u : 128u};
     return make_bf16_map(&m->qc, q_c, 3, qc_dims, qc_str, q_box) && make_bf16_map(&m->qr, q_r, 3, qr_dims, qr_str, q_box) &&
            make_bf16_map(&m->k, k, 3, k_dims, k_str, k_box) && make_bf16_map(&m->v, v, 3, k_dims, k_str, v_box) &&
-           make_bf16_map(&m->kr, k_r, 2, r_dims, r_str, r_box);
+           make_bf16_map(&m->kr, k_r, 2, r_dims, r_str, r_box) &&
+           make_bf16_map(&m->out, out, 3, qc_dims, qc_str, o_box);
 }
 
 template <bool kChunk, bool kPair>
@@ -76,7 +77,7 @@ mla_status launch_attend(const Maps& m, const mla::attend::Params& p, int worker
         "cudaFuncSetAttribute(max dynamic shared memory)");
     if (st != MLA_OK) return st;
     return mla::launch_dependent("attend kernel launch", kernel, dim3((unsigned)(kPair ? 2 * workers : workers)), dim3(kThreads),
-                                 Layout<kPair>::kSmemBytes, stream, m.qc, m.qr, m.k, m.kr, m.v, p);
+                                 Layout<kPair>::kSmemBytes, stream, m.qc, m.qr, m.k, m.kr, m.v, m.out, p);
 }
 
 mla_status sm_count(int* sms)
@@ -226,7 +227,7 @@ extern "C" MLA_API mla_status mla_prefix_attend(int32_t num_rows, int32_t prefix
     const Cut c = cut_prefix(num_rows, prefix_len, num_sms);
     if (workspace_bytes < c.total) return MLA_ERR_WORKSPACE;
     Maps m;
-    if (!make_maps(&m, q_c, q_r, k, v, k_r, k_r_stride, num_rows, prefix_len, c.pair)) return MLA_ERR_CUDA;
+    if (!make_maps(&m, q_c, q_r, k, v, k_r, k_r_stride, num_rows, prefix_len, c.pair, out)) return MLA_ERR_CUDA;
     mla::attend::Params p = {};
     p.rows = num_rows;
     p.keys = prefix_len;
@@ -234,8 +235,6 @@ extern "C" MLA_API mla_status mla_prefix_attend(int32_t num_rows, int32_t prefix
     p.groups = c.groups;
     p.dev_error = dev_error;
     p.timeout_ns = kTimeoutNs;
-    p.k = static_cast<const __nv_bfloat16*>(k);
-    p.v = static_cast<const __nv_bfloat16*>(v);
     p.tiles = c.tiles;
     p.rows_cap = c.rows_cap;
     p.ws_o = static_cast<float*>(workspace);
@@ -294,7 +293,7 @@ extern "C" MLA_API mla_status mla_prefill_window(mla_kv_dtype kv_dtype, const vo
     char* ws = static_cast<char*>(workspace);
     void *k = ws + s.k, *v = ws + s.v;
     Maps m;
-    if (!make_maps(&m, q_c, q_r, k, v, ws + 512 * 2, 576, chunk_len, s.keys, true)) return MLA_ERR_CUDA;
+    if (!make_maps(&m, q_c, q_r, k, v, ws + 512 * 2, 576, chunk_len, s.keys, true, out)) return MLA_ERR_CUDA;
     int sms = 0;
     mla_status st = sm_count(&sms);
     if (st != MLA_OK) return st;
@@ -309,8 +308,6 @@ extern "C" MLA_API mla_status mla_prefill_window(mla_kv_dtype kv_dtype, const vo
     p.groups = (chunk_len + 255) / 256;
     p.dev_error = dev_error;
     p.timeout_ns = kTimeoutNs;
-    p.k = static_cast<const __nv_bfloat16*>(k);
-    p.v = static_cast<const __nv_bfloat16*>(v);
     p.hi0 = seq_len - chunk_len - s.skip;
     p.window = std::min(window, seq_len);
     p.sinks = std::min(sinks, seq_len);

@@ -122,7 +122,6 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar)
 }
 
 // A bounded wait (as dev::wait_phase) that looks at the timer, which is slow to read, once in many polls.
-template <bool kCluster>
 __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t timeout_ns,
                                        uint32_t* dev_error)
 {
@@ -130,7 +129,7 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
     while (true) {
 #pragma unroll 1
         for (int k = 0; k < 64; ++k)
-            if (kCluster ? dev::mbar_try_wait_cluster(bar, parity) : dev::mbar_try_wait(bar, parity)) return true;
+            if (dev::mbar_try_wait(bar, parity)) return true;
         if (*abort) return false;
         if (dev::globaltimer_ns() - t0 > timeout_ns) {
             *abort = 1;
@@ -140,14 +139,12 @@ __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile i
     }
 }
 
-// The whole warp waits; the answer is a vote, the same in all lanes.  kCluster: the other CTA arrives too.
-template <bool kCluster = false>
+// The whole warp waits; the answer is a vote, the same in all lanes.  What the other CTA of a pair arrives for is
+// in tensor memory (tcgen05 fences order it) or came by its copies, so the wait acquires for the CTA alone.
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t phase, const WaitCtx& w)
 {
-    const uint32_t parity = phase & 1u;
-    if (__all_sync(0xffffffffu, kCluster ? dev::mbar_try_wait_cluster(bar, parity) : dev::mbar_try_wait(bar, parity)))
-        return true;
-    return __all_sync(0xffffffffu, wait_slow<kCluster>(bar, parity, w.abort, w.timeout_ns, w.dev_error));
+    if (__all_sync(0xffffffffu, dev::mbar_try_wait(bar, phase & 1u))) return true;
+    return __all_sync(0xffffffffu, wait_slow(bar, phase & 1u, w.abort, w.timeout_ns, w.dev_error));
 }
 
 __device__ __forceinline__ bool elect_lane()
@@ -243,18 +240,11 @@ __device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, const uint32_t (&r
           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 
-// `bytes` (a multiple of 16) from `p` into L2, without waiting.
-__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 constexpr int kTile = 128;                 // query rows of a tile, keys of a tile
 constexpr int kThreads = 32 * 11;
 constexpr int kSoftmaxWarp0 = 3;
 constexpr uint32_t kTmemCols = 512;        // stream t: S at 256 t, O at 256 t + 128
 constexpr float kRescaleLog2 = 32.f;       // P up to 2^32, l and O below 2^32 x keys x |v|: far from fp32's 2^127
-constexpr int kFetch = 4;                  // key tiles ahead that are brought into L2
 
 template <bool kPair>
 struct Layout {
@@ -269,7 +259,8 @@ struct Layout {
     static constexpr int kBarPReady = kBarSFull + 2;         // [stream], every softmax warp's arrival
     static constexpr int kBarODone = kBarPReady + 2;         // the segment's last PV has finished
     static constexpr int kBarOFree = kBarODone + 1;          // every softmax warp's arrival: the segment's O has been read
-    static constexpr int kBarEnd = kBarOFree + 1;            // every MMA has finished
+    static constexpr int kBarStage = kBarOFree + 1;          // [buffer], eight warps: the outputs staged there have left (chunk)
+    static constexpr int kBarEnd = kBarStage + 2;            // every MMA has finished
     static constexpr int kBars = kBarEnd + 1;
     static constexpr int kSmemBytes = kOffBar + 8 * kBars + 16;
     static_assert(kSmemBytes <= 232448, "a CTA's shared memory");
@@ -283,6 +274,8 @@ struct Layout {
 //   Q full       a query load into a buffer is issued after its Q empty (the last QK of the segment before).
 //   O done       once per segment; the next one's needs that segment's first PV, which waits for O free, for
 //                which every softmax warp has to have waited for O done.
+//   stage        a chunk's outputs leave through the query tile's buffer of their segment; the next query load into
+//                it waits for that too.  They have left by the second step of the segment behind it.
 //   ring         a slot is refilled only after its empty barrier, waited in order.
 
 struct Params {
@@ -299,7 +292,6 @@ struct Params {
     float* ws_lse;       // [slots][rows_cap]
     // chunk: query i sees the (compacted) keys c <= hi0 + i with c > hi0 + i - window or c < sinks
     int hi0, window, sinks;
-    const __nv_bfloat16 *k, *v;  // [128][keys][128]
     __nv_bfloat16* out;  // [rows][128][128]
 };
 
@@ -369,7 +361,8 @@ template <bool kChunk, bool kPair>
 __global__ void __cluster_dims__(kPair ? 2 : 1, 1, 1) __maxnreg__(168)
 attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__ CUtensorMap tm_qr,
               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
-              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p)
+              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_out,
+              const __grid_constant__ Params p)
 {
     using namespace dev;
     using L = Layout<kPair>;
@@ -393,6 +386,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             mbar_init(bar(L::kBarQEmpty + b), 1);
             mbar_init(bar(L::kBarSFull + b), 1);
             mbar_init(bar(L::kBarPReady + b), kWarps);
+            mbar_init(bar(L::kBarStage + b), 8);
         }
         mbar_init(bar(L::kBarODone), 1);
         mbar_init(bar(L::kBarOFree), kWarps);
@@ -429,28 +423,19 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         // the prefix's keys and values are read once by one group of rows, k_R by every head
         const uint64_t pol_kv = kChunk || p.groups > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
         const uint64_t pol_kr = l2_policy_evict_last();
-        // Keys and values of the tile kFetch ahead go into L2, so that a slot, which is free only a step or two
-        // before it is needed, is filled from there (the even CTA of a pair fetches the keys, the odd one the values).
-        // (Behind the tile's own loads, and at most two tiles a turn: at the start the first tiles come first.)
-        // Two walks: the keys are two steps ahead of the values.
+        // Two walks: the keys are two steps ahead of the values.  (The ring is all that is under way: bringing tiles
+        // into L2 ahead of it costs more than it gives once the pieces follow one another without a gap, for 64 rows
+        // and 8,192 tokens 90 us with the values two steps ahead, 95 with whole tiles and 124 with fourteen of them,
+        // against 87.)
         Walk<kChunk, kPair> walk_k(p);
         Segment seg_k;
         bool more_k = walk_k.next(p, seg_k);
-        int n_k = 0, fetched = 3;
-        const auto fetch = [&](int n) {
-            const int j0 = first_key(seg_k, n);
-            const uint32_t bytes = (uint32_t)min(kTile, p.keys - j0) * 256;
-            const int64_t at = ((int64_t)seg_k.head * p.keys + j0) * 128;
-            if (leader) {
-                if (rank == 0) prefetch_l2(p.k + at, bytes);
-                if (!kPair || rank == 1) prefetch_l2(p.v + at, bytes);
-            }
-        };
+        int n_k = 0;
         int r = 0, s = 0, phase = 0;
         bool ok = true;
         const uint32_t full0 = mma_bar(L::kBarFull);
         const auto take = [&]() {  // the next slot, free; its barrier expects the slot's bytes
-            ok = r < L::kSlots || wait_all<kPair>(bar(L::kBarEmpty + s), phase - 1, w);
+            ok = r < L::kSlots || wait_all(bar(L::kBarEmpty + s), phase - 1, w);
             if (ok && leader && rank == 0) mbar_arrive_expect_tx(bar(L::kBarFull + s), (kPair ? 2 : 1) * L::kSlot);
             return ok;
         };
@@ -483,10 +468,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 }
                 put();
             }
-            for (int two = 0; two < 2 && fetched < min(seg_k.cnt, n_k - 1 + kFetch); ++two, ++fetched) fetch(fetched);
             if (++n_k == seg_k.cnt) {
                 n_k = 0;
-                fetched = 3;
                 more_k = walk_k.next(p, seg_k);
             }
         };
@@ -534,7 +517,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         int n = 0;
         while (walk.next(p, seg)) {
             const int b = n & 1;
-            if (n >= 2 && !wait_all<kPair>(bar(L::kBarQEmpty + b), (n >> 1) - 1, w)) break;
+            if (n >= 2 && !wait_all(bar(L::kBarQEmpty + b), (n >> 1) - 1, w)) break;
+            if (kChunk && n >= 2 && !wait_all(bar(L::kBarStage + b), (n >> 1) - 1, w)) break;
             if (leader) {
                 const uint32_t full = mma_bar(L::kBarQFull + b), q = sbase + b * L::kQ;
                 const int row = seg.row0 + kTile * rank;
@@ -593,7 +577,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 const uint64_t a0 = q_desc + q_buf * 3 * kQChunk16;
 #pragma unroll 1
                 for (int c = 0; c < 3; ++c) {
-                    if (!wait_all<kPair>(bar(L::kBarFull + s), phase, w)) return ok = false;
+                    if (!wait_all(bar(L::kBarFull + s), phase, w)) return ok = false;
                     tc_fence_after();
                     const uint64_t a = a0 + c * kQChunk16, b = k_desc + s * kSlot16;
                     ss(d, a, b, c != 0 ? 1u : 0u);
@@ -610,7 +594,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 const uint32_t pt = tmem + 256 * t, d = pt + 128;
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
-                    if (!wait_all<kPair>(bar(L::kBarFull + s), phase, w)) return ok = false;
+                    if (!wait_all(bar(L::kBarFull + s), phase, w)) return ok = false;
                     tc_fence_after();
                     const uint64_t b = v_desc + s * kSlot16;
                     const uint32_t a = pt + 32 * c;
@@ -631,7 +615,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 if (!more_q) return true;
                 if (i_q == 0) {
                     q_buf = n_q & 1;
-                    if (!(ok = wait_all<kPair>(bar(L::kBarQFull + q_buf), n_q >> 1, w))) return false;
+                    if (!(ok = wait_all(bar(L::kBarQFull + q_buf), n_q >> 1, w))) return false;
                 }
                 if (!qk(g_q & 1)) return false;
                 ++g_q;
@@ -649,8 +633,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 const int steps = seg.cnt;
                 for (int i = 0; i < steps; ++i, ++g) {
                     const int t = g & 1;
-                    if (!(ok = wait_all<kPair>(bar(L::kBarPReady + t), g >> 1, w))) break;
-                    if (i == 0 && n_seg > 0 && !(ok = wait_all<kPair>(bar(L::kBarOFree), n_seg - 1, w))) break;
+                    if (!(ok = wait_all(bar(L::kBarPReady + t), g >> 1, w))) break;
+                    if (i == 0 && n_seg > 0 && !(ok = wait_all(bar(L::kBarOFree), n_seg - 1, w))) break;
                     tc_fence_after();
                     if (!pv(t, i < 2)) break;
                     if (i + 1 == steps) commit(bar(L::kBarODone));  // ahead of the next segment's scores
@@ -678,6 +662,14 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             }
         };
         int n_seg = 0, g = 0;  // segments, steps
+        int staged = -1;       // chunk: the buffer whose outputs are leaving
+        const auto release = [&]() {
+            if (lane == 0) {
+                bulk_wait_read();
+                mbar_arrive(bar(L::kBarStage + staged));
+            }
+            staged = -1;
+        };
         bool ok = true;
         while (ok && walk.next(p, seg)) {
             const int steps = seg.cnt, tile_row = seg.row0 + kTile * rank;
@@ -697,34 +689,46 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             for (int i = 0; i < steps; ++i, ++g) {
                 const int t = g & 1;
                 const uint32_t t_s = tmem + lane_base + 256 * t;
-                if (!(ok = wait_all<kPair>(bar(L::kBarSFull + t), g >> 1, w))) break;
+                if (!(ok = wait_all(bar(L::kBarSFull + t), g >> 1, w))) break;
                 tc_fence_after();
                 if (tile_row + warp_row < p.rows) {  // the warp has a row at all
                     uint32_t sr[64];
                     tmem_ld_16x128(t_s, sr);
                     tmem_wait_ld();
-                    // keys that a row does not see get -infinity
+                    // Keys that a row does not see get -infinity.  A thread's 32 columns of a row in order are
+                    // 0, 1, 8, 9, 16, ... from `col`; `upto` has a bit for each of them that is at most `c`.
                     const int j0 = first_key(seg, i);
+                    const auto upto = [](int c) {
+                        const int n = min(32, max(0, 2 * (c >> 3) + ((c & 7) ? 2 : 1)));
+                        return c < 0 ? 0u : n == 32 ? 0xffffffffu : (1u << n) - 1u;
+                    };
                     if (kChunk) {
-                        int hi[2], lo[2];
-                        bool whole = true;
+                        // the first and the last row of the warp see every key: no row of it needs a mask
+                        const int hi_first = p.hi0 + min(tile_row + warp_row, p.rows - 1);
+                        const int hi_last = p.hi0 + min(tile_row + warp_row + 15, p.rows - 1);
+                        if (j0 + kTile - 1 > hi_first || (j0 <= hi_last - p.window && j0 + kTile > p.sinks)) {
+                            uint32_t sees[2];
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            hi[x] = p.hi0 + min(tile_row + row + 8 * x, p.rows - 1);
-                            lo[x] = hi[x] - p.window + 1;
-                            whole = whole && j0 + kTile - 1 <= hi[x] && (j0 >= lo[x] || j0 + kTile <= p.sinks);
-                        }
-                        if (__any_sync(0xffffffffu, !whole)) {
-#pragma unroll
-                            for (int k = 0; k < 64; ++k) {
-                                const int j = j0 + 8 * (k >> 2) + col + (k & 1), x = (k >> 1) & 1;
-                                if (j > hi[x] || (j < lo[x] && j >= p.sinks)) sr[k] = 0xff800000u;
+                            for (int x = 0; x < 2; ++x) {
+                                const int hi = p.hi0 + min(tile_row + row + 8 * x, p.rows - 1), lo = hi - p.window + 1;
+                                const int j = j0 + col;
+                                sees[x] = upto(hi - j) & (~upto(lo - 1 - j) | upto(p.sinks - 1 - j));
                             }
+#pragma unroll
+                            for (int k = 0; k < 64; ++k)
+                                if (!(sees[(k >> 1) & 1] >> (2 * (k >> 2) + (k & 1)) & 1u)) sr[k] = 0xff800000u;
                         }
                     } else if (j0 + kTile > p.keys) {
+                        const uint32_t sees = upto(p.keys - 1 - j0 - col);
 #pragma unroll
                         for (int k = 0; k < 64; ++k)
-                            if (j0 + 8 * (k >> 2) + col + (k & 1) >= p.keys) sr[k] = 0xff800000u;
+                            if (!(sees >> (2 * (k >> 2) + (k & 1)) & 1u)) sr[k] = 0xff800000u;
+                    }
+                    // The running maximum of a segment's first step is its scores', that of the second the first one's;
+                    // every later step has its stream's.
+                    if (i == 1) {
+                        m[0] = m_other[0];
+                        m[1] = m_other[1];
                     }
                     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
                     uint32_t pk[2][16];
@@ -749,8 +753,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                         }
                     };
                     float mt[2];
-                    bool beyond = i < 2;  // the stream's first tile sets the maximum
-                    if (i >= 2) exponentials();
+                    bool beyond = i == 0;
+                    if (i > 0) exponentials();
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         float m2[2];  // two chains
@@ -802,10 +806,11 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 }
                 arrive(r_ready + 8 * t);
                 change();
+                if (kChunk && staged >= 0 && i == min(1, steps - 1)) release();
             }
             if (steps & 1) change();  // those of the segment's first stream are in m and l after an even number of steps
             const int t0 = (g - steps) & 1;  // that stream
-            if (!(ok = ok && wait_all<kPair>(bar(L::kBarODone), n_seg, w))) break;
+            if (!(ok = ok && wait_all(bar(L::kBarODone), n_seg, w))) break;
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < 2; ++x) {  // a quad has a row's sum
@@ -833,8 +838,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                             (top + log2f(total)) * 0.69314718055994531f;
                 }
                 const uint32_t t_o = tmem + lane_base + 128 + 256 * t0, t_o_other = tmem + lane_base + 128 + 256 * (t0 ^ 1);
-                const bool odd = lane & 1;
-                const int col4 = odd ? 8 + 2 * (lane & 2) : 2 * (lane & 2);  // bf16: of the 16 columns of two steps
                 uint32_t o[64];
                 tmem_ld_16x128(t_o, o);
                 tmem_wait_ld();
@@ -852,21 +855,33 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     }
                 }
                 arrive(r_free);  // the next segment's products may start
+                if (kChunk) {
+                    // through shared memory and out by TMA, clipped at the last row: rows lie 32 KB apart, and 8 bytes a
+                    // lane from registers took 2,100 cycles
+                    uint8_t* stage = smem + (n_seg & 1) * L::kQ;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int at = i + 8 * x;
-                    if (kChunk) {
-                        uint2* dst = reinterpret_cast<uint2*>(p.out + ((int64_t)at * 128 + seg.head) * 128 + col4);
+                    for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int k = 0; k < 16; k += 2) {
-                            const uint32_t lo = pack_bf16x2(__uint_as_float(o[4 * k + 2 * x]), __uint_as_float(o[4 * k + 2 * x + 1]));
-                            const uint32_t hi = pack_bf16x2(__uint_as_float(o[4 * k + 4 + 2 * x]), __uint_as_float(o[4 * k + 5 + 2 * x]));
-                            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
-                            if (at < p.rows) dst[2 * k] = odd ? make_uint2(other, hi) : make_uint2(lo, other);
+                        for (int k = 0; k < 16; ++k) {  // columns 8 k + col, + 1: chunk k & 7 of 128-byte rows, swizzled
+                            const int r = row + 8 * x;
+                            *reinterpret_cast<uint32_t*>(stage + (k >> 3) * 16384 + r * 128 + (((k & 7) ^ (r & 7)) << 4) + 2 * col) =
+                                pack_bf16x2(__uint_as_float(o[4 * k + 2 * x]), __uint_as_float(o[4 * k + 2 * x + 1]));
                         }
-                    } else if (at < p.rows) {
-                        float2* dst =
-                            reinterpret_cast<float2*>(p.ws_o + ((int64_t)seg.slot * p.rows_cap + (at - seg.row0)) * 128 + col);
+                    fence_proxy_async_cta();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const uint32_t from = smem_u32(stage) + warp_row * 128;
+                        tma_store_3d(&tm_out, from, 0, seg.head, tile_row + warp_row);
+                        tma_store_3d(&tm_out, from + 16384, 64, seg.head, tile_row + warp_row);
+                        bulk_commit();
+                    }
+                } else {
+                    // a quad's lanes write 32 bytes of a row side by side: whole sectors
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (i + 8 * x >= p.rows) continue;
+                        float2* dst = reinterpret_cast<float2*>(
+                            p.ws_o + ((int64_t)seg.slot * p.rows_cap + (i + 8 * x - seg.row0)) * 128 + col);
 #pragma unroll
                         for (int k = 0; k < 16; ++k)
                             dst[4 * k] = make_float2(__uint_as_float(o[4 * k + 2 * x]), __uint_as_float(o[4 * k + 2 * x + 1]));
@@ -875,8 +890,10 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             } else {
                 arrive(r_free);
             }
+            if (kChunk) staged = n_seg & 1;
             ++n_seg;
         }
+        if (kChunk && lane == 0) bulk_wait_all();
     }
     // After a wait that ran out an odd CTA's loads may be in flight without a barrier of its own: they land in
     // microseconds, and it waits a millisecond.

@@ -92,7 +92,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant
             const int row = (int)(at % kProducts) * 128;
 #pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
-                if (!(ok = r < kSlots || wait_all<true>(bar(kBarWEmpty + s), phase - 1, w))) break;
+                if (!(ok = r < kSlots || wait_all(bar(kBarWEmpty + s), phase - 1, w))) break;
                 if (leader) {
                     if (rank == 0) mbar_arrive_expect_tx(bar(kBarWFull + s), 2 * kChunk);
                     tma_load_2d_pair(sbase + kOffRing + s * kChunk, map, full + 8 * s, 64 * c, row, pol);
@@ -120,7 +120,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant
             part = 0;
 #pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
-                if (n > 0 && !(ok = wait_all<true>(bar(kBarAEmpty + c), n - 1, w))) break;
+                if (n > 0 && !(ok = wait_all(bar(kBarAEmpty + c), n - 1, w))) break;
                 if (leader) {
                     if (rank == 0) mbar_arrive_expect_tx(bar(kBarAFull + c), 2 * kChunk);
                     tma_load_2d_pair(sbase + c * kChunk, &tm_rows, full + 8 * c, 64 * c, row, pol);
@@ -142,12 +142,12 @@ expand_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant
             const bool fresh = at == first || at % kProducts == 0;
             const bool last = at + 1 == end || (at + 1) % kProducts == 0;
             const uint32_t d = tmem + 256 * (j & 1);
-            if (j >= 2 && !(ok = wait_all<true>(bar(kBarDFree + (j & 1)), (j >> 1) - 1, w))) break;
+            if (j >= 2 && !(ok = wait_all(bar(kBarDFree + (j & 1)), (j >> 1) - 1, w))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
-                if (fresh && !(ok = wait_all<true>(bar(kBarAFull + c), n, w))) break;
-                if (!(ok = wait_all<true>(bar(kBarWFull + s), phase, w))) break;
+                if (fresh && !(ok = wait_all(bar(kBarAFull + c), n, w))) break;
+                if (!(ok = wait_all(bar(kBarWFull + s), phase, w))) break;
                 tc_fence_after();
                 const uint64_t a = a_desc + c * kChunk16, b = w_desc + s * kChunk16;
                 mma_ss_pair(d, a, b, idesc, c != 0 ? 1u : 0u);
@@ -181,7 +181,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant
         __nv_bfloat16* const out = set == 0 ? p.k : p.v;
         int j = 0;
         for (int64_t at = first; at < end; ++at, ++j) {
-            if (!wait_all<true>(bar(kBarDFull + (j & 1)), j >> 1, w)) break;
+            if (!wait_all(bar(kBarDFull + (j & 1)), j >> 1, w)) break;
             tc_fence_after();
             __nv_bfloat16* const head = out + (at % kProducts) * p.rows * 128;
             const int64_t i0 = at / kProducts * kRowsTile + row;
