@@ -536,8 +536,8 @@ MLA_API mla_status mla_prefill_decompressed(mla_kv_dtype kv_dtype, const void* k
  * the absorbed form: 278,528 FLOP for each sequence and prefix token.  Here the prefix is decompressed
  * once (P1 section 4, path A) and kept, and each step's query rows attend to it together: 81,920 FLOP for
  * each row and token, and 64 KB of keys and values read for each token whatever the number of rows.  That
- * is faster from about 40 query rows on (256 rows: several times), and takes 66.7 KB of memory for each
- * prefix token.
+ * is faster from about 48 query rows on with 8,192 shared tokens or more, from about 100 with 2,048 (256
+ * rows over 16,384: 3.3 times), and takes 66.7 KB of memory for each prefix token.
  *
  * mla_prefix_open makes the prefix's keys and values from its cache pages:
  *   kv_dtype, kv_pool, kv_scale, kr_pool, num_pool_pages   the cache, as mla_gather_kv

@@ -811,8 +811,7 @@ def mla_prefill_window(*, kv_pool: torch.Tensor, block_table_row: torch.Tensor, 
     table, pages = _table_row(block_table_row, device)
     err = _whole(dev_error, "dev_error", torch.int32, (1,), device)
     if workspace is None:
-        workspace = torch.empty(mla_prefill_window_workspace_bytes(seq_len, T, window, sinks), dtype=torch.uint8,
-                                device=q_c.device)
+        workspace = _scratch(mla_prefill_window_workspace_bytes(seq_len, T, window, sinks), q_c.device, stream)
     ws = _whole(workspace, "workspace", workspace.dtype, tuple(workspace.shape), device)
     st = lib().mla_prefill_window(*cache, table, pages, int(seq_len), T, int(window), int(sinks), *ptrs,
                                   float(softmax_scale), ws, workspace.numel() * workspace.element_size(), out_ptr, err,
@@ -821,13 +820,41 @@ def mla_prefill_window(*, kv_pool: torch.Tensor, block_table_row: torch.Tensor, 
         _check("mla_prefill_window", st)
 
 
+def _scratch(size: int, device, stream) -> torch.Tensor:
+    """A workspace of one call on ``stream``, from that stream's memory: what is let go of when the call
+    returns is handed out again on that stream alone, behind the call's kernels."""
+    if stream is not None:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if handle != _stream(None):
+            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+                return torch.empty(max(16, size), dtype=torch.uint8, device=device)
+    return torch.empty(max(16, size), dtype=torch.uint8, device=device)
+
+
 def _cache(kv_pool, kv_scale, kr_pool, device: int):
     """The leading arguments of a call that reads a cache of any of the three kinds."""
-    dtype = _kv_dtype(kv_pool, kv_scale, kr_pool)
-    for name, t in (("kv_pool", kv_pool), ("kv_scale", kv_scale), ("kr_pool", kr_pool)):
-        if t is not None:
-            _whole(t, name, t.dtype, tuple(t.shape), device)
-    return dtype, kv_pool.data_ptr(), _ptr(kv_scale), _ptr(kr_pool), int(kv_pool.shape[0])
+    try:  # the checks in one expression; what it refuses is told below
+        pages, rows, width = kv_pool.shape
+        if kv_scale is None:
+            dtype, scale_ptr, kr_ptr = MLA_KV_BF16, None, None
+            fine = kv_pool.dtype is torch.bfloat16 and width == D_ROW
+        else:
+            dtype = MLA_KV_NVFP4 if width == NVFP4_ROW else MLA_KV_FP8_E4M3
+            fine = kv_pool.dtype is torch.uint8 and (width == D_C or width == NVFP4_ROW) and \
+                kv_scale.dtype is torch.float32 and kv_scale.shape == (pages, PAGE) and kv_scale.is_contiguous() and \
+                kv_scale.get_device() == device and kr_pool.dtype is torch.bfloat16 and \
+                kr_pool.shape == (pages, PAGE, D_R) and kr_pool.is_contiguous() and kr_pool.get_device() == device
+            scale_ptr, kr_ptr = kv_scale.data_ptr(), kr_pool.data_ptr()
+        fine = fine and rows == PAGE and kv_pool.is_contiguous() and kv_pool.get_device() == device
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _kv_dtype(kv_pool, kv_scale, kr_pool)
+        for name, t in (("kv_pool", kv_pool), ("kv_scale", kv_scale), ("kr_pool", kr_pool)):
+            if t is not None:
+                _whole(t, name, t.dtype, tuple(t.shape), device)
+        raise ValueError("cache: arguments that do not fit together")
+    return dtype, kv_pool.data_ptr(), scale_ptr, kr_ptr, pages
 
 
 def _table_row(row, device: int):
@@ -841,8 +868,8 @@ class SharedPrefix:
     current stream) and kept: keys ``k`` and values ``v`` [128 heads, tokens, 128] and rotary keys
     ``k_r`` [tokens, 64], 66.7 KB for each token.  ``block_table_row`` lists the prefix's pages, whose
     last may be partly filled.  For mla_prefix_attend, and for DecodeStep(prefix=...), whose sequences
-    are then the tokens behind the prefix.  Worth it from about 40 query rows on; fewer are faster
-    with block tables that list the shared pages themselves."""
+    are then the tokens behind the prefix.  Faster than block tables that list the shared pages
+    themselves from about 48 query rows on with 8,192 shared tokens or more, from about 100 with 2,048."""
 
     def __init__(self, prefix_len: int, *, w_uk: torch.Tensor, w_uv: torch.Tensor, kv_pool: torch.Tensor,
                  block_table_row: torch.Tensor, kv_scale: Optional[torch.Tensor] = None,
@@ -853,16 +880,19 @@ class SharedPrefix:
         weights = [_whole(t, name, bf16, (NUM_HEADS, D_HC, D_C), device) for t, name in ((w_uk, "w_uk"), (w_uv, "w_uv"))]
         cache = _cache(kv_pool, kv_scale, kr_pool, device)
         table, pages = _table_row(block_table_row, device)
-        where = dict(device=kv_pool.device)
-        err = torch.zeros(1, dtype=torch.int32, **where) if dev_error is None else dev_error
+        where = kv_pool.device
+        err = torch.zeros(1, dtype=torch.int32, device=where) if dev_error is None else dev_error
         err_ptr = _whole(err, "dev_error", torch.int32, (1,), device)
         if (P + PAGE - 1) // PAGE > pages:
             raise ValueError(f"block_table_row holds {pages} pages, the prefix needs {(P + PAGE - 1) // PAGE}")
-        rows = torch.empty(P, D_ROW, dtype=bf16, **where)
-        k, v = (torch.empty(NUM_HEADS, P, D_HC, dtype=bf16, **where) for _ in range(2))
-        _check("mla_prefix_open", lib().mla_prefix_open(*cache, table, pages, P, *weights, rows.data_ptr(), k.data_ptr(),
-                                                        v.data_ptr(), err_ptr, _stream(None)))
-        self._set(k, v, rows[:, D_C:], err, device)
+        rows = torch.empty((P, D_ROW), dtype=bf16, device=where)
+        k = torch.empty((NUM_HEADS, P, D_HC), dtype=bf16, device=where)
+        v = torch.empty((NUM_HEADS, P, D_HC), dtype=bf16, device=where)
+        st = lib().mla_prefix_open(*cache, table, pages, P, *weights, rows.data_ptr(), k.data_ptr(), v.data_ptr(), err_ptr,
+                                   _stream(None))
+        if st:
+            _check("mla_prefix_open", st)
+        self._set(k, v, rows.narrow(1, D_C, D_R), err, device)
 
     @classmethod
     def of(cls, k: torch.Tensor, v: torch.Tensor, k_r: torch.Tensor, dev_error: Optional[torch.Tensor] = None):
@@ -921,7 +951,7 @@ def mla_prefix_attend(prefix: SharedPrefix, q_c: torch.Tensor, q_r: torch.Tensor
     if prefix.device_index != device:
         raise ValueError(f"prefix: must be on the current CUDA device ({device})")
     if workspace is None:
-        workspace = prefix.workspace(R)
+        workspace = _scratch(prefix.workspace_bytes(R), q_c.device, stream)
     ws = _whole(workspace, "workspace", workspace.dtype, tuple(workspace.shape), device)
     err = prefix.dev_error if dev_error is None else dev_error
     sizes, keys = prefix._args

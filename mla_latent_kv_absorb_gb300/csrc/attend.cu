@@ -168,6 +168,33 @@ Span chunk_span(int32_t seq_len, int32_t chunk_len, int32_t window, int32_t sink
     return s;
 }
 
+// Whether a chunk's rows go to CTAs of 128 or to pairs of 256.  Each worker takes whole (head, group) segments in
+// rounds; a segment costs its key tiles and some 3,000 cycles.  A pair's tile takes 1,650 cycles and serves 256
+// rows; a CTA alone brings in the whole tile for 128, 1,850, but has fewer keys that only other rows of the
+// group see, and smaller pieces to share out.  Whole calls, pairs against CTAs alone: 257 queries under 511
+// 68.2 and 54.3 us, 1,024 under 512 107 and 103, 2,000 under 300 165 and 151, 4,096 under 1,024 421 and 429.
+constexpr int64_t kPairTile = 1650, kAloneTile = 1850, kSegment = 3000;
+
+struct ChunkCut {
+    bool pair;
+    int groups, workers;
+    int64_t cycles;
+};
+
+ChunkCut cut_chunk(bool pair, int32_t chunk_len, int32_t window, int32_t sinks, int32_t keys, int sms)
+{
+    ChunkCut c;
+    const int rows = pair ? 256 : 128;
+    c.pair = pair;
+    c.groups = (chunk_len + rows - 1) / rows;
+    c.workers = (int)std::min<int64_t>(pair ? std::max(1, sms / 2) : sms, (int64_t)c.groups * 128);
+    const int64_t rounds = ((int64_t)c.groups * 128 + c.workers - 1) / c.workers;
+    const int64_t seen = std::min<int64_t>(keys, (int64_t)window + rows - 1);
+    const int64_t tiles = (seen + 127) / 128 + (std::min<int64_t>(sinks, keys - seen) + 127) / 128;
+    c.cycles = rounds * (tiles * (pair ? kPairTile : kAloneTile) + kSegment);
+    return c;
+}
+
 bool chunk_sizes_ok(int32_t seq_len, int32_t chunk_len, int32_t window, int32_t sinks)
 {
     return seq_len >= 1 && chunk_len >= 1 && chunk_len <= seq_len && window >= 1 && sinks >= 0;
@@ -292,11 +319,14 @@ extern "C" MLA_API mla_status mla_prefill_window(mla_kv_dtype kv_dtype, const vo
     if (workspace_bytes < s.total) return MLA_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);
     void *k = ws + s.k, *v = ws + s.v;
-    Maps m;
-    if (!make_maps(&m, q_c, q_r, k, v, ws + 512 * 2, 576, chunk_len, s.keys, true, out)) return MLA_ERR_CUDA;
     int sms = 0;
     mla_status st = sm_count(&sms);
     if (st != MLA_OK) return st;
+    ChunkCut c = cut_chunk(true, chunk_len, window, sinks, s.keys, sms);
+    const ChunkCut alone = cut_chunk(false, chunk_len, window, sinks, s.keys, sms);
+    if (alone.cycles < c.cycles) c = alone;
+    Maps m;
+    if (!make_maps(&m, q_c, q_r, k, v, ws + 512 * 2, 576, chunk_len, s.keys, c.pair, out)) return MLA_ERR_CUDA;
     st = mla::gather_one_sequence(kv_dtype, kv_pool, kv_scale, kr_pool, num_pool_pages, block_table_row, max_pages, s.keys, ws,
                                   dev_error, stream, s.skip_from, s.skip);
     if (st == MLA_OK) st = expand_rows(ws, w_uk, w_uv, k, v, s.keys, dev_error, sms, stream);
@@ -305,12 +335,11 @@ extern "C" MLA_API mla_status mla_prefill_window(mla_kv_dtype kv_dtype, const vo
     p.rows = chunk_len;
     p.keys = s.keys;
     p.scale_log2 = softmax_scale * kLog2e;
-    p.groups = (chunk_len + 255) / 256;
+    p.groups = c.groups;
     p.dev_error = dev_error;
     p.timeout_ns = kTimeoutNs;
     p.hi0 = seq_len - chunk_len - s.skip;
     p.window = std::min(window, seq_len);
     p.sinks = std::min(sinks, seq_len);
-    p.out = static_cast<__nv_bfloat16*>(out);
-    return launch_attend<true, true>(m, p, (int)std::min<int64_t>(std::max(1, sms / 2), (int64_t)p.groups * 128), stream);
+    return c.pair ? launch_attend<true, true>(m, p, c.workers, stream) : launch_attend<true, false>(m, p, c.workers, stream);
 }

@@ -292,7 +292,6 @@ struct Params {
     float* ws_lse;       // [slots][rows_cap]
     // chunk: query i sees the (compacted) keys c <= hi0 + i with c > hi0 + i - window or c < sinks
     int hi0, window, sinks;
-    __nv_bfloat16* out;  // [rows][128][128]
 };
 
 // A worker's piece of one run.

@@ -164,3 +164,24 @@ def test_open_bad_page():
     w = au.normal(gen, 128, 128, 512)
     p = binding.SharedPrefix(130, w_uk=w, w_uv=w, block_table_row=torch.tensor([0, 9, 1], dtype=torch.int32, device="cuda"), **kv)
     assert binding.mla_read_device_error(p.dev_error) == binding.MLA_DEVERR_BAD_PAGE
+
+
+def test_workspace_is_the_streams(monkeypatch):
+    """A workspace that the call makes belongs to the stream that the call is sent to."""
+    x = draw(40, 300, 12)
+    want = attend(x)
+    prefix = binding.SharedPrefix.of(x["k"], x["v"], x["k_r"])
+    side, seen, empty = torch.cuda.Stream(), [], torch.empty
+    out = torch.empty_like(x["q_c"])
+    torch.cuda.synchronize()
+
+    def spy(*a, **kw):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*a, **kw)
+    for stream in (side, side.cuda_stream):
+        monkeypatch.setattr(torch, "empty", spy)
+        binding.mla_prefix_attend(prefix, x["q_c"], x["q_r"], out, own_out=x["own_out"], own_lse=x["own_lse"], stream=stream)
+        monkeypatch.undo()
+        side.synchronize()
+        assert seen == [side.cuda_stream] and torch.equal(out, want[0])
+        seen.clear()

@@ -92,6 +92,17 @@ def test_chunk_quantised(kind, S, T, W, n):
     au.check(out[:, heads], reference(x, heads), keys=min(S, W + n), **bounds(x, heads))
 
 
+# wide windows, whose rows go to pairs of CTAs when the groups of 256 are nearly full
+@pytest.mark.parametrize("S,T,W,n", [(2222, 250, 1024, 7), (1999, 499, 1500, 0), (1300, 1300, 1100, 0), (2500, 723, 2500, 0),
+                                     (2600, 1003, 1200, 700), (2500, 330, 1100, 900)])
+def test_chunk_wide(S, T, W, n):
+    x = draw(S, T, W, n, seed=S + T + W + n)
+    out = run(x, S, W, n)
+    heads = [0, 77, 127]
+    au.check(out[:, heads], reference(x, heads), keys=min(S, W + n), **bounds(x, heads), what=f"S={S} T={T} W={W} n={n}")
+    assert torch.isfinite(out.float()).all()
+
+
 def test_whole_window_is_the_causal_chunk():
     """A window as long as the sequence sees what mla_prefill_decompressed sees."""
     S, T = 900, 300
@@ -112,3 +123,25 @@ def test_workspace_given_and_guarded():
     ws = torch.full((size + 64,), 255, dtype=torch.uint8, device="cuda")
     assert torch.equal(run(x, S, W, n, workspace=ws[:-64]), run(x, S, W, n))
     assert (ws[-64:] == 255).all()
+
+
+def test_workspace_is_the_streams(monkeypatch):
+    """A workspace that the call makes belongs to the stream that the call is sent to."""
+    S, T, W, n = 600, 200, 100, 3
+    x = draw(S, T, W, n, seed=11)
+    want = run(x, S, W, n)
+    side, seen, empty = torch.cuda.Stream(), [], torch.empty
+    got, err = torch.empty_like(want), torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+
+    def spy(*a, **kw):
+        seen.append(torch.cuda.current_stream().cuda_stream)
+        return empty(*a, **kw)
+    for stream in (side, side.cuda_stream):
+        monkeypatch.setattr(torch, "empty", spy)
+        binding.mla_prefill_window(block_table_row=x["table"], seq_len=S, window=W, sinks=n, q_c=x["q_c"], q_r=x["q_r"],
+                                   w_uk=x["w_uk"], w_uv=x["w_uv"], out=got, dev_error=err, **x["kv"], stream=stream)
+        monkeypatch.undo()
+        side.synchronize()
+        assert seen == [side.cuda_stream] and torch.equal(got, want) and int(err) == 0
+        seen.clear()

@@ -1,7 +1,6 @@
 """The decode step under a sliding window with sinks, and behind a shared prefix, in 64 bits."""
 import math
 
-import numpy as np
 import pytest
 import torch
 
