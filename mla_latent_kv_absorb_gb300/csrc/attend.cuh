@@ -10,8 +10,10 @@
 // Keys and values are per head (page 1 section 4, path A): k, v [128 heads][keys][128] and k_R
 // [keys][64], so a (row, key) pair costs 2 * (192 + 128) * 128 FLOP where the absorbed form costs
 // 2 * (576 + 512) * 128, and 64 KB of keys and values are read for each prefix token however many
-// rows there are: with up to about 110 rows that is what bounds the prefix form (HBM), beyond it
-// the tensor cores.
+// rows there are: with up to some 220 rows that is what bounds the prefix form (HBM), beyond it
+// the tensor cores.  Measured with the merge: 64 rows x 8,192 keys 87 us, 93 % of the copy rate; 256 rows x 16,384
+// 256 us, 1.34 PFLOP/s, 70 % of what cuBLAS reaches (tensor pipe 70 % busy); a chunk of 4,096 queries under a
+// window of 1,024 319 us.
 //
 // A CTA holds a 128-row query tile of a head and streams 128-key tiles; with more than 128 rows a pair of CTAs
 // (two SMs, MMAs of M = 256) holds 256 rows, and each brings in half of every key tile (64 keys) and of every
@@ -928,7 +930,8 @@ constexpr int kMergeWarps = 8;
 
 // Joins the partials of the prefix (at most a few for one head and group) with the row's attention over
 // its own tokens by log-sum-exp.  Half a warp per (row, head), eight columns a lane: bound by HBM and L2 (own
-// outputs in, outputs out, partials from L2).
+// outputs in, outputs out, partials from L2).  256 rows over 16,384 keys: 12 us for 54 MB (a warp of four columns a
+// lane 17).
 __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __grid_constant__ Merge a)
 {
     const int lane = threadIdx.x & 15;

@@ -4,6 +4,7 @@
 //
 // for the rows c_i (512 values) of a prefix or of a chunk's span.  128 products (one head's keys and values) of
 // [256 rows x 512] by [512 x 256] for every tile of 256 rows, 33.5 MFLOP a row: bound by the tensor cores.
+// Measured: 8,192 rows 155 us (under ncu; 1.77 PFLOP/s, tensor pipe 87 % busy), 4,100 rows 78, 2,051 rows 47.
 //
 // A pair of CTAs (two SMs) takes a product: M = 256, each CTA with 128 of the rows and of the sums, and half of
 // N, the even one W_UK[h], the odd one W_UV[h].  Persistent: the products lie in one line, row tile by row tile,
