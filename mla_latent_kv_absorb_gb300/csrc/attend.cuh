@@ -947,6 +947,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
     while (c1 + 1 < a.workers && first_unit(c1 + 1, units, a.workers) < u1) ++c1;
     const int64_t at = row - group * a.group_rows;
     dev::griddep_wait();
+    dev::griddep_launch_dependents();
     // The row's own part and the first three of the prefix (more only with more workers than runs) are requested
     // together, in one round trip.
     constexpr int kAtOnce = 3;

@@ -110,6 +110,7 @@ expand_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant
                 drain_phase(bar(kBarWFull + k % kSlots), k / kSlots, w.timeout_ns);
     } else if (warp == 2) {
         griddep_wait();  // the rows come from the kernel before
+        griddep_launch_dependents();  // behind the wait: what starts now finds everything before this kernel written
         const bool leader = elect_lane();
         const uint64_t pol = l2_policy_evict_last();
         const uint32_t full = map_to_cta(bar(kBarAFull), 0);

@@ -19,11 +19,9 @@
 #include <cstdio>
 
 #include "../../include/mla.h"
+#include "launch.cuh"
 #include "nvtx_range.h"
-
-namespace mla {
-void set_last_error_text(const char* text);
-}
+#include "ptx.cuh"
 
 namespace mla::gather {
 
@@ -74,6 +72,10 @@ struct Args {
 // grid (ceil(max_pages * 64 / kWarps), B): warp w of CTA x takes token x * kWarps + w of sequence y.
 __global__ void __launch_bounds__(kWarps * 32) gather_kv_kernel(const Args a)
 {
+    if (!a.seq_lens) {  // one sequence: a dependent launch, whose rows the next kernel waits for in turn
+        dev::griddep_wait();
+        dev::griddep_launch_dependents();
+    }
     const int lane = threadIdx.x & 31, b = blockIdx.y;
     const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (t >= (a.seq_lens ? __ldg(a.seq_lens + b) : a.one_len)) return;
@@ -137,6 +139,7 @@ mla_status launch(const mla::gather::Args& a, int32_t max_pages, int32_t batch, 
     using namespace mla::gather;
     const int64_t tokens = (int64_t)max_pages * 64;
     const dim3 grid((unsigned)((tokens + kWarps - 1) / kWarps), (unsigned)batch), block(kWarps * 32);
+    if (!a.seq_lens) return mla::launch_dependent("gather kernel launch", gather_kv_kernel, grid, block, 0, stream, a);
     gather_kv_kernel<<<grid, block, 0, static_cast<cudaStream_t>(stream)>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) {
