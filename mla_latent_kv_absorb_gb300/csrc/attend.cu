@@ -47,7 +47,7 @@ bool cache_aligned(mla_kv_dtype kv_dtype, const void* kv_pool, const float* kv_s
 // The maps of q_c [rows][128][128], q_r [rows][128][64], k and v [128][keys][128] and k_r [keys] rows of
 // `kr_stride` elements: boxes of 64 columns by 128 rows, by 128 keys (64 in a pair), by 64 keys for the values.
 struct Maps {
-    CUtensorMap qc, qr, k, kr, v, out;  // out: a chunk's, boxes of 16 rows of one head by 64 columns
+    CUtensorMap qc, qr, k, kr, v, out;  // out: a chunk's alone, boxes of 16 rows of one head by 64 columns
 };
 
 bool make_maps(Maps* m, const void* q_c, const void* q_r, const void* k, const void* v, const void* k_r,
@@ -64,7 +64,7 @@ bool make_maps(Maps* m, const void* q_c, const void* q_r, const void* k, const v
     return make_bf16_map(&m->qc, q_c, 3, qc_dims, qc_str, q_box) && make_bf16_map(&m->qr, q_r, 3, qr_dims, qr_str, q_box) &&
            make_bf16_map(&m->k, k, 3, k_dims, k_str, k_box) && make_bf16_map(&m->v, v, 3, k_dims, k_str, v_box) &&
            make_bf16_map(&m->kr, k_r, 2, r_dims, r_str, r_box) &&
-           make_bf16_map(&m->out, out, 3, qc_dims, qc_str, o_box);
+           (!out || make_bf16_map(&m->out, out, 3, qc_dims, qc_str, o_box));
 }
 
 template <bool kChunk, bool kPair>
@@ -253,8 +253,8 @@ extern "C" MLA_API mla_status mla_prefix_attend(int32_t num_rows, int32_t prefix
     if (!prefix_sizes_fit(num_rows, prefix_len, num_sms)) return MLA_ERR_UNSUPPORTED;
     const Cut c = cut_prefix(num_rows, prefix_len, num_sms);
     if (workspace_bytes < c.total) return MLA_ERR_WORKSPACE;
-    Maps m;
-    if (!make_maps(&m, q_c, q_r, k, v, k_r, k_r_stride, num_rows, prefix_len, c.pair, out)) return MLA_ERR_CUDA;
+    Maps m = {};
+    if (!make_maps(&m, q_c, q_r, k, v, k_r, k_r_stride, num_rows, prefix_len, c.pair, nullptr)) return MLA_ERR_CUDA;
     mla::attend::Params p = {};
     p.rows = num_rows;
     p.keys = prefix_len;

@@ -300,6 +300,7 @@ struct Params {
 struct Segment {
     int head, row0, cnt;  // cnt key tiles
     int lead, base;       // key tile n begins at key 128 n below lead, at base + 128 (n - lead) behind it
+    int lead_end, end;    // no row of the group sees a key at or past these in the tiles below and from lead on
     int slot;             // the prefix's partial
 };
 
@@ -336,6 +337,8 @@ struct Walk {
             s.lead = (min(p.sinks, lo) + kTile - 1) / kTile;
             s.base = max(s.lead * kTile, lo);
             s.cnt = s.lead + (p.hi0 + last - s.base + kTile) / kTile;  // the last key is hi0 + last
+            s.end = p.hi0 + last + 1;
+            s.lead_end = min(s.end, s.base > s.lead * kTile ? p.sinks : s.lead * kTile);
             s.slot = 0;
             at += workers();
         } else {
@@ -345,6 +348,7 @@ struct Walk {
             s.cnt = (int)min((int64_t)(p.tiles - n0), end - at);
             s.lead = 0;
             s.base = n0 * kTile;
+            s.lead_end = s.end = p.keys;
             s.slot = worker() + run;
             at += s.cnt;
         }
@@ -355,6 +359,13 @@ struct Walk {
 __device__ __forceinline__ int first_key(const Segment& s, int n)
 {
     return n < s.lead ? n * kTile : s.base + (n - s.lead) * kTile;
+}
+
+// The keys of tile n that the products take: those that some row sees, up to a multiple of 32 (half of them are
+// a pair's CTA's).  The others' scores stay what they were, and the softmax masks them.
+__device__ __forceinline__ int tile_keys(const Segment& s, int n)
+{
+    return min(kTile, (((n < s.lead ? s.lead_end : s.end) - first_key(s, n)) + 31) & ~31);
 }
 
 template <bool kChunk, bool kPair>
@@ -449,7 +460,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         };
         const auto load_k = [&]() {  // the next key tile
             if (!more_k) return;
-            const int j0 = first_key(seg_k, n_k);
+            // (in a pair the odd CTA's keys follow the even one's)
+            const int j0 = first_key(seg_k, n_k) + (kPair ? rank * (tile_keys(seg_k, n_k) >> 1) : 0);
 #pragma unroll 1
             for (int c = 0; c < 3; ++c) {
                 if (!take()) return;
@@ -457,9 +469,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 if (leader) {
                     if (kPair) {
                         if (c < 2)
-                            tma_load_3d_pair(dst, &tm_k, full, 64 * c, j0 + 64 * rank, seg_k.head, pol_kv);
+                            tma_load_3d_pair(dst, &tm_k, full, 64 * c, j0, seg_k.head, pol_kv);
                         else
-                            tma_load_2d_pair(dst, &tm_kr, full, 0, j0 + 64 * rank, pol_kr);
+                            tma_load_2d_pair(dst, &tm_kr, full, 0, j0, pol_kr);
                     } else {
                         if (c < 2)
                             tma_load_3d(dst, &tm_k, full, 64 * c, j0, seg_k.head, pol_kv);
@@ -539,13 +551,14 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         for (int k = n > 2 ? n - 2 : 0; rank == 0 && k < n; ++k) drain_phase(bar(L::kBarQFull + (k & 1)), k >> 1, w.timeout_ns);
     } else if (warp == 1) {
         if (rank == 0) {
-            constexpr uint32_t idesc_qk = idesc_bf16(kPair ? 256 : 128, kTile, false, false);
+            constexpr uint32_t idesc_qk0 = idesc_bf16(kPair ? 256 : 128, 0, false, false);
+            uint32_t idesc_qk = 0;
             constexpr uint32_t idesc_pv = idesc_bf16(kPair ? 256 : 128, 128, false, true);
             const uint64_t q_desc = smem_desc(sbase, 16, 1024);
             const uint64_t k_desc = smem_desc(sbase + L::kOffRing, 16, 1024);
             const uint64_t v_desc = smem_desc(sbase + L::kOffRing, 8192, 1024);
             constexpr uint64_t kSlot16 = L::kSlot >> 4, kQChunk16 = 16384 >> 4;  // in the descriptors' 16-byte units
-            const auto ss = [](uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+            const auto ss = [&idesc_qk](uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
                 if (kPair)
                     mma_ss_pair(d, a, b, idesc_qk, acc);
                 else
@@ -573,8 +586,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 }
             };
             // Scores of stream t from the next three slots.
-            const auto qk = [&](int t) {
+            const auto qk = [&](int t, int keys) {
                 const uint32_t d = tmem + 256 * t;
+                idesc_qk = idesc_qk0 | (uint32_t)(keys >> 3) << 17;
                 const uint64_t a0 = q_desc + q_buf * 3 * kQChunk16;
 #pragma unroll 1
                 for (int c = 0; c < 3; ++c) {
@@ -591,7 +605,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 return true;
             };
             // O of stream t from its P and the next two slots.
-            const auto pv = [&](int t, bool first) {
+            const auto pv = [&](int t, bool first, int keys) {
                 const uint32_t pt = tmem + 256 * t, d = pt + 128;
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
@@ -599,10 +613,14 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     tc_fence_after();
                     const uint64_t b = v_desc + s * kSlot16;
                     const uint32_t a = pt + 32 * c;
-                    ts(d, a, b, first && c == 0 ? 0u : 1u);
-                    ts(d, a + 8, b + (2048 >> 4), 1u);
-                    ts(d, a + 16, b + (4096 >> 4), 1u);
-                    ts(d, a + 24, b + (6144 >> 4), 1u);
+                    if (keys > 64 * c) {
+                        ts(d, a, b, first && c == 0 ? 0u : 1u);
+                        ts(d, a + 8, b + (2048 >> 4), 1u);
+                    }
+                    if (keys > 64 * c + 32) {
+                        ts(d, a + 16, b + (4096 >> 4), 1u);
+                        ts(d, a + 24, b + (6144 >> 4), 1u);
+                    }
                     next_slot();
                 }
                 return true;
@@ -618,7 +636,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     q_buf = n_q & 1;
                     if (!(ok = wait_all(bar(L::kBarQFull + q_buf), n_q >> 1, w))) return false;
                 }
-                if (!qk(g_q & 1)) return false;
+                if (!qk(g_q & 1, tile_keys(seg_q, i_q))) return false;
                 ++g_q;
                 if (++i_q == seg_q.cnt) {
                     commit(bar(L::kBarQEmpty + q_buf));
@@ -637,7 +655,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     if (!(ok = wait_all(bar(L::kBarPReady + t), g >> 1, w))) break;
                     if (i == 0 && n_seg > 0 && !(ok = wait_all(bar(L::kBarOFree), n_seg - 1, w))) break;
                     tc_fence_after();
-                    if (!pv(t, i < 2)) break;
+                    if (!pv(t, i < 2, tile_keys(seg, i))) break;
                     if (i + 1 == steps) commit(bar(L::kBarODone));  // ahead of the next segment's scores
                     if (!next_qk()) break;
                 }
