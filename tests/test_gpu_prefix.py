@@ -185,3 +185,44 @@ def test_workspace_is_the_streams(monkeypatch):
         side.synchronize()
         assert seen == [side.cuda_stream] and torch.equal(out, want[0])
         seen.clear()
+
+
+def test_long_prefix():
+    """140,001 tokens: the last heads' keys and values lie behind 2^31 elements."""
+    P, heads = 140001, [0, 127]
+    gen = au.generator(21)
+    kv = au.make_cache(gen, (P + 63) // 64, "bf16")
+    table = torch.randperm((P + 63) // 64, generator=gen, device="cuda").int()
+    w_uk, w_uv = (au.normal(gen, 128, 128, 512, std=W_STD) for _ in range(2))
+    prefix = binding.SharedPrefix(P, w_uk=w_uk, w_uv=w_uv, block_table_row=table, **kv)
+    at = torch.tensor([0, 70000, P - 2, P - 1], device="cuda")
+    c, kr = au.cache_values(kv, table.long()[at // 64] * 64 + at % 64)
+    assert torch.equal(prefix.k_r[at].double(), kr)
+    for got, w in ((prefix.k, w_uk), (prefix.v, w_uv)):
+        want = torch.einsum("pc,hdc->hpd", c, w[heads].double())
+        size = torch.einsum("pc,hdc->hpd", c.abs(), w[heads].double().abs())
+        assert ((got[heads][:, at].double() - want).abs() <= au.U * want.abs() + 512 * 2.0 ** -23 * size).all()
+    for R in (3, 130):
+        q_c, q_r = au.normal(gen, R, 128, 128), au.normal(gen, R, 128, 64)
+        out, lse = torch.empty_like(q_c), torch.empty(R, 128, device="cuda")
+        binding.mla_prefix_attend(prefix, q_c, q_r, out, lse=lse)
+        assert binding.mla_read_device_error(prefix.dev_error) == 0
+        ref = au.attend64(q_c[:, heads], q_r[:, heads], prefix.k[heads], prefix.v[heads], prefix.k_r)
+        au.check(out[:, heads], ref, keys=P)
+        au.check_lse(lse[:, heads], ref, keys=P)
+
+
+def test_two_calls_at_once():
+    """Two streams with a workspace each share a prefix."""
+    x, y = draw(40, 700, 5), draw(150, 700, 6)
+    prefix = binding.SharedPrefix.of(x["k"], x["v"], x["k_r"])
+    y.update(k=x["k"], v=x["v"], k_r=x["k_r"])
+    want = attend(x)[0], attend(y)[0]
+    got = [torch.empty_like(w) for w in want]
+    streams, ws = [torch.cuda.Stream() for _ in got], [prefix.workspace(w.shape[0]) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, o, w, z in zip(streams, got, ws, (x, y)):
+            binding.mla_prefix_attend(prefix, z["q_c"], z["q_r"], o, own_out=z["own_out"], own_lse=z["own_lse"], workspace=w, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -145,3 +145,47 @@ def test_workspace_is_the_streams(monkeypatch):
         side.synchronize()
         assert seen == [side.cuda_stream] and torch.equal(got, want) and int(err) == 0
         seen.clear()
+
+
+def test_a_million_tokens():
+    """Behind a long context only the window's and the sinks' pages are touched: every other table entry is -1."""
+    S, T, W, n = 1048575, 130, 100, 70
+    x = draw(S, T, W, n, seed=31)
+    out = run(x, S, W, n)
+    heads = [1, 126]
+    au.check(out[:, heads], reference(x, heads), keys=W + n, **bounds(x, heads))
+
+
+@pytest.mark.parametrize("S,T,W,n", [(900, 300, 200, 70), (2222, 250, 1024, 7)])
+def test_captured_and_replayed(S, T, W, n):
+    x, y = draw(S, T, W, n, seed=41), draw(S, T, W, n, seed=42)
+    want = run(x, S, W, n), run(y, S, W, n)
+    ws = torch.empty(binding.mla_prefill_window_workspace_bytes(S, T, W, n), dtype=torch.uint8, device="cuda")
+    out, err = torch.empty_like(want[0]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    z = {k: x[k].clone() for k in ("table", "q_c", "q_r", "w_uk", "w_uv")}
+    pool = x["kv"]["kv_pool"].clone()
+    call = lambda: binding.mla_prefill_window(  # noqa: E731
+        block_table_row=z["table"], seq_len=S, window=W, sinks=n, q_c=z["q_c"], q_r=z["q_r"], w_uk=z["w_uk"], w_uv=z["w_uv"],
+        out=out, dev_error=err, workspace=ws, kv_pool=pool)
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for k in (0, 1, 0):
+        for name, t in z.items():
+            t.copy_((x, y)[k][name])
+        pool.copy_((x, y)[k]["kv"]["kv_pool"])
+        graph.replay()
+        assert torch.equal(out, want[k]) and binding.mla_read_device_error(err) == 0
+
+
+def test_bad_page():
+    """A page that does not exist is reported, and the call ends."""
+    S, T, W, n = 500, 200, 100, 3
+    x = draw(S, T, W, n, seed=51)
+    x["table"][6] = 1000000
+    out, err = torch.empty_like(x["q_c"]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(binding.mla_prefill_window_workspace_bytes(S, T, W, n), dtype=torch.uint8, device="cuda")
+    binding.mla_prefill_window(block_table_row=x["table"], seq_len=S, window=W, sinks=n, q_c=x["q_c"], q_r=x["q_r"],
+                               w_uk=x["w_uk"], w_uv=x["w_uv"], out=out, dev_error=err, workspace=ws, **x["kv"])
+    assert binding.mla_read_device_error(err) == binding.MLA_DEVERR_BAD_PAGE
