@@ -11,9 +11,9 @@
 // [keys][64], so a (row, key) pair costs 2 * (192 + 128) * 128 FLOP where the absorbed form costs
 // 2 * (576 + 512) * 128, and 64 KB of keys and values are read for each prefix token however many
 // rows there are: with up to some 220 rows that is what bounds the prefix form (HBM), beyond it
-// the tensor cores.  Measured with the merge: 64 rows x 8,192 keys 87 us, 93 % of the copy rate; 256 rows x 16,384
-// 256 us, 1.34 PFLOP/s, 70 % of what cuBLAS reaches (tensor pipe 70 % busy); a chunk of 4,096 queries under a
-// window of 1,024 319 us.
+// the tensor cores.  Measured with the merge: 64 rows x 8,192 keys 86 us, 93 % of the copy rate; 256 rows x 16,384
+// 260 us in a long run, 1.32 PFLOP/s (a plain library product 1.70 there), 216 alone (1.59; 1.91); a chunk of 4,096
+// queries under a window of 1,024 321 us.
 //
 // A CTA holds a 128-row query tile of a head and streams 128-key tiles; with more than 128 rows a pair of CTAs
 // (two SMs, MMAs of M = 256) holds 256 rows, and each brings in half of every key tile (64 keys) and of every
