@@ -18,10 +18,11 @@
 // A CTA holds a 128-row query tile of a head and streams 128-key tiles; with more than 128 rows a pair of CTAs
 // (two SMs, MMAs of M = 256) holds 256 rows, and each brings in half of every key tile (64 keys) and of every
 // value tile (64 dims).  Alone a CTA with 256 rows waited for its keys: 80 KB a tile and a ring of 128 KB.
-// It works on two "streams", every other key tile, each with a score buffer S, an output O and a running softmax
-// (m, l) of its own, joined at the end, so that one stream's softmax always has the other's products to hide
-// behind.  Step g is a key tile, of stream g & 1; the MMA order is PV(g), QK(g + 2), from one segment into the
-// next (a segment's own beginning and end took 3,500 of 24,000 cycles a segment of a chunk).
+// Step g is a key tile; the MMA order is PV(g), QK(g + 3), from one segment into the next (a segment's own
+// beginning and end took 3,500 of 24,000 cycles a segment of a chunk).  Three score buffers and one output fill the
+// tensor memory, so that two steps' scores lie ready when the softmax has finished with one.  (Two streams of every
+// other tile, each with a score buffer, an output and a running softmax of its own: chunk 4,096 under 1,024 456 us
+// for 444, prefix 64 x 8,192 85.3 for 84.8, 256 x 16,384 249 for 252.)
 //   QK:  S[rows x 128] = Q [rows x 192] (q_c | q_R: three 64-column chunks in shared memory)
 //                       x K tile [128 x 192] (k | k_R: three K-major chunks)
 //   PV:  O[rows x 128] += P [rows x 128] (bf16 in TMEM over the first half of S) x V tile (MN-major)
@@ -32,10 +33,11 @@
 // Warp 0 streams the ring, warp 2 the query tiles, warp 1 issues the MMAs, warps 3-10 are the softmax
 // of every step: a warp has 16 rows, a quad of lanes two of them (tcgen05.ld's 16x256b shape: lane l holds
 // columns 8 k + 2 (l & 3), + 1 of rows l / 4 and l / 4 + 8), so that a row's maximum is two shuffles away.
-// What bounds it with many rows is the chain QK -> softmax -> PV of a stream against the other stream's
-// products, so all eight warps work on one step: with four warps to a stream and a row a thread a step's softmax
-// took 1,530 cycles of that chain, more than a step's 20 MMAs of 64; with halves of a row that agree through
-// shared memory 1,450; this way 1,050.  The running maximum is the one of the stream's first tile and moves only
+// All eight warps work on one step: with four warps to every other step and a row a thread a step's softmax
+// took 1,530 cycles, with halves of a row that agree through shared memory 1,450; this way 1,050.  What bounds it with
+// many rows is no one thing: of some 1,700 cycles a step of 256 rows the MMAs execute 1,280; without any copies it
+// takes 1,500, without the exponentials or with a third of the score products hardly less.
+// The running maximum is that of the segment's first tile and moves only
 // when a score exceeds it by more than 32 (log2 units), which loses nothing: fp32 and bf16 round relative to the
 // value.  So a step takes its exponentials with the maximum that it has, looks at its scores beside that (no
 // exchange between lanes), and does them again in the rare other case.  P is rounded to bf16 for the PV product
@@ -58,28 +60,6 @@ using dev::WaitCtx;
 // softmax warps of its SM sub-partition (measured beside eight warps that issue FMAs all the time: 134 cycles
 // for an MMA of 64, against 71 this way).
 
-__device__ __forceinline__ void mma_ss_one(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_ts_one(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
 __device__ __forceinline__ void mma_commit_one(uint32_t bar)
 {
     asm volatile(
@@ -101,17 +81,6 @@ __device__ __forceinline__ void mma_ss_pair(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
 // Arrives on the barrier at this offset in both CTAs when all earlier MMAs of the pair have finished.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar)
 {
@@ -121,6 +90,57 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar)
         "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
         "h"((uint16_t)3)
         : "memory");
+}
+
+// A ring slot's four MMAs and the commit that frees it, in one election: K steps of 16 columns of A (32 bytes in
+// shared memory, 8 columns in tensor memory), of K-major keys (32 bytes) or of 16 MN-major rows of values (2,048 bytes).
+template <bool kPair>
+__device__ __forceinline__ void slot_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc, uint32_t bar)
+{
+#define MLA_SLOT_SS(GROUP, COMMIT)                                                          \
+    asm volatile(                                                                           \
+        "{\n\t.reg .pred p, t, e;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"                 \
+        "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"              \
+        "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"              \
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"                             \
+        "elect.sync _|e, 0xffffffff;\n\t"                                                  \
+        "@e tcgen05.mma." GROUP ".kind::f16 [%0], %1, %2, %3, p;\n\t"                      \
+        "@e tcgen05.mma." GROUP ".kind::f16 [%0], a1, b1, %3, t;\n\t"                      \
+        "@e tcgen05.mma." GROUP ".kind::f16 [%0], a2, b2, %3, t;\n\t"                      \
+        "@e tcgen05.mma." GROUP ".kind::f16 [%0], a3, b3, %3, t;\n\t"                      \
+        "@e tcgen05.commit." GROUP ".mbarrier::arrive::one.shared::cluster" COMMIT ";\n\t}" \
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc), "r"(bar), "h"((uint16_t)3) : "memory")
+    if (kPair)
+        MLA_SLOT_SS("cta_group::2", ".multicast::cluster.b64 [%5], %6");
+    else
+        MLA_SLOT_SS("cta_group::1", ".b64 [%5]");
+#undef MLA_SLOT_SS
+}
+
+// As slot_ss, with the first `pairs` (0, 1 or 2) pairs of the MMAs.
+template <bool kPair>
+__device__ __forceinline__ void slot_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc, int pairs,
+                                        uint32_t bar)
+{
+#define MLA_SLOT_TS(GROUP, COMMIT)                                                          \
+    asm volatile(                                                                           \
+        "{\n\t.reg .pred p, t, e, e1, e2;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t" \
+        "add.s32 a1, %1, 8;\n\tadd.s32 a2, %1, 16;\n\tadd.s32 a3, %1, 24;\n\t"            \
+        "add.s64 b1, %2, 128;\n\tadd.s64 b2, %2, 256;\n\tadd.s64 b3, %2, 384;\n\t"        \
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, %4, %4;\n\t"                             \
+        "elect.sync _|e, 0xffffffff;\n\t"                                                  \
+        "setp.gt.and.s32 e1, %5, 0, e;\n\tsetp.gt.and.s32 e2, %5, 1, e;\n\t"              \
+        "@e1 tcgen05.mma." GROUP ".kind::f16 [%0], [%1], %2, %3, p;\n\t"                   \
+        "@e1 tcgen05.mma." GROUP ".kind::f16 [%0], [a1], b1, %3, t;\n\t"                   \
+        "@e2 tcgen05.mma." GROUP ".kind::f16 [%0], [a2], b2, %3, t;\n\t"                   \
+        "@e2 tcgen05.mma." GROUP ".kind::f16 [%0], [a3], b3, %3, t;\n\t"                   \
+        "@e tcgen05.commit." GROUP ".mbarrier::arrive::one.shared::cluster" COMMIT ";\n\t}" \
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc), "r"(pairs), "r"(bar), "h"((uint16_t)3) : "memory")
+    if (kPair)
+        MLA_SLOT_TS("cta_group::2", ".multicast::cluster.b64 [%6], %7");
+    else
+        MLA_SLOT_TS("cta_group::1", ".b64 [%6]");
+#undef MLA_SLOT_TS
 }
 
 // A bounded wait (as dev::wait_phase) that looks at the timer, which is slow to read, once in many polls.
@@ -245,11 +265,13 @@ __device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, const uint32_t (&r
 constexpr int kTile = 128;                 // query rows of a tile, keys of a tile
 constexpr int kThreads = 32 * 11;
 constexpr int kSoftmaxWarp0 = 3;
-constexpr uint32_t kTmemCols = 512;        // stream t: S at 256 t, O at 256 t + 128
+constexpr uint32_t kTmemCols = 512;        // score buffer b at 128 b, O at 384
 constexpr float kRescaleLog2 = 32.f;       // P up to 2^32, l and O below 2^32 x keys x |v|: far from fp32's 2^127
 
 template <bool kPair>
 struct Layout {
+    static constexpr int kScores = 3;                        // score buffers, 128 columns each of tensor memory
+    static constexpr int kOCol = kScores * 128;              // the output's 128 columns
     static constexpr int kSlot = kPair ? 8192 : 16384;
     static constexpr int kSlots = 131072 / kSlot;
     static constexpr int kQ = 3 * 16384;                     // a query tile; the next segment's is loaded beside it
@@ -257,10 +279,10 @@ struct Layout {
     static constexpr int kOffBar = kOffRing + kSlots * kSlot;
     static constexpr int kBarFull = 0, kBarEmpty = kSlots;   // [slot]
     static constexpr int kBarQFull = 2 * kSlots, kBarQEmpty = kBarQFull + 2;  // [buffer]
-    static constexpr int kBarSFull = kBarQEmpty + 2;         // [stream]
-    static constexpr int kBarPReady = kBarSFull + 2;         // [stream], every softmax warp's arrival
-    static constexpr int kBarODone = kBarPReady + 2;         // the segment's last PV has finished
-    static constexpr int kBarOFree = kBarODone + 1;          // every softmax warp's arrival: the segment's O has been read
+    static constexpr int kBarSFull = kBarQEmpty + 2;         // [score buffer]
+    static constexpr int kBarPReady = kBarSFull + kScores;   // [score buffer], every softmax warp's arrival
+    static constexpr int kBarPV = kBarPReady + kScores;      // [score buffer], the PV of its P has finished
+    static constexpr int kBarOFree = kBarPV + kScores;          // every softmax warp's arrival: the segment's O has been read
     static constexpr int kBarStage = kBarOFree + 1;          // [buffer], eight warps: the outputs staged there have left (chunk)
     static constexpr int kBarEnd = kBarStage + 2;            // every MMA has finished
     static constexpr int kBars = kBarEnd + 1;
@@ -268,16 +290,18 @@ struct Layout {
     static_assert(kSmemBytes <= 232448, "a CTA's shared memory");
 };
 // In a pair the barriers on which the MMAs wait (full, Q full, P ready, O free) are the even CTA's, by both CTAs'
-// copies and warps; those that MMAs complete (empty, Q empty, S full, O done, end) are in both.
+// copies and warps; those that MMAs complete (empty, Q empty, S full, PV, end) are in both.
 // Phase bookkeeping.  A barrier waited by parity must never run two phases ahead of its waiter:
-//   S full [t]   completes once per step of stream t; QK(g + 2) is issued only after the MMA warp
+//   S full [b]   completes once per step of buffer b; QK(g + 3) is issued only after the MMA warp
 //                has seen P(g) ready, i.e. after the softmax has finished step g.
-//   P ready [t]  arrives once per step; P(g + 2) needs S(g + 2), issued after that wait.
+//   P ready [b]  arrives once per step; P(g + 3) needs S(g + 3), issued after that wait.
+//   PV [b]       waited for at a segment's end and before O is scaled, for the step before the next: the PV three
+//                steps ahead of it has finished (its S came after), PV(g + 3) needs P(g + 3).
 //   Q full       a query load into a buffer is issued after its Q empty (the last QK of the segment before).
-//   O done       once per segment; the next one's needs that segment's first PV, which waits for O free, for
-//                which every softmax warp has to have waited for O done.
+//   O free       once per segment; the next one's needs that segment's outputs, read after its last PV.
 //   stage        a chunk's outputs leave through the query tile's buffer of their segment; the next query load into
-//                it waits for that too.  They have left by the second step of the segment behind it.
+//                it waits for that too.  They have left by the first step of the segment behind it; the scores ahead of that step
+//                are of that segment, so nothing the step needs waits for that load.
 //   ring         a slot is refilled only after its empty barrier, waited in order.
 
 struct Params {
@@ -396,11 +420,13 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar(L::kBarQFull + b), 1);
             mbar_init(bar(L::kBarQEmpty + b), 1);
-            mbar_init(bar(L::kBarSFull + b), 1);
-            mbar_init(bar(L::kBarPReady + b), kWarps);
             mbar_init(bar(L::kBarStage + b), 8);
         }
-        mbar_init(bar(L::kBarODone), 1);
+        for (int b = 0; b < L::kScores; ++b) {
+            mbar_init(bar(L::kBarSFull + b), 1);
+            mbar_init(bar(L::kBarPReady + b), kWarps);
+            mbar_init(bar(L::kBarPV + b), 1);
+        }
         mbar_init(bar(L::kBarOFree), kWarps);
         mbar_init(bar(L::kBarEnd), 1);
         const bool misaligned = (sbase & 1023u) != 0;
@@ -435,14 +461,14 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         // the prefix's keys and values are read once by one group of rows, k_R by every head
         const uint64_t pol_kv = kChunk || p.groups > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
         const uint64_t pol_kr = l2_policy_evict_last();
-        // Two walks: the keys are two steps ahead of the values.  (The ring is all that is under way: bringing tiles
+        // Two walks: the keys are three steps ahead of the values, as the MMA warp takes them.  (The ring is all that is under way: bringing tiles
         // into L2 ahead of it costs more than it gives once the pieces follow one another without a gap, for 64 rows
         // and 8,192 tokens 90 us with the values two steps ahead, 95 with whole tiles and 124 with fourteen of them,
         // against 87.)
         Walk<kChunk, kPair> walk_k(p);
         Segment seg_k;
         bool more_k = walk_k.next(p, seg_k);
-        int n_k = 0;
+        int n_k = 0, g_k = 0, seg_no_k = 0;  // step of the segment, step, segment
         int r = 0, s = 0, phase = 0;
         bool ok = true;
         const uint32_t full0 = mma_bar(L::kBarFull);
@@ -459,7 +485,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             }
         };
         const auto load_k = [&]() {  // the next key tile
-            if (!more_k) return;
             // (in a pair the odd CTA's keys follow the even one's)
             const int j0 = first_key(seg_k, n_k) + (kPair ? rank * (tile_keys(seg_k, n_k) >> 1) : 0);
 #pragma unroll 1
@@ -481,10 +506,15 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 }
                 put();
             }
+            ++g_k;
             if (++n_k == seg_k.cnt) {
                 n_k = 0;
+                ++seg_no_k;
                 more_k = walk_k.next(p, seg_k);
             }
+        };
+        const auto keys_below = [&](int steps, int last_seg) {
+            while (ok && more_k && g_k < steps && (n_k > 0 || seg_no_k <= last_seg)) load_k();
         };
         const auto load_v = [&](int j0) {
 #pragma unroll 1
@@ -507,12 +537,11 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             tma_prefetch_desc(&tm_kr);
             tma_prefetch_desc(&tm_v);
         }
-        load_k();
-        if (ok) load_k();
-        while (ok && walk.next(p, seg)) {
-            for (int n = 0; ok && n < seg.cnt; ++n) {
+        keys_below(L::kScores, 1);
+        for (int g = 0, n_seg = 0; ok && walk.next(p, seg); ++n_seg) {
+            for (int n = 0; ok && n < seg.cnt; ++n, ++g) {
                 load_v(first_key(seg, n));
-                if (ok) load_k();
+                keys_below(g + 1 + L::kScores, n_seg + (n + 1 == seg.cnt ? 2 : 1));
             }
         }
         griddep_launch_dependents();  // the merge may be scheduled; it waits for this kernel's end
@@ -558,18 +587,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             const uint64_t k_desc = smem_desc(sbase + L::kOffRing, 16, 1024);
             const uint64_t v_desc = smem_desc(sbase + L::kOffRing, 8192, 1024);
             constexpr uint64_t kSlot16 = L::kSlot >> 4, kQChunk16 = 16384 >> 4;  // in the descriptors' 16-byte units
-            const auto ss = [&idesc_qk](uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
-                if (kPair)
-                    mma_ss_pair(d, a, b, idesc_qk, acc);
-                else
-                    mma_ss_one(d, a, b, idesc_qk, acc);
-            };
-            const auto ts = [](uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
-                if (kPair)
-                    mma_ts_pair(d, a, b, idesc_pv, acc);
-                else
-                    mma_ts_one(d, a, b, idesc_pv, acc);
-            };
             const auto commit = [](uint32_t b) {
                 if (kPair)
                     mma_commit_pair(b);
@@ -579,85 +596,82 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             int s = 0, phase = 0, q_buf = 0;  // the next slot, the segment's query tile
             bool ok = true;
             const auto next_slot = [&]() {
-                commit(bar(L::kBarEmpty + s));
                 if (++s == L::kSlots) {
                     s = 0;
                     ++phase;
                 }
             };
-            // Scores of stream t from the next three slots.
-            const auto qk = [&](int t, int keys) {
-                const uint32_t d = tmem + 256 * t;
+            // Scores into buffer b from the next three slots.
+            const auto qk = [&](int b, int keys) {
+                const uint32_t d = tmem + 128 * b;
                 idesc_qk = idesc_qk0 | (uint32_t)(keys >> 3) << 17;
                 const uint64_t a0 = q_desc + q_buf * 3 * kQChunk16;
 #pragma unroll 1
                 for (int c = 0; c < 3; ++c) {
                     if (!wait_all(bar(L::kBarFull + s), phase, w)) return ok = false;
                     tc_fence_after();
-                    const uint64_t a = a0 + c * kQChunk16, b = k_desc + s * kSlot16;
-                    ss(d, a, b, c != 0 ? 1u : 0u);
-                    ss(d, a + 2, b + 2, 1u);
-                    ss(d, a + 4, b + 4, 1u);
-                    ss(d, a + 6, b + 6, 1u);
+                    const uint64_t a = a0 + c * kQChunk16, k = k_desc + s * kSlot16;
+                    slot_ss<kPair>(d, a, k, idesc_qk, c != 0 ? 1u : 0u, bar(L::kBarEmpty + s));
                     next_slot();
                 }
-                commit(bar(L::kBarSFull + t));
+                commit(bar(L::kBarSFull + b));
                 return true;
             };
-            // O of stream t from its P and the next two slots.
-            const auto pv = [&](int t, bool first, int keys) {
-                const uint32_t pt = tmem + 256 * t, d = pt + 128;
+            // O from the P in buffer `buf` and the next two slots.
+            const auto pv = [&](int buf, bool first, int keys) {
+                const uint32_t pt = tmem + 128 * buf, d = tmem + L::kOCol;
 #pragma unroll 1
                 for (int c = 0; c < 2; ++c) {
                     if (!wait_all(bar(L::kBarFull + s), phase, w)) return ok = false;
                     tc_fence_after();
                     const uint64_t b = v_desc + s * kSlot16;
                     const uint32_t a = pt + 32 * c;
-                    if (keys > 64 * c) {
-                        ts(d, a, b, first && c == 0 ? 0u : 1u);
-                        ts(d, a + 8, b + (2048 >> 4), 1u);
-                    }
-                    if (keys > 64 * c + 32) {
-                        ts(d, a + 16, b + (4096 >> 4), 1u);
-                        ts(d, a + 24, b + (6144 >> 4), 1u);
-                    }
+                    slot_ts<kPair>(d, a, b, idesc_pv, first && c == 0 ? 0u : 1u, min(2, max(0, keys - 64 * c + 31) >> 5),
+                                   bar(L::kBarEmpty + s));
                     next_slot();
                 }
                 return true;
             };
-            // Two walks: the scores are two steps ahead of the outputs.
+            // Two walks: the scores are up to three steps ahead of the outputs.  The first of a segment waits for its
+            // query tile, whose buffer a chunk's outputs of the segment before the last left by: they need that
+            // segment's products to have been issued.
             Walk<kChunk, kPair> walk_q(p);
             Segment seg_q;
             bool more_q = walk_q.next(p, seg_q);
-            int n_q = 0, i_q = 0, g_q = 0;  // its segment, step of the segment, step
-            const auto next_qk = [&]() {
-                if (!more_q) return true;
-                if (i_q == 0) {
-                    q_buf = n_q & 1;
-                    if (!(ok = wait_all(bar(L::kBarQFull + q_buf), n_q >> 1, w))) return false;
-                }
-                if (!qk(g_q & 1, tile_keys(seg_q, i_q))) return false;
-                ++g_q;
-                if (++i_q == seg_q.cnt) {
-                    commit(bar(L::kBarQEmpty + q_buf));
-                    i_q = 0;
-                    ++n_q;
-                    more_q = walk_q.next(p, seg_q);
+            int n_q = 0, i_q = 0, g_q = 0, b_q = 0;  // its segment, step of the segment, step, score buffer
+            const auto scores_below = [&](int steps, int last_seg) {
+                while (more_q && g_q < steps && (i_q > 0 || n_q <= last_seg)) {
+                    if (i_q == 0) {
+                        q_buf = n_q & 1;
+                        if (!(ok = wait_all(bar(L::kBarQFull + q_buf), n_q >> 1, w))) return false;
+                    }
+                    if (!qk(b_q, tile_keys(seg_q, i_q))) return false;
+                    ++g_q;
+                    b_q = b_q + 1 == L::kScores ? 0 : b_q + 1;
+                    if (++i_q == seg_q.cnt) {
+                        commit(bar(L::kBarQEmpty + q_buf));
+                        i_q = 0;
+                        ++n_q;
+                        more_q = walk_q.next(p, seg_q);
+                    }
                 }
                 return true;
             };
-            if (next_qk()) next_qk();
-            int n_seg = 0, g = 0;  // segments, steps
+            scores_below(L::kScores, 1);
+            int n_seg = 0, g = 0, b = 0, b_phase = 0;  // segments, steps, score buffer and its round
             while (ok && walk.next(p, seg)) {
                 const int steps = seg.cnt;
                 for (int i = 0; i < steps; ++i, ++g) {
-                    const int t = g & 1;
-                    if (!(ok = wait_all(bar(L::kBarPReady + t), g >> 1, w))) break;
+                    if (!(ok = wait_all(bar(L::kBarPReady + b), b_phase, w))) break;
                     if (i == 0 && n_seg > 0 && !(ok = wait_all(bar(L::kBarOFree), n_seg - 1, w))) break;
                     tc_fence_after();
-                    if (!pv(t, i < 2, tile_keys(seg, i))) break;
-                    if (i + 1 == steps) commit(bar(L::kBarODone));  // ahead of the next segment's scores
-                    if (!next_qk()) break;
+                    if (!pv(b, i == 0, tile_keys(seg, i))) break;
+                    commit(bar(L::kBarPV + b));  // ahead of the next scores
+                    if (++b == L::kScores) {
+                        b = 0;
+                        ++b_phase;
+                    }
+                    if (!scores_below(g + 1 + L::kScores, n_seg + (i + 1 == steps ? 2 : 1))) break;
                 }
                 ++n_seg;
             }
@@ -680,7 +694,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     mbar_arrive(at);
             }
         };
-        int n_seg = 0, g = 0;  // segments, steps
+        int n_seg = 0, b = 0, b_phase = 0;  // segments, score buffer and its round
         int staged = -1;       // chunk: the buffer whose outputs are leaving
         const auto release = [&]() {
             if (lane == 0) {
@@ -690,25 +704,18 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
             staged = -1;
         };
         bool ok = true;
+        // The PV before the next step has finished (the scores of its step have been seen, so that the one three
+        // steps ahead of it has, and the next needs the next step's P).
+        const auto wait_pv = [&]() {
+            return wait_all(bar(L::kBarPV + (b == 0 ? L::kScores - 1 : b - 1)), b == 0 ? b_phase - 1 : b_phase, w);
+        };
         while (ok && walk.next(p, seg)) {
             const int steps = seg.cnt, tile_row = seg.row0 + kTile * rank;
-            // the running softmax of this step's stream and of the other, which change places after every step
-            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, m_other[2] = {-INFINITY, -INFINITY}, l_other[2] = {0.f, 0.f};
-            const auto change = [&]() {
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const float a = m[x], b = l[x];
-                    m[x] = m_other[x];
-                    l[x] = l_other[x];
-                    m_other[x] = a;
-                    l_other[x] = b;
-                }
-            };
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // the running softmax
 #pragma unroll 1
-            for (int i = 0; i < steps; ++i, ++g) {
-                const int t = g & 1;
-                const uint32_t t_s = tmem + lane_base + 256 * t;
-                if (!(ok = wait_all(bar(L::kBarSFull + t), g >> 1, w))) break;
+            for (int i = 0; i < steps; ++i) {
+                const uint32_t t_s = tmem + lane_base + 128 * b;
+                if (!(ok = wait_all(bar(L::kBarSFull + b), b_phase, w))) break;
                 tc_fence_after();
                 if (tile_row + warp_row < p.rows) {  // the warp has a row at all
                     uint32_t sr[64];
@@ -742,12 +749,6 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
 #pragma unroll
                         for (int k = 0; k < 64; ++k)
                             if (!(sees >> (2 * (k >> 2) + (k & 1)) & 1u)) sr[k] = 0xff800000u;
-                    }
-                    // The running maximum of a segment's first step is its scores', that of the second the first one's;
-                    // every later step has its stream's.
-                    if (i == 1) {
-                        m[0] = m_other[0];
-                        m[1] = m_other[1];
                     }
                     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
                     uint32_t pk[2][16];
@@ -798,17 +799,18 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                             if (grow) m[x] = mt[x];
                             l[x] *= f[x];
                         }
-                        if (i >= 2) {
-                            // O's earlier PVs have finished: S(g) complete implies it (QK(g) was issued after
-                            // PV(g - 2), and a commit covers every earlier MMA of the thread)
+                        if (i > 0 && __any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+                            if (!(ok = wait_pv())) break;
+                            tc_fence_after();
+                            const uint32_t t_o = tmem + lane_base + L::kOCol;
 #pragma unroll 1
                             for (int c = 0; c < 4; ++c) {
                                 uint32_t o[16];
-                                tmem_ld_16x32(t_s + 128 + 32 * c, o);
+                                tmem_ld_16x32(t_o + 32 * c, o);
                                 tmem_wait_ld();
 #pragma unroll
                                 for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[(k >> 1) & 1]);
-                                tmem_st_16x32(t_s + 128 + 32 * c, o);
+                                tmem_st_16x32(t_o + 32 * c, o);
                             }
                         }
                         exponentials();
@@ -823,56 +825,35 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                     }
                     tmem_wait_st();
                 }
-                arrive(r_ready + 8 * t);
-                change();
-                if (kChunk && staged >= 0 && i == min(1, steps - 1)) release();
+                arrive(r_ready + 8 * b);
+                if (++b == L::kScores) {
+                    b = 0;
+                    ++b_phase;
+                }
+                if (kChunk && staged >= 0) release();
             }
-            if (steps & 1) change();  // those of the segment's first stream are in m and l after an even number of steps
-            const int t0 = (g - steps) & 1;  // that stream
-            if (!(ok = ok && wait_all(bar(L::kBarODone), n_seg, w))) break;
+            if (!(ok = ok && wait_pv())) break;  // the segment's last
             tc_fence_after();
 #pragma unroll
             for (int x = 0; x < 2; ++x) {  // a quad has a row's sum
                 l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
                 l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-                l_other[x] += __shfl_xor_sync(0xffffffffu, l_other[x], 1);
-                l_other[x] += __shfl_xor_sync(0xffffffffu, l_other[x], 2);
             }
             if (tile_row + warp_row < p.rows) {
-                // The two streams joined.  A quad's lanes write 32 bytes of a row side by side, whole sectors: fp32 as
-                // they hold them, bf16 after two lanes have exchanged a pair of columns.
-                const bool two = steps > 1;  // else the other stream had no tile and its O holds nothing
                 const int i = tile_row + row;
-                float f0[2], f1[2];
+                float f[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const float top = two ? fmaxf(m[x], m_other[x]) : m[x];
-                    f0[x] = ex2_approx(m[x] - top);
-                    f1[x] = two ? ex2_approx(m_other[x] - top) : 0.f;
-                    const float total = l[x] * f0[x] + (two ? l_other[x] * f1[x] : 0.f);
-                    f0[x] /= total;
-                    f1[x] /= total;
+                    f[x] = 1.f / l[x];
                     if (!kChunk && i + 8 * x < p.rows && (lane & 3) == 0)
                         p.ws_lse[(int64_t)seg.slot * p.rows_cap + (i + 8 * x - seg.row0)] =
-                            (top + log2f(total)) * 0.69314718055994531f;
+                            (m[x] + log2f(l[x])) * 0.69314718055994531f;
                 }
-                const uint32_t t_o = tmem + lane_base + 128 + 256 * t0, t_o_other = tmem + lane_base + 128 + 256 * (t0 ^ 1);
                 uint32_t o[64];
-                tmem_ld_16x128(t_o, o);
+                tmem_ld_16x128(tmem + lane_base + L::kOCol, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 64; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f0[(k >> 1) & 1]);
-                if (two) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t b[16];
-                        tmem_ld_16x32(t_o_other + 32 * c, b);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            o[16 * c + k] = __float_as_uint(fmaf(__uint_as_float(b[k]), f1[(k >> 1) & 1], __uint_as_float(o[16 * c + k])));
-                    }
-                }
+                for (int k = 0; k < 64; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[(k >> 1) & 1]);
                 arrive(r_free);  // the next segment's products may start
                 if (kChunk) {
                     // through shared memory and out by TMA, clipped at the last row: rows lie 32 KB apart, and 8 bytes a
