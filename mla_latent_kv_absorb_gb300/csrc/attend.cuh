@@ -11,9 +11,9 @@
 // [keys][64], so a (row, key) pair costs 2 * (192 + 128) * 128 FLOP where the absorbed form costs
 // 2 * (576 + 512) * 128, and 64 KB of keys and values are read for each prefix token however many
 // rows there are: with up to some 220 rows that is what bounds the prefix form (HBM), beyond it
-// the tensor cores.  Measured with the merge: 64 rows x 8,192 keys 86 us, 93 % of the copy rate; 256 rows x 16,384
-// 260 us in a long run, 1.32 PFLOP/s (a plain library product 1.70 there), 216 alone (1.59; 1.91); a chunk of 4,096
-// queries under a window of 1,024 321 us.
+// the tensor cores.  Measured with the merge: 64 rows x 8,192 keys 85 us, 95 % of the copy rate; 256 rows x 16,384
+// 254 us in a long run, 1.35 PFLOP/s (a plain library product 1.70 there), 220 alone (1.56; 1.91); a chunk of 4,096
+// queries under a window of 1,024 303 us.
 //
 // A CTA holds a 128-row query tile of a head and streams 128-key tiles; with more than 128 rows a pair of CTAs
 // (two SMs, MMAs of M = 256) holds 256 rows, and each brings in half of every key tile (64 keys) and of every
@@ -282,7 +282,7 @@ struct Layout {
     static constexpr int kBarSFull = kBarQEmpty + 2;         // [score buffer]
     static constexpr int kBarPReady = kBarSFull + kScores;   // [score buffer], every softmax warp's arrival
     static constexpr int kBarPV = kBarPReady + kScores;      // [score buffer], the PV of its P has finished
-    static constexpr int kBarOFree = kBarPV + kScores;          // every softmax warp's arrival: the segment's O has been read
+    static constexpr int kBarOFree = kBarPV + kScores;       // every softmax warp's arrival: the segment's O has been read
     static constexpr int kBarStage = kBarOFree + 1;          // [buffer], eight warps: the outputs staged there have left (chunk)
     static constexpr int kBarEnd = kBarStage + 2;            // every MMA has finished
     static constexpr int kBars = kBarEnd + 1;
@@ -300,8 +300,8 @@ struct Layout {
 //   Q full       a query load into a buffer is issued after its Q empty (the last QK of the segment before).
 //   O free       once per segment; the next one's needs that segment's outputs, read after its last PV.
 //   stage        a chunk's outputs leave through the query tile's buffer of their segment; the next query load into
-//                it waits for that too.  They have left by the first step of the segment behind it; the scores ahead of that step
-//                are of that segment, so nothing the step needs waits for that load.
+//                it waits for that too.  They have left by the first step of the segment behind it; the scores ahead
+//                of that step are of that segment, so nothing the step needs waits for that load.
 //   ring         a slot is refilled only after its empty barrier, waited in order.
 
 struct Params {
@@ -462,9 +462,9 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         const uint64_t pol_kv = kChunk || p.groups > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
         const uint64_t pol_kr = l2_policy_evict_last();
         // Two walks: the keys are three steps ahead of the values, as the MMA warp takes them.  (The ring is all that is under way: bringing tiles
-        // into L2 ahead of it costs more than it gives once the pieces follow one another without a gap, for 64 rows
+        // into L2 ahead of it costs more than it gives once the pieces follow one another without a gap: for 64 rows
         // and 8,192 tokens 90 us with the values two steps ahead, 95 with whole tiles and 124 with fourteen of them,
-        // against 87.)
+        // where 87 was without.  Of 10 to 16 slots a pair takes the same time.)
         Walk<kChunk, kPair> walk_k(p);
         Segment seg_k;
         bool more_k = walk_k.next(p, seg_k);
