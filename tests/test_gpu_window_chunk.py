@@ -103,6 +103,16 @@ def test_chunk_wide(S, T, W, n):
     assert torch.isfinite(out.float()).all()
 
 
+# many short segments for each worker: one tile, two, three
+@pytest.mark.parametrize("S,T,W,n", [(2048, 2048, 1, 0), (2049, 2048, 1, 1), (2100, 2048, 130, 0), (4100, 2100, 130, 5)])
+def test_chunk_short_segments(S, T, W, n):
+    x = draw(S, T, W, n, seed=S + T + W + n)
+    out = run(x, S, W, n)
+    heads = [0, 77, 127]
+    au.check(out[:, heads], reference(x, heads), keys=min(S, W + n), **bounds(x, heads), what=f"S={S} T={T} W={W} n={n}")
+    assert torch.isfinite(out.float()).all()
+
+
 def test_whole_window_is_the_causal_chunk():
     """A window as long as the sequence sees what mla_prefill_decompressed sees."""
     S, T = 900, 300
