@@ -562,6 +562,8 @@ MLA_API mla_status mla_prefix_open(mla_kv_dtype kv_dtype, const void* kv_pool, c
  *   s_j = (q_c[r,h] . k[h,j] + q_R[r,h] . k_R[j]) * softmax_scale over all prefix tokens j,
  *   lse = logaddexp(own_lse, logsumexp_j s_j),
  *   out = exp(own_lse - lse) own_out + sum_j exp(s_j - lse) v[h,j].
+ * Tokens may score -infinity (k, but not v, may hold infinities); a row of which everything does, own_lse
+ * among it, gets zeros and an lse of -infinity.
  *   q_c, q_r    device bf16 [num_rows][128][128] / [num_rows][128][64] (already rotated: the prefix is
  *               positions 0 .. prefix_len - 1, the rows' own tokens lie behind it)
  *   k, v        device bf16 [128][prefix_len][128]; k_r device bf16, token j's 64 values at

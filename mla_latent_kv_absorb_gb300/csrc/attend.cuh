@@ -853,7 +853,8 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
                 tmem_ld_16x128(tmem + lane_base + L::kOCol, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int k = 0; k < 64; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f[(k >> 1) & 1]);
+                for (int k = 0; k < 64; ++k)  // a row whose scores were all -infinity has no sum: zeros
+                    o[k] = l[(k >> 1) & 1] == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * f[(k >> 1) & 1]);
                 arrive(r_free);  // the next segment's products may start
                 if (kChunk) {
                     // through shared memory and out by TMA, clipped at the last row: rows lie 32 KB apart, and 8 bytes a
@@ -966,6 +967,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
     }
     float top = fmaxf(fmaxf(own, part_lse[0]), fmaxf(part_lse[1], part_lse[2]));
     for (int c = c0 + kAtOnce; c <= c1; ++c) top = fmaxf(top, a.ws_lse[(int64_t)(c + run) * a.rows_cap + at]);
+    if (top == -INFINITY) top = 0.f;  // no part has seen a key: weights of zero, zeros out, a log-sum-exp of -infinity
     float total = 0.f, x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const auto add = [&](float part, const float4& o, const float4& q) {
         const float wgt = __expf(part - top);
@@ -990,7 +992,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) prefix_merge_kernel(const __
     if (own != -INFINITY)  // a row without own tokens may hold anything
         add(own, make_float4(dev::bf16_lo(own_o.x), dev::bf16_hi(own_o.x), dev::bf16_lo(own_o.y), dev::bf16_hi(own_o.y)),
             make_float4(dev::bf16_lo(own_o.z), dev::bf16_hi(own_o.z), dev::bf16_lo(own_o.w), dev::bf16_hi(own_o.w)));
-    const float inv = 1.f / total;
+    const float inv = total == 0.f ? 0.f : 1.f / total;
     reinterpret_cast<uint4*>(a.out + id * 128)[lane] =
         make_uint4(dev::pack_bf16x2(x[0] * inv, x[1] * inv), dev::pack_bf16x2(x[2] * inv, x[3] * inv),
                    dev::pack_bf16x2(x[4] * inv, x[5] * inv), dev::pack_bf16x2(x[6] * inv, x[7] * inv));
