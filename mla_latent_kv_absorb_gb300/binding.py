@@ -230,6 +230,12 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None, device=True):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _i32(x) -> int:
+    """A size for the C side, whose sizes have 32 bits: beyond them the nearest that they hold, not one that
+    wrapped round.  What is too small is refused there; a window or sinks past every length are those."""
+    return max(-1, min(int(x), 2 ** 31 - 1))
+
+
 # --------------------------------------------------------------------------- C ABI, same names
 
 def mla_plan_splits(seq_lens, num_sms: int, *, min_pages_per_split: int = 0, max_clusters: int = 0,
@@ -246,7 +252,7 @@ def mla_plan_splits(seq_lens, num_sms: int, *, min_pages_per_split: int = 0, max
         raise MlaError("mla_plan_splits", MLA_ERR_INVALID_ARG, "bad batch or SM count")
     buf = np.zeros(cap // 4, dtype=np.int32)
     opts = PlanOptions(int(min_pages_per_split), int(max_clusters), int(wait_timeout_ns), int(item_cost_pages),
-                       int(queries_per_seq), int(window), int(sinks))
+                       int(queries_per_seq), _i32(window), _i32(sinks))
     info = PlanInfo()
     st = lib().mla_plan_splits(lens.ctypes.data_as(ctypes.c_void_p), B, int(num_sms), ctypes.byref(opts),
                                buf.ctypes.data_as(ctypes.c_void_p), cap, ctypes.byref(info))
@@ -785,7 +791,7 @@ def prefill_chunk(seq_len: int, q_c: torch.Tensor, q_r: torch.Tensor, *, w_uk: t
 # --------------------------------------------------------------------------- windows and shared prefixes
 
 def mla_prefill_window_workspace_bytes(seq_len: int, chunk_len: int, window: int, sinks: int = 0) -> int:
-    size = int(lib().mla_prefill_window_workspace_bytes(int(seq_len), int(chunk_len), int(window), int(sinks)))
+    size = int(lib().mla_prefill_window_workspace_bytes(_i32(seq_len), _i32(chunk_len), _i32(window), _i32(sinks)))
     if size == 0:
         raise MlaError("mla_prefill_window_workspace_bytes", MLA_ERR_INVALID_ARG, "invalid sizes")
     return size
@@ -813,7 +819,7 @@ def mla_prefill_window(*, kv_pool: torch.Tensor, block_table_row: torch.Tensor, 
     if workspace is None:
         workspace = _scratch(mla_prefill_window_workspace_bytes(seq_len, T, window, sinks), q_c.device, stream)
     ws = _whole(workspace, "workspace", workspace.dtype, tuple(workspace.shape), device)
-    st = lib().mla_prefill_window(*cache, table, pages, int(seq_len), T, int(window), int(sinks), *ptrs,
+    st = lib().mla_prefill_window(*cache, table, pages, _i32(seq_len), T, _i32(window), _i32(sinks), *ptrs,
                                   float(softmax_scale), ws, workspace.numel() * workspace.element_size(), out_ptr, err,
                                   _stream(stream))
     if st:
@@ -918,7 +924,7 @@ class SharedPrefix:
         self._args = (self.prefix_len, self._num_sms), (k.data_ptr(), v.data_ptr(), k_r.data_ptr(), stride)
 
     def workspace_bytes(self, rows: int) -> int:
-        return int(lib().mla_prefix_attend_workspace_bytes(int(rows), self.prefix_len, self._num_sms))
+        return int(lib().mla_prefix_attend_workspace_bytes(_i32(rows), self.prefix_len, self._num_sms))
 
     def workspace(self, rows: int) -> torch.Tensor:
         """A workspace for mla_prefix_attend with that many query rows."""
@@ -1039,7 +1045,7 @@ class DecodeStep:
         self.batch = self.num_seqs * self.queries_per_seq
         self._plan_opts = dict(min_pages_per_split=min_pages_per_split, max_clusters=max_clusters,
                                wait_timeout_ns=wait_timeout_ns, item_cost_pages=item_cost_pages,
-                               queries_per_seq=self.queries_per_seq, window=int(window), sinks=int(sinks))
+                               queries_per_seq=self.queries_per_seq, window=_i32(window), sinks=_i32(sinks))
         self._num_sms = num_sms(self.device)
         self.plan_host, self.info = mla_plan_splits(self.seq_lens, self._num_sms, **self._plan_opts)
         self.plan_dev = torch.from_numpy(self.plan_host).to(self.device)
