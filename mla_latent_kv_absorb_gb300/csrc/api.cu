@@ -255,7 +255,6 @@ mla_status launch_decode_fp8(const mla_plan_info* info, const void* plan_dev, co
                          : nullptr;
     p.dev_error = dev_error;
     p.timeout_ns = (uint64_t)info->wait_timeout_ns;
-    p.sinks = std::min(info->sinks, 1 << 30);  // the kernel rounds it up to whole pages
     p.kv_scale = kv_scale;
 #ifdef MLA_DECODE_TRACE
     p.trace = g_trace;
@@ -349,7 +348,6 @@ mla_status launch_decode_bf16(const mla_plan_info* info, const void* plan_dev, c
                          : nullptr;
     p.dev_error = dev_error;
     p.timeout_ns = (uint64_t)info->wait_timeout_ns;
-    p.sinks = std::min(info->sinks, 1 << 30);  // the kernel rounds it up to whole pages
 #ifdef MLA_DECODE_TRACE
     p.trace = g_trace;
 #else

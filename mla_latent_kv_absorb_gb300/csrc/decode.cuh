@@ -201,7 +201,6 @@ struct Params {
     float* ws_lse;               // [partials][128]
     uint32_t* dev_error;
     uint64_t timeout_ns;
-    int32_t sinks;               // with a window: the first tokens that stay visible
     long long* trace;            // wait-cycle accounting (MLA_DECODE_TRACE builds only), else null
 };
 
@@ -223,8 +222,8 @@ __device__ __forceinline__ Item load_item(const int32_t* plan, int items_off, in
 template <bool kWindow>
 struct Seen {
     int seq_len, sinks, skip, hole_end;
-    __device__ __forceinline__ Seen(const Item& it, int sinks_)
-        : seq_len(it.seq_len), sinks(sinks_), skip(it.skip), hole_end(it.hole_end)
+    __device__ __forceinline__ Seen(const Item& it, const int32_t* plan)
+        : seq_len(it.seq_len), sinks(kWindow ? plan[kHdrSinks] : 0), skip(it.skip), hole_end(it.hole_end)
     {
     }
     __device__ __forceinline__ int page(int v) const { return !kWindow || v < ((sinks + 63) >> 6) ? v : v + skip; }
@@ -376,7 +375,7 @@ __device__ __forceinline__ void run_producer(const CUtensorMap* tm, const Params
     bool ok = true;
     for (int i = item_begin; i < item_end && ok; ++i) {
         const Item it = load_item(p.plan, items_off, i);
-        const Seen<kWindow> seen(it, p.sinks);
+        const Seen<kWindow> seen(it, p.plan);
         const int32_t* bt = p.block_table + (int64_t)it.table_row * p.max_pages;
         for (int pg0 = it.page_begin; pg0 < it.page_end && ok; pg0 += 32) {
             const int n = min(32, it.page_end - pg0);
@@ -435,7 +434,7 @@ __device__ __forceinline__ void score_producer(const CUtensorMap* tm, const CUte
     ok = __shfl_sync(0xffffffffu, ok, 0);
     for (int i = item_begin; i < item_end && ok; ++i) {
         const Item it = load_item(p.plan, items_off, i);
-        const Seen<kWindow> seen(it, p.sinks);
+        const Seen<kWindow> seen(it, p.plan);
         const int32_t* bt = p.block_table + (int64_t)it.table_row * p.max_pages;
         if (lane == 0) {
             // the item's q_abs rows (128 heads x 512 dims) as four ring entries of two 64-dim
@@ -759,7 +758,7 @@ __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, i
     int g = 0, G = 0;  // pages (messages) and four-page groups
     for (int i = item_begin; i < item_end; ++i) {
         const Item it = load_item(p.plan, items_off, i);
-        const Seen<kWindow> seen(it, p.sinks);
+        const Seen<kWindow> seen(it, p.plan);
         [[maybe_unused]] const long long tq0 = MLA_TRACE_NOW();
         if (set == 0) load_query_rope(p, it.seq, row, smem + kOffQR);
         __syncwarp();
@@ -1058,7 +1057,7 @@ __device__ __forceinline__ void value_correction(const Params& p, int item_begin
             if (flags & 2u) {
                 // slots that are not seen may hold anything (NaN): zero them so that
                 // p = 0 times them stays 0 in the PV contraction
-                const Seen<kWindow> seen(it, p.sinks);
+                const Seen<kWindow> seen(it, p.plan);
                 const int valid = seen.valid(t);
                 const int s = g % kValueStages;
                 if (!wait_warp(bars + 8 * (kFull0 + s), g / kValueStages, w)) goto done;

@@ -171,7 +171,6 @@ struct Params {
     float* ws_lse;               // [partials][128]
     uint32_t* dev_error;
     uint64_t timeout_ns;
-    int32_t sinks;               // with a window: the first tokens that stay visible
     const float* kv_scale;       // [pages][64] per-token scale of the e4m3 latent rows
     long long* trace;            // instrumented builds only, else null
 };
@@ -265,7 +264,7 @@ __device__ __forceinline__ void value_producer(const CUtensorMap* tm_c8, const P
     bool ok = true;
     for (int i = item_begin; i < item_end && ok; ++i) {
         const Item it = load_item(p.plan, items_off, i);
-        const Seen<kWindow> seen(it, p.sinks);
+        const Seen<kWindow> seen(it, p.plan);
         const int32_t* bt = p.block_table + (int64_t)it.table_row * p.max_pages;
         for (int pg0 = it.page_begin; pg0 < it.page_end && ok; pg0 += 32) {
             const int n = min(32, it.page_end - pg0);
@@ -320,7 +319,7 @@ __device__ __forceinline__ void score_producer(const CUtensorMap* tm_c8, const C
     bool ok = true;
     for (int i = item_begin; i < item_end && ok; ++i) {
         const Item it = load_item(p.plan, items_off, i);
-        const Seen<kWindow> seen(it, p.sinks);
+        const Seen<kWindow> seen(it, p.plan);
         const int32_t* bt = p.block_table + (int64_t)it.table_row * p.max_pages;
         if (lane == 0) {
             // the item's q_abs rows (128 heads x 512 dims) as four ring entries of two 64-dim
@@ -405,7 +404,7 @@ __device__ __forceinline__ void kr_convert(const CUtensorMap* tm_kr, const Param
     int G = 0;
     for (int i = item_begin; i < item_end; ++i) {
         const Item it = load_item(p.plan, items_off, i);
-        const Seen<kWindow> seen(it, p.sinks);
+        const Seen<kWindow> seen(it, p.plan);
         const int32_t* bt = p.block_table + (int64_t)it.table_row * p.max_pages;
         // largest scale over the item's tokens: lane k takes pages k, k + 32, ...; a page's
         // sixteen scale loads are in flight together, and the next page id is loaded before them,
@@ -812,7 +811,7 @@ __device__ __forceinline__ void score_softmax(const Params& p, int item_begin, i
     int g = 0, G = 0;  // pages (messages) and four-page groups
     for (int i = item_begin, n_item = 0; i < item_end; ++i, ++n_item) {
         const Item it = load_item(p.plan, items_off, i);
-        const Seen<kWindow> seen(it, p.sinks);
+        const Seen<kWindow> seen(it, p.plan);
         // The exchange slot of the query maxima: the group-max slot that the next group does not
         // use.  Group G - 1 (the previous item's last group, which also ran the l barrier) read it
         // before every softmax thread passed that barrier; group G + 1 writes it only after the
@@ -1101,7 +1100,7 @@ __device__ __forceinline__ void value_correction(const Params& p, int item_begin
             if (flags & 2u) {
                 // slots that are not seen may hold anything (NaN codes): zero them so that
                 // P~ = 0 times them stays 0 in the PV contraction
-                const Seen<kWindow> seen(it, p.sinks);
+                const Seen<kWindow> seen(it, p.plan);
                 const int valid = seen.valid(t);
                 const int s = g % kValueStages;
                 if (!wait_warp_ool(bars + 8 * (kFull0 + s), g / kValueStages, w)) goto done;

@@ -249,7 +249,7 @@ extern "C" mla_status mla_plan_splits(const int32_t* seq_lens, int32_t batch, in
     w[kHdrTimeoutLo] = (int32_t)(uint32_t)(timeout_ns & 0xffffffffu);
     w[kHdrTimeoutHi] = (int32_t)(uint32_t)((uint64_t)timeout_ns >> 32);
     w[kHdrQueriesPerSeq] = qps;
-    w[kHdrSinks] = sinks;
+    w[kHdrSinks] = std::min(sinks, 1 << 30);  // the kernels round it up to whole pages
     for (int64_t k = 0; k <= C; ++k) w[cl_off + k] = cluster_begin[k];
     std::memcpy(w + it_off, items.data(), (size_t)n_items * sizeof(PlanItem));
     if (n_comb) std::memcpy(w + cb_off, combine.data(), (size_t)n_comb * sizeof(PlanCombine));

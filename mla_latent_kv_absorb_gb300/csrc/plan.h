@@ -30,7 +30,7 @@ enum PlanHeader : int {
     kHdrTimeoutLo = 12,
     kHdrTimeoutHi = 13,
     kHdrQueriesPerSeq = 14,  // query tokens per sequence (1: ordinary decode)
-    kHdrSinks = 15,          // with a window: the first tokens that stay visible
+    kHdrSinks = 15,          // with a window: the first tokens that stay visible (at most 2^30, past every length)
 };
 
 // One work item: pages [page_begin, page_end) of query row `seq` (its visible context length
