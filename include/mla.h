@@ -569,7 +569,7 @@ MLA_API mla_status mla_prefix_open(mla_kv_dtype kv_dtype, const void* kv_pool, c
  *   k, v        device bf16 [128][prefix_len][128]; k_r device bf16, token j's 64 values at
  *               k_r + j * k_r_stride (elements, a multiple of 8, 64 .. 2^32)
  *   own_out     device bf16 [num_rows][128][128], own_lse device fp32 [num_rows][128] (natural log; -inf:
- *               no own tokens, that row of own_out is not read), or both NULL: the prefix alone
+ *               no own tokens, that row of own_out may hold anything), or both NULL: the prefix alone
  *   workspace   device, >= mla_prefix_attend_workspace_bytes(num_rows, prefix_len, num_sms); calls that
  *               may overlap need one each
  *   out         device bf16 [num_rows][128][128], may be own_out; otherwise shares no byte with the rest
@@ -578,7 +578,9 @@ MLA_API mla_status mla_prefix_open(mla_kv_dtype kv_dtype, const void* kv_pool, c
  *   dev_error   MLA_DEVERR_TIMEOUT for a bounded wait that ran out
  * bf16 and workspace pointers 16-byte aligned.  num_rows 0 enqueues nothing; more than 65,536 rows,
  * a prefix of more than 65535 * 128 tokens or more than 4,096 SMs are refused (MLA_ERR_UNSUPPORTED).
- * Results do not depend on the rows around them, and are the same from call to call. */
+ * For the same num_rows, prefix_len and num_sms a row's result is the same from call to call, whatever the
+ * other rows hold.  With another of the three the sums are split in other places, and results may differ
+ * in their rounding: a row decoded in batches of several sizes is not promised the same bits. */
 MLA_API size_t mla_prefix_attend_workspace_bytes(int32_t num_rows, int32_t prefix_len, int32_t num_sms);
 MLA_API mla_status mla_prefix_attend(int32_t num_rows, int32_t prefix_len, int32_t num_sms, const void* q_c,
                                      const void* q_r, const void* k, const void* v, const void* k_r,
