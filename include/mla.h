@@ -45,6 +45,13 @@
 extern "C" {
 #endif
 
+/* The structs below carry no size: a program is built with the header of the library that it loads.  The
+ * version counts their changes and those of signatures (2: window and sinks at the ends of mla_plan_options
+ * and mla_plan_info, which mla_plan_splits reads and writes); a program that opens a library by its path
+ * compares mla_abi_version() with the MLA_ABI_VERSION it was built with before any other call. */
+#define MLA_ABI_VERSION 2
+MLA_API int32_t mla_abi_version(void);
+
 #define MLA_NUM_HEADS 128
 #define MLA_HEAD_DIM 128   /* d_hc */
 #define MLA_LATENT_DIM 512 /* d_c  */

@@ -64,7 +64,10 @@ EXPORTS = ("mla_status_string", "mla_last_error_string", "mla_plan_bytes_max", "
            "mla_step_graph_destroy", "mla_prefill_workspace_bytes", "mla_prefill_decompressed",
            "mla_rope_init", "mla_rope", "mla_rope_append_kv", "mla_w4_packed_bytes", "mla_w4_pack",
            "mla_linear_w4", "mla_absorb_q_w4", "mla_out_proj_w4", "mla_prefix_open", "mla_prefix_attend_workspace_bytes",
-           "mla_prefix_attend", "mla_prefill_window_workspace_bytes", "mla_prefill_window")
+           "mla_prefix_attend", "mla_prefill_window_workspace_bytes", "mla_prefill_window", "mla_abi_version")
+
+# of the header that the structures and signatures here restate
+MLA_ABI_VERSION = 2
 
 # capacity of the library's fixed split-partial array (mla_decode_paged_static_ws)
 MLA_STATIC_WS_MAX_PARTIALS = 128
@@ -108,6 +111,9 @@ def lib() -> ctypes.CDLL:
         raise RuntimeError(f"{LIB_PATH} is missing: build it with __graft_entry__.build() or "
                            "python -m mla_latent_kv_absorb_gb300.build")
     L = ctypes.CDLL(LIB_PATH)
+    version = L.mla_abi_version() if hasattr(L, "mla_abi_version") else 1
+    if version != MLA_ABI_VERSION:
+        raise RuntimeError(f"{LIB_PATH} has ABI version {version}, this binding {MLA_ABI_VERSION}: build it again")
     P, i32, i64, sz, u32p = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
     L.mla_status_string.restype = ctypes.c_char_p
     L.mla_status_string.argtypes = [ctypes.c_int]

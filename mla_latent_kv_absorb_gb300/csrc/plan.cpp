@@ -34,6 +34,11 @@ constexpr int32_t kDefaultItemCostPages = 7;
 // 2 35.0; 64 sequences of one page on 8 pairs: the decode kernel takes 67 us, on 64 pairs some 21).
 constexpr int32_t kDefaultMinPages = 8, kWindowMinPages = 3;
 
+// A change of these sizes is a new MLA_ABI_VERSION.
+static_assert(sizeof(mla_plan_options) == 32 && sizeof(mla_plan_info) == 64, "ABI version 2");
+
+extern "C" int32_t mla_abi_version(void) { return MLA_ABI_VERSION; }
+
 extern "C" const char* mla_status_string(mla_status s)
 {
     switch (s) {
