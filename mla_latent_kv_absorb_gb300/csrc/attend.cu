@@ -88,7 +88,10 @@ mla_status sm_count(int* sms)
     return mla::cuda_status(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev), "cudaDeviceGetAttribute");
 }
 
-// The keys and values of `num` gathered rows of 576 for all heads: k and v [128][num][128].
+// The keys and values of `num` gathered rows of 576 for all heads: k and v [128][num][128].  Called directly
+// behind gather_one_sequence: the kernel reads the weights before it waits for the kernel ahead of it, and
+// what was launched before that one has ended by then only because the gather waits before it lets the next
+// kernel start.
 mla_status expand_rows(const void* rows, const void* w_uk, const void* w_uv, void* k, void* v, int32_t num,
                        uint32_t* dev_error, int sms, void* stream)
 {

@@ -82,7 +82,8 @@ expand_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant
 
     if (*abort_flag) {
     } else if (warp == 0) {
-        // the weights do not depend on the kernel before: they are under way while it ends
+        // The weights are under way while the gather ahead ends, which does not write them; whatever did has
+        // ended, because the gather lets this kernel start only behind its own wait (see expand_rows).
         const bool leader = elect_lane();
         const uint64_t pol = l2_policy_evict_last();
         const CUtensorMap* map = rank == 0 ? &tm_uk : &tm_uv;

@@ -73,6 +73,8 @@ struct Args {
 __global__ void __launch_bounds__(kWarps * 32) gather_kv_kernel(const Args a)
 {
     if (!a.seq_lens) {  // one sequence: a dependent launch, whose rows the next kernel waits for in turn
+        // In this order: the decompression reads its weights ahead of its own wait, and counts on all before
+        // this kernel having ended when it starts.
         dev::griddep_wait();
         dev::griddep_launch_dependents();
     }

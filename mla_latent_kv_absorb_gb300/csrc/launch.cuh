@@ -31,7 +31,10 @@ inline mla_status cuda_status(cudaError_t e, const char* where)
 }
 
 // The kernel may be scheduled while the kernel ahead of it in the stream still runs; it waits for
-// that kernel's end itself (griddepcontrol.wait) before it touches any caller memory.
+// that kernel's end itself (griddepcontrol.wait) before it touches any caller memory.  One kernel reads
+// ahead of that wait: expand_kernel its weights, which asks for a kernel ahead of it that lets its
+// dependents start only behind its own wait (see expand_rows); kernels that do so first (the step's
+// products, combine, tail) would let the weights be read while an earlier kernel still writes them.
 template <typename... KArgs, typename... Args>
 mla_status launch_dependent(const char* where, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                             void* stream, Args&&... args)
