@@ -76,8 +76,14 @@ mla_status launch_attend(const Maps& m, const mla::attend::Params& p, int worker
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<kPair>::kSmemBytes),
         "cudaFuncSetAttribute(max dynamic shared memory)");
     if (st != MLA_OK) return st;
-    return mla::launch_dependent("attend kernel launch", kernel, dim3((unsigned)(kPair ? 2 * workers : workers)), dim3(kThreads),
-                                 Layout<kPair>::kSmemBytes, stream, m.qc, m.qr, m.k, m.kr, m.v, m.out, p);
+    const auto launch = [&](const OutMap<kChunk>& out) {
+        return mla::launch_dependent("attend kernel launch", kernel, dim3((unsigned)(kPair ? 2 * workers : workers)),
+                                     dim3(kThreads), Layout<kPair>::kSmemBytes, stream, m.qc, m.qr, m.k, m.kr, m.v, out, p);
+    };
+    if constexpr (kChunk)
+        return launch(m.out);
+    else
+        return launch(NoMap{});
 }
 
 mla_status sm_count(int* sms)

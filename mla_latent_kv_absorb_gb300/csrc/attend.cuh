@@ -47,6 +47,8 @@
 // cut evenly, so that every SM streams the same number of bytes; a CTA's piece of one (head, group)
 // run is a segment, written as one partial.  Every wait is bounded.
 #pragma once
+#include <type_traits>
+
 #include "ptx.cuh"
 
 namespace mla {
@@ -354,7 +356,7 @@ struct Walk {
         if (at >= end) return false;
         if (kChunk) {
             // a head's groups lie side by side: their windows overlap and are read from L2
-            s.head = (int)at / p.groups;  // at most 128 x 32,768
+            s.head = (int)at / p.groups;  // at most 128 x 65,535: a chunk has at most 65,535 groups of 128 (kMaxKeys)
             s.row0 = ((int)at - s.head * p.groups) * kRows;
             const int last = min(s.row0 + kRows, p.rows) - 1;
             const int lo = max(0, p.hi0 + s.row0 - p.window + 1);  // the first key in the first row's window
@@ -392,12 +394,17 @@ __device__ __forceinline__ int tile_keys(const Segment& s, int n)
     return min(kTile, (((n < s.lead ? s.lead_end : s.end) - first_key(s, n)) + 31) & ~31);
 }
 
+// The map of the outputs, which a chunk alone writes by TMA.
+struct NoMap {};
+template <bool kChunk>
+using OutMap = std::conditional_t<kChunk, CUtensorMap, NoMap>;
+
 template <bool kChunk, bool kPair>
 // 11 warps: three SM sub-partitions hold three of them, 16K registers each: at most 3 x 32 x 168
 __global__ void __cluster_dims__(kPair ? 2 : 1, 1, 1) __maxnreg__(168)
 attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__ CUtensorMap tm_qr,
               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_kr,
-              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_out,
+              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ OutMap<kChunk> tm_out,
               const __grid_constant__ Params p)
 {
     using namespace dev;
@@ -420,7 +427,7 @@ attend_kernel(const __grid_constant__ CUtensorMap tm_qc, const __grid_constant__
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar(L::kBarQFull + b), 1);
             mbar_init(bar(L::kBarQEmpty + b), 1);
-            mbar_init(bar(L::kBarStage + b), 8);
+            if (kChunk) mbar_init(bar(L::kBarStage + b), 8);
         }
         for (int b = 0; b < L::kScores; ++b) {
             mbar_init(bar(L::kBarSFull + b), 1);
