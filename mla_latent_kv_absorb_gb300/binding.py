@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from contextlib import nullcontext
 from functools import partial
 from typing import Optional
 
@@ -832,15 +833,23 @@ def mla_prefill_window(*, kv_pool: torch.Tensor, block_table_row: torch.Tensor, 
         _check("mla_prefill_window", st)
 
 
-def _scratch(size: int, device, stream) -> torch.Tensor:
-    """A workspace of one call on ``stream``, from that stream's memory: what is let go of when the call
-    returns is handed out again on that stream alone, behind the call's kernels."""
+def _on(stream, device):
+    """A context with the stream that a call is sent to as the current one: what is allocated or filled in it
+    is that stream's, so that what is let go of when the call returns is handed out again on that stream
+    alone, behind the call's kernels."""
     if stream is not None:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         if handle != _stream(None):
-            with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
-                return torch.empty(max(16, size), dtype=torch.uint8, device=device)
-    return torch.empty(max(16, size), dtype=torch.uint8, device=device)
+            # (an ExternalStream of 0 would be a new stream, not the default one)
+            return torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device) if handle else
+                                     torch.cuda.default_stream(device))
+    return nullcontext()
+
+
+def _scratch(size: int, device, stream) -> torch.Tensor:
+    """A workspace of one call on ``stream``, from that stream's memory."""
+    with _on(stream, device):
+        return torch.empty(max(16, size), dtype=torch.uint8, device=device)
 
 
 def _cache(kv_pool, kv_scale, kr_pool, device: int):
