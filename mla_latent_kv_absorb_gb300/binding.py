@@ -757,7 +757,7 @@ def mla_prefill_decompressed(*, kv_pool: torch.Tensor, block_table_row: torch.Te
     _need(dev_error, "dev_error", torch.int32, (1,))
     need = int(lib().mla_prefill_workspace_bytes(int(seq_len)))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q_c.device)
+        workspace = _scratch(need, q_c.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     dtype = _kv_dtype(kv_pool, kv_scale, kr_pool)
     st = lib().mla_prefill_decompressed(dtype, _ptr(kv_pool), _ptr(kv_scale), _ptr(kr_pool), int(kv_pool.shape[0]),
@@ -778,21 +778,22 @@ def prefill_chunk(seq_len: int, q_c: torch.Tensor, q_r: torch.Tensor, *, w_uk: t
     (out [T, 128, 128], device error word)."""
     T = int(q_c.shape[0])
     bt = block_table_row.reshape(1, -1)
-    if T < threshold:
-        step = DecodeStep(np.array([seq_len], np.int32), w_uk=w_uk, w_uv=w_uv, kv_pool=kv_pool, block_table=bt,
-                          kv_scale=kv_scale, kr_pool=kr_pool, device=q_c.device, queries_per_seq=T,
-                          softmax_scale=softmax_scale, window=window, sinks=sinks)
-        return step.run(q_c, q_r, stream), step.dev_error
-    if isinstance(w_uk, W4Weight) or isinstance(w_uv, W4Weight):
-        raise ValueError(f"prefill_chunk: chunks of {threshold} or more new tokens read bf16 weights")
-    out = torch.empty(T, NUM_HEADS, D_HC, dtype=torch.bfloat16, device=q_c.device)
-    err = torch.zeros(1, dtype=torch.int32, device=q_c.device)
-    if sinks and not window:
-        raise ValueError("sinks need a window")
-    attend = partial(mla_prefill_window, window=window, sinks=sinks) if window else mla_prefill_decompressed
-    attend(kv_pool=kv_pool, block_table_row=bt[0], seq_len=seq_len, q_c=q_c, q_r=q_r, w_uk=w_uk, w_uv=w_uv, out=out,
-           dev_error=err, kv_scale=kv_scale, kr_pool=kr_pool, softmax_scale=softmax_scale, stream=stream)
-    return out, err
+    with _on(stream, q_c.device):  # the plan, the buffers and their zeros too
+        if T < threshold:
+            step = DecodeStep(np.array([seq_len], np.int32), w_uk=w_uk, w_uv=w_uv, kv_pool=kv_pool, block_table=bt,
+                              kv_scale=kv_scale, kr_pool=kr_pool, device=q_c.device, queries_per_seq=T,
+                              softmax_scale=softmax_scale, window=window, sinks=sinks)
+            return step.run(q_c, q_r), step.dev_error
+        if isinstance(w_uk, W4Weight) or isinstance(w_uv, W4Weight):
+            raise ValueError(f"prefill_chunk: chunks of {threshold} or more new tokens read bf16 weights")
+        if sinks and not window:
+            raise ValueError("sinks need a window")
+        out = torch.empty(T, NUM_HEADS, D_HC, dtype=torch.bfloat16, device=q_c.device)
+        err = torch.zeros(1, dtype=torch.int32, device=q_c.device)
+        attend = partial(mla_prefill_window, window=window, sinks=sinks) if window else mla_prefill_decompressed
+        attend(kv_pool=kv_pool, block_table_row=bt[0], seq_len=seq_len, q_c=q_c, q_r=q_r, w_uk=w_uk, w_uv=w_uv, out=out,
+               dev_error=err, kv_scale=kv_scale, kr_pool=kr_pool, softmax_scale=softmax_scale)
+        return out, err
 
 
 # --------------------------------------------------------------------------- windows and shared prefixes
