@@ -1065,6 +1065,7 @@ class DecodeStep:
         self._num_sms = num_sms(self.device)
         self.plan_host, self.info = mla_plan_splits(self.seq_lens, self._num_sms, **self._plan_opts)
         self.plan_dev = torch.from_numpy(self.plan_host).to(self.device)
+        self._plan_info = self.info  # of the plan that run takes; info is that of the last step, run_host's too
         self.w_uk, self.w_uv = w_uk, w_uv
         self.kv_pool, self.kv_scale, self.kr_pool = kv_pool, kv_scale, kr_pool
         self.block_table = block_table
@@ -1094,16 +1095,16 @@ class DecodeStep:
                   dev_error=self.dev_error, workspace=self.workspace, kv_scale=self.kv_scale, kr_pool=self.kr_pool,
                   softmax_scale=self.softmax_scale, stream=stream)
         if self.fused_absorb:
-            mla_absorb_decode_paged(self.info, self.plan_dev, q_c, self.w_uk, self.q_abs, self.absorb_sync, q_r, **kv)
+            mla_absorb_decode_paged(self._plan_info, self.plan_dev, q_c, self.w_uk, self.q_abs, self.absorb_sync, q_r, **kv)
         else:
             absorb = mla_absorb_q_w4 if isinstance(self.w_uk, W4Weight) else mla_absorb_q
             absorb(q_c, self.w_uk, self.q_abs, stream)
-            mla_decode_paged(self.info, self.plan_dev, self.q_abs, q_r, **kv)
+            mla_decode_paged(self._plan_info, self.plan_dev, self.q_abs, q_r, **kv)
         if self.fused_tail:
-            mla_merge_out_proj(self.info, self.plan_dev, self.workspace, self.o_lat, self.lse, self.w_uv, self.out,
+            mla_merge_out_proj(self._plan_info, self.plan_dev, self.workspace, self.o_lat, self.lse, self.w_uv, self.out,
                                self.dev_error, stream)
         else:
-            mla_combine_splits(self.info, self.plan_dev, self.workspace, self.o_lat, self.lse, stream)
+            mla_combine_splits(self._plan_info, self.plan_dev, self.workspace, self.o_lat, self.lse, stream)
             project = mla_out_proj_w4 if isinstance(self.w_uv, W4Weight) else mla_out_proj
             project(self.o_lat, self.w_uv, self.out, stream)
         if self.prefix is not None:
@@ -1276,7 +1277,7 @@ class DecodeStep:
         n += 2 if self.prefix is not None else 0
         if self.fused_tail:
             return n + 1
-        return n + 1 + (1 if self.info.num_combine > 0 else 0)
+        return n + 1 + (1 if self._plan_info.num_combine > 0 else 0)
 
 
 def graph_kernel_nodes(raw_graph: int) -> int:
