@@ -1087,6 +1087,7 @@ class DecodeStep:
             self.q_r = torch.empty(B, NUM_HEADS, D_R, dtype=torch.bfloat16, device=self.device)
         self.prefix = prefix
         self.prefix_workspace = None if prefix is None else prefix.workspace(B)
+        self._host_workspace = self.workspace  # run_host's: a larger one where its lengths need it
         self._h_stage = self._d_stage = None  # pinned host / device staging of run_host
         self._host_graph = None  # (mla_step_graph handle, key of the buffers and lengths it was made for)
 
@@ -1195,8 +1196,9 @@ class DecodeStep:
             self.seq_lens = lens.copy()
             _, info = mla_plan_splits(lens, self._num_sms, **self._plan_opts)
             ws = int(info.workspace_bytes)
-            if ws and (self.workspace is None or self.workspace.numel() * 4 < ws):
-                self.workspace = torch.empty(ws // 4, dtype=torch.float32, device=self.device)
+            if ws and (self._host_workspace is None or self._host_workspace.numel() * 4 < ws):
+                # (beside run's, whose address a graph of capture() holds)
+                self._host_workspace = torch.empty(ws // 4, dtype=torch.float32, device=self.device)
             if self._h_stage is None:
                 cap = int(lib().mla_plan_bytes_max(B, self._num_sms))
                 self._h_stage = torch.empty(cap // 4, dtype=torch.int32).pin_memory()
@@ -1216,8 +1218,8 @@ class DecodeStep:
         _need(out, "out", torch.bfloat16, (B, NUM_HEADS, D_HC), device=False)
         dtype = MLA_KV_BF16 if self.kv_scale is None else MLA_KV_FP8_E4M3
         bufs = StepBuffers(_addr(self._q_c_dev), _addr(self._q_r_dev), _addr(self.q_abs), _addr(bt_dev),
-                           _addr(self._d_stage), _addr(self.workspace),
-                           0 if self.workspace is None else self.workspace.numel() * 4, _addr(self.o_lat),
+                           _addr(self._d_stage), _addr(self._host_workspace),
+                           0 if self._host_workspace is None else self._host_workspace.numel() * 4, _addr(self.o_lat),
                            _addr(self.lse), _addr(self.out), _addr(self.dev_error), _addr(self._h_stage),
                            self._h_stage.numel() * 4)
         opts = PlanOptions(int(self._plan_opts["min_pages_per_split"]), int(self._plan_opts["max_clusters"]),
