@@ -737,7 +737,10 @@ def mla_out_proj_w4(o_lat: torch.Tensor, w_uv: W4Weight, out: torch.Tensor, stre
 
 
 # Chunks of at least this many new tokens take the decompressed form, shorter ones the absorbed
-# decode (page 1 section 3, kPrefillThresh in mla_config.h; section 6 measures the switch).
+# decode (page 1 section 3, kPrefillThresh in mla_config.h; section 6 measures the switch).  Under a
+# window the decompression is of the window alone and pays much earlier: from some 16 new tokens on under
+# 512, 32 to 64 under 1,024, 64 to 96 under 4,096 (255 tokens under 1,024: some 155 us absorbed, 71 in the
+# chunk form).  The default is the same there, and `threshold` says otherwise.
 PREFILL_THRESHOLD = 256
 
 

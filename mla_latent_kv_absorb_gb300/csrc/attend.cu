@@ -181,7 +181,8 @@ Span chunk_span(int32_t seq_len, int32_t chunk_len, int32_t window, int32_t sink
 // rounds; a segment costs its key tiles and some 3,000 cycles.  A pair's tile takes 1,650 cycles and serves 256
 // rows; a CTA alone brings in the whole tile for 128, 1,850, but has fewer keys that only other rows of the
 // group see, and smaller pieces to share out.  Whole calls, pairs against CTAs alone: 257 queries under 511
-// 59.0 and 49.3 us, 1,024 under 512 99.3 and 97.4, 2,000 under 300 153 and 145, 4,096 under 1,024 415 and 423.
+// 59.0 and 49.3 us, 1,024 under 512 99.3 and 97.4, 2,000 under 300 153 and 145, 4,096 under 1,024 415 and 423; where
+// the two estimates lie close it can miss: 4,096 under 128 take CTAs alone, 242 us, where pairs take 236.
 constexpr int64_t kPairTile = 1650, kAloneTile = 1850, kSegment = 3000;
 
 struct ChunkCut {

@@ -4,7 +4,9 @@
 //
 // for the rows c_i (512 values) of a prefix or of a chunk's span.  128 products (one head's keys and values) of
 // [256 rows x 512] by [512 x 256] for every tile of 256 rows, 33.5 MFLOP a row: bound by the tensor cores.
-// Measured: 8,192 rows 155 us (under ncu; 1.77 PFLOP/s, tensor pipe 87 % busy), 4,100 rows 78, 2,051 rows 47.
+// Measured: 8,192 rows 152 us (under ncu; 1.81 PFLOP/s, tensor pipe 83 % busy), 4,100 rows 79.5, 2,051 rows 48.
+// The rows are bf16, as mla_gather_kv gives them: of an FP8 or NVFP4 cache the product of code and token scale has been
+// rounded once more (opened keys and values 0.0023 off 64 bits for 0.0017, relative L2).
 //
 // A pair of CTAs (two SMs) takes a product: M = 256, each CTA with 128 of the rows and of the sums, and half of
 // N, the even one W_UK[h], the odd one W_UV[h].  Persistent: the products lie in one line, row tile by row tile,

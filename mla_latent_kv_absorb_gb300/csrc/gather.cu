@@ -97,6 +97,8 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kv_kernel(const Args a)
         if (lane < 8) dst[64 + lane] = __ldg(src + 64 + lane);
         return;
     }
+    // The rows leave as bf16, the type of the caches without codes and of the matrix instructions that read them, so
+    // that one row layout serves all three caches: code times scale is rounded once, by half a step at most.
     const float sigma = __ldg(a.scale + tok);
     float v[16];
     if (a.kv_dtype == MLA_KV_FP8_E4M3) {

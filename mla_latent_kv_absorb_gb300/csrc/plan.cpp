@@ -30,8 +30,10 @@ constexpr int32_t kDefaultItemCostPages = 7;
 
 // Least pages of an item.  Without a window contexts are long and eight keep the merge small.  Under a window
 // a step is short, and what counts is that every pair has something to do: three, and a pair for every row
-// while there are pairs (one sequence with a window of 4,096, graph replays: 8 pages 39.6 us, 4 36.9, 3 35.2,
-// 2 35.0; 64 sequences of one page on 8 pairs: the decode kernel takes 67 us, on 64 pairs some 21).
+// while there are pairs (64 sequences of one page on 8 pairs: the decode kernel takes 67 us, on 64 pairs some 21).
+// Steps of 1, 2, 3, 4 and 8 pages at least (graph replays behind an L2 flush, us): one sequence under 4,096 46 44 42 43
+// 46, from FP8 53 51 51 53 59; under 1,024 39 39 39 43 46; two under 512 39 40 42 42 44; four under 4,096 44 44 44 44
+// 50; eight under 2,048 45 46 45 45 54, from FP8 50 51 52 52 63; with 64 rows and more all the same.
 constexpr int32_t kDefaultMinPages = 8, kWindowMinPages = 3;
 
 // A change of these sizes is a new MLA_ABI_VERSION.
